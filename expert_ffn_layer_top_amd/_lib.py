@@ -28,6 +28,9 @@ SIGNATURES = {
     "moe_route_balance_workspace_bytes": (_sz, [_i, _i]),
     "moe_route_balance": (_i, [_p, _p, _i, _i, _i, _p, _p, _p, _sz, _p]),
     "moe_route_topk_bwd_balance": (_i, [_p, _p, _p, _p, _p, ctypes.c_float, _i, _i, _i, _p, _p]),
+    "moe_route_scored": (_i, [_p, _p, _i, _i, _i, _i, _i, _i, _i, _i, ctypes.c_float, _p, _p, _p, _p, _p, _p, _i,
+                              _p, _p, _p, _sz, _p]),
+    "moe_route_scored_bwd": (_i, [_p, _p, _p, _i, _i, _i, _i, _i, ctypes.c_float, _p, _p]),
     "moe_permute": (_i, [_i, _p, _p, _p, _i, _i, _i, _p, _p, _p]),
     "moe_unpermute_combine": (_i, [_p, _p, _p, _i, _i, _i, _p, _p]),
     "moe_unpermute_combine_bwd": (_i, [_p, _p, _p, _p, _i, _i, _i, _p, _p, _p]),
@@ -58,6 +61,15 @@ SIGNATURES = {
                                             _p, _p]),
     "moe_grouped_gemm_wgrad_gate_up": (_i, [_i, _i, _i, _i, _i, _p, _p, _p, _p, _p, _p, _p, _p, _p,
                                             _p, _p]),
+    "moe_fp8b_quantize_rows": (_i, [_p, _p, _i, _i, _i, _p, _p, _p]),
+    "moe_fp8b_quantize_rows_grouped": (_i, [_p, _p, _p, _p, _p, _i, _i, _i, _p, _p, _p, _p, _p]),
+    "moe_fp8b_quantize_weights": (_i, [_p, _i, _i, _i, _p, _p, _p, _p, _p]),
+    "moe_grouped_gemm_gate_up_fp8b": (_i, [_i] * 4 + [_p] * 11),
+    "moe_grouped_gemm_down_fp8b": (_i, [_i] * 4 + [_p] * 7),
+    "moe_grouped_gemm_dgrad_down_fp8b": (_i, [_i] * 4 + [_p] * 10),
+    "moe_grouped_gemm_dgrad_gate_up_fp8b": (_i, [_i] * 4 + [_p] * 11),
+    "moe_grouped_gemm_wgrad_down_fp8b": (_i, [_i] * 4 + [_p] * 8),
+    "moe_grouped_gemm_wgrad_gate_up_fp8b": (_i, [_i] * 4 + [_p] * 11),
 }
 
 

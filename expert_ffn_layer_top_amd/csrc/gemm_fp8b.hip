@@ -1,0 +1,709 @@
+// Device-scheduled grouped GEMMs of the SwiGLU expert FFN on E4M3 codes with one fp32 scale per block
+// of 128 along the contraction dimension, forward and backward, on the fp8 matrix cores
+// (v_mfma_f32_16x16x128_f8f6f4: one instruction contracts exactly one block).
+//
+//   out[r][c] = sum over blocks b of  sa[b][r] * sb * sum over k in b of qa[r][k] qb[c][k]
+//
+// sb is one value per 128 x 128 block of a weight matrix (forward and dgrad products), or one per
+// column and block (weight gradients, where both operands are blocks of 128 tokens).  A block's sum
+// comes out of the matrix core in fp32 and is scaled into the running sum by fp32 FMAs, so nothing is
+// rounded between the codes and the one rounding to bf16 at the end.
+//
+// Products and operands (all codes K-contiguous):
+//   FWD1   xq [n][d]           x  W_gate, W_up [f][d]               -> G, U, A = silu(G) U
+//   FWD2   aq [n][f]           x  W_down [d][f]                     -> Yexp
+//   DGRAD1 dyq [n][d]          x  W_down^T [f][d]                   -> dG, dU (SwiGLU backward)
+//   DGRAD2 dgq | duq [n][f]    x  W_gate^T | W_up^T [d][f]          -> dXp   (two contractions, one sum)
+//   WGRAD_DOWN  dy^T [d][P]    x  a^T [f][P]                        -> dW_down[e]
+//   WGRAD_GU    dg^T | du^T [f][P]  x  x^T [d][P]                   -> dW_gate[e], dW_up[e]
+// where P is the padded token axis: expert e owns positions [offsets_pad[e], offsets_pad[e + 1]), whole
+// blocks of 128.
+//
+// Tile: 256 x 256 outputs per workgroup of eight waves, 64 rows x 128 columns each (two waves per
+// SIMD).  The running sums must be plain vector registers, since vector instructions cannot use
+// accumulation registers as operands: 128 of a wave's 256, which is why the waves are half the size of
+// the MXFP8 kernel's, whose scales the matrix core applies.  While one wave's FMAs run (4 per MFMA), the
+// other's MFMAs keep the matrix core busy.  K steps of 128 go through a two-stage LDS ring filled by
+// LDS-DMA loads, XOR-swizzled 16-byte chunks, one barrier per step; the steps of a workgroup's tiles
+// form one stream.  Lane l of a fragment holds row l % 16, bytes 16 (l / 16) .. + 15 and
+// 64 + 16 (l / 16) .. + 15 of the step (any order serves, being the same for both operands); the product
+// takes columns from the first operand, so a lane ends with 4 consecutive columns of one row and
+// needs one row scale per 16 x 16 tile.
+#include <type_traits>
+
+#include "common.h"
+#include "fp8b_common.h"
+#include "gemm_epilogue.h"
+#include "gemm_sched.h"
+
+namespace moe {
+namespace g8b {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) void lds_void;
+typedef __attribute__((address_space(3))) uint8_t lds_u8;
+
+constexpr int BM = 256;
+constexpr int BN = 256;
+constexpr int BK = 128;                            // codes (bytes) per K step = one scale block
+constexpr int NTH = 512;
+constexpr int OP_BYTES = BM * BK;                  // 32 KiB per operand per stage
+constexpr int SC_BYTES = BM * 4;                   // one scale per row per stage
+constexpr int A_RING = 0;
+constexpr int B_RING = 2 * OP_BYTES;
+constexpr int SA_RING = 4 * OP_BYTES;
+constexpr int SB_RING = SA_RING + 2 * SC_BYTES;
+constexpr int LDS_TOTAL = SB_RING + 2 * SC_BYTES;  // 132 KiB
+constexpr int STG_BYTES = 2 * OP_BYTES / 8;        // epilogue staging per wave, in the stage just consumed
+
+__shared__ __attribute__((aligned(1024))) uint8_t lds_ring[LDS_TOTAL];
+
+__device__ __forceinline__ uint32_t lds_addr(const uint8_t* p) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((const lds_u8*)(p)));
+}
+
+enum Mode { FWD1 = 0, FWD2 = 1, DGRAD1 = 2, DGRAD2 = 3, WGRAD_DOWN = 4, WGRAD_GU = 5 };
+
+struct Params {
+  int cm, cn;                   // tile order: cells of cm m-tiles x cn n-tiles
+  const int32_t* offsets;
+  const int32_t* offsets_pad;   // WGRAD: padded token offsets
+  int E, n, d, f;
+  int P;                        // WGRAD: length of the padded token axis
+  const uint8_t* a0; const float* a0s;
+  const uint8_t* a1; const float* a1s;
+  const uint8_t* b0; const float* b0s;
+  const uint8_t* b1; const float* b1s;
+  const uint16_t* g;
+  const uint16_t* u;
+  uint16_t* o0;
+  uint16_t* o1;
+  uint16_t* o2;
+};
+
+template <int B, int E, class F>
+__device__ __forceinline__ void static_for(F&& f) {
+  if constexpr (B < E) {
+    f(std::integral_constant<int, B>{});
+    static_for<B + 1, E>(f);
+  }
+}
+
+constexpr bool is_wgrad(int mode) { return mode >= WGRAD_DOWN; }
+
+// Row r (128 bytes = 8 chunks of 16), chunk c stored at position c ^ ((r >> 1) & 7).
+__device__ __forceinline__ int kc_off(int r, int c) { return r * 128 + ((c ^ ((r >> 1) & 7)) << 4); }
+
+struct Tile {
+  int e, m0, m_end, n0, half;
+  int k_begin;   // WGRAD: first padded token position of the expert
+  int k_len;     // WGRAD: its padded tokens
+};
+
+template <int MODE>
+__host__ __device__ __forceinline__ int n_total(int d, int f) {
+  return (MODE == FWD1 || MODE == DGRAD1 || MODE == WGRAD_DOWN) ? f : d;
+}
+template <int MODE>
+__host__ __device__ __forceinline__ int n_tile_width() { return MODE == FWD1 ? BN / 2 : BN; }
+// contraction length of one operand (DGRAD2 runs two of them); the padded tokens for weight gradients
+template <int MODE>
+__host__ __device__ __forceinline__ int k_one(int d, int f) { return (MODE == FWD1 || MODE == DGRAD1) ? d : f; }
+template <int MODE>
+__host__ __device__ __forceinline__ int m_total(int d, int f) { return MODE == WGRAD_DOWN ? d : f; }
+
+using gsched::MTiles;
+
+// The tile with linear id `lid`: each expert owns a contiguous run of ids, its tiles in cell order.
+template <int MODE>
+__device__ __forceinline__ Tile tile_at(const Params& p, const MTiles& mts, int ntiles_n, int lid) {
+  Tile t{};
+  int mi, nt;
+  if constexpr (!is_wgrad(MODE)) {
+    int e, first;
+    gsched::mtile_find(mts, lid / ntiles_n, e, first);
+    e = __builtin_amdgcn_readfirstlane(e);
+    first = __builtin_amdgcn_readfirstlane(first);
+    const int r0 = p.offsets[e], r1 = p.offsets[e + 1];
+    gsched::cell_order(lid - first * ntiles_n, (r1 - r0 + BM - 1) / BM, ntiles_n, p.cm, p.cn, mi, nt);
+    t.e = e;
+    t.m0 = r0 + mi * BM;
+    t.m_end = r1;
+  } else {
+    const int Mtot = m_total<MODE>(p.d, p.f);
+    const int mt = (Mtot + BM - 1) / BM, rows = mt * (MODE == WGRAD_GU ? 2 : 1);
+    t.e = lid / (rows * ntiles_n);
+    gsched::cell_order(lid - t.e * rows * ntiles_n, rows, ntiles_n, p.cm, p.cn, mi, nt);
+    t.half = mi >= mt ? 1 : 0;
+    t.m0 = (mi - t.half * mt) * BM;
+    t.m_end = Mtot;
+    t.k_begin = p.offsets_pad[t.e];
+    t.k_len = p.offsets_pad[t.e + 1] - t.k_begin;
+  }
+  t.n0 = nt * n_tile_width<MODE>();
+  t.e = __builtin_amdgcn_readfirstlane(t.e);
+  t.m0 = __builtin_amdgcn_readfirstlane(t.m0);
+  t.m_end = __builtin_amdgcn_readfirstlane(t.m_end);
+  t.n0 = __builtin_amdgcn_readfirstlane(t.n0);
+  t.half = __builtin_amdgcn_readfirstlane(t.half);
+  t.k_begin = __builtin_amdgcn_readfirstlane(t.k_begin);
+  t.k_len = __builtin_amdgcn_readfirstlane(t.k_len);
+  return t;
+}
+
+// One wave's DMA sources of a tile: the codes' descriptor, bounded to the operand's extent (r1: the
+// second operand of DGRAD2), and where its row scales start (block 0, this tile's first row; row
+// scales of block b are `pitch` floats further each, and `rows` of them exist).
+struct TileSrc {
+  __amdgpu_buffer_rsrc_t r0, r1;
+  const float* s0;
+  const float* s1;
+  int rows;
+  int nk;   // K steps
+};
+
+template <int MODE>
+__device__ __forceinline__ TileSrc empty_src(const Params& p) {
+  TileSrc s{};
+  s.r0 = gep::rsrc(p.a0, 0);
+  s.r1 = s.r0;
+  s.s0 = p.a0s;
+  s.s1 = p.a0s;
+  return s;
+}
+
+template <int MODE>
+__device__ __forceinline__ TileSrc tile_src(const Params& p, const Tile& t, bool role_b, int h) {
+  TileSrc s{};
+  const int Kone = k_one<MODE>(p.d, p.f);
+  if constexpr (is_wgrad(MODE)) {
+    s.nk = (t.k_len + BK - 1) / BK;
+    const int C = role_b ? n_total<MODE>(p.d, p.f) : m_total<MODE>(p.d, p.f);
+    const int c0 = role_b ? t.n0 : t.m0;
+    const uint8_t* base = role_b ? p.b0 : (MODE == WGRAD_GU && t.half ? p.a1 : p.a0);
+    const float* sbase = role_b ? p.b0s : (MODE == WGRAD_GU && t.half ? p.a1s : p.a0s);
+    s.r0 = gep::rsrc(base + static_cast<long long>(c0) * p.P + t.k_begin, static_cast<long long>(C - c0) * p.P - t.k_begin);
+    s.r1 = s.r0;
+    s.s0 = sbase + static_cast<long long>(t.k_begin / BK) * C + c0;
+    s.s1 = s.s0;
+    s.rows = C - c0;
+  } else {
+    s.nk = static_cast<int>(fp8b_blocks(Kone)) * (MODE == DGRAD2 ? 2 : 1);
+    if (!role_b) {
+      const long long rows = static_cast<long long>(p.n) - t.m0;
+      s.r0 = gep::rsrc(p.a0 + static_cast<long long>(t.m0) * Kone, rows * Kone);
+      s.s0 = p.a0s + t.m0;
+      s.r1 = s.r0;
+      s.s1 = s.s0;
+      if constexpr (MODE == DGRAD2) {
+        s.r1 = gep::rsrc(p.a1 + static_cast<long long>(t.m0) * Kone, rows * Kone);
+        s.s1 = p.a1s + t.m0;
+      }
+      s.rows = static_cast<int>(rows);
+    } else {
+      const int N = n_total<MODE>(p.d, p.f);
+      const long long off = (static_cast<long long>(t.e) * N + t.n0) * Kone;
+      const long long bytes = static_cast<long long>(N - t.n0) * Kone;
+      s.r0 = gep::rsrc((MODE == FWD1 && h >= 2 ? p.b1 : p.b0) + off, bytes);
+      s.r1 = s.r0;
+      if constexpr (MODE == DGRAD2) s.r1 = gep::rsrc(p.b1 + off, bytes);
+      s.s0 = p.a0s;
+      s.s1 = p.a0s;
+    }
+  }
+  return s;
+}
+
+// Scale of the weight block that K block kb (of operand half `half`) and the tile's columns from
+// `col` on belong to; lane l asks for block kb + l.  Columns and blocks past the matrix read a
+// neighbour's scale, which only meets codes that read as zero.
+template <int MODE>
+__device__ __forceinline__ float weight_scale(const Params& p, const Tile& t, int col, int half, int kb) {
+  if constexpr (is_wgrad(MODE)) return 0.f;
+  const int N = n_total<MODE>(p.d, p.f);
+  const int nb = static_cast<int>(fp8b_blocks(N)), kbs = static_cast<int>(fp8b_blocks(k_one<MODE>(p.d, p.f)));
+  const int c = min(col / kFp8bBlock, nb - 1);
+  const int k = min(kb + static_cast<int>(threadIdx.x & 63), kbs - 1);
+  const float* s = half ? p.b1s : p.b0s;
+  return s[(static_cast<long long>(t.e) * nb + c) * kbs + k];
+}
+
+template <int OFF>
+__device__ __forceinline__ void ds_b128(i32x4& v, uint32_t addr) {
+  asm volatile("ds_read_b128 %0, %1 offset:%2" : "=v"(v) : "v"(addr), "i"(OFF));
+}
+template <int OFF>
+__device__ __forceinline__ void ds_f128(f32x4& v, uint32_t addr) {
+  asm volatile("ds_read_b128 %0, %1 offset:%2" : "=v"(v) : "v"(addr), "i"(OFF));
+}
+template <int OFF>
+__device__ __forceinline__ void ds_f32(float& v, uint32_t addr) {
+  asm volatile("ds_read_b32 %0, %1 offset:%2" : "=v"(v) : "v"(addr), "i"(OFF));
+}
+
+// Fragment Q (16 rows): both 16-byte chunks of this lane.
+template <int Q>
+__device__ __forceinline__ void read_frag(i32x8& v, uint32_t a0, uint32_t a1) {
+  i32x4 lo, hi;
+  ds_b128<2048 * Q>(lo, a0);
+  ds_b128<2048 * Q>(hi, a1);
+  v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// Waits until at most N LDS reads are outstanding and ties the registers that have then landed.
+template <int N>
+__device__ __forceinline__ void wait_rows(i32x8 (&a)[4], float (&sa)[4]) {
+  asm volatile("s_waitcnt lgkmcnt(%8)"
+               : "+v"(a[0]), "+v"(a[1]), "+v"(a[2]), "+v"(a[3]), "+v"(sa[0]), "+v"(sa[1]), "+v"(sa[2]), "+v"(sa[3])
+               : "n"(N));
+}
+template <int N>
+__device__ __forceinline__ void wait_col(i32x8& b) {
+  asm volatile("s_waitcnt lgkmcnt(%1)" : "+v"(b) : "n"(N));
+}
+template <int N>
+__device__ __forceinline__ void wait_col(i32x8& b, f32x4& sb) {
+  asm volatile("s_waitcnt lgkmcnt(%2)" : "+v"(b), "+v"(sb) : "n"(N));
+}
+
+__device__ __forceinline__ f32x4 mfma_block(const i32x8& x, const i32x8& y) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+}
+
+// Writes the tile's results, staged through this wave's 8 KiB of the stage just consumed.
+template <int MODE>
+__device__ __forceinline__ void epilogue(const Params& p, const Tile& t, f32x4 (&acc)[8][4], int wm, int wn, int lane,
+                                         uint32_t stg) {
+  using gep::u32x2;
+  using gep::u32x4;
+  const int row0 = t.m0 + 64 * wm;
+  const int rows_valid = t.m_end - row0;
+  if constexpr (MODE == FWD1) {
+    const int col0 = t.n0 + 64 * wn, cv = p.f - col0;
+    auto store = [&](uint16_t* out, auto&& val) {
+      const auto r = gep::out_rsrc(out, p.n, p.f, row0, col0);
+      gep::sfor<0, 2>([&](auto q) {
+        u32x2 v[2][4];
+        gep::sfor<0, 2>([&](auto jj) { gep::sfor<0, 4>([&](auto i) { v[jj][i] = val(i, std::integral_constant<int, 2 * q + jj>{}); }); });
+        gep::stage_out_round<4, 2>(v, q, r, rows_valid, cv, p.f, stg, lane);
+      });
+    };
+    if (p.o0 != nullptr) {
+      store(p.o0, [&](auto i, auto j) { return gep::pack4(acc[i][j]); });
+      store(p.o1, [&](auto i, auto j) { return gep::pack4(acc[i + 4][j]); });
+    }
+    store(p.o2, [&](auto i, auto j) {
+      f32x4 av;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) av[e] = acc[i][j][e] * gep::sigmoid(acc[i][j][e]) * acc[i + 4][j][e];
+      return gep::pack4(av);
+    });
+  } else if constexpr (MODE == DGRAD1) {
+    const int col0 = t.n0 + 128 * wn, cv = p.f - col0;
+    const auto rg = gep::out_rsrc(p.g, p.n, p.f, row0, col0), ru = gep::out_rsrc(p.u, p.n, p.f, row0, col0);
+    const auto rdg = gep::out_rsrc(p.o0, p.n, p.f, row0, col0), rdu = gep::out_rsrc(p.o1, p.n, p.f, row0, col0);
+    gep::sfor<0, 4>([&](auto q) {
+      u32x2 gm[1][8], um[1][8];
+      u32x4 gl[4], ul[4];
+      gep::load_rows<1>(rg, q, rows_valid, cv, p.f, lane, gl);
+      gep::load_rows<1>(ru, q, rows_valid, cv, p.f, lane, ul);
+      gep::stage_in_round<1>(gl, gm, stg, lane);
+      gep::stage_in_round<1>(ul, um, stg, lane);
+      gep::sfor<0, 8>([&](auto i) {
+        const u32x2 g2 = gm[0][i], u2 = um[0][i];
+        const float gv[4] = {bf16_lo(g2.x), bf16_hi(g2.x), bf16_lo(g2.y), bf16_hi(g2.y)};
+        const float uv[4] = {bf16_lo(u2.x), bf16_hi(u2.x), bf16_lo(u2.y), bf16_hi(u2.y)};
+        float dgv[4], duv[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float da = acc[i][q][e], sg = gep::sigmoid(gv[e]);
+          dgv[e] = da * uv[e] * sg * (1.0f + gv[e] * (1.0f - sg));
+          duv[e] = da * gv[e] * sg;
+        }
+        gm[0][i] = u32x2{pack_bf16x2(dgv[0], dgv[1]), pack_bf16x2(dgv[2], dgv[3])};
+        um[0][i] = u32x2{pack_bf16x2(duv[0], duv[1]), pack_bf16x2(duv[2], duv[3])};
+      });
+      gep::stage_out_round<8, 1>(gm, q, rdg, rows_valid, cv, p.f, stg, lane);
+      gep::stage_out_round<8, 1>(um, q, rdu, rows_valid, cv, p.f, stg, lane);
+    });
+  } else {
+    const int N = n_total<MODE>(p.d, p.f);
+    const int col0 = t.n0 + 128 * wn, cv = N - col0;
+    uint16_t* out = p.o0;
+    long long rows = p.n;
+    if constexpr (is_wgrad(MODE)) {
+      rows = m_total<MODE>(p.d, p.f);
+      out = (MODE == WGRAD_GU && t.half ? p.o1 : p.o0) + static_cast<long long>(t.e) * rows * N;
+    }
+    const auto r = gep::out_rsrc(out, rows, N, row0, col0);
+    gep::sfor<0, 2>([&](auto q) {
+      u32x2 v[2][8];
+      gep::sfor<0, 2>([&](auto jj) { gep::sfor<0, 8>([&](auto i) { v[jj][i] = gep::pack4(acc[i][2 * q + jj]); }); });
+      gep::stage_out_round<8, 2>(v, q, r, rows_valid, cv, N, stg, lane);
+    });
+  }
+}
+
+// Where a K step is read from: codes and row scales, its byte offset in a row, and the bytes of the row
+// from there on (TAIL: the contraction length is no multiple of 128, and the last step's rest reads zero).
+struct Step {
+  __amdgpu_buffer_rsrc_t r, rs;
+  int soff, left;
+};
+
+template <int MODE, bool TAIL>
+__device__ __forceinline__ void grouped_gemm(const Params& p) {
+  constexpr bool WG = is_wgrad(MODE);
+  const int tid = threadIdx.x;
+  const int lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  const bool role_b = wave < 4;    // waves 0-3 stream the column operand, 4-7 the row operand
+  const int h = wave & 3;          // 64 rows each
+
+  // ---- device-side schedule (as the MXFP8 products)
+  constexpr int NTW = MODE == FWD1 ? BN / 2 : BN;
+  const int ntiles_n = (n_total<MODE>(p.d, p.f) + NTW - 1) / NTW;
+  MTiles mts{};
+  int total;
+  bool deal = false;
+  if constexpr (!WG) {
+    mts = gsched::mtile_scan<BM>(p.offsets, p.E);
+    total = mts.total * ntiles_n;
+  } else {
+    total = p.E * ((m_total<MODE>(p.d, p.f) + BM - 1) / BM) * (MODE == WGRAD_GU ? 2 : 1) * ntiles_n;
+    deal = gsched::wgrad_skewed(p.offsets, p.E, p.n);
+  }
+  const int G = gridDim.x;   // a multiple of 8
+  const int bid = blockIdx.x;
+  int lid, lstep, lend;
+  if (deal) {
+    lid = bid;
+    lstep = G;
+    lend = total;
+  } else {
+    const int per = (total + 7) >> 3;
+    const int x = bid & 7;
+    lid = x * per + (bid >> 3);
+    lstep = G >> 3;
+    lend = (x + 1) * per < total ? (x + 1) * per : total;
+  }
+  lid = __builtin_amdgcn_readfirstlane(lid);
+  lend = __builtin_amdgcn_readfirstlane(lend);
+  if (lid >= lend) return;
+  int rn = 1;
+  auto deal_lid = [&](int r) { return r * G + ((r & 1) ? (G - 1 - bid) : bid); };
+  int lid_n = deal ? deal_lid(1) : lid + lstep;
+
+  const int Kone = k_one<MODE>(p.d, p.f);
+  const int kb_one = static_cast<int>(fp8b_blocks(Kone));
+  const int ld = WG ? p.P : Kone;                    // bytes per operand row
+  const int spitch = WG ? (role_b ? n_total<MODE>(p.d, p.f) : m_total<MODE>(p.d, p.f)) : p.n;
+
+  Tile t = tile_at<MODE>(p, mts, ntiles_n, lid);
+  TileSrc cur = tile_src<MODE>(p, t, role_b, h);
+  Tile tn = t;
+  TileSrc nxt = empty_src<MODE>(p);
+  // weight scales: lane l of w0 holds K block l's (w1: of the up product / of the second contraction)
+  const int wcol = MODE == FWD1 ? 0 : 128 * wn;
+  float w0 = weight_scale<MODE>(p, t, t.n0 + wcol, 0, 0), w1 = 0.f, w0n = 0.f, w1n = 0.f;
+  if constexpr (MODE == FWD1 || MODE == DGRAD2) w1 = weight_scale<MODE>(p, t, t.n0 + wcol, 1, 0);
+  auto look_ahead = [&]() {
+    tn = tile_at<MODE>(p, mts, ntiles_n, lid_n);
+    nxt = tile_src<MODE>(p, tn, role_b, h);
+    w0n = weight_scale<MODE>(p, tn, tn.n0 + wcol, 0, 0);
+    if constexpr (MODE == FWD1 || MODE == DGRAD2) w1n = weight_scale<MODE>(p, tn, tn.n0 + wcol, 1, 0);
+  };
+  if (lid_n < lend) look_ahead();
+
+  // DMA: instruction i covers rows 64 h + 8 i + lane / 8 of the operand's 256 (FWD1's column operand:
+  // rows of the gate's or the up matrix's 128), chunk position lane % 8
+  const int row_h = (MODE == FWD1 && role_b) ? 64 * (h & 1) : 64 * h;
+  const int chunk = (lane & 7) ^ (lane >> 4);        // of even instructions; odd ones: chunk ^ 4
+  const int vo = (row_h + (lane >> 3)) * ld + 16 * chunk;
+  const int vo_odd = (row_h + (lane >> 3)) * ld + 16 * (chunk ^ 4);
+  uint8_t* const dst0 = lds_ring + (role_b ? B_RING : A_RING) + h * 8192;
+  uint8_t* const sdst0 = lds_ring + (role_b ? SB_RING : SA_RING) + h * 256;
+
+  auto step_of = [&](const TileSrc& s, int k) {
+    Step st{s.r0, s.r0, k * BK, BK};
+    const float* sc = s.s0;
+    int kb = k;
+    if constexpr (MODE == DGRAD2) {
+      if (k >= kb_one) { st.r = s.r1; sc = s.s1; kb = k - kb_one; st.soff = kb * BK; }
+    }
+    if constexpr (TAIL) st.left = Kone - st.soff;
+    if (k >= s.nk) { st.r = gep::rsrc(p.a0, 0); st.soff = 0; }
+    const bool scales = (WG || !role_b) && k < s.nk;
+    st.rs = gep::rsrc(sc + static_cast<long long>(kb) * spitch, scales ? 4LL * s.rows : 0);
+    return st;
+  };
+  auto issue = [&](auto i, const Step& st, uint8_t* dst) {
+    int off = ((i & 1) ? vo_odd : vo) + 8 * i * ld;
+    if constexpr (TAIL) off = 16 * ((i & 1) ? chunk ^ 4 : chunk) < st.left ? off : static_cast<int>(gep::OOB);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(st.r, (lds_void*)(dst + i * 1024), 16, off, st.soff, 0, 0);
+  };
+  auto issue_scales = [&](const Step& st, uint8_t* dst) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(st.rs, (lds_void*)dst, 4, 4 * (64 * h + lane), 0, 0, 0);
+  };
+
+  const uint32_t ring = lds_addr(lds_ring);
+  const uint32_t kc0 = kc_off(lane & 15, lane >> 4), kc1 = kc_off(lane & 15, 4 + (lane >> 4));
+  const uint32_t a_off = A_RING + wm * 8192;
+  const uint32_t b_off = B_RING + (MODE == FWD1 ? 8192 * wn : 16384 * wn);
+  const uint32_t sa_off = SA_RING + 4 * (64 * wm + (lane & 15));
+  const uint32_t sb_off = SB_RING + 4 * (128 * wn + 4 * (lane >> 4));
+
+  f32x4 acc[8][4];
+  auto zero_acc = [&]() {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  };
+  zero_acc();
+  int st = 0, kt = 0;
+  bool ready = false;
+  for (;;) {
+    if (!ready && cur.nk > 0) {
+      const Step s0 = step_of(cur, 0);
+      static_for<0, 8>([&](auto i) { issue(i, s0, dst0 + st * OP_BYTES); });
+      if (WG || !role_b) issue_scales(s0, sdst0 + st * SC_BYTES);
+      ready = true;
+    }
+    bool next_ready = false;
+    while (kt < cur.nk) {
+      // step kt is in LDS everywhere, and every wave is done with step kt - 1, whose stage takes the next
+      asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+      const bool here = kt + 1 < cur.nk;
+      next_ready = !here && nxt.nk > 0;
+      const Step ns = here ? step_of(cur, kt + 1) : step_of(nxt, 0);
+      // this step's weight scales (each 64 K blocks the registers are filled again)
+      float ws0 = 1.f, ws1 = 1.f;
+      if constexpr (!WG) {
+        const bool second = MODE == DGRAD2 && kt >= kb_one;
+        const int kb = second ? kt - kb_one : kt;
+        if (kb >= 64 && (kb & 63) == 0) {
+          if (MODE != DGRAD2 || !second) w0 = weight_scale<MODE>(p, t, t.n0 + wcol, 0, kb);
+          if (MODE == FWD1 || second) w1 = weight_scale<MODE>(p, t, t.n0 + wcol, 1, kb);
+        }
+        ws0 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(second ? w1 : w0), kb & 63));
+        if constexpr (MODE == FWD1) ws1 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(w1), kb & 63));
+      }
+      const uint32_t so = ring + st * OP_BYTES, sso = ring + st * SC_BYTES;
+      const uint32_t fa0 = so + a_off + kc0, fa1 = so + a_off + kc1, fb0 = so + b_off + kc0, fb1 = so + b_off + kc1;
+      uint8_t* const dst = dst0 + (st ^ 1) * OP_BYTES;
+      i32x8 fa[4], fb[2];
+      float sa[4], ca[4], cb[4];
+      f32x4 sb[2], tmp[4];
+      f32x4 sp = {0.f, 0.f, 0.f, 0.f};   // column scales of the fragment whose sums are in tmp
+      // FWD1: column fragments 0-3 are the gate's rows of this wave, 4-7 the up matrix's (128 rows on)
+      auto bq = [](auto i) { return std::integral_constant<int, MODE == FWD1 && i >= 4 ? i + 4 : i>{}; };
+      static_for<0, 4>([&](auto j) {
+        read_frag<j>(fa[j], fa0, fa1);
+        ds_f32<64 * j>(sa[j], sso + sa_off);
+      });
+      read_frag<0>(fb[0], fb0, fb1);
+      if constexpr (WG) ds_f128<0>(sb[0], sso + sb_off);
+      static_for<0, 8>([&](auto i) {
+        constexpr int c = i & 1;
+        if constexpr (i == 0) {
+          if (WG || !role_b) issue_scales(ns, sdst0 + (st ^ 1) * SC_BYTES);
+        }
+        issue(i, ns, dst);
+        if constexpr (i < 7) {
+          read_frag<bq(std::integral_constant<int, i + 1>{}).value>(fb[c ^ 1], fb0, fb1);
+          if constexpr (WG) ds_f128<64 * (i + 1)>(sb[c ^ 1], sso + sb_off);
+        }
+        constexpr int after = i < 7 ? (WG ? 3 : 2) : 0;
+        if constexpr (WG) wait_col<after>(fb[c], sb[c]);
+        else wait_col<after>(fb[c]);
+        if constexpr (i == 0) {
+          wait_rows<after>(fa, sa);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            ca[j] = WG ? sa[j] : sa[j] * ws0;
+            cb[j] = MODE == FWD1 ? sa[j] * ws1 : 0.f;
+          }
+        }
+        // a block sum enters the running sum just before its register takes the next fragment's, three
+        // MFMAs after its own was issued
+        auto add = [&](auto ii, auto j) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float w = WG ? sp[e] * sa[j] : (MODE == FWD1 && ii >= 4 ? cb[j] : ca[j]);
+            acc[ii][j][e] = fmaf(tmp[j][e], w, acc[ii][j][e]);
+          }
+        };
+        static_for<0, 4>([&](auto j) {
+          if constexpr (i > 0) add(std::integral_constant<int, i - 1>{}, j);
+          tmp[j] = mfma_block(fb[c], fa[j]);
+          __builtin_amdgcn_sched_barrier(0);   // the compiler would pull the FMAs up to their MFMA and wait there
+        });
+        if constexpr (WG) sp = sb[c];
+        if constexpr (i == 7) static_for<0, 4>([&](auto j) { add(i, j); });
+      });
+      st ^= 1;
+      ++kt;
+    }
+    // ---- tile done (or empty): once every wave has read the last step, its stage serves as staging
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    const uint32_t spent = ring + (st ^ 1) * OP_BYTES + (wave < 4 ? A_RING : B_RING) + (wave & 3) * STG_BYTES;
+    epilogue<MODE>(p, t, acc, wm, wn, lane, spent);
+    if (lid_n >= lend) break;
+    zero_acc();
+    ready = next_ready;
+    t = tn;
+    cur = nxt;
+    w0 = w0n;
+    w1 = w1n;
+    kt = 0;
+    lid_n = deal ? deal_lid(++rn) : lid_n + lstep;
+    if (lid_n < lend) look_ahead();
+    else nxt = empty_src<MODE>(p);
+  }
+  // no LDS-DMA may still be writing when the workgroup ends
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+}
+
+template <int MODE, bool TAIL>
+__global__ __launch_bounds__(NTH, 2) void grouped_gemm_fp8b_kernel(Params p) {
+  grouped_gemm<MODE, TAIL>(p);
+}
+
+// Tile cells per product, as measured for the MXFP8 products of the same tile and operand bytes.
+template <int MODE>
+void tile_cells(Params& p) {
+  p.cm = 1;
+  p.cn = 1 << 20;
+  if (MODE == FWD1 || MODE == DGRAD2) { p.cm = 8; p.cn = 2; }
+  if (MODE == WGRAD_DOWN) { p.cm = 8; p.cn = 4; }
+}
+
+template <int MODE>
+int launch(const Params& p0, hipStream_t s) {
+  Params p = p0;
+  tile_cells<MODE>(p);
+  const long long nt = (n_total<MODE>(p.d, p.f) + n_tile_width<MODE>() - 1) / n_tile_width<MODE>();
+  long long upper;
+  if (is_wgrad(MODE)) {
+    upper = static_cast<long long>(p.E) * ((m_total<MODE>(p.d, p.f) + BM - 1) / BM) * (MODE == WGRAD_GU ? 2 : 1) * nt;
+    MOE_REQUIRE(static_cast<long long>(p.P) * BM < 0x7fffffffLL, MOE_ERR_UNSUPPORTED, "padded token axis too long");
+  } else {
+    upper = (static_cast<long long>(p.n / BM) + p.E) * nt;
+    MOE_REQUIRE(static_cast<long long>(k_one<MODE>(p.d, p.f)) * BM < 0x7fffffffLL, MOE_ERR_UNSUPPORTED, "rows too long");
+  }
+  MOE_REQUIRE(upper < (1LL << 31), MOE_ERR_UNSUPPORTED, "too many tiles");
+  const unsigned g = static_cast<unsigned>(gemm_workgroups(upper));
+  if constexpr (is_wgrad(MODE)) {
+    grouped_gemm_fp8b_kernel<MODE, false><<<g, NTH, 0, s>>>(p);
+  } else {
+    if (k_one<MODE>(p.d, p.f) % BK != 0) grouped_gemm_fp8b_kernel<MODE, true><<<g, NTH, 0, s>>>(p);
+    else grouped_gemm_fp8b_kernel<MODE, false><<<g, NTH, 0, s>>>(p);
+  }
+  return check_launch("grouped_gemm_fp8b");
+}
+
+int check_gemm(int E, int n, int d, int f, const int32_t* offsets) {
+  MOE_REQUIRE(E >= 1 && E <= 256, MOE_ERR_UNSUPPORTED, "E must be in [1, 256] (got %d)", E);
+  MOE_REQUIRE(n >= 1, MOE_ERR_UNSUPPORTED, "n must be >= 1 (got %d)", n);
+  MOE_REQUIRE(d >= 64 && d % 64 == 0 && f >= 64 && f % 64 == 0, MOE_ERR_UNSUPPORTED,
+              "d and f must be positive multiples of 64 (got %d, %d)", d, f);
+  MOE_CHECK_PTR(offsets);
+  return MOE_OK;
+}
+
+}  // namespace g8b
+}  // namespace moe
+
+using namespace moe;
+
+#define FP8B_OPERAND(p) \
+  do { MOE_CHECK_PTR(p); MOE_CHECK_ALIGN(p); } while (0)
+
+extern "C" int moe_grouped_gemm_gate_up_fp8b(int E, int n, int d, int f, const int32_t* offsets, const uint8_t* xq,
+                                             const float* xs, const uint8_t* w_gate, const float* w_gate_s,
+                                             const uint8_t* w_up, const float* w_up_s, uint16_t* g, uint16_t* u,
+                                             uint16_t* a, void* stream) {
+  if (int st = g8b::check_gemm(E, n, d, f, offsets)) return st;
+  FP8B_OPERAND(xq); FP8B_OPERAND(xs); FP8B_OPERAND(w_gate); FP8B_OPERAND(w_gate_s);
+  FP8B_OPERAND(w_up); FP8B_OPERAND(w_up_s); FP8B_OPERAND(a);
+  MOE_REQUIRE((g == nullptr) == (u == nullptr), MOE_ERR_INVALID_ARG, "g and u come together");
+  if (g) { MOE_CHECK_ALIGN(g); MOE_CHECK_ALIGN(u); }
+  g8b::Params p{};
+  p.offsets = offsets; p.E = E; p.n = n; p.d = d; p.f = f;
+  p.a0 = xq; p.a0s = xs; p.b0 = w_gate; p.b0s = w_gate_s; p.b1 = w_up; p.b1s = w_up_s;
+  p.o0 = g; p.o1 = u; p.o2 = a;
+  return g8b::launch<g8b::FWD1>(p, as_stream(stream));
+}
+
+extern "C" int moe_grouped_gemm_down_fp8b(int E, int n, int d, int f, const int32_t* offsets, const uint8_t* aq,
+                                          const float* as, const uint8_t* w_down, const float* w_down_s, uint16_t* yexp,
+                                          void* stream) {
+  if (int st = g8b::check_gemm(E, n, d, f, offsets)) return st;
+  FP8B_OPERAND(aq); FP8B_OPERAND(as); FP8B_OPERAND(w_down); FP8B_OPERAND(w_down_s); FP8B_OPERAND(yexp);
+  g8b::Params p{};
+  p.offsets = offsets; p.E = E; p.n = n; p.d = d; p.f = f;
+  p.a0 = aq; p.a0s = as; p.b0 = w_down; p.b0s = w_down_s; p.o0 = yexp;
+  return g8b::launch<g8b::FWD2>(p, as_stream(stream));
+}
+
+extern "C" int moe_grouped_gemm_dgrad_down_fp8b(int E, int n, int d, int f, const int32_t* offsets, const uint8_t* dyq,
+                                                const float* dys, const uint8_t* w_down_t, const float* w_down_t_s,
+                                                const uint16_t* g, const uint16_t* u, uint16_t* dg, uint16_t* du,
+                                                void* stream) {
+  if (int st = g8b::check_gemm(E, n, d, f, offsets)) return st;
+  FP8B_OPERAND(dyq); FP8B_OPERAND(dys); FP8B_OPERAND(w_down_t); FP8B_OPERAND(w_down_t_s);
+  FP8B_OPERAND(g); FP8B_OPERAND(u); FP8B_OPERAND(dg); FP8B_OPERAND(du);
+  g8b::Params p{};
+  p.offsets = offsets; p.E = E; p.n = n; p.d = d; p.f = f;
+  p.a0 = dyq; p.a0s = dys; p.b0 = w_down_t; p.b0s = w_down_t_s; p.g = g; p.u = u; p.o0 = dg; p.o1 = du;
+  return g8b::launch<g8b::DGRAD1>(p, as_stream(stream));
+}
+
+extern "C" int moe_grouped_gemm_dgrad_gate_up_fp8b(int E, int n, int d, int f, const int32_t* offsets,
+                                                   const uint8_t* dgq, const float* dgs, const uint8_t* duq,
+                                                   const float* dus, const uint8_t* w_gate_t, const float* w_gate_t_s,
+                                                   const uint8_t* w_up_t, const float* w_up_t_s, uint16_t* dxp,
+                                                   void* stream) {
+  if (int st = g8b::check_gemm(E, n, d, f, offsets)) return st;
+  FP8B_OPERAND(dgq); FP8B_OPERAND(dgs); FP8B_OPERAND(duq); FP8B_OPERAND(dus);
+  FP8B_OPERAND(w_gate_t); FP8B_OPERAND(w_gate_t_s); FP8B_OPERAND(w_up_t); FP8B_OPERAND(w_up_t_s); FP8B_OPERAND(dxp);
+  g8b::Params p{};
+  p.offsets = offsets; p.E = E; p.n = n; p.d = d; p.f = f;
+  p.a0 = dgq; p.a0s = dgs; p.a1 = duq; p.a1s = dus;
+  p.b0 = w_gate_t; p.b0s = w_gate_t_s; p.b1 = w_up_t; p.b1s = w_up_t_s; p.o0 = dxp;
+  return g8b::launch<g8b::DGRAD2>(p, as_stream(stream));
+}
+
+extern "C" int moe_grouped_gemm_wgrad_down_fp8b(int E, int n, int d, int f, const int32_t* offsets,
+                                                const int32_t* offsets_pad, const uint8_t* dyT, const float* dyTs,
+                                                const uint8_t* aT, const float* aTs, uint16_t* dw_down, void* stream) {
+  if (int st = g8b::check_gemm(E, n, d, f, offsets)) return st;
+  MOE_CHECK_PTR(offsets_pad);
+  FP8B_OPERAND(dyT); FP8B_OPERAND(dyTs); FP8B_OPERAND(aT); FP8B_OPERAND(aTs); FP8B_OPERAND(dw_down);
+  g8b::Params p{};
+  p.offsets = offsets; p.offsets_pad = offsets_pad; p.E = E; p.n = n; p.d = d; p.f = f;
+  p.P = moe_mx_pad_cap(n, E);
+  MOE_REQUIRE(p.P > 0, MOE_ERR_UNSUPPORTED, "padded token axis too long");
+  p.a0 = dyT; p.a0s = dyTs; p.b0 = aT; p.b0s = aTs; p.o0 = dw_down;
+  return g8b::launch<g8b::WGRAD_DOWN>(p, as_stream(stream));
+}
+
+extern "C" int moe_grouped_gemm_wgrad_gate_up_fp8b(int E, int n, int d, int f, const int32_t* offsets,
+                                                   const int32_t* offsets_pad, const uint8_t* dgT, const float* dgTs,
+                                                   const uint8_t* duT, const float* duTs, const uint8_t* xT,
+                                                   const float* xTs, uint16_t* dw_gate, uint16_t* dw_up, void* stream) {
+  if (int st = g8b::check_gemm(E, n, d, f, offsets)) return st;
+  MOE_CHECK_PTR(offsets_pad);
+  FP8B_OPERAND(dgT); FP8B_OPERAND(dgTs); FP8B_OPERAND(duT); FP8B_OPERAND(duTs); FP8B_OPERAND(xT); FP8B_OPERAND(xTs);
+  FP8B_OPERAND(dw_gate); FP8B_OPERAND(dw_up);
+  g8b::Params p{};
+  p.offsets = offsets; p.offsets_pad = offsets_pad; p.E = E; p.n = n; p.d = d; p.f = f;
+  p.P = moe_mx_pad_cap(n, E);
+  MOE_REQUIRE(p.P > 0, MOE_ERR_UNSUPPORTED, "padded token axis too long");
+  p.a0 = dgT; p.a0s = dgTs; p.a1 = duT; p.a1s = duTs; p.b0 = xT; p.b0s = xTs; p.o0 = dw_gate; p.o1 = dw_up;
+  return g8b::launch<g8b::WGRAD_GU>(p, as_stream(stream));
+}

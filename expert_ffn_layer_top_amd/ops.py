@@ -64,6 +64,12 @@ def _empty(shape, dtype, like):
     return torch.empty(shape, dtype=dtype, device=like.device)
 
 
+def _call_on(like, name, *args):
+    """Calls `name` with `like`'s device current, on that device's current stream (the last argument)."""
+    with torch.cuda.device(like.device):
+        call(name, *args, _stream(like))
+
+
 def _mx_pad_cap(n, E):
     # moe_mx_pad_cap: n + 128 E rounded up to a multiple of 128 (the library's padded token axis,
     # long enough for any pad up to 128)
@@ -163,6 +169,72 @@ def route_balance(probs, counts, k):
     call("moe_route_balance", _ptr(probs), _ptr(counts), T, E, k, _ptr(p_mean), _ptr(stats), _ptr(ws), nbytes,
          _stream(probs))
     return p_mean, stats
+
+
+# ---------------------------------------------------------------- scored router
+
+_SCORES = {"sigmoid": 0, "softmax": 1}
+
+
+def _score(score):
+    _need(score in _SCORES, f"score must be one of {sorted(_SCORES)}, got {score!r}")
+    return _SCORES[score]
+
+
+def route_scored(logits, k, score="sigmoid", bias=None, n_group=1, topk_group=1, group_top=1, renormalize=True,
+                 scale=1.0, want_scores=False, pad=None, want_row_token=True):
+    """Router with a score for every expert ("sigmoid" of its logit, or "softmax" over all), a bias [E]
+    fp32 added for the choice alone, and groups: of n_group groups of E / n_group experts, the topk_group
+    with the largest sum of their group_top best (score + bias); of their experts the k best.  Gates are
+    scale * score, over the chosen scores' sum with renormalize.  Returns the same dict as route_topk, with
+    scores [T,E] fp32 (or None) for probs.  A logit of -inf or NaN, or a bias of -inf, marks an expert that
+    is not there: it is chosen after every other one of the kept groups, and with a gate of 0 (a bias alone
+    leaves its gate)."""
+    _check(logits, torch.float32, "logits", ndim=2)
+    T, E = logits.shape
+    score = _score(score)
+    _need(T >= 1 and 1 <= E <= 256, f"logits: need T >= 1 and 1 <= E <= 256, got {list(logits.shape)}")
+    _need(pad is None or pad >= 1, "pad must be >= 1")
+    _need(n_group >= 1 and E % n_group == 0, f"n_group = {n_group} must divide E = {E}")
+    _need(1 <= topk_group <= n_group, f"topk_group = {topk_group} must be in [1, n_group = {n_group}]")
+    _need(group_top in (1, 2), "group_top must be 1 or 2")
+    _need(1 <= k <= min(16, topk_group * (E // n_group)),
+          f"k = {k} must be in [1, 16] and at most the {topk_group * (E // n_group)} experts of the kept groups")
+    if bias is not None:
+        _check(bias, torch.float32, "bias", (E,))
+    _on_gpu(logits, bias)
+    out = dict(
+        topk_idx=_empty((T, k), torch.int32, logits),
+        topk_gate=_empty((T, k), torch.float32, logits),
+        scores=_empty((T, E), torch.float32, logits) if want_scores else None,
+        counts=_empty((E,), torch.int32, logits),
+        offsets=_empty((E + 1,), torch.int32, logits),
+        offsets_pad=_empty((E + 1,), torch.int32, logits) if pad else None,
+        dest=_empty((T, k), torch.int32, logits),
+        row_token=_empty((T * k,), torch.int32, logits) if want_row_token else None,
+    )
+    nbytes = lib.moe_route_workspace_bytes(T, E, k)
+    ws = _empty((max(nbytes, 1),), torch.uint8, logits)
+    _call_on(logits, "moe_route_scored", _ptr(logits), _ptr(bias), T, E, k, score, n_group, topk_group, group_top,
+             int(bool(renormalize)), float(scale), _ptr(out["topk_idx"]), _ptr(out["topk_gate"]), _ptr(out["scores"]),
+             _ptr(out["counts"]), _ptr(out["offsets"]), _ptr(out["offsets_pad"]), int(pad or 0), _ptr(out["dest"]),
+             _ptr(out["row_token"]), _ptr(ws), nbytes)
+    return out
+
+
+def route_scored_bwd(logits, topk_idx, d_gate, score="sigmoid", renormalize=True, scale=1.0):
+    """d_logits [T,E] fp32: the gradient of route_scored's gates with the choice held fixed."""
+    _check(logits, torch.float32, "logits", ndim=2)
+    T, E = logits.shape
+    score = _score(score)
+    _check(topk_idx, torch.int32, "topk_idx", (T, None))
+    k = topk_idx.shape[1]
+    _check(d_gate, torch.float32, "d_gate", (T, k))
+    _on_gpu(logits, topk_idx, d_gate)
+    dl = _empty((T, E), torch.float32, logits)
+    _call_on(logits, "moe_route_scored_bwd", _ptr(logits), _ptr(topk_idx), _ptr(d_gate), T, E, k, score,
+             int(bool(renormalize)), float(scale), _ptr(dl))
+    return dl
 
 
 # ---------------------------------------------------------------- rows
@@ -696,4 +768,196 @@ def grouped_gemm_wgrad_gate_up(dg_t, du_t, xp_t, offsets, n, offsets_pad=None, s
     dwu = _empty((E, f, d), torch.bfloat16, dg_t)
     call("moe_grouped_gemm_wgrad_gate_up", dtype, E, n, d, f, _ptr(offsets), _ptr(offsets_pad), _ptr(dg_t),
          _ptr(sc[0]), _ptr(du_t), _ptr(sc[1]), _ptr(xp_t), _ptr(sc[2]), _ptr(dwg), _ptr(dwu), _stream(dg_t))
+    return dwg, dwu
+
+
+# ------------------------------------------------- block-128 E4M3 (one fp32 scale per block of 128)
+
+def _blocks(x):
+    return -(-x // 128)
+
+
+def fp8b_quantize_rows(x, dest=None):
+    """(q [n, C] E4M3 bytes, s [ceil(C/128), n] fp32): blocks of 128 along each row of x [T, C] bf16, in x's
+    order or, with dest [T, k], each row written to its k rows of the expert buffers (n = T k)."""
+    _check(x, torch.bfloat16, "x", ndim=2)
+    T, C = x.shape
+    _need(T >= 1 and C >= 64 and C % 64 == 0, f"x: need T >= 1 and C a multiple of 64, got {list(x.shape)}")
+    k = 1
+    if dest is not None:
+        _check(dest, torch.int32, "dest", (T, None))
+        k = dest.shape[1]
+        _need(1 <= k <= 16, f"dest: k = {k} must be in [1, 16]")
+    _on_gpu(x, dest)
+    q = _empty((T * k, C), torch.uint8, x)
+    s = _empty((_blocks(C), T * k), torch.float32, x)
+    _call_on(x, "moe_fp8b_quantize_rows", _ptr(x), _ptr(dest), T, C, k, _ptr(q), _ptr(s))
+    return q, s
+
+
+def fp8b_quantize_rows_grouped(x, offsets, offsets_pad, row_token=None, row_gate=None, want_rows=True):
+    """Both layouts of a grouped bf16 tensor from one read: the row blocks (q [n, C], s [ceil(C/128), n]; None,
+    None without want_rows) and the blocks of 128 tokens of one expert, transposed (qT [C, P], sT [P/128, C],
+    P = mx_pad_cap(n, E)).  Grouped row r is x[r], or x[row_token[r]], times row_gate[r] where given.
+    offsets_pad: a router's padded offsets with pad = 128 (or a multiple)."""
+    _check(offsets, torch.int32, "offsets", ndim=1)
+    E = offsets.shape[0] - 1
+    _need(1 <= E <= 256, f"offsets must hold E + 1 entries with 1 <= E <= 256, got {E + 1}")
+    _check(offsets_pad, torch.int32, "offsets_pad", (E + 1,))
+    _check(x, torch.bfloat16, "x", ndim=2)
+    n, C = x.shape
+    if row_token is not None:
+        _check(row_token, torch.int32, "row_token", ndim=1)
+        n = row_token.shape[0]
+    if row_gate is not None:
+        _check(row_gate, torch.float32, "row_gate", (n,))
+    _need(n >= 1 and C >= 64 and C % 64 == 0, f"need n >= 1 and C a multiple of 64, got n = {n}, C = {C}")
+    _on_gpu(x, offsets, offsets_pad, row_token, row_gate)
+    P = _mx_pad_cap(n, E)
+    q = _empty((n, C), torch.uint8, x) if want_rows else None
+    s = _empty((_blocks(C), n), torch.float32, x) if want_rows else None
+    qT = _empty((C, P), torch.uint8, x)
+    sT = _empty((P // 128, C), torch.float32, x)
+    _call_on(x, "moe_fp8b_quantize_rows_grouped", _ptr(x), _ptr(row_token), _ptr(row_gate), _ptr(offsets),
+             _ptr(offsets_pad), E, n, C, _ptr(q), _ptr(s), _ptr(qT), _ptr(sT))
+    return q, s, qT, sT
+
+
+def fp8b_quantize_weights(w, want_transposed=True):
+    """w [E, R, C] bf16 (or [R, C]) in blocks of 128 x 128: (q, s [.., ceil(R/128), ceil(C/128)], qT [.., C, R],
+    sT [.., ceil(C/128), ceil(R/128)]); qT and sT (the same codes and scales transposed, for the products that
+    contract over R) are None without want_transposed."""
+    _check(w, torch.bfloat16, "w")
+    E, R, C = _rc(w)
+    _need(E >= 1 and R >= 64 and C >= 64 and R % 64 == 0 and C % 64 == 0,
+          f"w: rows and columns must be multiples of 64, got {list(w.shape)}")
+    _on_gpu(w)
+    lead = tuple(w.shape[:-2])
+    q = _empty((*lead, R, C), torch.uint8, w)
+    s = _empty((*lead, _blocks(R), _blocks(C)), torch.float32, w)
+    qT = _empty((*lead, C, R), torch.uint8, w) if want_transposed else None
+    sT = _empty((*lead, _blocks(C), _blocks(R)), torch.float32, w) if want_transposed else None
+    _call_on(w, "moe_fp8b_quantize_weights", _ptr(w), E, R, C, _ptr(q), _ptr(s), _ptr(qT), _ptr(sT))
+    return q, s, qT, sT
+
+
+def _fp8b_rows(q, s, name, n=None, C=None):
+    _check(q, torch.uint8, name, (n, C))
+    n, C = q.shape
+    _check(s, torch.float32, name + "_s", (_blocks(C), n))
+    return n, C
+
+
+def _fp8b_weight(q, s, name, shape=(None, None, None)):
+    _check(q, torch.uint8, name, shape)
+    E, R, C = q.shape
+    _check(s, torch.float32, name + "_s", (E, _blocks(R), _blocks(C)))
+    return E, R, C
+
+
+def _fp8b_sizes(offsets, E, n, d, f):
+    _check(offsets, torch.int32, "offsets", (E + 1,))
+    _need(1 <= E <= 256 and n >= 1, f"need 1 <= E <= 256 and n >= 1, got E = {E}, n = {n}")
+    _need(d >= 64 and d % 64 == 0 and f >= 64 and f % 64 == 0,
+          f"d = {d} and f = {f} must be positive multiples of 64")
+
+
+def grouped_gemm_gate_up_fp8b(xq, xq_s, offsets, w_gate, w_gate_s, w_up, w_up_s, want_gu=True):
+    """(g, u, a [n,f]) bf16: the first grouped product with the SwiGLU epilogue on block-128 E4M3 operands:
+    xq, xq_s as fp8b_quantize_rows gives them, w_gate, w_up [E,f,d] with fp8b_quantize_weights' scales.
+    g and u are None without want_gu (a serving pass)."""
+    E, f, d = _fp8b_weight(w_gate, w_gate_s, "w_gate")
+    _fp8b_weight(w_up, w_up_s, "w_up", (E, f, d))
+    n, _ = _fp8b_rows(xq, xq_s, "xq", C=d)
+    _fp8b_sizes(offsets, E, n, d, f)
+    _on_gpu(xq, xq_s, offsets, w_gate, w_gate_s, w_up, w_up_s)
+    g = _empty((n, f), torch.bfloat16, xq) if want_gu else None
+    u = _empty((n, f), torch.bfloat16, xq) if want_gu else None
+    a = _empty((n, f), torch.bfloat16, xq)
+    _call_on(xq, "moe_grouped_gemm_gate_up_fp8b", E, n, d, f, _ptr(offsets), _ptr(xq), _ptr(xq_s), _ptr(w_gate),
+             _ptr(w_gate_s), _ptr(w_up), _ptr(w_up_s), _ptr(g), _ptr(u), _ptr(a))
+    return g, u, a
+
+
+def grouped_gemm_down_fp8b(aq, aq_s, offsets, w_down, w_down_s):
+    """yexp [n,d] bf16 = a W_down[e]^T per expert: aq, aq_s from fp8b_quantize_rows(a), w_down [E,d,f]."""
+    E, d, f = _fp8b_weight(w_down, w_down_s, "w_down")
+    n, _ = _fp8b_rows(aq, aq_s, "aq", C=f)
+    _fp8b_sizes(offsets, E, n, d, f)
+    _on_gpu(aq, aq_s, offsets, w_down, w_down_s)
+    yexp = _empty((n, d), torch.bfloat16, aq)
+    _call_on(aq, "moe_grouped_gemm_down_fp8b", E, n, d, f, _ptr(offsets), _ptr(aq), _ptr(aq_s), _ptr(w_down),
+             _ptr(w_down_s), _ptr(yexp))
+    return yexp
+
+
+def grouped_gemm_dgrad_down_fp8b(dyq, dyq_s, offsets, w_down_t, w_down_t_s, g, u):
+    """(dg, du) [n,f] bf16: da = dyexp W_down[e] through the SwiGLU backward of (g, u); w_down_t [E,f,d] and its
+    scales are fp8b_quantize_weights' qT, sT."""
+    E, f, d = _fp8b_weight(w_down_t, w_down_t_s, "w_down_t")
+    n, _ = _fp8b_rows(dyq, dyq_s, "dyq", C=d)
+    _check(g, torch.bfloat16, "g", (n, f))
+    _check(u, torch.bfloat16, "u", (n, f))
+    _fp8b_sizes(offsets, E, n, d, f)
+    _on_gpu(dyq, dyq_s, offsets, w_down_t, w_down_t_s, g, u)
+    dg = _empty((n, f), torch.bfloat16, g)
+    du = _empty((n, f), torch.bfloat16, g)
+    _call_on(g, "moe_grouped_gemm_dgrad_down_fp8b", E, n, d, f, _ptr(offsets), _ptr(dyq), _ptr(dyq_s), _ptr(w_down_t),
+             _ptr(w_down_t_s), _ptr(g), _ptr(u), _ptr(dg), _ptr(du))
+    return dg, du
+
+
+def grouped_gemm_dgrad_gate_up_fp8b(dgq, dgq_s, duq, duq_s, offsets, w_gate_t, w_gate_t_s, w_up_t, w_up_t_s):
+    """dxp [n,d] bf16 = dg W_gate[e] + du W_up[e]; w_gate_t, w_up_t [E,d,f] are fp8b_quantize_weights' qT."""
+    E, d, f = _fp8b_weight(w_gate_t, w_gate_t_s, "w_gate_t")
+    _fp8b_weight(w_up_t, w_up_t_s, "w_up_t", (E, d, f))
+    n, _ = _fp8b_rows(dgq, dgq_s, "dgq", C=f)
+    _fp8b_rows(duq, duq_s, "duq", n, f)
+    _fp8b_sizes(offsets, E, n, d, f)
+    _on_gpu(dgq, dgq_s, duq, duq_s, offsets, w_gate_t, w_gate_t_s, w_up_t, w_up_t_s)
+    dxp = _empty((n, d), torch.bfloat16, dgq)
+    _call_on(dgq, "moe_grouped_gemm_dgrad_gate_up_fp8b", E, n, d, f, _ptr(offsets), _ptr(dgq), _ptr(dgq_s), _ptr(duq),
+             _ptr(duq_s), _ptr(w_gate_t), _ptr(w_gate_t_s), _ptr(w_up_t), _ptr(w_up_t_s), _ptr(dxp))
+    return dxp
+
+
+def _fp8b_tokens(q, s, name, P, C=None):
+    _check(q, torch.uint8, name, (C, P))
+    _check(s, torch.float32, name + "_s", (P // 128, q.shape[0]))
+    return q.shape[0]
+
+
+def _fp8b_token_axis(offsets, offsets_pad, n):
+    _check(offsets, torch.int32, "offsets", ndim=1)
+    E = offsets.shape[0] - 1
+    _need(1 <= E <= 256, f"offsets must hold E + 1 entries with 1 <= E <= 256, got {E + 1}")
+    _check(offsets_pad, torch.int32, "offsets_pad", (E + 1,))
+    return E, _mx_pad_cap(n, E)
+
+
+def grouped_gemm_wgrad_down_fp8b(dyT, dyT_s, aT, aT_s, offsets, offsets_pad, n):
+    """dw_down [E,d,f] bf16 = dyexp_e^T a_e from fp8b_quantize_rows_grouped's qT, sT of dyexp and a."""
+    E, P = _fp8b_token_axis(offsets, offsets_pad, n)
+    d = _fp8b_tokens(dyT, dyT_s, "dyT", P)
+    f = _fp8b_tokens(aT, aT_s, "aT", P)
+    _fp8b_sizes(offsets, E, n, d, f)
+    _on_gpu(dyT, dyT_s, aT, aT_s, offsets, offsets_pad)
+    dw = _empty((E, d, f), torch.bfloat16, dyT)
+    _call_on(dyT, "moe_grouped_gemm_wgrad_down_fp8b", E, n, d, f, _ptr(offsets), _ptr(offsets_pad), _ptr(dyT),
+             _ptr(dyT_s), _ptr(aT), _ptr(aT_s), _ptr(dw))
+    return dw
+
+
+def grouped_gemm_wgrad_gate_up_fp8b(dgT, dgT_s, duT, duT_s, xT, xT_s, offsets, offsets_pad, n):
+    """(dw_gate, dw_up) [E,f,d] bf16 = dg_e^T xp_e, du_e^T xp_e from fp8b_quantize_rows_grouped's qT, sT."""
+    E, P = _fp8b_token_axis(offsets, offsets_pad, n)
+    f = _fp8b_tokens(dgT, dgT_s, "dgT", P)
+    _fp8b_tokens(duT, duT_s, "duT", P, f)
+    d = _fp8b_tokens(xT, xT_s, "xT", P)
+    _fp8b_sizes(offsets, E, n, d, f)
+    _on_gpu(dgT, dgT_s, duT, duT_s, xT, xT_s, offsets, offsets_pad)
+    dwg = _empty((E, f, d), torch.bfloat16, dgT)
+    dwu = _empty((E, f, d), torch.bfloat16, dgT)
+    _call_on(dgT, "moe_grouped_gemm_wgrad_gate_up_fp8b", E, n, d, f, _ptr(offsets), _ptr(offsets_pad), _ptr(dgT),
+             _ptr(dgT_s), _ptr(duT), _ptr(duT_s), _ptr(xT), _ptr(xT_s), _ptr(dwg), _ptr(dwu))
     return dwg, dwu

@@ -76,6 +76,9 @@ typedef enum {
 
 enum { MOE_BF16 = 0, MOE_MXFP8 = 1 };
 
+/* Score functions of moe_route_scored. */
+enum { MOE_SCORE_SIGMOID = 0, MOE_SCORE_SOFTMAX = 1 };
+
 /* Version of this ABI (MOE_MI355X_ABI_VERSION of the built library). */
 int moe_abi_version(void);
 /* Static text for a status code. */
@@ -176,6 +179,40 @@ int moe_route_balance(const float* probs, const int32_t* counts, int T, int E, i
 int moe_route_topk_bwd_balance(const float* topk_gate, const int32_t* topk_idx, const float* d_gate,
                                const float* probs, const int32_t* counts, float weight, int T, int E,
                                int k, float* d_logits, void* stream);
+
+/* ---------------------------------------------------------------- scored router */
+
+/* Router with a score for every expert, a bias for balance and groups of experts ([news] lead
+ * paragraphs: a router sends each token to a small selection of experts; "Large expert pools are the
+ * best fit"), and the same device-resident row metadata as moe_route_topk:
+ *   s[t,e]  MOE_SCORE_SIGMOID: 1 / (1 + exp(-l)),  MOE_SCORE_SOFTMAX: exp(l - max) / sum over all E;
+ *   c[t,e] = s + bias[e] (bias [E] fp32 or NULL: added for the choice, never to a gate);
+ *   the value of a group of E / n_group consecutive experts is the sum of its group_top (1 or 2)
+ *   largest c; the topk_group groups of largest value are kept (topk_group = n_group: all);
+ *   topk_idx: the k experts of largest c in the kept groups (of largest logit without a bias),
+ *   descending; ties go to the lower index, for groups and for experts;
+ *   topk_gate = scale * s, divided by the sum of the k chosen s where `renormalize` is nonzero (all 0
+ *   where that sum is 0).
+ * Scores and choice are computed in 64 bits, so the chosen experts do not depend on how fp32 rounds an
+ * exponential.  A logit of -inf or NaN marks an absent expert (score 0, never counted in a group's
+ * value, chosen only after every present expert of the kept groups); a bias of -inf excludes an expert
+ * in the same way, and NaN biases count as -inf; a logit of +inf counts as the largest finite float.
+ *   in   logits [T,E] fp32;  out  as moe_route_topk; scores_or_null [T,E] fp32: every s.
+ * Needs n_group dividing E, 1 <= topk_group <= n_group, k <= topk_group * E / n_group, finite scale;
+ * workspace moe_route_workspace_bytes(T, E, k). */
+int moe_route_scored(const float* logits, const float* bias_or_null, int T, int E, int k, int score,
+                     int n_group, int topk_group, int group_top, int renormalize, float scale,
+                     int32_t* topk_idx, float* topk_gate, float* scores_or_null, int32_t* counts,
+                     int32_t* offsets, int32_t* offsets_pad_or_null, int pad, int32_t* dest,
+                     int32_t* row_token_or_null, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradient of moe_route_scored's gates with the choice held fixed: d_logits [T,E] fp32 from d_gate
+ * [T,k] (the bias has none).  With dg = scale * d_gate and, where renormalised, g = s / sum of the
+ * chosen s and ds_j = (dg_j - sum_i g_i dg_i) / sum s (else ds_j = dg_j): sigmoid dl_j = s_j (1 - s_j)
+ * ds_j; softmax dl_e = s_e (ds_e - sum_i s_i ds_i), which is 0 off the chosen experts when
+ * renormalised.  A topk_idx outside [0, E) takes no part; one that repeats adds up. */
+int moe_route_scored_bwd(const float* logits, const int32_t* topk_idx, const float* d_gate, int T, int E,
+                         int k, int score, int renormalize, float scale, float* d_logits, void* stream);
 
 /* ---------------------------------------------------------------- rows */
 
@@ -444,6 +481,81 @@ int moe_grouped_gemm_wgrad_gate_up(int dtype, int E, int n, int d, int f, const 
                                    const uint8_t* du_t_scale, const void* xp_t,
                                    const uint8_t* xp_t_scale, uint16_t* dw_gate, uint16_t* dw_up,
                                    void* stream);
+
+/* ---------------------------------------------------------------- block-128 E4M3
+ *
+ * 8-bit operands with one fp32 scale per block of 128 along the contraction dimension ([news] "MXFP8
+ * reduces compute and memory costs": 8-bit floats with a separate scale per small block of values; here
+ * larger blocks and fp32 scales, the form of weights that were trained or stored that way).
+ * Arithmetic of a block: amax = max(2^-100, largest |v|); inv = 448 / amax rounded to fp32;
+ * code = E4M3 of v * inv (fp32 product, round to nearest even); scale = amax * (1/448), both rounded to
+ * fp32.  A code stands for code * scale.  Non-finite inputs are unsupported.
+ * Blocks start at multiples of 128; the last one of an axis may be partial (sizes are multiples of 64).
+ * Scales of rows are block-major: [ceil(K/128)][rows].  Scales of a weight matrix [R][C] are one per
+ * 128 x 128 block: [ceil(R/128)][ceil(C/128)]. */
+
+/* Row blocks of x [T][C] bf16: without dest (k = 1) q [T][C], s [ceil(C/128)][T]; with dest [T][k] each
+ * row goes to its k rows of the expert buffers: q [T*k][C], s [ceil(C/128)][T*k].  C a multiple of 64,
+ * 1 <= k <= 16, all pointers 16-byte aligned. */
+int moe_fp8b_quantize_rows(const uint16_t* x, const int32_t* dest_or_null, int T, int C, int k, uint8_t* q,
+                           float* s, void* stream);
+
+/* Blocks of 128 tokens of one expert, transposed (the weight-gradient operands), and the row blocks of
+ * the same rows from one read: grouped row r is in[r], or in[row_token[r]] where row_token is given, times
+ * row_gate[r] (fp32 product rounded to bf16) where that is given.  Expert e's row i sits at position
+ * offsets_pad[e] + i of the padded token axis of length P = moe_mx_pad_cap(n, E); offsets_pad must be a
+ * router's padded offsets with pad a multiple of 128.
+ *   out  qT [C][P], sT [P/128][C] (zeros and their scale 2^-100 / 448 at every other position);
+ *        q_or_null [n][C] and s_or_null [ceil(C/128)][n]: the row blocks, rows from offsets[E] on left as
+ *        they were.  C a multiple of 64, 1 <= E <= 256. */
+int moe_fp8b_quantize_rows_grouped(const uint16_t* in, const int32_t* row_token_or_null,
+                                   const float* row_gate_or_null, const int32_t* offsets,
+                                   const int32_t* offsets_pad, int E, int n, int C, uint8_t* q_or_null,
+                                   float* s_or_null, uint8_t* qT, float* sT, void* stream);
+
+/* Weights w [E][R][C] bf16 in blocks of 128 x 128: q [E][R][C], s [E][ceil(R/128)][ceil(C/128)], and
+ * where qT and sT are given the same codes and scales transposed, [E][C][R] and
+ * [E][ceil(C/128)][ceil(R/128)].  R and C multiples of 64. */
+int moe_fp8b_quantize_weights(const uint16_t* w, int E, int R, int C, uint8_t* q, float* s,
+                              uint8_t* qT_or_null, float* sT_or_null, void* stream);
+
+/* The grouped products of moe_grouped_gemm_swiglu and its backward on block-128 E4M3 operands, one
+ * kernel per call, fp32 accumulation, bf16 outputs; the expert row ranges are read from `offsets` on the
+ * device, and output rows from offsets[E] on are left as they were.  d and f multiples of 64 (all of a
+ * weight's and an activation's blocks along them start at multiples of 128).
+ * gate_up: xq [n][d], xs [ceil(d/128)][n]; w_gate, w_up [E][f][d] with their block scales;
+ *   a = silu(g) * u, and g, u where both are given (NULL: a serving pass that needs only a).
+ * down: aq [n][f], as [ceil(f/128)][n]; w_down [E][d][f]; yexp [n][d].
+ * dgrad_down: dyq [n][d], dys; w_down_t [E][f][d] (moe_fp8b_quantize_weights' qT, sT); dg, du [n][f]
+ *   through the SwiGLU backward of (g, u).
+ * dgrad_gate_up: dgq, duq [n][f] and scales; w_gate_t, w_up_t [E][d][f]; dxp [n][d].
+ * wgrad_down, wgrad_gate_up: moe_fp8b_quantize_rows_grouped's qT, sT of dyexp, a, dg, du, xp;
+ *   dw_down [E][d][f], dw_gate, dw_up [E][f][d], zeros for experts without rows. */
+int moe_grouped_gemm_gate_up_fp8b(int E, int n, int d, int f, const int32_t* offsets, const uint8_t* xq,
+                                  const float* xs, const uint8_t* w_gate, const float* w_gate_s,
+                                  const uint8_t* w_up, const float* w_up_s, uint16_t* g_or_null,
+                                  uint16_t* u_or_null, uint16_t* a, void* stream);
+int moe_grouped_gemm_down_fp8b(int E, int n, int d, int f, const int32_t* offsets, const uint8_t* aq,
+                               const float* as, const uint8_t* w_down, const float* w_down_s,
+                               uint16_t* yexp, void* stream);
+int moe_grouped_gemm_dgrad_down_fp8b(int E, int n, int d, int f, const int32_t* offsets,
+                                     const uint8_t* dyq, const float* dys, const uint8_t* w_down_t,
+                                     const float* w_down_t_s, const uint16_t* g, const uint16_t* u,
+                                     uint16_t* dg, uint16_t* du, void* stream);
+int moe_grouped_gemm_dgrad_gate_up_fp8b(int E, int n, int d, int f, const int32_t* offsets,
+                                        const uint8_t* dgq, const float* dgs, const uint8_t* duq,
+                                        const float* dus, const uint8_t* w_gate_t,
+                                        const float* w_gate_t_s, const uint8_t* w_up_t,
+                                        const float* w_up_t_s, uint16_t* dxp, void* stream);
+int moe_grouped_gemm_wgrad_down_fp8b(int E, int n, int d, int f, const int32_t* offsets,
+                                     const int32_t* offsets_pad, const uint8_t* dyT, const float* dyTs,
+                                     const uint8_t* aT, const float* aTs, uint16_t* dw_down,
+                                     void* stream);
+int moe_grouped_gemm_wgrad_gate_up_fp8b(int E, int n, int d, int f, const int32_t* offsets,
+                                        const int32_t* offsets_pad, const uint8_t* dgT, const float* dgTs,
+                                        const uint8_t* duT, const float* duTs, const uint8_t* xT,
+                                        const float* xTs, uint16_t* dw_gate, uint16_t* dw_up,
+                                        void* stream);
 
 #ifdef __cplusplus
 }

@@ -27,10 +27,12 @@ Modules
   moe      the layer's steps, forward and backward, one function per library entry point
   moe_mx   the layer with every expert product on MXFP8 operands, as a chain of those steps
   mxfp8    MX block quantisation (row blocks, column blocks, grouped token blocks)
+  scored   the scored router (sigmoid or softmax scores, balance bias, expert groups) and its gradient
+  fp8b     block-128 E4M3 quantisation and the grouped expert products on such operands
   sampled  per-row / per-expert evaluators for checking full-size runs on samples
 
 Every function here is pinned in tests/test_oracle_*.py against something other than
 itself (brute force, closed forms, invariants, CPU torch, exhaustive enumeration).
 """
 
-from . import codecs, moe, moe_mx, mxfp8, sampled  # noqa: F401
+from . import codecs, fp8b, moe, moe_mx, mxfp8, sampled, scored  # noqa: F401
