@@ -131,9 +131,9 @@ def test_quantize_rows_grouped_leaves_rows_behind_the_last_group():
     x, o, op = bf16_to_dev(b), i32_to_dev(off), i32_to_dev(offp)
     P = (n + 3 * 128 + 127) // 128 * 128
     q = torch.full((n, C), 77, dtype=torch.uint8, device=dev())
-    s = torch.full((2, n), -3.0, device=dev())
+    s = torch.full((2, n), -3.0, dtype=torch.float32, device=dev())
     qT = torch.empty((C, P), dtype=torch.uint8, device=dev())
-    sT = torch.empty((P // 128, C), device=dev())
+    sT = torch.empty((P // 128, C), dtype=torch.float32, device=dev())
     call("moe_fp8b_quantize_rows_grouped", x.data_ptr(), None, None, o.data_ptr(), op.data_ptr(), 3, n, C, q.data_ptr(),
          s.data_ptr(), qT.data_ptr(), sT.data_ptr(), torch.cuda.current_stream().cuda_stream)
     wq, ws = fp8b.quantize_rows(v[:100])
