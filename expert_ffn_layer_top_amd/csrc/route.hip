@@ -21,12 +21,14 @@
 #include <mutex>
 
 #include "common.h"
-#include "route_meta.h"
 
 namespace moe {
 namespace {
 
+constexpr int kRouteBlock = 64;    // tokens per block (one bit each in a 64-bit mask)
 constexpr int kGroup = 16;         // lanes per token
+constexpr int kMaxK = 16;
+constexpr int kMaxE = 256;
 constexpr int kScanBatch = 16;   // hist loads in flight per scan thread
 
 // Order-preserving map of a float to uint32 (larger float -> larger key); -0 is folded to +0
@@ -388,15 +390,6 @@ int enqueue_route(const float* logits, int T, int E, int k, int32_t* topk_idx, f
   else if (nq <= 8) route_topk_local<8><<<nb, 1024, 0, s>>>(logits, T, E, k, topk_idx, topk_gate, probs, dest, hist);
   else route_topk_local<16><<<nb, 1024, 0, s>>>(logits, T, E, k, topk_idx, topk_gate, probs, dest, hist);
   if (int st = check_launch("route_topk_local")) return st;
-  return enqueue_route_metadata(topk_idx, T, E, k, counts, offsets, offsets_pad, pad, dest, row_token, hist, s);
-}
-
-}  // namespace
-
-int enqueue_route_metadata(const int32_t* topk_idx, int T, int E, int k, int32_t* counts, int32_t* offsets,
-                           int32_t* offsets_pad, int pad, int32_t* dest, int32_t* row_token, int32_t* hist,
-                           hipStream_t s) {
-  const int nb = (T + kRouteBlock - 1) / kRouteBlock;
   int ep_log2 = 0;
   while ((1 << ep_log2) < E) ++ep_log2;
   route_scan<<<1, 1024, 0, s>>>(hist, nb, E, ep_log2, counts, offsets, offsets_pad, offsets_pad ? pad : 1);
@@ -405,8 +398,6 @@ int enqueue_route_metadata(const int32_t* topk_idx, int T, int E, int k, int32_t
   route_finalize<<<static_cast<unsigned>((n + 255) / 256), 256, 0, s>>>(topk_idx, dest, hist, offsets, T, k, E, row_token);
   return check_launch("route_finalize");
 }
-
-namespace {
 
 // ---- the no-allocation variant's scratch: the per-block counts in a file-scope device array.
 // Every GPU the library runs on holds its own copy until the process ends.  Host code never

@@ -2,33 +2,49 @@
 // them), a bias for balance that is added for the choice alone, the best groups of experts, the k
 // best experts of those, and gates from the unbiased scores; its gradient.
 //
-//   s[e] = sigmoid(l[e]) or exp(l[e] - max) / sum                 (64 bits)
-//   c[e] = s[e] + bias[e]                                         (64 bits; -inf where l[e] is -inf or NaN)
+//   s[e] = sigmoid(l[e]) or exp(l[e] - max) / sum
+//   c[e] = s[e] + bias[e]                                         (-inf where l[e] is -inf or NaN)
 //   v[g] = sum of the group_top largest c of group g              (E / n_group experts each)
 //   choice: the topk_group groups of largest v, of their experts the k of largest c (of largest l
 //   where there is no bias), ties to the lower index; gate = scale * s / (sum of the chosen s)
 //
-// The choice is made in 64 bits: with 256 experts a batch of 32768 tokens has a handful whose k-th and
-// next value differ by less than one fp32 rounding, and a choice that depends on how fp32 rounds an
-// exponential would differ between implementations and moves every later row of two experts.
+// The choice is the one that 64-bit scores make: with 256 experts a batch of 32768 tokens has a handful
+// whose k-th and next value differ by less than one fp32 rounding, and a choice that depends on how fp32
+// rounds an exponential would differ between implementations and move every later row of two experts.
+// Computing it all in 64 bits is what the first version did, and it was bound by those exponentials (130
+// us for 32768 tokens of 256 experts).  So a token is chosen from fp32 scores with a bound on their error,
+// and the few tokens (about 1 in 700 there) where two values that the choice separates are closer than the
+// bound are chosen again from 64-bit ones.  A gate is computed from its logit in 64 bits always, all of a
+// block's gates together.
 #include <cmath>
 
 #include "common.h"
-#include "route_meta.h"
 
 namespace moe {
 namespace {
 
-constexpr int kWaveTokens = 4;                 // tokens of a wave, one after the other
-constexpr int kBlockWaves = kRouteBlock / kWaveTokens;
-constexpr int kQ = kMaxE / 64;                 // experts of a lane: lane + 64 q
+constexpr int kRouteBlock = 64;                // tokens per block (one bit each in a 64-bit mask)
+constexpr int kMaxK = 16;
+constexpr int kMaxE = 256;
+constexpr int kThreads = 1024;
+constexpr int kWaves = kThreads / 64;
+constexpr int kWaveTokens = kRouteBlock / kWaves;   // tokens of a wave, one after the other
+constexpr int kQ = kMaxE / 64;                 // experts of a lane: kQ lane .. kQ lane + kQ - 1
+constexpr int kOut = INT32_MIN;                // key of an expert that cannot be chosen (any more)
 
 // A logit as the router reads it: NaN counts as -inf (an absent expert), +inf as the largest float.
 __device__ __forceinline__ float clean_logit(float l) {
   return l != l ? -INFINITY : fminf(l, 3.4028234663852886e38f);
 }
 
-// Order-preserving map of a double to uint64 (larger value -> larger key, -0 as +0, never 0).
+// Order-preserving map of a float to int (-0 as +0; never kOut), and back.
+__device__ __forceinline__ int float_key(float v) {
+  const int b = __float_as_int(v + 0.0f);
+  return b ^ ((b >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float key_float(int k) { return __int_as_float(k ^ ((k >> 31) & 0x7fffffff)); }
+
+// The same for a double, to uint64 (never 0).
 __device__ __forceinline__ unsigned long long double_key(double v) {
   const long long b = __double_as_longlong(v + 0.0);
   return b < 0 ? ~static_cast<unsigned long long>(b) : static_cast<unsigned long long>(b) | 0x8000000000000000ull;
@@ -38,6 +54,21 @@ __device__ __forceinline__ double wave_sum_f64(double v) {
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
   return v;
+}
+
+// Largest key over the wave, as a scalar: row shifts within 16 lanes, then broadcasts across rows.
+template <int CTRL>
+__device__ __forceinline__ int dpp_max(int v) {
+  return max(v, __builtin_amdgcn_update_dpp(v, v, CTRL, 0xf, 0xf, false));
+}
+__device__ __forceinline__ int wave_max_key(int v) {
+  v = dpp_max<0x111>(v);
+  v = dpp_max<0x112>(v);
+  v = dpp_max<0x114>(v);
+  v = dpp_max<0x118>(v);
+  v = dpp_max<0x142>(v);
+  v = dpp_max<0x143>(v);
+  return __builtin_amdgcn_readlane(v, 63);
 }
 
 // Orders the wave's LDS accesses before and after (lanes of one wave exchange values through LDS).
@@ -53,55 +84,45 @@ struct ScoredArgs {
   float scale;
 };
 
-// One wave per token.  Returns, in lane j < k, the j-th chosen expert and its gate.
-__device__ __forceinline__ void route_token(const ScoredArgs& a, long long t, int lane, double* s_choice,
-                                            float* __restrict__ scores, int& my_e, float& my_gate) {
-  const float* row = a.logits + t * a.E;
-  float l[kQ];
-  double p[kQ];
-  float m = -INFINITY;
-#pragma unroll
-  for (int q = 0; q < kQ; ++q) {
-    const int e = lane + 64 * q;
-    l[q] = e < a.E ? clean_logit(row[e]) : -INFINITY;
-    m = fmaxf(m, l[q]);
-  }
+// The k chosen experts of one token in lanes 0 .. k-1, from 64-bit scores; one wave per token.
+// `scores`: this token's row of the score output, or null.
+__device__ __forceinline__ int choose_exact(const ScoredArgs& a, const float (&l)[kQ], int lane, double* s_choice,
+                                            float* __restrict__ scores) {
+  const int e0 = kQ * lane;
+  double c[kQ];
   if (a.score == MOE_SCORE_SIGMOID) {
 #pragma unroll
-    for (int q = 0; q < kQ; ++q) p[q] = 1.0 / (1.0 + exp(-static_cast<double>(l[q])));
+    for (int q = 0; q < kQ; ++q) c[q] = 1.0 / (1.0 + exp(-static_cast<double>(l[q])));
   } else {
+    float m = fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3]));
     m = wave_max(m);
     const double md = m == -INFINITY ? 0.0 : static_cast<double>(m);
     double sum = 0.0;
 #pragma unroll
     for (int q = 0; q < kQ; ++q) {
-      p[q] = exp(static_cast<double>(l[q]) - md);
-      sum += p[q];
+      c[q] = exp(static_cast<double>(l[q]) - md);
+      sum += c[q];
     }
     sum = wave_sum_f64(sum);
     const double inv = sum > 0.0 ? 1.0 / sum : 0.0;
 #pragma unroll
-    for (int q = 0; q < kQ; ++q) p[q] *= inv;
+    for (int q = 0; q < kQ; ++q) c[q] *= inv;
   }
   if (scores != nullptr) {
 #pragma unroll
     for (int q = 0; q < kQ; ++q)
-      if (lane + 64 * q < a.E) scores[t * a.E + lane + 64 * q] = static_cast<float>(p[q]);
+      if (e0 + q < a.E) scores[e0 + q] = static_cast<float>(c[q]);
   }
-  double c[kQ];
 #pragma unroll
   for (int q = 0; q < kQ; ++q) {
-    const int e = lane + 64 * q;
-    c[q] = a.bias != nullptr && e < a.E ? p[q] + static_cast<double>(a.bias[e]) : p[q];
+    if (a.bias != nullptr && e0 + q < a.E) c[q] += static_cast<double>(a.bias[e0 + q]);
     if (l[q] == -INFINITY || c[q] != c[q]) c[q] = -INFINITY;
   }
-  // which of this lane's experts lie in a chosen group
-  unsigned inside = (1u << kQ) - 1u;
+  unsigned inside = (1u << kQ) - 1u;             // which of this lane's experts lie in a kept group
   if (a.topk_group < a.n_group) {
     const int per = a.E / a.n_group;
 #pragma unroll
-    for (int q = 0; q < kQ; ++q)
-      if (lane + 64 * q < a.E) s_choice[lane + 64 * q] = c[q];
+    for (int q = 0; q < kQ; ++q) s_choice[e0 + q] = c[q];
     wave_lds_sync();
     unsigned long long gkey[kQ];
 #pragma unroll
@@ -115,8 +136,7 @@ __device__ __forceinline__ void route_token(const ScoredArgs& a, long long t, in
           b1 = v > b0 ? b0 : (v > b1 ? v : b1);
           b0 = v > b0 ? v : b0;
         }
-        const double v = a.group_top == 1 || b1 == -INFINITY ? b0 : b0 + b1;
-        gkey[q] = double_key(v);
+        gkey[q] = double_key(a.group_top == 1 || b1 == -INFINITY ? b0 : b0 + b1);
       }
     }
     inside = 0u;
@@ -134,7 +154,7 @@ __device__ __forceinline__ void route_token(const ScoredArgs& a, long long t, in
 #pragma unroll
       for (int q = 0; q < kQ; ++q) {
         if (lane + 64 * q == g) gkey[q] = 0ull;
-        if (lane + 64 * q >= g * per && lane + 64 * q < (g + 1) * per) inside |= 1u << q;
+        if (e0 + q >= g * per && e0 + q < (g + 1) * per) inside |= 1u << q;
       }
     }
     wave_lds_sync();
@@ -142,149 +162,486 @@ __device__ __forceinline__ void route_token(const ScoredArgs& a, long long t, in
   unsigned long long key[kQ];
 #pragma unroll
   for (int q = 0; q < kQ; ++q) {
-    const int e = lane + 64 * q;
     const double v = a.bias != nullptr ? c[q] : static_cast<double>(l[q]);
-    key[q] = e < a.E && (inside >> q & 1u) ? double_key(v) : 0ull;
+    key[q] = e0 + q < a.E && (inside >> q & 1u) ? double_key(v) : 0ull;
   }
-  my_e = 0;
-  double my_p = 0.0;
+  int my_e = 0;
   for (int j = 0; j < a.k; ++j) {
     unsigned long long best = key[0];
+    int bq = 0;
 #pragma unroll
-    for (int q = 1; q < kQ; ++q) best = key[q] > best ? key[q] : best;
-    best = wave_max_u64(best);
-    int e = -1;
-#pragma unroll
-    for (int q = 0; q < kQ; ++q) {
-      const unsigned long long hit = __ballot(key[q] == best);
-      if (e < 0 && hit) e = 64 * q + __ffsll(static_cast<long long>(hit)) - 1;
-    }
-    e = __builtin_amdgcn_readfirstlane(e);
-    double pe = p[0];
-#pragma unroll
-    for (int q = 1; q < kQ; ++q) pe = (e >> 6) == q ? p[q] : pe;
-    pe = __shfl(pe, e & 63, 64);
-    if (lane == j) { my_e = e; my_p = pe; }
+    for (int q = 1; q < kQ; ++q)
+      if (key[q] > best) { best = key[q]; bq = q; }
+    const unsigned long long top = wave_max_u64(best);
+    const int src = __ffsll(static_cast<long long>(__ballot(best == top))) - 1;   // lower lanes hold lower experts
+    const int e = kQ * src + __shfl(bq, src, 64);
+    if (lane == j) my_e = e;
 #pragma unroll
     for (int q = 0; q < kQ; ++q)
-      if (lane + 64 * q == e) key[q] = 0ull;
+      if (e0 + q == e) key[q] = 0ull;
   }
-  double gate = my_p;
-  if (a.renormalize) {
-    const double sum = wave_sum_f64(my_p);
-    gate = sum > 0.0 ? my_p / sum : 0.0;
-  }
-  my_gate = static_cast<float>(gate * static_cast<double>(a.scale));
+  return my_e;
 }
 
-// 64 tokens per block of 16 waves; the row metadata as the other router's first kernel leaves it.
-__global__ __launch_bounds__(1024) void route_scored_local(ScoredArgs a, int32_t* __restrict__ topk_idx,
-                                                           float* __restrict__ topk_gate, float* __restrict__ scores,
-                                                           int32_t* __restrict__ local_rank,
-                                                           int32_t* __restrict__ hist) {
+// The same choice from fp32 scores, with my_e valid where the result is true: whether every comparison
+// that the choice rests on is wider than the scores' error.  A score is off by less than 2^-22: the
+// argument of the exponential by |l| 2^-24 of the result (l e^-|l| < 0.37), exponential and reciprocal by a
+// unit each (2^-23), sums by less than that; adding the bias rounds to 2^-24 of the sum.  Two values
+// further apart than 2^-20 + 2^-22 |value| are in the same order in 64 bits.  Logits compare exactly.
+// m_out, sum_out: the softmax's maximum and sum.
+__device__ __forceinline__ bool choose_fast(const ScoredArgs& a, const float (&l)[kQ], const float (&bias)[kQ], int lane,
+                                            float* s_choice, int& my_e, float& m_out, float& sum_out) {
+  const int e0 = kQ * lane;
+  const bool grouped = a.topk_group < a.n_group;
+  float c[kQ];
+  m_out = 0.f;
+  sum_out = 1.f;
+  if (a.score == MOE_SCORE_SOFTMAX) {
+    float m = fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3]));
+    m = key_float(wave_max_key(float_key(m)));
+    m_out = m == -INFINITY ? 0.f : m;
+    float sum = 0.f;
+#pragma unroll
+    for (int q = 0; q < kQ; ++q) {
+      c[q] = __expf(l[q] - m_out);
+      sum += c[q];
+    }
+    sum_out = wave_sum(sum);
+    const float inv = sum_out > 0.f ? 1.f / sum_out : 0.f;
+#pragma unroll
+    for (int q = 0; q < kQ; ++q) c[q] *= inv;
+  } else if (a.bias != nullptr || grouped) {
+#pragma unroll
+    for (int q = 0; q < kQ; ++q) c[q] = __builtin_amdgcn_rcpf(1.f + __expf(-l[q]));
+  }
+  if (a.bias != nullptr || grouped) {
+#pragma unroll
+    for (int q = 0; q < kQ; ++q) {
+      c[q] += bias[q];
+      if (l[q] == -INFINITY || c[q] != c[q]) c[q] = -INFINITY;
+    }
+  }
+  bool sure = true;
+  int key[kQ];
+#pragma unroll
+  for (int q = 0; q < kQ; ++q) key[q] = e0 + q < a.E ? float_key(a.bias != nullptr ? c[q] : l[q]) : kOut;
+  if (grouped) {
+    if (a.n_group > 64) return false;
+    const int per = a.E / a.n_group, lanes = per / kQ;
+    // v: the value of the lane's group, groups `stride` lanes apart.  Groups of whole aligned runs of 4, 8, ..
+    // experts merge the best two of each lane, others (20 or 40 experts, say) are walked in LDS, a lane each.
+    const bool aligned = per % kQ == 0 && (lanes & (lanes - 1)) == 0;
+    const int stride = aligned ? lanes : 1;
+    float b0, b1;
+    if (aligned) {
+      b0 = fmaxf(c[0], c[1]);
+      b1 = fminf(c[0], c[1]);
+#pragma unroll
+      for (int q = 2; q < kQ; ++q) {
+        b1 = fmaxf(b1, fminf(b0, c[q]));
+        b0 = fmaxf(b0, c[q]);
+      }
+      for (int o = 1; o < lanes; o <<= 1) {
+        const float p0 = __shfl_xor(b0, o, 64), p1 = __shfl_xor(b1, o, 64);
+        b1 = fmaxf(fminf(b0, p0), fmaxf(b1, p1));
+        b0 = fmaxf(b0, p0);
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < kQ; ++q) s_choice[e0 + q] = c[q];
+      wave_lds_sync();
+      b0 = b1 = -INFINITY;
+      if (lane < a.n_group) {
+        for (int i = 0; i < per; ++i) {
+          const float x = s_choice[lane * per + i];
+          b1 = fmaxf(b1, fminf(b0, x));
+          b0 = fmaxf(b0, x);
+        }
+      }
+      wave_lds_sync();
+    }
+    const float v = a.group_top == 1 || b1 == -INFINITY ? b0 : b0 + b1;
+    // kept: at most topk_group groups (itself among them) are as large within the margin; dropped: at
+    // least that many are larger beyond it; neither: not sure
+    const float tol = v > -INFINITY ? 0x1p-19f + 0x1p-21f * fabsf(v) : 0.f;
+    int maybe = 0, above = 0;
+    for (int i = 0; i < a.n_group; ++i) {
+      const float w = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), i * stride));
+      maybe += w >= v - tol ? 1 : 0;
+      above += w > v + tol ? 1 : 0;
+    }
+    const bool in = maybe <= a.topk_group;
+    const bool counts = lane < a.n_group * stride;       // lanes that hold a group
+    if (__ballot(counts && ((!in && above < a.topk_group) || v == INFINITY)) != 0ull) return false;
+    const unsigned long long kept = __ballot(counts && in);
+#pragma unroll
+    for (int q = 0; q < kQ; ++q) {
+      const int g = aligned ? lane : (e0 + q) / per;
+      if (!(kept >> (g & 63) & 1ull)) key[q] = kOut;
+    }
+  }
+  // each lane's experts in descending order (stable: adjacent swaps of strictly larger keys), their
+  // positions in the bytes of `order`
+  int pos[kQ] = {0, 1, 2, 3};
+  auto swap = [&](int i) {
+    const bool up = key[i + 1] > key[i];
+    const int x = key[i], y = pos[i];
+    key[i] = up ? key[i + 1] : x;
+    key[i + 1] = up ? x : key[i + 1];
+    pos[i] = up ? pos[i + 1] : y;
+    pos[i + 1] = up ? y : pos[i + 1];
+  };
+  swap(0); swap(1); swap(2);
+  swap(0); swap(1);
+  swap(0);
+  unsigned order = pos[0] | pos[1] << 8 | pos[2] << 16 | pos[3] << 24;
+  my_e = 0;
+  float last = 0.f;
+  const int rounds = a.k + (a.bias != nullptr ? 1 : 0);
+  for (int j = 0; j < rounds; ++j) {
+    const int m = wave_max_key(key[0]);
+    if (a.bias != nullptr) {
+      const float v = key_float(m);
+      if (j > 0 && m != kOut) sure = sure && last - v > 0x1p-20f + 0x1p-22f * fabsf(last);
+      if (j > 0 && m == kOut) sure = sure && last > -INFINITY;
+      last = v;
+    }
+    if (j == a.k) break;
+    const int src = __ffsll(static_cast<long long>(__ballot(key[0] == m))) - 1;
+    const int e = kQ * src + (__builtin_amdgcn_readlane(order, src) & 0xff);
+    my_e = lane == j ? e : my_e;
+    const bool pop = lane == src;
+    key[0] = pop ? key[1] : key[0];
+    key[1] = pop ? key[2] : key[1];
+    key[2] = pop ? key[3] : key[2];
+    key[3] = pop ? kOut : key[3];
+    order = pop ? order >> 8 : order;
+  }
+  return sure;
+}
+
+// Inclusive scan over the 256 first threads of two values at once (every thread of the block calls it).
+__device__ __forceinline__ void scan256(int& x, int& y, int (*s_part)[2]) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int p = __shfl_up(x, o, 64), q = __shfl_up(y, o, 64);
+    if (lane >= o) { x += p; y += q; }
+  }
+  if (lane == 63 && wave < 4) { s_part[wave][0] = x; s_part[wave][1] = y; }
+  __syncthreads();
+  for (int w = 0; w < wave && w < 3; ++w) { x += s_part[w][0]; y += s_part[w][1]; }
+}
+
+struct MetaOut {
+  int32_t* counts;
+  int32_t* offsets;
+  int32_t* offsets_pad;
+  int pad;
+  int32_t* dest;
+  int32_t* row_token;
+};
+
+// Offsets of the experts from their counts: thread e < 256 gives its count, and afterwards holds in
+// s_off[e] its first row; `lead` also writes offsets and offsets_pad.
+__device__ __forceinline__ void expert_offsets(int count, int E, const MetaOut& m, bool lead, int* s_off,
+                                               int (*s_part)[2]) {
+  const int e = threadIdx.x;
+  const int padded = m.offsets_pad != nullptr ? (count + m.pad - 1) / m.pad * m.pad : 0;
+  int x = count, y = padded;
+  scan256(x, y, s_part);
+  if (e < kMaxE) s_off[e] = x - count;
+  if (lead && e < E) {
+    m.offsets[e + 1] = x;
+    if (e == 0) m.offsets[0] = 0;
+    if (m.offsets_pad != nullptr) {
+      m.offsets_pad[e + 1] = y;
+      if (e == 0) m.offsets_pad[0] = 0;
+    }
+  }
+  __syncthreads();
+}
+
+// 64 tokens per block of 16 waves, one token at a time per wave.  Each (token, slot) sets its token's bit
+// in its expert's 64-bit mask, so a row's rank among the block's rows of its expert is a popcount of the
+// lower bits.  SINGLE: one block has all tokens and finishes the metadata; else it leaves the ranks in
+// dest and its counts in hist [E][blocks].
+template <bool SINGLE>
+__global__ __launch_bounds__(kThreads) void route_scored_local(ScoredArgs a, int32_t* __restrict__ topk_idx,
+                                                               float* __restrict__ topk_gate,
+                                                               float* __restrict__ scores, int32_t* __restrict__ hist,
+                                                               MetaOut out) {
   __shared__ unsigned long long s_mask[kMaxE];
   __shared__ int s_e[kRouteBlock][kMaxK];
-  __shared__ double s_choice[kBlockWaves][kMaxE];
+  __shared__ float s_max[kRouteBlock], s_sum[kRouteBlock];
+  __shared__ double s_choice[kWaves][kMaxE];
+  __shared__ int s_off[kMaxE];
+  __shared__ int s_part[4][2];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const long long t0 = static_cast<long long>(blockIdx.x) * kRouteBlock;
-  for (int e = tid; e < a.E; e += 1024) s_mask[e] = 0ull;
+  if (tid < kMaxE) s_mask[tid] = 0ull;
   __syncthreads();
+  // a wave's rows are all loaded first
+  float l[kWaveTokens][kQ];
+  float bias[kQ];
+#pragma unroll
+  for (int q = 0; q < kQ; ++q)
+    bias[q] = a.bias != nullptr && kQ * lane + q < a.E ? a.bias[kQ * lane + q] : 0.f;
+#pragma unroll
+  for (int i = 0; i < kWaveTokens; ++i) {
+    const long long t = t0 + wave * kWaveTokens + i;
+    const bool live = t < a.T;
+    if ((a.E & 3) == 0) {
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      const bool in = live && kQ * lane < a.E;
+      if (in) v = *reinterpret_cast<const float4*>(a.logits + t * a.E + kQ * lane);
+      l[i][0] = in ? v.x : -INFINITY; l[i][1] = in ? v.y : -INFINITY;
+      l[i][2] = in ? v.z : -INFINITY; l[i][3] = in ? v.w : -INFINITY;
+    } else {
+#pragma unroll
+      for (int q = 0; q < kQ; ++q)
+        l[i][q] = live && kQ * lane + q < a.E ? a.logits[t * a.E + kQ * lane + q] : -INFINITY;
+    }
+  }
+#pragma unroll
   for (int i = 0; i < kWaveTokens; ++i) {
     const int tl = wave * kWaveTokens + i;
     const long long t = t0 + tl;
     if (t >= a.T) break;
+#pragma unroll
+    for (int q = 0; q < kQ; ++q) l[i][q] = clean_logit(l[i][q]);
     int e;
-    float gate;
-    route_token(a, t, lane, s_choice[wave], scores, e, gate);
+    float m, sum;
+    const bool sure = choose_fast(a, l[i], bias, lane, reinterpret_cast<float*>(s_choice[wave]), e, m, sum);
+    if (__ballot(!sure) != 0ull || scores != nullptr)
+      e = choose_exact(a, l[i], lane, s_choice[wave], scores != nullptr ? scores + t * a.E : nullptr);
     if (lane < a.k) {
-      topk_idx[t * a.k + lane] = e;
-      topk_gate[t * a.k + lane] = gate;
       s_e[tl][lane] = e;
       atomicOr(&s_mask[e], 1ull << tl);
     }
+    if (lane == 0) { s_max[tl] = m; s_sum[tl] = sum; }
   }
   __syncthreads();
-  for (int i = tid; i < kRouteBlock * a.k; i += 1024) {
-    const int tl = i / a.k, j = i - tl * a.k;
+  // ---- gates: 16 lanes per token, from the chosen logits in 64 bits
+  {
+    const int tl = tid >> 4, j = tid & 15;
     const long long t = t0 + tl;
-    if (t < a.T) local_rank[t * a.k + j] = __popcll(s_mask[s_e[tl][j]] & ((1ull << tl) - 1ull));
+    const bool live = t < a.T && j < a.k;
+    const int e = live ? s_e[tl][j] : 0;
+    double p = 0.0;
+    if (live) {
+      const double lj = static_cast<double>(clean_logit(a.logits[t * a.E + e]));
+      p = a.score == MOE_SCORE_SIGMOID ? 1.0 / (1.0 + exp(-lj)) : exp(lj - static_cast<double>(s_max[tl]));
+    }
+    double gate = p;
+    if (a.renormalize) {
+      double sum = p;
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
+      gate = sum > 0.0 ? p / sum : 0.0;
+    } else if (a.score == MOE_SCORE_SOFTMAX && live) {
+      gate = s_sum[tl] > 0.f ? p / static_cast<double>(s_sum[tl]) : 0.0;
+    }
+    if (live) {
+      topk_idx[t * a.k + j] = e;
+      topk_gate[t * a.k + j] = static_cast<float>(gate * static_cast<double>(a.scale));
+    }
+    if constexpr (SINGLE) {
+      const int count = tid < a.E ? __popcll(s_mask[tid]) : 0;
+      if (tid < a.E) out.counts[tid] = count;
+      expert_offsets(count, a.E, out, true, s_off, s_part);
+    }
+    if (live) {
+      const int rank = __popcll(s_mask[e] & ((1ull << tl) - 1ull));
+      if constexpr (SINGLE) {
+        const int r = s_off[e] + rank;
+        out.dest[t * a.k + j] = r;
+        if (out.row_token != nullptr) out.row_token[r] = static_cast<int32_t>(t);
+      } else {
+        out.dest[t * a.k + j] = rank;
+      }
+    }
   }
-  for (int e = tid; e < a.E; e += 1024) hist[static_cast<long long>(blockIdx.x) * a.E + e] = __popcll(s_mask[e]);
+  if constexpr (!SINGLE)
+    for (int e = tid; e < a.E; e += kThreads)
+      hist[static_cast<long long>(e) * gridDim.x + blockIdx.x] = __popcll(s_mask[e]);
 }
 
-// Gradient with the choice held fixed, one wave per token:
+// One wave per expert: its block counts become exclusive prefixes, their sum counts[e].
+__global__ __launch_bounds__(256) void route_scored_scan(int32_t* __restrict__ hist, int nb, int E,
+                                                         int32_t* __restrict__ counts) {
+  const int e = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+  if (e >= E) return;
+  int32_t* h = hist + static_cast<long long>(e) * nb;
+  int carry = 0;
+  for (int b0 = 0; b0 < nb; b0 += 256) {          // 4 consecutive entries per lane
+    int v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = b0 + 4 * lane + i < nb ? h[b0 + 4 * lane + i] : 0;
+    const int own = v[0] + v[1] + v[2] + v[3];
+    int incl = own;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int p = __shfl_up(incl, o, 64);
+      if (lane >= o) incl += p;
+    }
+    int run = carry + incl - own;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (b0 + 4 * lane + i < nb) h[b0 + 4 * lane + i] = run;
+      run += v[i];
+    }
+    carry += __shfl(incl, 63, 64);
+  }
+  if (lane == 0) counts[e] = carry;
+}
+
+// Rows: the expert's first row + its rows in earlier blocks + the rank in the block.  Every workgroup
+// scans the 256 counts itself.
+constexpr int kFinalThreads = 256, kFinalItems = 4;
+__global__ __launch_bounds__(kFinalThreads) void route_scored_finalize(const int32_t* __restrict__ topk_idx,
+                                                                       const int32_t* __restrict__ hist, int nb,
+                                                                       long long n, int k, int E, MetaOut out) {
+  __shared__ int s_off[kMaxE];
+  __shared__ int s_part[4][2];
+  const int e_t = threadIdx.x;
+  const int count = e_t < E ? out.counts[e_t] : 0;
+  const long long i0 = static_cast<long long>(blockIdx.x) * kFinalThreads * kFinalItems + threadIdx.x;
+  int e[kFinalItems], rank[kFinalItems];
+#pragma unroll
+  for (int i = 0; i < kFinalItems; ++i) {
+    const long long at = i0 + i * kFinalThreads;
+    e[i] = at < n ? topk_idx[at] : 0;
+    rank[i] = at < n ? out.dest[at] : 0;
+  }
+#pragma unroll
+  for (int i = 0; i < kFinalItems; ++i) {
+    const long long at = i0 + i * kFinalThreads;
+    if (at < n) rank[i] += hist[static_cast<long long>(e[i]) * nb + at / k / kRouteBlock];
+  }
+  expert_offsets(count, E, out, blockIdx.x == 0, s_off, s_part);
+#pragma unroll
+  for (int i = 0; i < kFinalItems; ++i) {
+    const long long at = i0 + i * kFinalThreads;
+    if (at < n) {
+      const int r = s_off[e[i]] + rank[i];
+      out.dest[at] = r;
+      if (out.row_token != nullptr) out.row_token[r] = static_cast<int32_t>(at / k);
+    }
+  }
+}
+
+// ---- gradient, with the choice held fixed:
 //   sigmoid  dl = s (1 - s) ds,  softmax  dl[e] = s[e] (ds[e] - sum s ds),  ds of the chosen experts from
 //   the gates (renormalised: ds_j = (dg_j - sum g dg) / sum s), 0 elsewhere.
-// Renormalised gates come from the chosen logits alone, in the log domain, so scores that underflow
-// still give finite ratios; only the plain softmax needs (and has) a gradient at every expert.
-__global__ __launch_bounds__(256) void route_scored_bwd_kernel(const float* __restrict__ logits,
-                                                               const int32_t* __restrict__ idx,
-                                                               const float* __restrict__ dgate, int T, int E, int k,
-                                                               int score, int renormalize, float scale,
-                                                               float* __restrict__ dlogits) {
-  const long long t = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63;
-  if (t >= T) return;
-  int e_l = lane < k ? idx[t * k + lane] : -1;
-  if (e_l >= E) e_l = -1;                          // no expert of this layer: no gradient
-  const float l_l = e_l >= 0 ? clean_logit(logits[t * E + e_l]) : -INFINITY;
-  const float dg = e_l >= 0 ? dgate[t * k + lane] * scale : 0.f;
-  float val;                        // lane j: the gradient at the j-th chosen expert (plain softmax: p dg)
-  float pe[kQ];                     // plain softmax: scores of experts lane + 64 q
-  float inner = 0.f;
-  const bool dense = score == MOE_SCORE_SOFTMAX && !renormalize;
-  if (dense) {
+// Renormalised gates come from the chosen logits alone, in the log domain, so scores that underflow still
+// give finite ratios; only the plain softmax needs (and has) a gradient at every expert.
+// Bound by its bytes (the gradient written, and the logits read by the plain softmax).  A wave takes four
+// tokens, 16 lanes each, and forms their rows in LDS, so rows come and go as whole 16-byte runs.
+constexpr int kBwdTokens = 4, kBwdWaves = 4;
+
+__device__ __forceinline__ float group_sum16(float v) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+  return v;
+}
+__device__ __forceinline__ float group_max16(float v) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
+  return v;
+}
+
+template <bool DENSE>
+__global__ __launch_bounds__(64 * kBwdWaves) void route_scored_bwd_kernel(const float* __restrict__ logits,
+                                                                         const int32_t* __restrict__ idx,
+                                                                         const float* __restrict__ dgate, int T, int E,
+                                                                         int k, int score, int renormalize, float scale,
+                                                                         float* __restrict__ dlogits) {
+  // rows 16 floats past a multiple of 64 apart, so the four tokens' lanes use different banks
+  __shared__ __attribute__((aligned(16))) float s_row[kBwdWaves][kBwdTokens][kMaxE + 16];
+  __shared__ int s_e[kBwdWaves][kBwdTokens][kMaxK];
+  __shared__ float s_v[kBwdWaves][kBwdTokens][kMaxK];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int tok = lane >> 4, j = lane & 15;
+  const long long t0 = (static_cast<long long>(blockIdx.x) * kBwdWaves + wave) * kBwdTokens;
+  if (t0 >= T) return;
+  const long long t = t0 + tok;
+  const bool vec = (E & 3) == 0;
+  float(*row)[kMaxE + 16] = s_row[wave];
+  const bool live = t < T && j < k;
+  int e = live ? idx[t * k + j] : -1;
+  if (e >= E) e = -1;                              // no expert of this layer: no gradient
+  const float l = e >= 0 ? clean_logit(logits[t * E + e]) : -INFINITY;
+  const float dg = e >= 0 ? dgate[t * k + j] * scale : 0.f;
+  float val, inner = 0.f;
+  float pe[kMaxE / 16];                            // DENSE: scores of experts j + 16 i
+  if constexpr (DENSE) {
+#pragma unroll
+    for (int i = 0; i < kBwdTokens; ++i) {
+      if (t0 + i >= T) break;
+      if (vec) {
+        if (4 * lane < E) *reinterpret_cast<float4*>(&row[i][4 * lane]) = *reinterpret_cast<const float4*>(logits + (t0 + i) * E + 4 * lane);
+      } else {
+        for (int c = lane; c < E; c += 64) row[i][c] = logits[(t0 + i) * E + c];
+      }
+    }
+    wave_lds_sync();
     float m = -INFINITY;
 #pragma unroll
-    for (int q = 0; q < kQ; ++q) {
-      pe[q] = lane + 64 * q < E ? clean_logit(logits[t * E + lane + 64 * q]) : -INFINITY;
-      m = fmaxf(m, pe[q]);
+    for (int i = 0; i < kMaxE / 16; ++i) {
+      pe[i] = t < T && j + 16 * i < E ? clean_logit(row[tok][j + 16 * i]) : -INFINITY;
+      m = fmaxf(m, pe[i]);
     }
-    m = wave_max(m);
+    m = group_max16(m);
     m = m == -INFINITY ? 0.f : m;
     float sum = 0.f;
 #pragma unroll
-    for (int q = 0; q < kQ; ++q) {
-      pe[q] = expf(pe[q] - m);
-      sum += pe[q];
+    for (int i = 0; i < kMaxE / 16; ++i) {
+      pe[i] = j + 16 * i < E ? expf(pe[i] - m) : 0.f;
+      sum += pe[i];
     }
-    sum = wave_sum(sum);
+    sum = group_sum16(sum);
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
-    for (int q = 0; q < kQ; ++q) pe[q] *= inv;
-    val = expf(l_l - m) * inv * dg;
-    inner = wave_sum(val);
+    for (int i = 0; i < kMaxE / 16; ++i) pe[i] *= inv;
+    val = expf(l - m) * inv * dg;
+    inner = group_sum16(val);
   } else if (renormalize) {
     // log sigmoid(l) = min(l, 0) - log(1 + exp(-|l|))
-    const float w = score == MOE_SCORE_SIGMOID ? fminf(l_l, 0.f) - log1pf(expf(-fabsf(l_l))) : l_l;
-    float m = wave_max(w);
+    const float w = score == MOE_SCORE_SIGMOID ? fminf(l, 0.f) - log1pf(expf(-fabsf(l))) : l;
+    float m = group_max16(w);
     m = m == -INFINITY ? 0.f : m;
-    const float ex = l_l == -INFINITY ? 0.f : expf(w - m);
-    const float sum = wave_sum(ex);
+    const float ex = l == -INFINITY ? 0.f : expf(w - m);
+    const float sum = group_sum16(ex);
     const float g = sum > 0.f ? ex / sum : 0.f;
-    val = g * (dg - wave_sum(g * dg));
-    if (score == MOE_SCORE_SIGMOID) val *= 1.f / (1.f + expf(l_l));
+    val = g * (dg - group_sum16(g * dg));
+    if (score == MOE_SCORE_SIGMOID) val *= 1.f / (1.f + expf(l));
   } else {
-    const float ex = expf(-fabsf(l_l));            // s (1 - s) = e / (1 + e)^2 with e = exp(-|l|)
+    const float ex = expf(-fabsf(l));              // s (1 - s) = x / (1 + x)^2 with x = exp(-|l|)
     val = ex / ((1.f + ex) * (1.f + ex)) * dg;
   }
-  int ej[kMaxK];
-  float vj[kMaxK];
+  // a repeated expert gets the sum of its slots, in slot order
+  s_e[wave][tok][j] = e;
+  s_v[wave][tok][j] = val;
+  wave_lds_sync();
+  float total = 0.f;
+  for (int i = 0; i < k; ++i) total += s_e[wave][tok][i] == e ? s_v[wave][tok][i] : 0.f;
 #pragma unroll
-  for (int j = 0; j < kMaxK; ++j) {
-    ej[j] = __shfl(e_l, j, 64);
-    vj[j] = __shfl(val, j, 64);
-  }
+  for (int i = 0; i < kMaxE / 16; ++i)
+    if (j + 16 * i < E) row[tok][j + 16 * i] = DENSE ? -pe[i] * inner : 0.f;
+  wave_lds_sync();
+  const float base = e >= 0 ? row[tok][e] : 0.f;
+  wave_lds_sync();
+  if (e >= 0) row[tok][e] = base + total;
+  wave_lds_sync();
 #pragma unroll
-  for (int q = 0; q < kQ; ++q) {
-    const int e = lane + 64 * q;
-    if (e >= E) break;
-    float v = 0.f;
-#pragma unroll
-    for (int j = 0; j < kMaxK; ++j)
-      if (j < k && ej[j] == e) v += vj[j];
-    if (dense) v -= pe[q] * inner;
-    dlogits[t * E + e] = v;
+  for (int i = 0; i < kBwdTokens; ++i) {
+    if (t0 + i >= T) break;
+    if (vec) {
+      if (4 * lane < E) *reinterpret_cast<float4*>(dlogits + (t0 + i) * E + 4 * lane) = *reinterpret_cast<const float4*>(&row[i][4 * lane]);
+    } else {
+      for (int c = lane; c < E; c += 64) dlogits[(t0 + i) * E + c] = row[i][c];
+    }
   }
 }
 
@@ -325,18 +682,38 @@ extern "C" int moe_route_scored(const float* logits, const float* bias, int T, i
   MOE_REQUIRE(ws != nullptr && ws_bytes >= need, MOE_ERR_WORKSPACE, "route workspace: need %zu bytes", need);
   MOE_CHECK_ALIGN(ws);
   const ScoredArgs a{logits, bias, T, E, k, score, n_group, topk_group, group_top, renormalize, scale};
+  const MetaOut out{counts, offsets, offsets_pad, pad, dest, row_token};
   int32_t* hist = static_cast<int32_t*>(ws);
   hipStream_t s = as_stream(stream);
-  route_scored_local<<<(T + kRouteBlock - 1) / kRouteBlock, 1024, 0, s>>>(a, topk_idx, topk_gate, scores, dest, hist);
+  if (T <= kRouteBlock) {
+    route_scored_local<true><<<1, kThreads, 0, s>>>(a, topk_idx, topk_gate, scores, hist, out);
+    return check_launch("route_scored_local");
+  }
+  const int nb = (T + kRouteBlock - 1) / kRouteBlock;
+  const long long n = static_cast<long long>(T) * k;
+  route_scored_local<false><<<nb, kThreads, 0, s>>>(a, topk_idx, topk_gate, scores, hist, out);
   if (int st = check_launch("route_scored_local")) return st;
-  return enqueue_route_metadata(topk_idx, T, E, k, counts, offsets, offsets_pad, pad, dest, row_token, hist, s);
+  route_scored_scan<<<(E + 3) / 4, 256, 0, s>>>(hist, nb, E, counts);
+  if (int st = check_launch("route_scored_scan")) return st;
+  constexpr int per = kFinalThreads * kFinalItems;
+  route_scored_finalize<<<static_cast<unsigned>((n + per - 1) / per), kFinalThreads, 0, s>>>(topk_idx, hist, nb, n, k, E,
+                                                                                          out);
+  return check_launch("route_scored_finalize");
 }
 
 extern "C" int moe_route_scored_bwd(const float* logits, const int32_t* topk_idx, const float* d_gate, int T, int E,
                                     int k, int score, int renormalize, float scale, float* d_logits, void* stream) {
   if (int st = check_scored(T, E, k, score, scale)) return st;
   MOE_CHECK_PTR(logits); MOE_CHECK_PTR(topk_idx); MOE_CHECK_PTR(d_gate); MOE_CHECK_PTR(d_logits);
-  route_scored_bwd_kernel<<<static_cast<unsigned>((static_cast<long long>(T) + 3) / 4), 256, 0, as_stream(stream)>>>(
-      logits, topk_idx, d_gate, T, E, k, score, renormalize, scale, d_logits);
+  MOE_CHECK_ALIGN(logits); MOE_CHECK_ALIGN(d_logits);
+  constexpr int per = kBwdWaves * kBwdTokens;
+  const unsigned blocks = static_cast<unsigned>((static_cast<long long>(T) + per - 1) / per);
+  hipStream_t s = as_stream(stream);
+  if (score == MOE_SCORE_SOFTMAX && !renormalize)
+    route_scored_bwd_kernel<true><<<blocks, 64 * kBwdWaves, 0, s>>>(logits, topk_idx, d_gate, T, E, k, score, renormalize,
+                                                                   scale, d_logits);
+  else
+    route_scored_bwd_kernel<false><<<blocks, 64 * kBwdWaves, 0, s>>>(logits, topk_idx, d_gate, T, E, k, score, renormalize,
+                                                                    scale, d_logits);
   return check_launch("route_scored_bwd");
 }
