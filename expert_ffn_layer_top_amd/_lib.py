@@ -28,6 +28,7 @@ SIGNATURES = {
     "moe_route_balance_workspace_bytes": (_sz, [_i, _i]),
     "moe_route_balance": (_i, [_p, _p, _i, _i, _i, _p, _p, _p, _sz, _p]),
     "moe_route_topk_bwd_balance": (_i, [_p, _p, _p, _p, _p, ctypes.c_float, _i, _i, _i, _p, _p]),
+    "moe_route_scored_workspace_bytes": (_sz, [_i, _i, _i]),
     "moe_route_scored": (_i, [_p, _p, _i, _i, _i, _i, _i, _i, _i, _i, ctypes.c_float, _p, _p, _p, _p, _p, _p, _i,
                               _p, _p, _p, _sz, _p]),
     "moe_route_scored_bwd": (_i, [_p, _p, _p, _i, _i, _i, _i, _i, ctypes.c_float, _p, _p]),

@@ -59,7 +59,7 @@ __device__ __forceinline__ double wave_sum_f64(double v) {
 // Largest key over the wave, as a scalar: row shifts within 16 lanes, then broadcasts across rows.
 template <int CTRL>
 __device__ __forceinline__ int dpp_max(int v) {
-  return max(v, __builtin_amdgcn_update_dpp(v, v, CTRL, 0xf, 0xf, false));
+  return max(v, __builtin_amdgcn_update_dpp(kOut, v, CTRL, 0xf, 0xf, false));   // folds into one v_max
 }
 __device__ __forceinline__ int wave_max_key(int v) {
   v = dpp_max<0x111>(v);
@@ -85,61 +85,64 @@ struct ScoredArgs {
 };
 
 // The k chosen experts of one token in lanes 0 .. k-1, from 64-bit scores; one wave per token.
-// `scores`: this token's row of the score output, or null.
-__device__ __forceinline__ int choose_exact(const ScoredArgs& a, const float (&l)[kQ], int lane, double* s_choice,
+// `scores`: this token's row of the score output, or null.  Rarely taken, so it keeps its values in LDS and
+// its loops rolled: unrolled, its exponentials set the kernel's registers and halved the waves in flight.
+__device__ __forceinline__ int choose_exact(const ScoredArgs& a, const float (&l)[kQ], int lane, double* s_c,
                                             float* __restrict__ scores) {
   const int e0 = kQ * lane;
-  double c[kQ];
-  if (a.score == MOE_SCORE_SIGMOID) {
+  const double ninf = -INFINITY;
 #pragma unroll
-    for (int q = 0; q < kQ; ++q) c[q] = 1.0 / (1.0 + exp(-static_cast<double>(l[q])));
-  } else {
-    float m = fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3]));
-    m = wave_max(m);
+  for (int q = 0; q < kQ; ++q) s_c[e0 + q] = static_cast<double>(l[q]);
+  double inv = 1.0;
+  if (a.score == MOE_SCORE_SOFTMAX) {
+    const float m = wave_max(fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])));
     const double md = m == -INFINITY ? 0.0 : static_cast<double>(m);
     double sum = 0.0;
-#pragma unroll
+#pragma unroll 1
     for (int q = 0; q < kQ; ++q) {
-      c[q] = exp(static_cast<double>(l[q]) - md);
-      sum += c[q];
+      const double x = exp(s_c[e0 + q] - md);
+      s_c[e0 + q] = x;
+      sum += x;
     }
     sum = wave_sum_f64(sum);
-    const double inv = sum > 0.0 ? 1.0 / sum : 0.0;
-#pragma unroll
-    for (int q = 0; q < kQ; ++q) c[q] *= inv;
+    inv = sum > 0.0 ? 1.0 / sum : 0.0;
   }
-  if (scores != nullptr) {
-#pragma unroll
-    for (int q = 0; q < kQ; ++q)
-      if (e0 + q < a.E) scores[e0 + q] = static_cast<float>(c[q]);
-  }
-#pragma unroll
+#pragma unroll 1
   for (int q = 0; q < kQ; ++q) {
-    if (a.bias != nullptr && e0 + q < a.E) c[q] += static_cast<double>(a.bias[e0 + q]);
-    if (l[q] == -INFINITY || c[q] != c[q]) c[q] = -INFINITY;
+    const int e = e0 + q;
+    const double x = s_c[e];
+    const double p = a.score == MOE_SCORE_SIGMOID ? 1.0 / (1.0 + exp(-x)) : x * inv;
+    const float lq = q == 0 ? l[0] : (q == 1 ? l[1] : (q == 2 ? l[2] : l[3]));
+    double c = p;
+    if (e < a.E) {
+      if (scores != nullptr) scores[e] = static_cast<float>(p);
+      if (a.bias != nullptr) c += static_cast<double>(a.bias[e]);
+    }
+    s_c[e] = lq == -INFINITY || c != c ? ninf : c;
   }
-  unsigned inside = (1u << kQ) - 1u;             // which of this lane's experts lie in a kept group
+  wave_lds_sync();
+  unsigned long long kept[kQ] = {~0ull, ~0ull, ~0ull, ~0ull};     // kept groups, 64 to a word
+  const int per = a.E / a.n_group;
   if (a.topk_group < a.n_group) {
-    const int per = a.E / a.n_group;
 #pragma unroll
-    for (int q = 0; q < kQ; ++q) s_choice[e0 + q] = c[q];
-    wave_lds_sync();
+    for (int q = 0; q < kQ; ++q) kept[q] = 0ull;
     unsigned long long gkey[kQ];
 #pragma unroll
     for (int q = 0; q < kQ; ++q) {
       const int g = lane + 64 * q;
       gkey[q] = 0ull;
       if (g < a.n_group) {
-        double b0 = -INFINITY, b1 = -INFINITY;
+        double b0 = ninf, b1 = ninf;
+#pragma unroll 1
         for (int i = 0; i < per; ++i) {
-          const double v = s_choice[g * per + i];
+          const double v = s_c[g * per + i];
           b1 = v > b0 ? b0 : (v > b1 ? v : b1);
           b0 = v > b0 ? v : b0;
         }
-        gkey[q] = double_key(a.group_top == 1 || b1 == -INFINITY ? b0 : b0 + b1);
+        gkey[q] = double_key(a.group_top == 1 || b1 == ninf ? b0 : b0 + b1);
       }
     }
-    inside = 0u;
+#pragma unroll 1
     for (int r = 0; r < a.topk_group; ++r) {
       unsigned long long best = gkey[0];
 #pragma unroll
@@ -154,18 +157,22 @@ __device__ __forceinline__ int choose_exact(const ScoredArgs& a, const float (&l
 #pragma unroll
       for (int q = 0; q < kQ; ++q) {
         if (lane + 64 * q == g) gkey[q] = 0ull;
-        if (e0 + q >= g * per && e0 + q < (g + 1) * per) inside |= 1u << q;
+        if (g >> 6 == q) kept[q] |= 1ull << (g & 63);
       }
     }
-    wave_lds_sync();
   }
   unsigned long long key[kQ];
 #pragma unroll
   for (int q = 0; q < kQ; ++q) {
-    const double v = a.bias != nullptr ? c[q] : static_cast<double>(l[q]);
-    key[q] = e0 + q < a.E && (inside >> q & 1u) ? double_key(v) : 0ull;
+    const int e = e0 + q, g = e / per;
+    unsigned long long word = kept[0];
+#pragma unroll
+    for (int i = 1; i < kQ; ++i) word = g >> 6 == i ? kept[i] : word;
+    const double v = a.bias != nullptr ? s_c[e] : static_cast<double>(l[q]);
+    key[q] = e < a.E && (word >> (g & 63) & 1ull) ? double_key(v) : 0ull;
   }
   int my_e = 0;
+#pragma unroll 1
   for (int j = 0; j < a.k; ++j) {
     unsigned long long best = key[0];
     int bq = 0;
@@ -180,6 +187,7 @@ __device__ __forceinline__ int choose_exact(const ScoredArgs& a, const float (&l
     for (int q = 0; q < kQ; ++q)
       if (e0 + q == e) key[q] = 0ull;
   }
+  wave_lds_sync();
   return my_e;
 }
 
@@ -362,15 +370,78 @@ __device__ __forceinline__ void expert_offsets(int count, int E, const MetaOut& 
   __syncthreads();
 }
 
-// 64 tokens per block of 16 waves, one token at a time per wave.  Each (token, slot) sets its token's bit
-// in its expert's 64-bit mask, so a row's rank among the block's rows of its expert is a popcount of the
-// lower bits.  SINGLE: one block has all tokens and finishes the metadata; else it leaves the ranks in
-// dest and its counts in hist [E][blocks].
+__device__ __forceinline__ float group_sum16(float v) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+  return v;
+}
+__device__ __forceinline__ float group_max16(float v) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
+  return v;
+}
+
+// One token's logits, 4 per lane (-inf past the experts and past the tokens).
+__device__ __forceinline__ void load_logits(const ScoredArgs& a, long long t, int lane, float (&l)[kQ]) {
+  if ((a.E & 3) == 0) {
+    const bool in = t < a.T && kQ * lane < a.E;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (in) v = *reinterpret_cast<const float4*>(a.logits + t * a.E + kQ * lane);
+    l[0] = in ? v.x : -INFINITY; l[1] = in ? v.y : -INFINITY;
+    l[2] = in ? v.z : -INFINITY; l[3] = in ? v.w : -INFINITY;
+  } else {
+#pragma unroll
+    for (int q = 0; q < kQ; ++q)
+      l[q] = t < a.T && kQ * lane + q < a.E ? a.logits[t * a.E + kQ * lane + q] : -INFINITY;
+  }
+}
+
+__device__ __forceinline__ void load_bias(const ScoredArgs& a, int lane, float (&bias)[kQ]) {
+#pragma unroll
+  for (int q = 0; q < kQ; ++q)
+    bias[q] = a.bias != nullptr && kQ * lane + q < a.E ? a.bias[kQ * lane + q] : 0.f;
+}
+
+// First kernel of more than 64 tokens: the fp32 choice, a wave per token, -1 in the token's first slot where
+// that does not decide it.  Apart from the 64-bit code, whose registers (96 instead of 56) would halve the
+// waves in flight: this kernel is bound by the latency of its chains of reductions.
+constexpr int kChooseWaves = 4, kChooseTokens = 4;
+__global__ __launch_bounds__(64 * kChooseWaves, 8) void route_scored_choose(ScoredArgs a, int32_t* __restrict__ topk_idx,
+                                                                           float2* __restrict__ softmax_sums) {
+  __shared__ float s_choice[kChooseWaves][kMaxE];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const long long t0 = (static_cast<long long>(blockIdx.x) * kChooseWaves + wave) * kChooseTokens;
+  float bias[kQ], next[kQ];
+  load_bias(a, lane, bias);
+  load_logits(a, t0, lane, next);
+#pragma unroll 1
+  for (int i = 0; i < kChooseTokens; ++i) {
+    const long long t = t0 + i;
+    if (t >= a.T) break;
+    float l[kQ];
+#pragma unroll
+    for (int q = 0; q < kQ; ++q) l[q] = clean_logit(next[q]);
+    if (i + 1 < kChooseTokens) load_logits(a, t + 1, lane, next);
+    int e;
+    float m, sum;
+    const bool sure = choose_fast(a, l, bias, lane, s_choice[wave], e, m, sum);
+    if (__ballot(!sure) != 0ull) e = -1;
+    if (lane < a.k) topk_idx[t * a.k + lane] = e;
+    if (softmax_sums != nullptr && lane == 0) softmax_sums[t] = make_float2(m, sum);
+  }
+}
+
+// 64 tokens per block of 16 waves: the choices that are not made yet, every gate (16 lanes per token, from
+// the chosen logits in 64 bits) and the block's part of the row metadata.  Each (token, slot) sets its
+// token's bit in its expert's 64-bit mask, so a row's rank among the block's rows of its expert is a
+// popcount of the lower bits.  SINGLE: one block has all tokens, makes the whole choice and finishes the
+// metadata; else it leaves the ranks in dest and its counts in hist [E][blocks].
 template <bool SINGLE>
 __global__ __launch_bounds__(kThreads) void route_scored_local(ScoredArgs a, int32_t* __restrict__ topk_idx,
                                                                float* __restrict__ topk_gate,
-                                                               float* __restrict__ scores, int32_t* __restrict__ hist,
-                                                               MetaOut out) {
+                                                               float* __restrict__ scores,
+                                                               const float2* __restrict__ softmax_sums,
+                                                               int32_t* __restrict__ hist, MetaOut out) {
   __shared__ unsigned long long s_mask[kMaxE];
   __shared__ int s_e[kRouteBlock][kMaxK];
   __shared__ float s_max[kRouteBlock], s_sum[kRouteBlock];
@@ -378,93 +449,96 @@ __global__ __launch_bounds__(kThreads) void route_scored_local(ScoredArgs a, int
   __shared__ int s_off[kMaxE];
   __shared__ int s_part[4][2];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tl = tid >> 4, j = tid & 15;
   const long long t0 = static_cast<long long>(blockIdx.x) * kRouteBlock;
+  const long long t = t0 + tl;
+  const bool live = t < a.T && j < a.k;
   if (tid < kMaxE) s_mask[tid] = 0ull;
-  __syncthreads();
-  // a wave's rows are all loaded first
-  float l[kWaveTokens][kQ];
-  float bias[kQ];
+  if constexpr (SINGLE) {
+    // the tokens dealt over the waves, so that a few tokens are a wave each
+    float bias[kQ];
+    load_bias(a, lane, bias);
+#pragma unroll 1
+    for (int i = wave; i < a.T; i += kWaves) {
+      float l[kQ];
+      load_logits(a, i, lane, l);
 #pragma unroll
-  for (int q = 0; q < kQ; ++q)
-    bias[q] = a.bias != nullptr && kQ * lane + q < a.E ? a.bias[kQ * lane + q] : 0.f;
+      for (int q = 0; q < kQ; ++q) l[q] = clean_logit(l[q]);
+      int e;
+      float m, sum;
+      const bool sure = choose_fast(a, l, bias, lane, reinterpret_cast<float*>(s_choice[wave]), e, m, sum);
+      if (__ballot(!sure) != 0ull || scores != nullptr)
+        e = choose_exact(a, l, lane, s_choice[wave], scores != nullptr ? scores + static_cast<long long>(i) * a.E : nullptr);
+      if (lane < a.k) s_e[i][lane] = e;
+      if (lane == 0) { s_max[i] = m; s_sum[i] = sum; }
+    }
+  } else {
+    if (live) s_e[tl][j] = topk_idx[t * a.k + j];
+    if (softmax_sums != nullptr && j == 0 && t < a.T) {
+      const float2 v = softmax_sums[t];
+      s_max[tl] = v.x;
+      s_sum[tl] = v.y;
+    }
+    wave_lds_sync();                             // a wave reads back its own four tokens
+#pragma unroll 1
+    for (int i = 0; i < kWaveTokens; ++i) {
+      const int it = wave * kWaveTokens + i;
+      if (t0 + it >= a.T) break;
+      if (scores == nullptr && s_e[it][0] >= 0) continue;
+      float l[kQ];
+      load_logits(a, t0 + it, lane, l);
 #pragma unroll
-  for (int i = 0; i < kWaveTokens; ++i) {
-    const long long t = t0 + wave * kWaveTokens + i;
-    const bool live = t < a.T;
-    if ((a.E & 3) == 0) {
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      const bool in = live && kQ * lane < a.E;
-      if (in) v = *reinterpret_cast<const float4*>(a.logits + t * a.E + kQ * lane);
-      l[i][0] = in ? v.x : -INFINITY; l[i][1] = in ? v.y : -INFINITY;
-      l[i][2] = in ? v.z : -INFINITY; l[i][3] = in ? v.w : -INFINITY;
-    } else {
-#pragma unroll
-      for (int q = 0; q < kQ; ++q)
-        l[i][q] = live && kQ * lane + q < a.E ? a.logits[t * a.E + kQ * lane + q] : -INFINITY;
+      for (int q = 0; q < kQ; ++q) l[q] = clean_logit(l[q]);
+      const int e = choose_exact(a, l, lane, s_choice[wave], scores != nullptr ? scores + (t0 + it) * a.E : nullptr);
+      if (lane < a.k) s_e[it][lane] = e;
     }
   }
-#pragma unroll
-  for (int i = 0; i < kWaveTokens; ++i) {
-    const int tl = wave * kWaveTokens + i;
-    const long long t = t0 + tl;
-    if (t >= a.T) break;
-#pragma unroll
-    for (int q = 0; q < kQ; ++q) l[i][q] = clean_logit(l[i][q]);
-    int e;
-    float m, sum;
-    const bool sure = choose_fast(a, l[i], bias, lane, reinterpret_cast<float*>(s_choice[wave]), e, m, sum);
-    if (__ballot(!sure) != 0ull || scores != nullptr)
-      e = choose_exact(a, l[i], lane, s_choice[wave], scores != nullptr ? scores + t * a.E : nullptr);
-    if (lane < a.k) {
-      s_e[tl][lane] = e;
-      atomicOr(&s_mask[e], 1ull << tl);
-    }
-    if (lane == 0) { s_max[tl] = m; s_sum[tl] = sum; }
-  }
   __syncthreads();
-  // ---- gates: 16 lanes per token, from the chosen logits in 64 bits
+  const int e = live ? s_e[tl][j] : 0;
+  if (live) atomicOr(&s_mask[e], 1ull << tl);
   {
-    const int tl = tid >> 4, j = tid & 15;
-    const long long t = t0 + tl;
-    const bool live = t < a.T && j < a.k;
-    const int e = live ? s_e[tl][j] : 0;
-    double p = 0.0;
-    if (live) {
-      const double lj = static_cast<double>(clean_logit(a.logits[t * a.E + e]));
-      p = a.score == MOE_SCORE_SIGMOID ? 1.0 / (1.0 + exp(-lj)) : exp(lj - static_cast<double>(s_max[tl]));
+    float lj = live ? clean_logit(a.logits[t * a.E + e]) : -INFINITY;
+    double p = 0.0, gate;
+    if (a.score == MOE_SCORE_SIGMOID) {
+      p = 1.0 / (1.0 + exp(-static_cast<double>(lj)));
+    } else {
+      // renormalised, the row's maximum cancels and the chosen logits' own serves
+      float m = group_max16(lj);
+      if (!a.renormalize) m = t < a.T ? s_max[tl] : 0.f;
+      p = lj == -INFINITY ? 0.0 : exp(static_cast<double>(lj) - static_cast<double>(m));
     }
-    double gate = p;
     if (a.renormalize) {
       double sum = p;
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
       gate = sum > 0.0 ? p / sum : 0.0;
-    } else if (a.score == MOE_SCORE_SOFTMAX && live) {
-      gate = s_sum[tl] > 0.f ? p / static_cast<double>(s_sum[tl]) : 0.0;
+    } else {
+      gate = a.score == MOE_SCORE_SIGMOID ? p : (live && s_sum[tl] > 0.f ? p / static_cast<double>(s_sum[tl]) : 0.0);
     }
     if (live) {
       topk_idx[t * a.k + j] = e;
       topk_gate[t * a.k + j] = static_cast<float>(gate * static_cast<double>(a.scale));
     }
+  }
+  __syncthreads();
+  if constexpr (SINGLE) {
+    const int count = tid < a.E ? __popcll(s_mask[tid]) : 0;
+    if (tid < a.E) out.counts[tid] = count;
+    expert_offsets(count, a.E, out, true, s_off, s_part);
+  }
+  if (live) {
+    const int rank = __popcll(s_mask[e] & ((1ull << tl) - 1ull));
     if constexpr (SINGLE) {
-      const int count = tid < a.E ? __popcll(s_mask[tid]) : 0;
-      if (tid < a.E) out.counts[tid] = count;
-      expert_offsets(count, a.E, out, true, s_off, s_part);
-    }
-    if (live) {
-      const int rank = __popcll(s_mask[e] & ((1ull << tl) - 1ull));
-      if constexpr (SINGLE) {
-        const int r = s_off[e] + rank;
-        out.dest[t * a.k + j] = r;
-        if (out.row_token != nullptr) out.row_token[r] = static_cast<int32_t>(t);
-      } else {
-        out.dest[t * a.k + j] = rank;
-      }
+      const int r = s_off[e] + rank;
+      out.dest[t * a.k + j] = r;
+      if (out.row_token != nullptr) out.row_token[r] = static_cast<int32_t>(t);
+    } else {
+      out.dest[t * a.k + j] = rank;
     }
   }
   if constexpr (!SINGLE)
-    for (int e = tid; e < a.E; e += kThreads)
-      hist[static_cast<long long>(e) * gridDim.x + blockIdx.x] = __popcll(s_mask[e]);
+    for (int i = tid; i < a.E; i += kThreads)
+      hist[static_cast<long long>(i) * gridDim.x + blockIdx.x] = __popcll(s_mask[i]);
 }
 
 // One wave per expert: its block counts become exclusive prefixes, their sum counts[e].
@@ -539,17 +613,6 @@ __global__ __launch_bounds__(kFinalThreads) void route_scored_finalize(const int
 // Bound by its bytes (the gradient written, and the logits read by the plain softmax).  A wave takes four
 // tokens, 16 lanes each, and forms their rows in LDS, so rows come and go as whole 16-byte runs.
 constexpr int kBwdTokens = 4, kBwdWaves = 4;
-
-__device__ __forceinline__ float group_sum16(float v) {
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
-  return v;
-}
-__device__ __forceinline__ float group_max16(float v) {
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
-  return v;
-}
 
 template <bool DENSE>
 __global__ __launch_bounds__(64 * kBwdWaves) void route_scored_bwd_kernel(const float* __restrict__ logits,
@@ -645,6 +708,11 @@ __global__ __launch_bounds__(64 * kBwdWaves) void route_scored_bwd_kernel(const 
   }
 }
 
+// Bytes of the block counts, and with the softmax's maximum and sum of every token behind them.
+size_t hist_bytes(int T, int E) {
+  return (static_cast<size_t>(T) + kRouteBlock - 1) / kRouteBlock * E * sizeof(int32_t) / 16 * 16 + 16;
+}
+
 int check_scored(int T, int E, int k, int score, float scale) {
   if (int st = check_layer_shape(T, E, k)) return st;
   MOE_REQUIRE(score == MOE_SCORE_SIGMOID || score == MOE_SCORE_SOFTMAX, MOE_ERR_INVALID_ARG,
@@ -657,6 +725,12 @@ int check_scored(int T, int E, int k, int score, float scale) {
 }  // namespace moe
 
 using namespace moe;
+
+extern "C" size_t moe_route_scored_workspace_bytes(int T, int E, int k) {
+  (void)k;
+  if (T <= kRouteBlock || E < 1) return 0;
+  return hist_bytes(T, E) + static_cast<size_t>(T) * sizeof(float2);
+}
 
 extern "C" int moe_route_scored(const float* logits, const float* bias, int T, int E, int k, int score, int n_group,
                                 int topk_group, int group_top, int renormalize, float scale, int32_t* topk_idx,
@@ -678,20 +752,27 @@ extern "C" int moe_route_scored(const float* logits, const float* bias, int T, i
   if (scores) MOE_CHECK_ALIGN(scores);
   if (offsets_pad) { MOE_CHECK_ALIGN(offsets_pad); MOE_REQUIRE(pad >= 1, MOE_ERR_INVALID_ARG, "pad must be >= 1"); }
   if (row_token) MOE_CHECK_ALIGN(row_token);
-  const size_t need = moe_route_workspace_bytes(T, E, k);
-  MOE_REQUIRE(ws != nullptr && ws_bytes >= need, MOE_ERR_WORKSPACE, "route workspace: need %zu bytes", need);
+  const size_t need = moe_route_scored_workspace_bytes(T, E, k);
+  MOE_REQUIRE(need == 0 || (ws != nullptr && ws_bytes >= need), MOE_ERR_WORKSPACE, "route workspace: need %zu bytes", need);
   MOE_CHECK_ALIGN(ws);
   const ScoredArgs a{logits, bias, T, E, k, score, n_group, topk_group, group_top, renormalize, scale};
   const MetaOut out{counts, offsets, offsets_pad, pad, dest, row_token};
   int32_t* hist = static_cast<int32_t*>(ws);
   hipStream_t s = as_stream(stream);
   if (T <= kRouteBlock) {
-    route_scored_local<true><<<1, kThreads, 0, s>>>(a, topk_idx, topk_gate, scores, hist, out);
+    route_scored_local<true><<<1, kThreads, 0, s>>>(a, topk_idx, topk_gate, scores, nullptr, hist, out);
     return check_launch("route_scored_local");
   }
   const int nb = (T + kRouteBlock - 1) / kRouteBlock;
   const long long n = static_cast<long long>(T) * k;
-  route_scored_local<false><<<nb, kThreads, 0, s>>>(a, topk_idx, topk_gate, scores, hist, out);
+  float2* sums = score == MOE_SCORE_SOFTMAX && !renormalize
+                     ? reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + hist_bytes(T, E))
+                     : nullptr;
+  constexpr int chosen = kChooseWaves * kChooseTokens;
+  route_scored_choose<<<static_cast<unsigned>((static_cast<long long>(T) + chosen - 1) / chosen), 64 * kChooseWaves, 0,
+                        s>>>(a, topk_idx, sums);
+  if (int st = check_launch("route_scored_choose")) return st;
+  route_scored_local<false><<<nb, kThreads, 0, s>>>(a, topk_idx, topk_gate, scores, sums, hist, out);
   if (int st = check_launch("route_scored_local")) return st;
   route_scored_scan<<<(E + 3) / 4, 256, 0, s>>>(hist, nb, E, counts);
   if (int st = check_launch("route_scored_scan")) return st;

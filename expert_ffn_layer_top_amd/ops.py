@@ -64,10 +64,48 @@ def _empty(shape, dtype, like):
     return torch.empty(shape, dtype=dtype, device=like.device)
 
 
-def _call_on(like, name, *args):
-    """Calls `name` with `like`'s device current, on that device's current stream (the last argument)."""
-    with torch.cuda.device(like.device):
-        call(name, *args, _stream(like))
+# The calls below are used for single tokens too, where the host's own time counts: a call of four
+# tensors spent 11 us on the host with a device context, a stream object and one check function per
+# argument, and 6 us with the forms here (the kernel launch itself takes 2.5).
+
+def _is(t, dtype, shape, name):
+    """_check for a fully known shape, with one comparison where all is well."""
+    if not (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.is_contiguous()):
+        _check(t, dtype, name, shape)
+
+
+def _device_of(*ts):
+    """The index of the GPU that every tensor (or None) is on."""
+    d = ts[0].get_device()
+    for t in ts:
+        if t is not None and t.get_device() != d:
+            d = -1
+    if d < 0:
+        _on_gpu(*ts)
+    return d
+
+
+def _new(shape, dtype, device):
+    """An uninitialised contiguous tensor of one or two or three dims on GPU `device`."""
+    if len(shape) == 2:
+        stride = (shape[1], 1)
+    elif len(shape) == 3:
+        stride = (shape[1] * shape[2], shape[2], 1)
+    else:
+        stride = (1,)
+    return torch.empty_strided(shape, stride, dtype=dtype, device=_devices[device])
+
+
+_devices = [torch.device("cuda", i) for i in range(64)]
+
+
+def _call_on(device, name, *args):
+    """Calls `name` with GPU `device` current, on that device's current stream (the last argument)."""
+    if torch.cuda.current_device() == device:
+        call(name, *args, torch._C._cuda_getCurrentRawStream(device))
+    else:
+        with torch.cuda.device(device):
+            call(name, *args, torch._C._cuda_getCurrentRawStream(device))
 
 
 def _mx_pad_cap(n, E):
@@ -177,7 +215,8 @@ _SCORES = {"sigmoid": 0, "softmax": 1}
 
 
 def _score(score):
-    _need(score in _SCORES, f"score must be one of {sorted(_SCORES)}, got {score!r}")
+    if score not in _SCORES:
+        raise ValueError(f"score must be one of {sorted(_SCORES)}, got {score!r}")
     return _SCORES[score]
 
 
@@ -193,29 +232,35 @@ def route_scored(logits, k, score="sigmoid", bias=None, n_group=1, topk_group=1,
     _check(logits, torch.float32, "logits", ndim=2)
     T, E = logits.shape
     score = _score(score)
-    _need(T >= 1 and 1 <= E <= 256, f"logits: need T >= 1 and 1 <= E <= 256, got {list(logits.shape)}")
-    _need(pad is None or pad >= 1, "pad must be >= 1")
-    _need(n_group >= 1 and E % n_group == 0, f"n_group = {n_group} must divide E = {E}")
-    _need(1 <= topk_group <= n_group, f"topk_group = {topk_group} must be in [1, n_group = {n_group}]")
-    _need(group_top in (1, 2), "group_top must be 1 or 2")
-    _need(1 <= k <= min(16, topk_group * (E // n_group)),
-          f"k = {k} must be in [1, 16] and at most the {topk_group * (E // n_group)} experts of the kept groups")
+    if not (T >= 1 and 1 <= E <= 256):
+        raise ValueError(f"logits: need T >= 1 and 1 <= E <= 256, got {list(logits.shape)}")
+    if not (pad is None or pad >= 1):
+        raise ValueError("pad must be >= 1")
+    if not (n_group >= 1 and E % n_group == 0):
+        raise ValueError(f"n_group = {n_group} must divide E = {E}")
+    if not 1 <= topk_group <= n_group:
+        raise ValueError(f"topk_group = {topk_group} must be in [1, n_group = {n_group}]")
+    if group_top not in (1, 2):
+        raise ValueError("group_top must be 1 or 2")
+    if not 1 <= k <= min(16, topk_group * (E // n_group)):
+        raise ValueError(f"k = {k} must be in [1, 16] and at most the {topk_group * (E // n_group)} experts of the "
+                         f"kept groups")
     if bias is not None:
-        _check(bias, torch.float32, "bias", (E,))
-    _on_gpu(logits, bias)
+        _is(bias, torch.float32, (E,), "bias")
+    dev = _device_of(logits, bias)
     out = dict(
-        topk_idx=_empty((T, k), torch.int32, logits),
-        topk_gate=_empty((T, k), torch.float32, logits),
-        scores=_empty((T, E), torch.float32, logits) if want_scores else None,
-        counts=_empty((E,), torch.int32, logits),
-        offsets=_empty((E + 1,), torch.int32, logits),
-        offsets_pad=_empty((E + 1,), torch.int32, logits) if pad else None,
-        dest=_empty((T, k), torch.int32, logits),
-        row_token=_empty((T * k,), torch.int32, logits) if want_row_token else None,
+        topk_idx=_new((T, k), torch.int32, dev),
+        topk_gate=_new((T, k), torch.float32, dev),
+        scores=_new((T, E), torch.float32, dev) if want_scores else None,
+        counts=_new((E,), torch.int32, dev),
+        offsets=_new((E + 1,), torch.int32, dev),
+        offsets_pad=_new((E + 1,), torch.int32, dev) if pad else None,
+        dest=_new((T, k), torch.int32, dev),
+        row_token=_new((T * k,), torch.int32, dev) if want_row_token else None,
     )
-    nbytes = lib.moe_route_workspace_bytes(T, E, k)
-    ws = _empty((max(nbytes, 1),), torch.uint8, logits)
-    _call_on(logits, "moe_route_scored", _ptr(logits), _ptr(bias), T, E, k, score, n_group, topk_group, group_top,
+    nbytes = lib.moe_route_scored_workspace_bytes(T, E, k)
+    ws = _new((nbytes,), torch.uint8, dev) if nbytes else None
+    _call_on(dev, "moe_route_scored", _ptr(logits), _ptr(bias), T, E, k, score, n_group, topk_group, group_top,
              int(bool(renormalize)), float(scale), _ptr(out["topk_idx"]), _ptr(out["topk_gate"]), _ptr(out["scores"]),
              _ptr(out["counts"]), _ptr(out["offsets"]), _ptr(out["offsets_pad"]), int(pad or 0), _ptr(out["dest"]),
              _ptr(out["row_token"]), _ptr(ws), nbytes)
@@ -229,10 +274,10 @@ def route_scored_bwd(logits, topk_idx, d_gate, score="sigmoid", renormalize=True
     score = _score(score)
     _check(topk_idx, torch.int32, "topk_idx", (T, None))
     k = topk_idx.shape[1]
-    _check(d_gate, torch.float32, "d_gate", (T, k))
-    _on_gpu(logits, topk_idx, d_gate)
-    dl = _empty((T, E), torch.float32, logits)
-    _call_on(logits, "moe_route_scored_bwd", _ptr(logits), _ptr(topk_idx), _ptr(d_gate), T, E, k, score,
+    _is(d_gate, torch.float32, (T, k), "d_gate")
+    dev = _device_of(logits, topk_idx, d_gate)
+    dl = _new((T, E), torch.float32, dev)
+    _call_on(dev, "moe_route_scored_bwd", _ptr(logits), _ptr(topk_idx), _ptr(d_gate), T, E, k, score,
              int(bool(renormalize)), float(scale), _ptr(dl))
     return dl
 
@@ -782,16 +827,18 @@ def fp8b_quantize_rows(x, dest=None):
     order or, with dest [T, k], each row written to its k rows of the expert buffers (n = T k)."""
     _check(x, torch.bfloat16, "x", ndim=2)
     T, C = x.shape
-    _need(T >= 1 and C >= 64 and C % 64 == 0, f"x: need T >= 1 and C a multiple of 64, got {list(x.shape)}")
+    if T < 1 or C < 64 or C % 64:
+        raise ValueError(f"x: need T >= 1 and C a multiple of 64, got {list(x.shape)}")
     k = 1
     if dest is not None:
         _check(dest, torch.int32, "dest", (T, None))
         k = dest.shape[1]
-        _need(1 <= k <= 16, f"dest: k = {k} must be in [1, 16]")
-    _on_gpu(x, dest)
-    q = _empty((T * k, C), torch.uint8, x)
-    s = _empty((_blocks(C), T * k), torch.float32, x)
-    _call_on(x, "moe_fp8b_quantize_rows", _ptr(x), _ptr(dest), T, C, k, _ptr(q), _ptr(s))
+        if not 1 <= k <= 16:
+            raise ValueError(f"dest: k = {k} must be in [1, 16]")
+    dev = _device_of(x, dest)
+    q = _new((T * k, C), torch.uint8, dev)
+    s = _new((_blocks(C), T * k), torch.float32, dev)
+    _call_on(dev, "moe_fp8b_quantize_rows", _ptr(x), _ptr(dest), T, C, k, _ptr(q), _ptr(s))
     return q, s
 
 
@@ -811,14 +858,15 @@ def fp8b_quantize_rows_grouped(x, offsets, offsets_pad, row_token=None, row_gate
         n = row_token.shape[0]
     if row_gate is not None:
         _check(row_gate, torch.float32, "row_gate", (n,))
-    _need(n >= 1 and C >= 64 and C % 64 == 0, f"need n >= 1 and C a multiple of 64, got n = {n}, C = {C}")
-    _on_gpu(x, offsets, offsets_pad, row_token, row_gate)
+    if n < 1 or C < 64 or C % 64:
+        raise ValueError(f"need n >= 1 and C a multiple of 64, got n = {n}, C = {C}")
+    dev = _device_of(x, offsets, offsets_pad, row_token, row_gate)
     P = _mx_pad_cap(n, E)
-    q = _empty((n, C), torch.uint8, x) if want_rows else None
-    s = _empty((_blocks(C), n), torch.float32, x) if want_rows else None
-    qT = _empty((C, P), torch.uint8, x)
-    sT = _empty((P // 128, C), torch.float32, x)
-    _call_on(x, "moe_fp8b_quantize_rows_grouped", _ptr(x), _ptr(row_token), _ptr(row_gate), _ptr(offsets),
+    q = _new((n, C), torch.uint8, dev) if want_rows else None
+    s = _new((_blocks(C), n), torch.float32, dev) if want_rows else None
+    qT = _new((C, P), torch.uint8, dev)
+    sT = _new((P // 128, C), torch.float32, dev)
+    _call_on(dev, "moe_fp8b_quantize_rows_grouped", _ptr(x), _ptr(row_token), _ptr(row_gate), _ptr(offsets),
              _ptr(offsets_pad), E, n, C, _ptr(q), _ptr(s), _ptr(qT), _ptr(sT))
     return q, s, qT, sT
 
@@ -831,35 +879,44 @@ def fp8b_quantize_weights(w, want_transposed=True):
     E, R, C = _rc(w)
     _need(E >= 1 and R >= 64 and C >= 64 and R % 64 == 0 and C % 64 == 0,
           f"w: rows and columns must be multiples of 64, got {list(w.shape)}")
-    _on_gpu(w)
+    dev = _device_of(w)
     lead = tuple(w.shape[:-2])
-    q = _empty((*lead, R, C), torch.uint8, w)
-    s = _empty((*lead, _blocks(R), _blocks(C)), torch.float32, w)
-    qT = _empty((*lead, C, R), torch.uint8, w) if want_transposed else None
-    sT = _empty((*lead, _blocks(C), _blocks(R)), torch.float32, w) if want_transposed else None
-    _call_on(w, "moe_fp8b_quantize_weights", _ptr(w), E, R, C, _ptr(q), _ptr(s), _ptr(qT), _ptr(sT))
+    q = _new((*lead, R, C), torch.uint8, dev)
+    s = _new((*lead, _blocks(R), _blocks(C)), torch.float32, dev)
+    qT = _new((*lead, C, R), torch.uint8, dev) if want_transposed else None
+    sT = _new((*lead, _blocks(C), _blocks(R)), torch.float32, dev) if want_transposed else None
+    _call_on(dev, "moe_fp8b_quantize_weights", _ptr(w), E, R, C, _ptr(q), _ptr(s), _ptr(qT), _ptr(sT))
     return q, s, qT, sT
 
 
-def _fp8b_rows(q, s, name, n=None, C=None):
-    _check(q, torch.uint8, name, (n, C))
-    n, C = q.shape
-    _check(s, torch.float32, name + "_s", (_blocks(C), n))
-    return n, C
+def _fp8b_rows(q, s, name, n, C):
+    """Row codes [n, C] (n None: any) and their scales; returns n."""
+    if n is None:
+        _check(q, torch.uint8, name, (None, C))
+        n = q.shape[0]
+    else:
+        _is(q, torch.uint8, (n, C), name)
+    _is(s, torch.float32, (-(-C // 128), n), name + "_s")
+    return n
 
 
-def _fp8b_weight(q, s, name, shape=(None, None, None)):
-    _check(q, torch.uint8, name, shape)
-    E, R, C = q.shape
-    _check(s, torch.float32, name + "_s", (E, _blocks(R), _blocks(C)))
+def _fp8b_weight(q, s, name, shape=None):
+    if shape is None:
+        _check(q, torch.uint8, name, ndim=3)
+        shape = q.shape
+    else:
+        _is(q, torch.uint8, shape, name)
+    E, R, C = shape
+    _is(s, torch.float32, (E, -(-R // 128), -(-C // 128)), name + "_s")
     return E, R, C
 
 
 def _fp8b_sizes(offsets, E, n, d, f):
-    _check(offsets, torch.int32, "offsets", (E + 1,))
-    _need(1 <= E <= 256 and n >= 1, f"need 1 <= E <= 256 and n >= 1, got E = {E}, n = {n}")
-    _need(d >= 64 and d % 64 == 0 and f >= 64 and f % 64 == 0,
-          f"d = {d} and f = {f} must be positive multiples of 64")
+    _is(offsets, torch.int32, (E + 1,), "offsets")
+    if not (1 <= E <= 256 and n >= 1):
+        raise ValueError(f"need 1 <= E <= 256 and n >= 1, got E = {E}, n = {n}")
+    if d < 64 or f < 64 or d % 64 or f % 64:
+        raise ValueError(f"d = {d} and f = {f} must be positive multiples of 64")
 
 
 def grouped_gemm_gate_up_fp8b(xq, xq_s, offsets, w_gate, w_gate_s, w_up, w_up_s, want_gu=True):
@@ -868,13 +925,13 @@ def grouped_gemm_gate_up_fp8b(xq, xq_s, offsets, w_gate, w_gate_s, w_up, w_up_s,
     g and u are None without want_gu (a serving pass)."""
     E, f, d = _fp8b_weight(w_gate, w_gate_s, "w_gate")
     _fp8b_weight(w_up, w_up_s, "w_up", (E, f, d))
-    n, _ = _fp8b_rows(xq, xq_s, "xq", C=d)
+    n = _fp8b_rows(xq, xq_s, "xq", None, d)
     _fp8b_sizes(offsets, E, n, d, f)
-    _on_gpu(xq, xq_s, offsets, w_gate, w_gate_s, w_up, w_up_s)
-    g = _empty((n, f), torch.bfloat16, xq) if want_gu else None
-    u = _empty((n, f), torch.bfloat16, xq) if want_gu else None
-    a = _empty((n, f), torch.bfloat16, xq)
-    _call_on(xq, "moe_grouped_gemm_gate_up_fp8b", E, n, d, f, _ptr(offsets), _ptr(xq), _ptr(xq_s), _ptr(w_gate),
+    dev = _device_of(xq, xq_s, offsets, w_gate, w_gate_s, w_up, w_up_s)
+    g = _new((n, f), torch.bfloat16, dev) if want_gu else None
+    u = _new((n, f), torch.bfloat16, dev) if want_gu else None
+    a = _new((n, f), torch.bfloat16, dev)
+    _call_on(dev, "moe_grouped_gemm_gate_up_fp8b", E, n, d, f, _ptr(offsets), _ptr(xq), _ptr(xq_s), _ptr(w_gate),
              _ptr(w_gate_s), _ptr(w_up), _ptr(w_up_s), _ptr(g), _ptr(u), _ptr(a))
     return g, u, a
 
@@ -882,11 +939,11 @@ def grouped_gemm_gate_up_fp8b(xq, xq_s, offsets, w_gate, w_gate_s, w_up, w_up_s,
 def grouped_gemm_down_fp8b(aq, aq_s, offsets, w_down, w_down_s):
     """yexp [n,d] bf16 = a W_down[e]^T per expert: aq, aq_s from fp8b_quantize_rows(a), w_down [E,d,f]."""
     E, d, f = _fp8b_weight(w_down, w_down_s, "w_down")
-    n, _ = _fp8b_rows(aq, aq_s, "aq", C=f)
+    n = _fp8b_rows(aq, aq_s, "aq", None, f)
     _fp8b_sizes(offsets, E, n, d, f)
-    _on_gpu(aq, aq_s, offsets, w_down, w_down_s)
-    yexp = _empty((n, d), torch.bfloat16, aq)
-    _call_on(aq, "moe_grouped_gemm_down_fp8b", E, n, d, f, _ptr(offsets), _ptr(aq), _ptr(aq_s), _ptr(w_down),
+    dev = _device_of(aq, aq_s, offsets, w_down, w_down_s)
+    yexp = _new((n, d), torch.bfloat16, dev)
+    _call_on(dev, "moe_grouped_gemm_down_fp8b", E, n, d, f, _ptr(offsets), _ptr(aq), _ptr(aq_s), _ptr(w_down),
              _ptr(w_down_s), _ptr(yexp))
     return yexp
 
@@ -895,14 +952,14 @@ def grouped_gemm_dgrad_down_fp8b(dyq, dyq_s, offsets, w_down_t, w_down_t_s, g, u
     """(dg, du) [n,f] bf16: da = dyexp W_down[e] through the SwiGLU backward of (g, u); w_down_t [E,f,d] and its
     scales are fp8b_quantize_weights' qT, sT."""
     E, f, d = _fp8b_weight(w_down_t, w_down_t_s, "w_down_t")
-    n, _ = _fp8b_rows(dyq, dyq_s, "dyq", C=d)
+    n = _fp8b_rows(dyq, dyq_s, "dyq", None, d)
     _check(g, torch.bfloat16, "g", (n, f))
     _check(u, torch.bfloat16, "u", (n, f))
     _fp8b_sizes(offsets, E, n, d, f)
-    _on_gpu(dyq, dyq_s, offsets, w_down_t, w_down_t_s, g, u)
-    dg = _empty((n, f), torch.bfloat16, g)
-    du = _empty((n, f), torch.bfloat16, g)
-    _call_on(g, "moe_grouped_gemm_dgrad_down_fp8b", E, n, d, f, _ptr(offsets), _ptr(dyq), _ptr(dyq_s), _ptr(w_down_t),
+    dev = _device_of(dyq, dyq_s, offsets, w_down_t, w_down_t_s, g, u)
+    dg = _new((n, f), torch.bfloat16, dev)
+    du = _new((n, f), torch.bfloat16, dev)
+    _call_on(dev, "moe_grouped_gemm_dgrad_down_fp8b", E, n, d, f, _ptr(offsets), _ptr(dyq), _ptr(dyq_s), _ptr(w_down_t),
              _ptr(w_down_t_s), _ptr(g), _ptr(u), _ptr(dg), _ptr(du))
     return dg, du
 
@@ -911,12 +968,12 @@ def grouped_gemm_dgrad_gate_up_fp8b(dgq, dgq_s, duq, duq_s, offsets, w_gate_t, w
     """dxp [n,d] bf16 = dg W_gate[e] + du W_up[e]; w_gate_t, w_up_t [E,d,f] are fp8b_quantize_weights' qT."""
     E, d, f = _fp8b_weight(w_gate_t, w_gate_t_s, "w_gate_t")
     _fp8b_weight(w_up_t, w_up_t_s, "w_up_t", (E, d, f))
-    n, _ = _fp8b_rows(dgq, dgq_s, "dgq", C=f)
+    n = _fp8b_rows(dgq, dgq_s, "dgq", None, f)
     _fp8b_rows(duq, duq_s, "duq", n, f)
     _fp8b_sizes(offsets, E, n, d, f)
-    _on_gpu(dgq, dgq_s, duq, duq_s, offsets, w_gate_t, w_gate_t_s, w_up_t, w_up_t_s)
-    dxp = _empty((n, d), torch.bfloat16, dgq)
-    _call_on(dgq, "moe_grouped_gemm_dgrad_gate_up_fp8b", E, n, d, f, _ptr(offsets), _ptr(dgq), _ptr(dgq_s), _ptr(duq),
+    dev = _device_of(dgq, dgq_s, duq, duq_s, offsets, w_gate_t, w_gate_t_s, w_up_t, w_up_t_s)
+    dxp = _new((n, d), torch.bfloat16, dev)
+    _call_on(dev, "moe_grouped_gemm_dgrad_gate_up_fp8b", E, n, d, f, _ptr(offsets), _ptr(dgq), _ptr(dgq_s), _ptr(duq),
              _ptr(duq_s), _ptr(w_gate_t), _ptr(w_gate_t_s), _ptr(w_up_t), _ptr(w_up_t_s), _ptr(dxp))
     return dxp
 
@@ -941,9 +998,9 @@ def grouped_gemm_wgrad_down_fp8b(dyT, dyT_s, aT, aT_s, offsets, offsets_pad, n):
     d = _fp8b_tokens(dyT, dyT_s, "dyT", P)
     f = _fp8b_tokens(aT, aT_s, "aT", P)
     _fp8b_sizes(offsets, E, n, d, f)
-    _on_gpu(dyT, dyT_s, aT, aT_s, offsets, offsets_pad)
-    dw = _empty((E, d, f), torch.bfloat16, dyT)
-    _call_on(dyT, "moe_grouped_gemm_wgrad_down_fp8b", E, n, d, f, _ptr(offsets), _ptr(offsets_pad), _ptr(dyT),
+    dev = _device_of(dyT, dyT_s, aT, aT_s, offsets, offsets_pad)
+    dw = _new((E, d, f), torch.bfloat16, dev)
+    _call_on(dev, "moe_grouped_gemm_wgrad_down_fp8b", E, n, d, f, _ptr(offsets), _ptr(offsets_pad), _ptr(dyT),
              _ptr(dyT_s), _ptr(aT), _ptr(aT_s), _ptr(dw))
     return dw
 
@@ -955,9 +1012,9 @@ def grouped_gemm_wgrad_gate_up_fp8b(dgT, dgT_s, duT, duT_s, xT, xT_s, offsets, o
     _fp8b_tokens(duT, duT_s, "duT", P, f)
     d = _fp8b_tokens(xT, xT_s, "xT", P)
     _fp8b_sizes(offsets, E, n, d, f)
-    _on_gpu(dgT, dgT_s, duT, duT_s, xT, xT_s, offsets, offsets_pad)
-    dwg = _empty((E, f, d), torch.bfloat16, dgT)
-    dwu = _empty((E, f, d), torch.bfloat16, dgT)
-    _call_on(dgT, "moe_grouped_gemm_wgrad_gate_up_fp8b", E, n, d, f, _ptr(offsets), _ptr(offsets_pad), _ptr(dgT),
+    dev = _device_of(dgT, dgT_s, duT, duT_s, xT, xT_s, offsets, offsets_pad)
+    dwg = _new((E, f, d), torch.bfloat16, dev)
+    dwu = _new((E, f, d), torch.bfloat16, dev)
+    _call_on(dev, "moe_grouped_gemm_wgrad_gate_up_fp8b", E, n, d, f, _ptr(offsets), _ptr(offsets_pad), _ptr(dgT),
              _ptr(dgT_s), _ptr(duT), _ptr(duT_s), _ptr(xT), _ptr(xT_s), _ptr(dwg), _ptr(dwu))
     return dwg, dwu

@@ -192,14 +192,15 @@ int moe_route_topk_bwd_balance(const float* topk_gate, const int32_t* topk_idx, 
  *   topk_idx: the k experts of largest c in the kept groups (of largest logit without a bias),
  *   descending; ties go to the lower index, for groups and for experts;
  *   topk_gate = scale * s, divided by the sum of the k chosen s where `renormalize` is nonzero (all 0
- *   where that sum is 0).
+ *   where every chosen expert is absent, or every sigmoid below the smallest double).
  * Scores and choice are computed in 64 bits, so the chosen experts do not depend on how fp32 rounds an
  * exponential.  A logit of -inf or NaN marks an absent expert (score 0, never counted in a group's
  * value, chosen only after every present expert of the kept groups); a bias of -inf excludes an expert
  * in the same way, and NaN biases count as -inf; a logit of +inf counts as the largest finite float.
  *   in   logits [T,E] fp32;  out  as moe_route_topk; scores_or_null [T,E] fp32: every s.
  * Needs n_group dividing E, 1 <= topk_group <= n_group, k <= topk_group * E / n_group, finite scale;
- * workspace moe_route_workspace_bytes(T, E, k). */
+ * workspace moe_route_scored_workspace_bytes(T, E, k): none (NULL) up to 64 tokens. */
+size_t moe_route_scored_workspace_bytes(int T, int E, int k);
 int moe_route_scored(const float* logits, const float* bias_or_null, int T, int E, int k, int score,
                      int n_group, int topk_group, int group_top, int renormalize, float scale,
                      int32_t* topk_idx, float* topk_gate, float* scores_or_null, int32_t* counts,

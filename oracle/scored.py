@@ -44,7 +44,9 @@ def route(logits, k, score="sigmoid", bias=None, n_group=1, topk_group=1, group_
         inside = [e for e in range(E) if e // per in kept]
         chosen = sorted(inside, key=lambda e: (-rank[e], e))[:k]
         w = s[chosen]
-        if renormalize:
+        if renormalize and score == "softmax":      # the sum over all experts cancels
+            w = scores(l[chosen], score)[1]
+        elif renormalize:
             w = w / w.sum() if w.sum() > 0 else np.zeros(k)
         idx[t], gate[t], all_scores[t] = chosen, w * scale, s
     return idx, gate, all_scores

@@ -121,7 +121,9 @@ def test_c_entry_points_refuse_before_any_launch():
     assert route(tg=0) == UNSUPPORTED and route(top=3) == UNSUPPORTED and route(k=9, tg=1) == UNSUPPORTED
     assert route(score=2) == INVALID and route(logits=None) == INVALID and route(bias=odd) == INVALID
     assert route(scale=float("nan")) == INVALID and route(pad=0) == INVALID
-    assert route(ws=None) == WORKSPACE and route(nbytes=16) == WORKSPACE
+    size = L.moe_route_scored_workspace_bytes
+    assert size(64, 256, 8) == 0 and size(65, 256, 8) == 2 * 256 * 4 + 16 + 65 * 8 and size(1000, 3, 2) == 16 * 3 * 4 + 16 + 8000
+    assert route(T=65, ws=None) == WORKSPACE and route(T=65, nbytes=16) == WORKSPACE
     assert L.moe_route_scored_bwd(p, p, p, 4, 8, 2, 7, 1, 1.0, p, None) == INVALID
     assert L.moe_route_scored_bwd(p, None, p, 4, 8, 2, 0, 1, 1.0, p, None) == INVALID
     assert L.moe_route_scored_bwd(p, p, p, 4, 8, 9, 0, 1, 1.0, p, None) == UNSUPPORTED
