@@ -29,6 +29,10 @@
 // 64 + 16 (l / 16) .. + 15 of the step (any order serves, being the same for both operands); the product
 // takes columns from the first operand, so a lane ends with 4 consecutive columns of one row and
 // needs one row scale per 16 x 16 tile.
+#include <algorithm>
+#include <cmath>
+#include <cstdlib>
+#include <cstring>
 #include <type_traits>
 
 #include "common.h"
@@ -606,6 +610,388 @@ int launch(const Params& p0, hipStream_t s) {
   return check_launch("grouped_gemm_fp8b");
 }
 
+// ------------------------------------------------------------------ few rows per expert
+//
+// What the forms for few rows write per lane: 4 consecutive columns of one row (`second`: FWD1's up
+// accumulators, which with `v` make the activation).
+template <int MODE>
+__device__ __forceinline__ void store4(const Params& p, long long at, const f32x4& v, const f32x4& second) {
+  typedef gep::u32x2 u32x2;
+  if constexpr (MODE == FWD1) {
+    if (p.o0 != nullptr) {
+      *reinterpret_cast<u32x2*>(p.o0 + at) = gep::pack4(v);
+      *reinterpret_cast<u32x2*>(p.o1 + at) = gep::pack4(second);
+    }
+    f32x4 av;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) av[e] = v[e] * gep::sigmoid(v[e]) * second[e];
+    *reinterpret_cast<u32x2*>(p.o2 + at) = gep::pack4(av);
+  } else if constexpr (MODE == DGRAD1) {
+    const u32x2 g2 = *reinterpret_cast<const u32x2*>(p.g + at), u2 = *reinterpret_cast<const u32x2*>(p.u + at);
+    const float gv[4] = {bf16_lo(g2.x), bf16_hi(g2.x), bf16_lo(g2.y), bf16_hi(g2.y)};
+    const float uv[4] = {bf16_lo(u2.x), bf16_hi(u2.x), bf16_lo(u2.y), bf16_hi(u2.y)};
+    f32x4 dg, du;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float sg = gep::sigmoid(gv[e]);
+      dg[e] = v[e] * uv[e] * sg * (1.0f + gv[e] * (1.0f - sg));
+      du[e] = v[e] * gv[e] * sg;
+    }
+    *reinterpret_cast<u32x2*>(p.o0 + at) = gep::pack4(dg);
+    *reinterpret_cast<u32x2*>(p.o1 + at) = gep::pack4(du);
+  } else {
+    *reinterpret_cast<u32x2*>(p.o0 + at) = gep::pack4(v);
+  }
+}
+
+// The expert of row group mu (groups of R rows, an expert's last one partial; experts in order) and the
+// group's place in it; false past the last group.  Lane l of round r holds expert 64 r + l; prefix sums by
+// row shifts, as this stands between the launch and the first load of a weight.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp_add(int v) {
+  return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xf, false);
+}
+template <int R>
+__device__ __forceinline__ bool find_group(const int32_t* __restrict__ offsets, int E, int mu, int& e, int& r0, int& r1) {
+  const int lane = threadIdx.x & 63;
+  int carry = 0;
+  for (int base = 0; base < E; base += 64) {
+    const int ex = min(base + lane, E - 1);
+    const int lo = offsets[ex], hi = offsets[ex + 1];
+    const int groups = base + lane < E ? (hi - lo + R - 1) / R : 0;
+    int incl = groups;
+    incl = dpp_add<0x111, 0xf>(incl);
+    incl = dpp_add<0x112, 0xf>(incl);
+    incl = dpp_add<0x114, 0xf>(incl);
+    incl = dpp_add<0x118, 0xf>(incl);
+    incl = dpp_add<0x142, 0xa>(incl);
+    incl = dpp_add<0x143, 0xc>(incl);
+    const int before = carry + incl - groups;
+    const unsigned long long hit = __ballot(groups > 0 && before <= mu && mu < before + groups);
+    if (hit) {
+      const int src = __ffsll(static_cast<long long>(hit)) - 1;
+      e = base + src;
+      r0 = __builtin_amdgcn_readlane(lo, src) + (mu - __builtin_amdgcn_readlane(before, src)) * R;
+      r1 = __builtin_amdgcn_readlane(hi, src);
+      return true;
+    }
+    carry += __builtin_amdgcn_readlane(incl, 63);
+  }
+  return false;
+}
+
+// A few rows per expert on average (single tokens, small decoding batches): a product reads every weight
+// of the experts that have rows once and does next to nothing with it, so the kernel is a stream of weights.
+// Each wave takes up to 16 rows of one expert and 32 weight rows: 32 output columns, or in FWD1 the gate
+// and the up rows of 16.  It loads weight fragments straight into registers (no LDS: a weight is used by one
+// wave only), D K steps ahead and together with the rows' codes and scales (loads return in order, so what
+// is used together is loaded together).  The 4 waves of a workgroup split the contraction KS ways, summed in
+// wave order through LDS, where the columns alone make too few waves.
+constexpr int SKINNY_ROWS = 16;
+
+struct SkinnyStep {
+  i32x8 w[2];
+  i32x8 x;
+  float sx;
+};
+
+template <int MODE, int KS>
+__device__ __forceinline__ void grouped_skinny(const Params& p) {
+  constexpr int D = 4;
+  constexpr int WC = MODE == FWD1 ? 16 : 32;       // columns of a wave
+  constexpr int CBW = 4 / KS;                      // column blocks per workgroup
+  __shared__ float s_sum[4][8][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int ks = wave % KS;
+  const int N = n_total<MODE>(p.d, p.f), K = k_one<MODE>(p.d, p.f);
+  const int KB = static_cast<int>(fp8b_blocks(K)), NB = static_cast<int>(fp8b_blocks(N));
+  const int groups = (N / WC + CBW - 1) / CBW;
+  const int mu = blockIdx.x / groups;
+  const int cb = (blockIdx.x - mu * groups) * CBW + wave / KS;
+  int e, r0, r1;
+  if (!find_group<SKINNY_ROWS>(p.offsets, p.E, mu, e, r0, r1)) return;
+  const int rows = min(SKINNY_ROWS, r1 - r0);
+  const bool active = cb * WC < N;
+  const int n0 = active ? cb * WC : 0;
+  const int lr = lane & 15, lk = 16 * (lane >> 4);
+
+  const long long woff = (static_cast<long long>(e) * N + n0 + lr) * K + lk;
+  const uint8_t* const wp[2] = {p.b0 + woff, MODE == FWD1 ? p.b1 + woff : p.b0 + woff + 16LL * K};
+  const int row = r0 + min(lr, rows - 1);          // lanes past the rows repeat the last one
+  const uint8_t* const xp = p.a0 + static_cast<long long>(row) * K + lk;
+  const float* const sp = p.a0s + row;
+  auto load = [&](SkinnyStep& s, int kb) {
+    const long long at = static_cast<long long>(kb) * BK;
+    const bool tail = at + 64 >= K;                  // only the block's first half exists
+    auto frag = [&](const uint8_t* q) {
+      const i32x4 lo = *reinterpret_cast<const i32x4*>(q + at);
+      i32x4 hi = {0, 0, 0, 0};
+      if (!tail) hi = *reinterpret_cast<const i32x4*>(q + at + 64);
+      return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    };
+#pragma unroll
+    for (int w = 0; w < 2; ++w) s.w[w] = frag(wp[w]);
+    s.x = frag(xp);
+    s.sx = sp[static_cast<long long>(kb) * p.n];
+  };
+  f32x4 acc[2] = {};
+  const long long sw_row = (static_cast<long long>(e) * NB + n0 / kFp8bBlock) * KB;
+  if (active) {
+    for (int base = 0; base < KB; base += 64) {      // lane l holds the weight scale of block base + l
+      const int at = min(base + lane, KB - 1);
+      const float ws0 = p.b0s[sw_row + at], ws1 = MODE == FWD1 ? p.b1s[sw_row + at] : ws0;
+      const int end = min(KB, base + 64);
+      SkinnyStep s[D];
+      int kb = base + ks;
+#pragma unroll
+      for (int i = 0; i < D; ++i)
+        if (kb + i * KS < end) load(s[i], kb + i * KS);
+      while (kb < end) {
+#pragma unroll
+        for (int i = 0; i < D; ++i) {
+          if (kb < end) {
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              const float sw = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(w ? ws1 : ws0), kb - base));
+              const f32x4 t = mfma_block(s[i].w[w], s[i].x);
+              const float c = sw * s[i].sx;
+#pragma unroll
+              for (int q = 0; q < 4; ++q) acc[w][q] = fmaf(t[q], c, acc[w][q]);
+            }
+            if (kb + D * KS < end) load(s[i], kb + D * KS);
+            kb += KS;
+          }
+        }
+      }
+    }
+  }
+  if constexpr (KS > 1) {
+#pragma unroll
+    for (int w = 0; w < 2; ++w)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) s_sum[wave][w * 4 + q][lane] = acc[w][q];
+    __syncthreads();
+    if (ks != 0) return;
+#pragma unroll
+    for (int o = 1; o < KS; ++o)
+#pragma unroll
+      for (int w = 0; w < 2; ++w)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc[w][q] += s_sum[wave + o][w * 4 + q][lane];
+  }
+  if (!active || lr >= rows) return;
+  const long long at = static_cast<long long>(r0 + lr) * N + n0 + 4 * (lane >> 4);
+  store4<MODE>(p, at, acc[0], acc[1]);
+  if constexpr (MODE != FWD1) store4<MODE>(p, at + 16, acc[1], acc[1]);
+}
+
+template <int MODE, int KS>
+__global__ __launch_bounds__(256) void grouped_skinny_fp8b_kernel(Params p) {
+  grouped_skinny<MODE, KS>(p);
+}
+
+template <int MODE>
+int launch_skinny(const Params& p, hipStream_t s) {
+  const int cols = n_total<MODE>(p.d, p.f) / (MODE == FWD1 ? 16 : 32);
+  const long long units = p.n / SKINNY_ROWS + std::min(p.n, p.E);     // at least the row groups of all experts
+  // as many ways to split the contraction as give every compute unit 8 waves, with 3 steps left for each
+  const int kb = static_cast<int>(fp8b_blocks(k_one<MODE>(p.d, p.f)));
+  int ks = 1;
+  while (ks < 4 && units * cols * ks < 8LL * cu_count() && kb >= 6 * ks) ks *= 2;
+  const long long blocks = units * ((cols + 4 / ks - 1) / (4 / ks));
+  MOE_REQUIRE(blocks < (1LL << 31), MOE_ERR_UNSUPPORTED, "too many tiles");
+  const unsigned g = static_cast<unsigned>(blocks);
+  if (ks == 1) grouped_skinny_fp8b_kernel<MODE, 1><<<g, 256, 0, s>>>(p);
+  else if (ks == 2) grouped_skinny_fp8b_kernel<MODE, 2><<<g, 256, 0, s>>>(p);
+  else grouped_skinny_fp8b_kernel<MODE, 4><<<g, 256, 0, s>>>(p);
+  return check_launch("grouped_gemm_fp8b (few rows)");
+}
+
+// Up to some 100 rows per expert on average: the stream of weights still sets the time, but a weight meets
+// enough rows that it should come through LDS once for all of them.  Tiles of 64 rows x 128 weight rows
+// (FWD1: the gate and the up rows of 64 columns), four waves of 64 rows x 32, two LDS stages of 24 KiB, one
+// workgroup per tile: three of them share a compute unit, so that each one's waits, prologue and epilogue
+// are covered by the others' loads.
+constexpr int MID_BM = 64, MID_BN = 128;
+constexpr int MID_A = MID_BM * BK, MID_B = MID_BN * BK, MID_STAGE = MID_A + MID_B + MID_BM * 4;
+
+template <int MODE, bool TAIL>
+__device__ __forceinline__ void grouped_mid(const Params& p, uint8_t* lds) {
+  constexpr int TC = MODE == FWD1 ? 64 : MID_BN;   // columns of a tile
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int N = n_total<MODE>(p.d, p.f), K = k_one<MODE>(p.d, p.f);
+  const int nt = (N + TC - 1) / TC, kb_one = static_cast<int>(fp8b_blocks(K));
+  // tiles dealt to the XCDs in contiguous runs, row groups of one column tile side by side
+  const MTiles mts = gsched::mtile_scan<MID_BM>(p.offsets, p.E);
+  const int total = mts.total * nt, per = (total + 7) >> 3;
+  const int lid = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+  if (static_cast<int>(blockIdx.x >> 3) >= per || lid >= total) return;
+  int e, first, mi, ni;
+  gsched::mtile_find(mts, lid / nt, e, first);
+  e = __builtin_amdgcn_readfirstlane(e);
+  first = __builtin_amdgcn_readfirstlane(first);
+  const int r0 = p.offsets[e], r1 = p.offsets[e + 1];
+  gsched::cell_order(lid - first * nt, (r1 - r0 + MID_BM - 1) / MID_BM, nt, 1 << 20, 1, mi, ni);
+  const int m0 = __builtin_amdgcn_readfirstlane(r0 + mi * MID_BM), m_end = __builtin_amdgcn_readfirstlane(r1);
+  const int n0 = __builtin_amdgcn_readfirstlane(ni * TC);
+
+  // DMA: this wave loads weight rows 32 wave .. + 31 and operand rows 16 wave .. + 15 of the tile (8 rows per
+  // instruction); wave 0 the rows' scales
+  const int wrow = MODE == FWD1 ? 32 * (wave & 1) : 32 * wave;
+  const bool up = MODE == FWD1 && wave >= 2;
+  const long long woff = (static_cast<long long>(e) * N + n0) * K, wbytes = static_cast<long long>(N - n0) * K;
+  const auto rw0 = gep::rsrc((up ? p.b1 : p.b0) + woff, wbytes);
+  const auto rw1 = MODE == DGRAD2 ? gep::rsrc(p.b1 + woff, wbytes) : rw0;
+  const long long xoff = static_cast<long long>(m0) * K, xbytes = (static_cast<long long>(p.n) - m0) * K;
+  const auto rx0 = gep::rsrc(p.a0 + xoff, xbytes);
+  const auto rx1 = MODE == DGRAD2 ? gep::rsrc(p.a1 + xoff, xbytes) : rx0;
+  const int chunk = (lane & 7) ^ (lane >> 4);
+  const uint32_t base = lds_addr(lds);
+  const int nk = kb_one * (MODE == DGRAD2 ? 2 : 1);
+  auto issue = [&](int k, int st) {
+    const bool second = MODE == DGRAD2 && k >= kb_one;
+    const int kb = second ? k - kb_one : k;
+    const auto rw = second ? rw1 : rw0;
+    const auto rx = second ? rx1 : rx0;
+    uint8_t* const dst = lds + st * MID_STAGE;
+    const int left = K - kb * BK;
+    static_for<0, 4>([&](auto i) {
+      const int c = (i & 1) ? chunk ^ 4 : chunk;
+      int off = (wrow + 8 * i + (lane >> 3)) * K + 16 * c;
+      if (TAIL && 16 * c >= left) off = static_cast<int>(gep::OOB);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(dst + MID_A + (4 * wave + i) * 1024), 16, off, kb * BK, 0, 0);
+    });
+    static_for<0, 2>([&](auto i) {
+      const int c = (i & 1) ? chunk ^ 4 : chunk;
+      int off = (16 * wave + 8 * i + (lane >> 3)) * K + 16 * c;
+      if (TAIL && 16 * c >= left) off = static_cast<int>(gep::OOB);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_void*)(dst + (2 * wave + i) * 1024), 16, off, kb * BK, 0, 0);
+    });
+    if (wave == 0) {
+      const float* sc = (second ? p.a1s : p.a0s) + static_cast<long long>(kb) * p.n + m0;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(gep::rsrc(sc, 4LL * (p.n - m0)), (lds_void*)(dst + MID_A + MID_B), 4,
+                                               4 * lane, 0, 0, 0);
+    }
+  };
+  Tile t{};
+  t.e = e;
+  float w0 = 0.f, w1 = 0.f;                        // weight scales: lane l holds K block l's
+  f32x4 acc[2][4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  issue(0, 0);
+  const uint32_t kc0 = kc_off(lane & 15, lane >> 4), kc1 = kc_off(lane & 15, 4 + (lane >> 4));
+  const uint32_t b_off = MID_A + (MODE == FWD1 ? 2048 : 4096) * wave;
+  for (int k = 0; k < nk; ++k) {
+    const bool second = MODE == DGRAD2 && k >= kb_one;
+    const int kb = second ? k - kb_one : k;
+    if ((kb & 63) == 0) {
+      w0 = weight_scale<MODE>(p, t, n0, second ? 1 : 0, kb);
+      if constexpr (MODE == FWD1) w1 = weight_scale<MODE>(p, t, n0, 1, kb);
+    }
+    const float ws0 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(w0), kb & 63));
+    const float ws1 = MODE == FWD1 ? __int_as_float(__builtin_amdgcn_readlane(__float_as_int(w1), kb & 63)) : ws0;
+    asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+    if (k + 1 < nk) issue(k + 1, (k + 1) & 1);
+    const uint32_t so = base + (k & 1) * MID_STAGE;
+    i32x8 fa[4], fb[2];
+    float sa[4];
+    static_for<0, 4>([&](auto j) {
+      read_frag<j>(fa[j], so + kc0, so + kc1);
+      ds_f32<64 * j>(sa[j], so + MID_A + MID_B + 4 * (lane & 15));
+    });
+    read_frag<0>(fb[0], so + b_off + kc0, so + b_off + kc1);
+    read_frag<MODE == FWD1 ? 4 : 1>(fb[1], so + b_off + kc0, so + b_off + kc1);
+    wait_col<2>(fb[0]);
+    wait_rows<2>(fa, sa);
+    f32x4 tmp[2][4];
+    static_for<0, 4>([&](auto j) { tmp[0][j] = mfma_block(fb[0], fa[j]); });
+    wait_col<0>(fb[1]);
+    static_for<0, 4>([&](auto j) { tmp[1][j] = mfma_block(fb[1], fa[j]); });
+    static_for<0, 2>([&](auto i) {
+      static_for<0, 4>([&](auto j) {
+        const float c = sa[j] * (i ? ws1 : ws0);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc[i][j][q] = fmaf(tmp[i][j][q], c, acc[i][j][q]);
+      });
+    });
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int r = m0 + 16 * j + (lane & 15);
+    if (r >= m_end) continue;
+    const int col = n0 + (MODE == FWD1 ? 16 : 32) * wave + 4 * (lane >> 4);
+    const long long at = static_cast<long long>(r) * N + col;
+    if (col < N) store4<MODE>(p, at, acc[0][j], acc[1][j]);
+    if (MODE != FWD1 && col + 16 < N) store4<MODE>(p, at + 16, acc[1][j], acc[1][j]);
+  }
+}
+
+template <int MODE, bool TAIL>
+__global__ __launch_bounds__(256, 3) void grouped_mid_fp8b_kernel(Params p) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * MID_STAGE];
+  grouped_mid<MODE, TAIL>(p, lds);
+}
+
+template <int MODE>
+int launch_mid(const Params& p, hipStream_t s) {
+  const int K = k_one<MODE>(p.d, p.f), tc = MODE == FWD1 ? 64 : MID_BN;
+  const long long blocks = (static_cast<long long>(p.n / MID_BM) + std::min(p.n, p.E)) * ((n_total<MODE>(p.d, p.f) + tc - 1) / tc);
+  MOE_REQUIRE(blocks < (1LL << 31) - 8, MOE_ERR_UNSUPPORTED, "too many tiles");
+  MOE_REQUIRE(static_cast<long long>(K) * MID_BN < 0x7fffffffLL, MOE_ERR_UNSUPPORTED, "rows too long");
+  const unsigned g = static_cast<unsigned>((blocks + 7) / 8 * 8);
+  if (K % BK != 0) grouped_mid_fp8b_kernel<MODE, true><<<g, 256, 0, s>>>(p);
+  else grouped_mid_fp8b_kernel<MODE, false><<<g, 256, 0, s>>>(p);
+  return check_launch("grouped_gemm_fp8b (64-row tiles)");
+}
+
+// Which form runs a product over rows, from host-visible sizes (the row counts stay on the device).
+//   few rows:  forward products of at most 6 rows per expert on average.  Measured (64 experts, d 2048, f
+//              1024, gate/up + down, us; 64-row tiles in brackets): 1 row 36 + 19 [37 + 18], 4 rows 48 + 29
+//              [56 + 33], 16 rows 73 + 39 [56 + 33]; one token of 8 experts at d 7168, f 2048 43 + 25 [57 + 24].
+//   else whichever of the two tilings the estimate below says is faster: both run a number of rounds of tiles
+//   over the compute units, and a 256-row tile costs more per round than 64-row tiles of the same work but
+//   streams fewer bytes, so few or ragged rounds go to the small tiles.  Per tile, measured over KB = K / 128
+//   steps: 1.9 KB + 10 us (256 rows), 0.4 KB + 1.3 us per 64-row tile of three sharing a unit, and at least
+//   0.65 KB + 3 us for one alone.  Measured on both sides of the choice (gate/up + down, us, 256-row tiles
+//   first): 64 experts, d 7168, f 2048, 64 rows each 519 + 269, 431 + 228; 128 rows 530 + 275, 567 + 291;
+//   16 experts, d 2112, f 1344, 256 rows 74 + 30, 55 + 30; 1024 rows 143 + 74, 165 + 92; one expert, d = f =
+//   4096, 256 rows 54 + 47, 22 + 21.
+// MOE_FP8B_FORM = few, mid or big sets the form (tests run every form on the same cases).
+enum Form { FEW, MID, BIG };
+template <int MODE>
+Form choose_form(const Params& p) {
+  if (const char* env = getenv("MOE_FP8B_FORM")) {
+    if (!strcmp(env, "few") && (MODE == FWD1 || MODE == FWD2)) return FEW;
+    if (!strcmp(env, "mid") || !strcmp(env, "few")) return MID;
+    if (!strcmp(env, "big")) return BIG;
+  }
+  if ((MODE == FWD1 || MODE == FWD2) && p.n <= 6LL * p.E) return FEW;
+  const double kb = static_cast<double>(fp8b_blocks(k_one<MODE>(p.d, p.f))) * (MODE == DGRAD2 ? 2 : 1);
+  const double busy = std::min(p.n, p.E), mean = p.n / busy;
+  const int N = n_total<MODE>(p.d, p.f), cus = cu_count();
+  auto rounds = [&](int bm, int cols) {            // an expert's last row tile is half full on average
+    const double mt = mean <= 0.84 * bm ? busy : static_cast<double>(p.n) / bm + 0.5 * busy;
+    return std::ceil(mt * ((N + cols - 1) / cols) / cus);
+  };
+  const double big = rounds(BM, n_tile_width<MODE>()) * (1.9 * kb + 10.0);
+  const double mid = std::max(rounds(MID_BM, MODE == FWD1 ? 64 : MID_BN) * (0.4 * kb + 1.3), 0.65 * kb + 3.0);
+  return mid < big ? MID : BIG;
+}
+
+template <int MODE>
+int launch_rows(const Params& p, hipStream_t s) {
+  const Form form = choose_form<MODE>(p);
+  if constexpr (MODE == FWD1 || MODE == FWD2) {
+    if (form == FEW) return launch_skinny<MODE>(p, s);
+  }
+  return form == MID ? launch_mid<MODE>(p, s) : launch<MODE>(p, s);
+}
+
 int check_gemm(int E, int n, int d, int f, const int32_t* offsets) {
   MOE_REQUIRE(E >= 1 && E <= 256, MOE_ERR_UNSUPPORTED, "E must be in [1, 256] (got %d)", E);
   MOE_REQUIRE(n >= 1, MOE_ERR_UNSUPPORTED, "n must be >= 1 (got %d)", n);
@@ -636,7 +1022,7 @@ extern "C" int moe_grouped_gemm_gate_up_fp8b(int E, int n, int d, int f, const i
   p.offsets = offsets; p.E = E; p.n = n; p.d = d; p.f = f;
   p.a0 = xq; p.a0s = xs; p.b0 = w_gate; p.b0s = w_gate_s; p.b1 = w_up; p.b1s = w_up_s;
   p.o0 = g; p.o1 = u; p.o2 = a;
-  return g8b::launch<g8b::FWD1>(p, as_stream(stream));
+  return g8b::launch_rows<g8b::FWD1>(p, as_stream(stream));
 }
 
 extern "C" int moe_grouped_gemm_down_fp8b(int E, int n, int d, int f, const int32_t* offsets, const uint8_t* aq,
@@ -647,7 +1033,7 @@ extern "C" int moe_grouped_gemm_down_fp8b(int E, int n, int d, int f, const int3
   g8b::Params p{};
   p.offsets = offsets; p.E = E; p.n = n; p.d = d; p.f = f;
   p.a0 = aq; p.a0s = as; p.b0 = w_down; p.b0s = w_down_s; p.o0 = yexp;
-  return g8b::launch<g8b::FWD2>(p, as_stream(stream));
+  return g8b::launch_rows<g8b::FWD2>(p, as_stream(stream));
 }
 
 extern "C" int moe_grouped_gemm_dgrad_down_fp8b(int E, int n, int d, int f, const int32_t* offsets, const uint8_t* dyq,
@@ -660,7 +1046,7 @@ extern "C" int moe_grouped_gemm_dgrad_down_fp8b(int E, int n, int d, int f, cons
   g8b::Params p{};
   p.offsets = offsets; p.E = E; p.n = n; p.d = d; p.f = f;
   p.a0 = dyq; p.a0s = dys; p.b0 = w_down_t; p.b0s = w_down_t_s; p.g = g; p.u = u; p.o0 = dg; p.o1 = du;
-  return g8b::launch<g8b::DGRAD1>(p, as_stream(stream));
+  return g8b::launch_rows<g8b::DGRAD1>(p, as_stream(stream));
 }
 
 extern "C" int moe_grouped_gemm_dgrad_gate_up_fp8b(int E, int n, int d, int f, const int32_t* offsets,
@@ -675,7 +1061,7 @@ extern "C" int moe_grouped_gemm_dgrad_gate_up_fp8b(int E, int n, int d, int f, c
   p.offsets = offsets; p.E = E; p.n = n; p.d = d; p.f = f;
   p.a0 = dgq; p.a0s = dgs; p.a1 = duq; p.a1s = dus;
   p.b0 = w_gate_t; p.b0s = w_gate_t_s; p.b1 = w_up_t; p.b1s = w_up_t_s; p.o0 = dxp;
-  return g8b::launch<g8b::DGRAD2>(p, as_stream(stream));
+  return g8b::launch_rows<g8b::DGRAD2>(p, as_stream(stream));
 }
 
 extern "C" int moe_grouped_gemm_wgrad_down_fp8b(int E, int n, int d, int f, const int32_t* offsets,

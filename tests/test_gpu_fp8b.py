@@ -174,6 +174,14 @@ PRODUCTS = [
 IDS = [f"{i}-{d}-{f}" for i, (_, d, f) in enumerate(PRODUCTS)]
 
 
+@pytest.fixture(params=["", "few", "mid", "big"])
+def form(request, monkeypatch):
+    """The library's own choice of kernel, and each of the three that it chooses from."""
+    if request.param:
+        monkeypatch.setenv("MOE_FP8B_FORM", request.param)
+    return request.param
+
+
 class Case:
     """Random operands of one product case: device tensors, and the values that they stand for."""
 
@@ -214,13 +222,13 @@ def silu_slack(g, u, dg, du):
 
 
 @pytest.mark.parametrize("counts,d,f", PRODUCTS, ids=IDS)
-def test_forward_products(counts, d, f):
+def test_forward_products(counts, d, f, form):
     from expert_ffn_layer_top_amd import ops
     c = Case(counts, d, f)
     x, xv = c.rows(d)
     wg, wgv = c.weight(f, d)
     wu, wuv = c.weight(f, d)
-    note(f"gate_up_fp8b n={c.n} E={c.E} d={d} f={f}")
+    note(f"gate_up_fp8b {form} n={c.n} E={c.E} d={d} f={f}")
     g, u, a = ops.grouped_gemm_gate_up_fp8b(*x, c.offsets, *wg, *wu)
     gr, gs, lgs = fp8b.grouped_nt(xv, wgv, c.off)
     ur, us, lus = fp8b.grouped_nt(xv, wuv, c.off)
@@ -232,21 +240,21 @@ def test_forward_products(counts, d, f):
     assert none_g is None and none_u is None and torch.equal(a, a2)
     q, qv = c.rows(f)
     wd, wdv = c.weight(d, f)
-    note(f"down_fp8b n={c.n} E={c.E} d={d} f={f}")
+    note(f"down_fp8b {form} n={c.n} E={c.E} d={d} f={f}")
     y = ops.grouped_gemm_down_fp8b(*q, c.offsets, *wd)
     yr, ys, lys = fp8b.grouped_nt(qv, wdv, c.off)
     assert_bf16(y, yr, sum_tol(ys, lys, f), "yexp")
 
 
 @pytest.mark.parametrize("counts,d,f", PRODUCTS, ids=IDS)
-def test_dgrad_products(counts, d, f):
+def test_dgrad_products(counts, d, f, form):
     from expert_ffn_layer_top_amd import ops
     c = Case(counts, d, f, seed=1)
     dy, dyv = c.rows(d)
     wd, wdv = c.weight(f, d)
     g, gv = c.bf16(f)
     u, uv = c.bf16(f)
-    note(f"dgrad_down_fp8b n={c.n} E={c.E} d={d} f={f}")
+    note(f"dgrad_down_fp8b {form} n={c.n} E={c.E} d={d} f={f}")
     dg, du = ops.grouped_gemm_dgrad_down_fp8b(*dy, c.offsets, *wd, g, u)
     da, size, lsize = fp8b.grouped_nt(dyv, wdv, c.off)
     off = sum_tol(size, lsize, d)
@@ -259,7 +267,7 @@ def test_dgrad_products(counts, d, f):
     q, qv = c.rows(f)
     wg, wgv = c.weight(d, f)
     wu, wuv = c.weight(d, f)
-    note(f"dgrad_gate_up_fp8b n={c.n} E={c.E} d={d} f={f}")
+    note(f"dgrad_gate_up_fp8b {form} n={c.n} E={c.E} d={d} f={f}")
     dxp = ops.grouped_gemm_dgrad_gate_up_fp8b(*p, *q, c.offsets, *wg, *wu)
     r0, s0, ls0 = fp8b.grouped_nt(pv, wgv, c.off)
     r1, s1, ls1 = fp8b.grouped_nt(qv, wuv, c.off)
@@ -291,7 +299,7 @@ def test_wgrad_products(counts, d, f):
 
 
 @pytest.mark.parametrize("K", [8192, 8256, 16384 + 192])
-def test_long_contractions(K):
+def test_long_contractions(K, form):
     """More blocks than one register of weight scales holds (64), along d and along f."""
     from expert_ffn_layer_top_amd import ops
     c = Case([5, 0, 20], K, 64, seed=3)
@@ -312,7 +320,7 @@ def test_long_contractions(K):
     assert_bf16(dxp, r0 + r1, sum_tol(s0 + s1, ls0 + ls1, 2 * K), "dxp")
 
 
-def test_rows_behind_the_last_group_are_left():
+def test_rows_behind_the_last_group_are_left(form):
     from expert_ffn_layer_top_amd._lib import call
     c = Case([20, 0, 13], 128, 192, seed=5)
     n = 50                                                 # 17 rows that belong to no expert
@@ -342,6 +350,7 @@ def test_many_tiles_per_workgroup(monkeypatch):
         return (*ops.grouped_gemm_gate_up_fp8b(*x, c.offsets, *wg, *wu),
                 ops.grouped_gemm_wgrad_down_fp8b(*dyT, *aT, c.offsets, c.offsets_pad, c.n))
 
+    monkeypatch.setenv("MOE_FP8B_FORM", "big")
     full = run()
     monkeypatch.setenv("MOE_GG_WORKGROUPS", "8")
     note("fp8b products with 8 workgroups")
@@ -350,7 +359,7 @@ def test_many_tiles_per_workgroup(monkeypatch):
         assert torch.equal(p, q)
 
 
-def test_streams_and_replayed_graph():
+def test_streams_and_replayed_graph(form):
     """The whole forward and backward in a captured graph, replayed between eager runs, and on a side stream."""
     from expert_ffn_layer_top_amd import ops
     c = Case([100, 0, 31, 200], 256, 192, seed=7)
