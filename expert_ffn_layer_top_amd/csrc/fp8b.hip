@@ -9,6 +9,8 @@
 //             [E, ceil(R/128), ceil(C/128)] and its transpose
 // Scales are block-major, so one K step of a product reads the scales of its 256 rows as one run.
 // All are HBM-bound: 2 bytes read, 1 + 4/128 bytes written per element and layout.
+#include <type_traits>
+
 #include "fp8b_common.h"
 
 namespace moe {
@@ -70,39 +72,57 @@ __device__ __forceinline__ void store_transposed(const uint8_t* s_t, uint8_t* __
   }
 }
 
-// Transposes 8 x 8 codes in registers (row i: 8 columns' codes) and stages them as 8 column chunks.
+// Transposes 8 x 8 codes in registers (row i: 8 columns' codes) and stages them as 8 column chunks: four
+// 4 x 4 byte blocks, eight byte permutes each.
 __device__ __forceinline__ void stage_transposed(const uint2 (&o)[8], uint8_t* s_t, int cg, int pg) {
+  uint32_t t[8][2];                                // [column][half of its 8 positions]
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    uint32_t w[2];
+  for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t a = j < 4 ? o[4 * h].x : o[4 * h].y, b = j < 4 ? o[4 * h + 1].x : o[4 * h + 1].y;
-      const uint32_t c = j < 4 ? o[4 * h + 2].x : o[4 * h + 2].y, d = j < 4 ? o[4 * h + 3].x : o[4 * h + 3].y;
-      const int sh = 8 * (j & 3);
-      w[h] = ((a >> sh) & 0xffu) | (((b >> sh) & 0xffu) << 8) | (((c >> sh) & 0xffu) << 16) | (((d >> sh) & 0xffu) << 24);
+    for (int c = 0; c < 2; ++c) {
+      const uint32_t r0 = c ? o[4 * h].y : o[4 * h].x, r1 = c ? o[4 * h + 1].y : o[4 * h + 1].x;
+      const uint32_t r2 = c ? o[4 * h + 2].y : o[4 * h + 2].x, r3 = c ? o[4 * h + 3].y : o[4 * h + 3].x;
+      // bytes 0-3 of a permute's selector address its second operand, 4-7 its first
+      const uint32_t a = __builtin_amdgcn_perm(r1, r0, 0x05010400u), b = __builtin_amdgcn_perm(r1, r0, 0x07030602u);
+      const uint32_t d = __builtin_amdgcn_perm(r3, r2, 0x05010400u), e = __builtin_amdgcn_perm(r3, r2, 0x07030602u);
+      t[4 * c + 0][h] = __builtin_amdgcn_perm(d, a, 0x05040100u);
+      t[4 * c + 1][h] = __builtin_amdgcn_perm(d, a, 0x07060302u);
+      t[4 * c + 2][h] = __builtin_amdgcn_perm(e, b, 0x05040100u);
+      t[4 * c + 3][h] = __builtin_amdgcn_perm(e, b, 0x07060302u);
     }
-    *reinterpret_cast<uint2*>(s_t + tcode_off(8 * cg + j, pg)) = make_uint2(w[0], w[1]);
-  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) *reinterpret_cast<uint2*>(s_t + tcode_off(8 * cg + j, pg)) = make_uint2(t[j][0], t[j][1]);
 }
 
 // Column steps a grouped workgroup takes along its band of 128 positions.
 constexpr int kBandSteps = 4;
 
+// Work item of block `id` when XCD x (block ids = x mod 8, each XCD with its own L2) takes a contiguous run
+// of the items, so that neighbours of a band share an L2.
+__device__ __forceinline__ long long run_item(long long id, long long total) {
+  const long long per = total >> 3, extra = total & 7;
+  const long long x = id & 7;
+  return x * per + (x < extra ? x : extra) + (id >> 3);
+}
+
 // Grouped rows: padded position p of expert e holds grouped row r = offsets[e] + p - offsets_pad[e] while
 // that is below offsets[e + 1]; its data is in[row_token ? row_token[r] : r], times row_gate[r] rounded
 // to bf16 where given.  ROWS: also the real rows' row layout, q [n][C] and s [ceil(C/128)][n].
-template <bool ROWS>
+// A division per block: lane i of a row's 16 makes the factors of the thread group's row i, and one thread
+// those of each column.
+template <bool ROWS, bool GATE>
 __global__ __launch_bounds__(kTileThreads) void fp8b_grouped_kernel(
     const uint16_t* __restrict__ in, const int32_t* __restrict__ row_token, const float* __restrict__ row_gate,
     const int32_t* __restrict__ offsets, const int32_t* __restrict__ offsets_pad, int E, int C, long long n, long long P,
     uint8_t* __restrict__ q, float* __restrict__ s, uint8_t* __restrict__ qT, float* __restrict__ sT, int cgroups) {
   __shared__ __attribute__((aligned(16))) uint8_t s_t[kTile * kTile];
-  __shared__ uint32_t s_amax[16][kTile];
+  __shared__ __attribute__((aligned(16))) uint32_t s_amax[kTileThreads / 64][kTile / 2];
+  __shared__ __attribute__((aligned(16))) float s_inv[kTile];
   __shared__ int s_row[kTile];
   const int tid = threadIdx.x, cg = tid & 15, pg = tid >> 4;
-  const long long p0 = static_cast<long long>(blockIdx.x / cgroups) * kTile;
-  int c0 = static_cast<int>(blockIdx.x % cgroups) * kTile * kBandSteps;
+  const long long item = run_item(blockIdx.x, gridDim.x);
+  const long long p0 = item / cgroups * kTile;
+  int c0 = static_cast<int>(item % cgroups) * kTile * kBandSteps;
   if (tid < kTile) {
     const long long p = p0 + tid;
     int r = -1;
@@ -118,68 +138,86 @@ __global__ __launch_bounds__(kTileThreads) void fp8b_grouped_kernel(
     s_row[tid] = r;
   }
   __syncthreads();
-  int row[8];
-  long long src[8];
-  float gate[8];
+  // the thread's eight positions are consecutive rows of one expert as far as they are rows at all
+  const int row0 = s_row[8 * pg];
+  unsigned live = 0;
+  int src[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    row[i] = s_row[8 * pg + i];
-    src[i] = row[i] < 0 ? -1 : (row_token != nullptr ? row_token[row[i]] : row[i]);
-    gate[i] = row_gate != nullptr && row[i] >= 0 ? row_gate[row[i]] : 1.f;
+    if (row0 >= 0 && s_row[8 * pg + i] == row0 + i) live |= 1u << i;
+    src[i] = (live >> i & 1u) ? (row_token != nullptr ? row_token[row0 + i] : row0 + i) : -1;
+  }
+  float gate[8];
+  if constexpr (GATE) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) gate[i] = (live >> i & 1u) ? row_gate[row0 + i] : 1.f;
   }
   for (int step = 0; step < kBandSteps && c0 < C; ++step, c0 += kTile) {
     const int col = c0 + 8 * cg;
+    const bool in_cols = col < C;
     uint4 v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       v[i] = make_uint4(0, 0, 0, 0);
-      if (src[i] >= 0 && col < C) v[i] = *reinterpret_cast<const uint4*>(in + src[i] * C + col);
+      if (src[i] >= 0 && in_cols) v[i] = *reinterpret_cast<const uint4*>(in + static_cast<long long>(src[i]) * C + col);
     }
-    uint32_t cmax[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) cmax[j] = 0;
+    uint32_t cmax[4] = {0, 0, 0, 0};
+    uint32_t my_amax = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-      if (row_gate != nullptr) {
+      if constexpr (GATE) {
+        uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
         for (int h = 0; h < 4; ++h) w[h] = pack_bf16x2(gate[i] * bf16_lo(w[h]), gate[i] * bf16_hi(w[h]));
         v[i] = make_uint4(w[0], w[1], w[2], w[3]);
       }
+      const uint32_t m[4] = {abs_pair(v[i].x), abs_pair(v[i].y), abs_pair(v[i].z), abs_pair(v[i].w)};
 #pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        cmax[2 * h] = max(cmax[2 * h], w[h] & 0x7fffu);
-        cmax[2 * h + 1] = max(cmax[2 * h + 1], (w[h] >> 16) & 0x7fffu);
-      }
+      for (int h = 0; h < 4; ++h) cmax[h] = max_pair(cmax[h], m[h]);
       if constexpr (ROWS) {
-        const Fp8bScale f = fp8b_scale(max16(fp8b_amax8(w)));
-        if (row[i] >= 0 && col < C) {
-          *reinterpret_cast<uint2*>(q + static_cast<long long>(row[i]) * C + col) = fp8b_encode8(w, f.inv);
-          if (cg == 0) s[(c0 / kTile) * n + row[i]] = f.scale;
-        }
+        const uint32_t rmax = max16(max_of_pair(max_pair(max_pair(m[0], m[1]), max_pair(m[2], m[3]))));
+        my_amax = (cg & 7) == i ? rmax : my_amax;
       }
     }
-    __syncthreads();                 // the previous step's readers are done with the LDS
-#pragma unroll
-    for (int j = 0; j < 8; ++j) s_amax[pg][8 * cg + j] = cmax[j];
-    __syncthreads();
-    float inv[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      uint32_t m = 0;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) m = max(m, s_amax[i][8 * cg + j]);
-      const Fp8bScale f = fp8b_scale(m);
-      inv[j] = f.inv;
-      if (pg == 0 && col < C) sT[(p0 / kTile) * C + col + j] = f.scale;
+    if constexpr (ROWS) {
+      const Fp8bScale f = fp8b_scale(my_amax);
+      if (cg < 8 && (live >> cg & 1u)) s[(c0 / kTile) * n + row0 + cg] = f.scale;
+      uint8_t* const qrow = q + static_cast<long long>(row0) * C + col;
+      auto put = [&](auto i) {
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        const uint2 o = fp8b_encode8(w, row_lane<i>(f.inv));
+        if ((live >> i & 1u) && in_cols) *reinterpret_cast<uint2*>(qrow + static_cast<long long>(i) * C) = o;
+        __builtin_amdgcn_sched_barrier(0);   // one row's codes at a time: all eight at once took 70 more registers
+      };
+      put(std::integral_constant<int, 0>{}); put(std::integral_constant<int, 1>{});
+      put(std::integral_constant<int, 2>{}); put(std::integral_constant<int, 3>{});
+      put(std::integral_constant<int, 4>{}); put(std::integral_constant<int, 5>{});
+      put(std::integral_constant<int, 6>{}); put(std::integral_constant<int, 7>{});
     }
+    // column maxima: over the wave's four position groups, then over the four waves
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      cmax[h] = max_pair(cmax[h], static_cast<uint32_t>(__shfl_xor(static_cast<int>(cmax[h]), 16, 64)));
+      cmax[h] = max_pair(cmax[h], static_cast<uint32_t>(__shfl_xor(static_cast<int>(cmax[h]), 32, 64)));
+    }
+    if ((tid & 63) < 16) *reinterpret_cast<uint4*>(&s_amax[tid >> 6][4 * cg]) = make_uint4(cmax[0], cmax[1], cmax[2], cmax[3]);
+    __syncthreads();
+    if (tid < kTile) {
+      const uint32_t m = max_pair(max_pair(s_amax[0][tid >> 1], s_amax[1][tid >> 1]),
+                                  max_pair(s_amax[2][tid >> 1], s_amax[3][tid >> 1]));
+      const Fp8bScale f = fp8b_scale((tid & 1) ? m >> 16 : m & 0xffffu);
+      s_inv[tid] = f.inv;
+      if (c0 + tid < C) sT[(p0 / kTile) * C + c0 + tid] = f.scale;
+    }
+    __syncthreads();
+    const float4 ia = *reinterpret_cast<const float4*>(&s_inv[8 * cg]), ib = *reinterpret_cast<const float4*>(&s_inv[8 * cg + 4]);
     uint2 o[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      o[i] = make_uint2(fp8b_encode4(bf16_lo(v[i].x) * inv[0], bf16_hi(v[i].x) * inv[1], bf16_lo(v[i].y) * inv[2],
-                                     bf16_hi(v[i].y) * inv[3]),
-                        fp8b_encode4(bf16_lo(v[i].z) * inv[4], bf16_hi(v[i].z) * inv[5], bf16_lo(v[i].w) * inv[6],
-                                     bf16_hi(v[i].w) * inv[7]));
+      o[i] = make_uint2(fp8b_encode4(bf16_lo(v[i].x) * ia.x, bf16_hi(v[i].x) * ia.y, bf16_lo(v[i].y) * ia.z,
+                                     bf16_hi(v[i].y) * ia.w),
+                        fp8b_encode4(bf16_lo(v[i].z) * ib.x, bf16_hi(v[i].z) * ib.y, bf16_lo(v[i].w) * ib.z,
+                                     bf16_hi(v[i].w) * ib.w));
     stage_transposed(o, s_t, cg, pg);
     __syncthreads();
     store_transposed(s_t, qT + c0 * P + p0, P, C - c0, kTile);
@@ -276,12 +314,12 @@ extern "C" int moe_fp8b_quantize_rows_grouped(const uint16_t* in, const int32_t*
   const long long blocks = static_cast<long long>(P / kTile) * cgroups;
   MOE_REQUIRE(blocks <= 0x7fffffffLL, MOE_ERR_UNSUPPORTED, "too many tiles");
   hipStream_t st = as_stream(stream);
-  if (q)
-    fp8b_grouped_kernel<true><<<static_cast<unsigned>(blocks), kTileThreads, 0, st>>>(
-        in, row_token, row_gate, offsets, offsets_pad, E, C, n, P, q, s, qT, sT, cgroups);
-  else
-    fp8b_grouped_kernel<false><<<static_cast<unsigned>(blocks), kTileThreads, 0, st>>>(
-        in, row_token, row_gate, offsets, offsets_pad, E, C, n, P, q, s, qT, sT, cgroups);
+  auto run = [&](auto kernel) {
+    kernel<<<static_cast<unsigned>(blocks), kTileThreads, 0, st>>>(in, row_token, row_gate, offsets, offsets_pad, E, C, n, P,
+                                                                   q, s, qT, sT, cgroups);
+  };
+  if (q) row_gate ? run(fp8b_grouped_kernel<true, true>) : run(fp8b_grouped_kernel<true, false>);
+  else row_gate ? run(fp8b_grouped_kernel<false, true>) : run(fp8b_grouped_kernel<false, false>);
   return check_launch("fp8b_quantize_rows_grouped");
 }
 
