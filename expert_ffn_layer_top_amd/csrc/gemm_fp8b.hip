@@ -63,6 +63,7 @@ constexpr int LDS_TOTAL = SB_RING + 2 * SC_BYTES;  // 132 KiB
 constexpr int STG_BYTES = 2 * OP_BYTES / 8;        // epilogue staging per wave, in the stage just consumed
 
 __shared__ __attribute__((aligned(1024))) uint8_t lds_ring[LDS_TOTAL];
+__shared__ int tile_map[256];                      // row tiles before each expert's
 
 __device__ __forceinline__ uint32_t lds_addr(const uint8_t* p) {
   return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((const lds_u8*)(p)));
@@ -120,15 +121,33 @@ __host__ __device__ __forceinline__ int m_total(int d, int f) { return MODE == W
 
 using gsched::MTiles;
 
+// The row tiles before each expert's, kept in LDS (in registers they spilled others): every wave writes all
+// of it, the same values, and so reads back its own.  Returns the number of row tiles.
+__device__ __forceinline__ int store_map(const Params& p) {
+  const MTiles m = gsched::mtile_scan<BM>(p.offsets, p.E);
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) tile_map[64 * r + lane] = 64 * r + lane < p.E ? m.excl[r] : INT32_MAX;
+  return m.total;
+}
+// The expert that owns row tile mt: the last one with at most mt tiles before it (`first` of them).
+__device__ __forceinline__ int map_find(int mt, int& first) {
+  const int lane = threadIdx.x & 63;
+  int count = 0;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) count += __popcll(__ballot(tile_map[64 * r + lane] <= mt));
+  first = tile_map[count - 1];
+  return count - 1;
+}
+
 // The tile with linear id `lid`: each expert owns a contiguous run of ids, its tiles in cell order.
 template <int MODE>
-__device__ __forceinline__ Tile tile_at(const Params& p, const MTiles& mts, int ntiles_n, int lid) {
+__device__ __forceinline__ Tile tile_at(const Params& p, int ntiles_n, int lid) {
   Tile t{};
   int mi, nt;
   if constexpr (!is_wgrad(MODE)) {
-    int e, first;
-    gsched::mtile_find(mts, lid / ntiles_n, e, first);
-    e = __builtin_amdgcn_readfirstlane(e);
+    int first;
+    const int e = __builtin_amdgcn_readfirstlane(map_find(lid / ntiles_n, first));
     first = __builtin_amdgcn_readfirstlane(first);
     const int r0 = p.offsets[e], r1 = p.offsets[e + 1];
     gsched::cell_order(lid - first * ntiles_n, (r1 - r0 + BM - 1) / BM, ntiles_n, p.cm, p.cn, mi, nt);
@@ -308,6 +327,7 @@ __device__ __forceinline__ void epilogue(const Params& p, const Tile& t, f32x4 (
     const int col0 = t.n0 + 128 * wn, cv = p.f - col0;
     const auto rg = gep::out_rsrc(p.g, p.n, p.f, row0, col0), ru = gep::out_rsrc(p.u, p.n, p.f, row0, col0);
     const auto rdg = gep::out_rsrc(p.o0, p.n, p.f, row0, col0), rdu = gep::out_rsrc(p.o1, p.n, p.f, row0, col0);
+    // (8-byte loads straight into the product's layout, a round ahead, ran the product 13% slower)
     gep::sfor<0, 4>([&](auto q) {
       u32x2 gm[1][8], um[1][8];
       u32x4 gl[4], ul[4];
@@ -342,10 +362,10 @@ __device__ __forceinline__ void epilogue(const Params& p, const Tile& t, f32x4 (
       out = (MODE == WGRAD_GU && t.half ? p.o1 : p.o0) + static_cast<long long>(t.e) * rows * N;
     }
     const auto r = gep::out_rsrc(out, rows, N, row0, col0);
-    gep::sfor<0, 2>([&](auto q) {
-      u32x2 v[2][8];
-      gep::sfor<0, 2>([&](auto jj) { gep::sfor<0, 8>([&](auto i) { v[jj][i] = gep::pack4(acc[i][2 * q + jj]); }); });
-      gep::stage_out_round<8, 2>(v, q, r, rows_valid, cv, N, stg, lane);
+    gep::sfor<0, 4>([&](auto q) {
+      u32x2 v[1][8];
+      gep::sfor<0, 8>([&](auto i) { v[0][i] = gep::pack4(acc[i][q]); });
+      gep::stage_out_round<8, 1>(v, q, r, rows_valid, cv, N, stg, lane);
     });
   }
 }
@@ -370,12 +390,10 @@ __device__ __forceinline__ void grouped_gemm(const Params& p) {
   // ---- device-side schedule (as the MXFP8 products)
   constexpr int NTW = MODE == FWD1 ? BN / 2 : BN;
   const int ntiles_n = (n_total<MODE>(p.d, p.f) + NTW - 1) / NTW;
-  MTiles mts{};
   int total;
   bool deal = false;
   if constexpr (!WG) {
-    mts = gsched::mtile_scan<BM>(p.offsets, p.E);
-    total = mts.total * ntiles_n;
+    total = store_map(p) * ntiles_n;
   } else {
     total = p.E * ((m_total<MODE>(p.d, p.f) + BM - 1) / BM) * (MODE == WGRAD_GU ? 2 : 1) * ntiles_n;
     deal = gsched::wgrad_skewed(p.offsets, p.E, p.n);
@@ -406,7 +424,7 @@ __device__ __forceinline__ void grouped_gemm(const Params& p) {
   const int ld = WG ? p.P : Kone;                    // bytes per operand row
   const int spitch = WG ? (role_b ? n_total<MODE>(p.d, p.f) : m_total<MODE>(p.d, p.f)) : p.n;
 
-  Tile t = tile_at<MODE>(p, mts, ntiles_n, lid);
+  Tile t = tile_at<MODE>(p, ntiles_n, lid);
   TileSrc cur = tile_src<MODE>(p, t, role_b, h);
   Tile tn = t;
   TileSrc nxt = empty_src<MODE>(p);
@@ -415,7 +433,7 @@ __device__ __forceinline__ void grouped_gemm(const Params& p) {
   float w0 = weight_scale<MODE>(p, t, t.n0 + wcol, 0, 0), w1 = 0.f, w0n = 0.f, w1n = 0.f;
   if constexpr (MODE == FWD1 || MODE == DGRAD2) w1 = weight_scale<MODE>(p, t, t.n0 + wcol, 1, 0);
   auto look_ahead = [&]() {
-    tn = tile_at<MODE>(p, mts, ntiles_n, lid_n);
+    tn = tile_at<MODE>(p, ntiles_n, lid_n);
     nxt = tile_src<MODE>(p, tn, role_b, h);
     w0n = weight_scale<MODE>(p, tn, tn.n0 + wcol, 0, 0);
     if constexpr (MODE == FWD1 || MODE == DGRAD2) w1n = weight_scale<MODE>(p, tn, tn.n0 + wcol, 1, 0);
@@ -445,7 +463,9 @@ __device__ __forceinline__ void grouped_gemm(const Params& p) {
     return st;
   };
   auto issue = [&](auto i, const Step& st, uint8_t* dst) {
-    int off = ((i & 1) ? vo_odd : vo) + 8 * i * ld;
+    int off = (i & 1) ? vo_odd : vo;
+    asm volatile("" : "+v"(off));      // added up here each time: kept, the eight offsets spilled other registers
+    off += 8 * i * ld;
     if constexpr (TAIL) off = 16 * ((i & 1) ? chunk ^ 4 : chunk) < st.left ? off : static_cast<int>(gep::OOB);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(st.r, (lds_void*)(dst + i * 1024), 16, off, st.soff, 0, 0);
   };
@@ -808,179 +828,352 @@ int launch_skinny(const Params& p, hipStream_t s) {
   return check_launch("grouped_gemm_fp8b (few rows)");
 }
 
-// Up to some 100 rows per expert on average: the stream of weights still sets the time, but a weight meets
-// enough rows that it should come through LDS once for all of them.  Tiles of 64 rows x 128 weight rows
-// (FWD1: the gate and the up rows of 64 columns), four waves of 64 rows x 32, two LDS stages of 24 KiB, one
-// workgroup per tile: three of them share a compute unit, so that each one's waits, prologue and epilogue
-// are covered by the others' loads.
-constexpr int MID_BM = 64, MID_BN = 128;
-constexpr int MID_A = MID_BM * BK, MID_B = MID_BN * BK, MID_STAGE = MID_A + MID_B + MID_BM * 4;
+// The small tiles: 64 or 128 rows x 128 column rows (FWD1: the gate and the up rows of 64 columns), four
+// waves, two LDS stages, one workgroup per tile, three (64 rows) or two (128) workgroups on a compute unit,
+// so that each one's waits, prologue and epilogue are covered by the others' loads and products.  64-row
+// tiles serve up to some 100 rows per expert, where the stream of weights sets the time but a weight meets
+// enough rows that it should come through LDS once for all of them; 128-row tiles serve products whose
+// 256-row tiles would be few, ragged, or short (few K steps for each epilogue, as the weight gradients of a
+// few hundred tokens).  A wave has 64 rows x 32 columns, or 64 x 64.
+constexpr int SM_BN = 128;
+template <int BM>
+struct Small {
+  static constexpr int NF = BM / 32;                       // 16-column fragments of a wave
+  static constexpr int A = BM * BK, B = SM_BN * BK;
+  static constexpr int SA = A + B, SB = SA + BM * 4;       // the stage's scales, one float per row
+  static constexpr int STAGE = SB + SM_BN * 4;
+  static constexpr int PER_CU = BM == 64 ? 3 : 2;
+};
 
-template <int MODE, bool TAIL>
-__device__ __forceinline__ void grouped_mid(const Params& p, uint8_t* lds) {
-  constexpr int TC = MODE == FWD1 ? 64 : MID_BN;   // columns of a tile
+template <int MODE, int BM, bool TAIL>
+__device__ __forceinline__ void grouped_small(const Params& p, uint8_t* lds) {
+  constexpr bool WG = is_wgrad(MODE);
+  using S = Small<BM>;
+  constexpr int NF = S::NF;
+  constexpr int TC = MODE == FWD1 ? SM_BN / 2 : SM_BN;     // output columns of a tile
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = BM == 128 ? wave >> 1 : 0, wn = BM == 128 ? wave & 1 : wave;
   const int N = n_total<MODE>(p.d, p.f), K = k_one<MODE>(p.d, p.f);
   const int nt = (N + TC - 1) / TC, kb_one = static_cast<int>(fp8b_blocks(K));
-  // tiles dealt to the XCDs in contiguous runs, row groups of one column tile side by side
-  const MTiles mts = gsched::mtile_scan<MID_BM>(p.offsets, p.E);
-  const int total = mts.total * nt, per = (total + 7) >> 3;
-  const int lid = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-  if (static_cast<int>(blockIdx.x >> 3) >= per || lid >= total) return;
-  int e, first, mi, ni;
-  gsched::mtile_find(mts, lid / nt, e, first);
-  e = __builtin_amdgcn_readfirstlane(e);
-  first = __builtin_amdgcn_readfirstlane(first);
-  const int r0 = p.offsets[e], r1 = p.offsets[e + 1];
-  gsched::cell_order(lid - first * nt, (r1 - r0 + MID_BM - 1) / MID_BM, nt, 1 << 20, 1, mi, ni);
-  const int m0 = __builtin_amdgcn_readfirstlane(r0 + mi * MID_BM), m_end = __builtin_amdgcn_readfirstlane(r1);
-  const int n0 = __builtin_amdgcn_readfirstlane(ni * TC);
+  // tiles dealt to the XCDs in contiguous runs, the row tiles of one column tile side by side
+  MTiles mts{};
+  int total, mtw = 0;
+  if constexpr (WG) {
+    mtw = (m_total<MODE>(p.d, p.f) + BM - 1) / BM * (MODE == WGRAD_GU ? 2 : 1);
+    total = p.E * mtw * nt;
+  } else {
+    mts = gsched::mtile_scan<BM>(p.offsets, p.E);
+    total = mts.total * nt;
+  }
+  // (round-robin for weight gradients of a hot expert, whose long tiles would otherwise share an XCD)
+  const int per = (total + 7) >> 3;
+  int lid = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+  if (static_cast<int>(blockIdx.x >> 3) >= per) lid = total;
+  if (WG && gsched::wgrad_skewed(p.offsets, p.E, p.n)) lid = blockIdx.x;
+  if (lid >= total) return;
+  Tile t{};
+  int mi, ni, nk = kb_one * (MODE == DGRAD2 ? 2 : 1);
+  if constexpr (WG) {
+    const int Mtot = m_total<MODE>(p.d, p.f), mt = (Mtot + BM - 1) / BM;
+    t.e = __builtin_amdgcn_readfirstlane(lid / (mtw * nt));
+    gsched::cell_order(lid - t.e * mtw * nt, mtw, nt, 4, 4, mi, ni);
+    t.half = __builtin_amdgcn_readfirstlane(mi >= mt ? 1 : 0);
+    t.m0 = __builtin_amdgcn_readfirstlane((mi - t.half * mt) * BM);
+    t.m_end = Mtot;
+    t.k_begin = __builtin_amdgcn_readfirstlane(p.offsets_pad[t.e]);
+    nk = __builtin_amdgcn_readfirstlane((p.offsets_pad[t.e + 1] - t.k_begin) / BK);
+  } else {
+    int e, first;
+    gsched::mtile_find(mts, lid / nt, e, first);
+    t.e = __builtin_amdgcn_readfirstlane(e);
+    first = __builtin_amdgcn_readfirstlane(first);
+    const int r0 = p.offsets[t.e], r1 = p.offsets[t.e + 1];
+    gsched::cell_order(lid - first * nt, (r1 - r0 + BM - 1) / BM, nt, 1 << 20, 1, mi, ni);
+    t.m0 = __builtin_amdgcn_readfirstlane(r0 + mi * BM);
+    t.m_end = __builtin_amdgcn_readfirstlane(r1);
+  }
+  t.n0 = __builtin_amdgcn_readfirstlane(ni * TC);
 
-  // DMA: this wave loads weight rows 32 wave .. + 31 and operand rows 16 wave .. + 15 of the tile (8 rows per
-  // instruction); wave 0 the rows' scales
+  // DMA: each wave loads a quarter of both operands, 8 rows per instruction (FWD1: waves 0, 1 the gate's
+  // rows, 2, 3 the up matrix's); the first BM / 64 waves the rows' scales, and of weight gradients waves
+  // 2, 3 the columns'
+  const int ld = WG ? p.P : K;
   const int wrow = MODE == FWD1 ? 32 * (wave & 1) : 32 * wave;
-  const bool up = MODE == FWD1 && wave >= 2;
-  const long long woff = (static_cast<long long>(e) * N + n0) * K, wbytes = static_cast<long long>(N - n0) * K;
-  const auto rw0 = gep::rsrc((up ? p.b1 : p.b0) + woff, wbytes);
-  const auto rw1 = MODE == DGRAD2 ? gep::rsrc(p.b1 + woff, wbytes) : rw0;
-  const long long xoff = static_cast<long long>(m0) * K, xbytes = (static_cast<long long>(p.n) - m0) * K;
-  const auto rx0 = gep::rsrc(p.a0 + xoff, xbytes);
-  const auto rx1 = MODE == DGRAD2 ? gep::rsrc(p.a1 + xoff, xbytes) : rx0;
+  const uint8_t *xb0, *xb1 = nullptr, *wb0, *wb1 = nullptr;
+  const float *xs0, *xs1 = nullptr;
+  long long xbytes, wbytes;
+  int xrows, xpitch;
+  if constexpr (WG) {
+    const bool second = MODE == WGRAD_GU && t.half;
+    xb0 = (second ? p.a1 : p.a0) + static_cast<long long>(t.m0) * p.P + t.k_begin;
+    xbytes = static_cast<long long>(t.m_end - t.m0) * p.P - t.k_begin;
+    wb0 = p.b0 + static_cast<long long>(t.n0) * p.P + t.k_begin;
+    wbytes = static_cast<long long>(N - t.n0) * p.P - t.k_begin;
+    xpitch = t.m_end;
+    xrows = t.m_end - t.m0;
+    xs0 = (second ? p.a1s : p.a0s) + static_cast<long long>(t.k_begin / BK) * t.m_end + t.m0;
+  } else {
+    const long long woff = (static_cast<long long>(t.e) * N + t.n0) * K;
+    wb0 = (MODE == FWD1 && wave >= 2 ? p.b1 : p.b0) + woff;
+    wb1 = p.b1 + woff;
+    wbytes = static_cast<long long>(N - t.n0) * K;
+    xrows = p.n - t.m0;
+    xpitch = p.n;
+    xb0 = p.a0 + static_cast<long long>(t.m0) * K;
+    xb1 = p.a1 + static_cast<long long>(t.m0) * K;
+    xbytes = static_cast<long long>(xrows) * K;
+    xs0 = p.a0s + t.m0;
+    xs1 = p.a1s + t.m0;
+  }
   const int chunk = (lane & 7) ^ (lane >> 4);
-  const uint32_t base = lds_addr(lds);
-  const int nk = kb_one * (MODE == DGRAD2 ? 2 : 1);
   auto issue = [&](int k, int st) {
     const bool second = MODE == DGRAD2 && k >= kb_one;
     const int kb = second ? k - kb_one : k;
-    const auto rw = second ? rw1 : rw0;
-    const auto rx = second ? rx1 : rx0;
-    uint8_t* const dst = lds + st * MID_STAGE;
+    const auto rw = gep::rsrc(second ? wb1 : wb0, wbytes);
+    const auto rx = gep::rsrc(second ? xb1 : xb0, xbytes);
+    uint8_t* const dst = lds + st * S::STAGE;
     const int left = K - kb * BK;
-    static_for<0, 4>([&](auto i) {
+    auto load = [&](auto i, const __amdgpu_buffer_rsrc_t& r, int row, uint8_t* to) {
       const int c = (i & 1) ? chunk ^ 4 : chunk;
-      int off = (wrow + 8 * i + (lane >> 3)) * K + 16 * c;
+      int off = (row + 8 * i + (lane >> 3)) * ld + 16 * c;
       if (TAIL && 16 * c >= left) off = static_cast<int>(gep::OOB);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void*)(dst + MID_A + (4 * wave + i) * 1024), 16, off, kb * BK, 0, 0);
-    });
-    static_for<0, 2>([&](auto i) {
-      const int c = (i & 1) ? chunk ^ 4 : chunk;
-      int off = (16 * wave + 8 * i + (lane >> 3)) * K + 16 * c;
-      if (TAIL && 16 * c >= left) off = static_cast<int>(gep::OOB);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_void*)(dst + (2 * wave + i) * 1024), 16, off, kb * BK, 0, 0);
-    });
-    if (wave == 0) {
-      const float* sc = (second ? p.a1s : p.a0s) + static_cast<long long>(kb) * p.n + m0;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(gep::rsrc(sc, 4LL * (p.n - m0)), (lds_void*)(dst + MID_A + MID_B), 4,
-                                               4 * lane, 0, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)to, 16, off, kb * BK, 0, 0);
+    };
+    static_for<0, 4>([&](auto i) { load(i, rw, wrow, dst + S::A + (4 * wave + i) * 1024); });
+    static_for<0, BM / 32>([&](auto i) { load(i, rx, BM / 4 * wave, dst + (BM / 32 * wave + i) * 1024); });
+    if (wave < BM / 64) {
+      const float* sc = (second ? xs1 : xs0) + static_cast<long long>(kb) * xpitch;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(gep::rsrc(sc, 4LL * xrows), (lds_void*)(dst + S::SA + 256 * wave), 4,
+                                               4 * (64 * wave + lane), 0, 0, 0);
+    }
+    if (WG && wave >= 2) {
+      const float* sc = p.b0s + static_cast<long long>(t.k_begin / BK + kb) * N + t.n0;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(gep::rsrc(sc, 4LL * (N - t.n0)), (lds_void*)(dst + S::SB + 256 * (wave - 2)),
+                                               4, 4 * (64 * (wave - 2) + lane), 0, 0, 0);
     }
   };
-  Tile t{};
-  t.e = e;
   float w0 = 0.f, w1 = 0.f;                        // weight scales: lane l holds K block l's
-  f32x4 acc[2][4];
+  f32x4 acc[NF][4];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < NF; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  issue(0, 0);
+  if (nk > 0) issue(0, 0);
+  const uint32_t base = lds_addr(lds);
   const uint32_t kc0 = kc_off(lane & 15, lane >> 4), kc1 = kc_off(lane & 15, 4 + (lane >> 4));
-  const uint32_t b_off = MID_A + (MODE == FWD1 ? 2048 : 4096) * wave;
+  const uint32_t a_off = 8192 * wm, b_off = S::A + (MODE == FWD1 ? 1024 : 2048) * NF * wn;
+  const uint32_t sa_off = S::SA + 4 * (64 * wm + (lane & 15)), sb_off = S::SB + 4 * (16 * NF * wn + 4 * (lane >> 4));
   for (int k = 0; k < nk; ++k) {
-    const bool second = MODE == DGRAD2 && k >= kb_one;
-    const int kb = second ? k - kb_one : k;
-    if ((kb & 63) == 0) {
-      w0 = weight_scale<MODE>(p, t, n0, second ? 1 : 0, kb);
-      if constexpr (MODE == FWD1) w1 = weight_scale<MODE>(p, t, n0, 1, kb);
+    float ws0 = 1.f, ws1 = 1.f;
+    if constexpr (!WG) {
+      const bool second = MODE == DGRAD2 && k >= kb_one;
+      const int kb = second ? k - kb_one : k;
+      if ((kb & 63) == 0) {
+        w0 = weight_scale<MODE>(p, t, t.n0, second ? 1 : 0, kb);
+        if constexpr (MODE == FWD1) w1 = weight_scale<MODE>(p, t, t.n0, 1, kb);
+      }
+      ws0 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(w0), kb & 63));
+      if constexpr (MODE == FWD1) ws1 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(w1), kb & 63));
     }
-    const float ws0 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(w0), kb & 63));
-    const float ws1 = MODE == FWD1 ? __int_as_float(__builtin_amdgcn_readlane(__float_as_int(w1), kb & 63)) : ws0;
     asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
     if (k + 1 < nk) issue(k + 1, (k + 1) & 1);
-    const uint32_t so = base + (k & 1) * MID_STAGE;
+    const uint32_t so = base + (k & 1) * S::STAGE;
     i32x8 fa[4], fb[2];
-    float sa[4];
+    float sa[4], ca[4], cb[4];
+    f32x4 sb[2], sp = {0.f, 0.f, 0.f, 0.f}, tmp[4];
     static_for<0, 4>([&](auto j) {
-      read_frag<j>(fa[j], so + kc0, so + kc1);
-      ds_f32<64 * j>(sa[j], so + MID_A + MID_B + 4 * (lane & 15));
+      read_frag<j>(fa[j], so + a_off + kc0, so + a_off + kc1);
+      ds_f32<64 * j>(sa[j], so + sa_off);
     });
-    read_frag<0>(fb[0], so + b_off + kc0, so + b_off + kc1);
-    read_frag<MODE == FWD1 ? 4 : 1>(fb[1], so + b_off + kc0, so + b_off + kc1);
-    wait_col<2>(fb[0]);
-    wait_rows<2>(fa, sa);
-    f32x4 tmp[2][4];
-    static_for<0, 4>([&](auto j) { tmp[0][j] = mfma_block(fb[0], fa[j]); });
-    wait_col<0>(fb[1]);
-    static_for<0, 4>([&](auto j) { tmp[1][j] = mfma_block(fb[1], fa[j]); });
-    static_for<0, 2>([&](auto i) {
+    // FWD1: fragments below NF / 2 are the gate's, the others the up matrix's (64 rows on)
+    auto col_frag = [&](auto i) {
+      constexpr int q = MODE == FWD1 && i >= NF / 2 ? i - NF / 2 + 4 : i;
+      read_frag<q>(fb[i & 1], so + b_off + kc0, so + b_off + kc1);
+      if constexpr (WG) ds_f128<64 * i>(sb[i & 1], so + sb_off);
+    };
+    col_frag(std::integral_constant<int, 0>{});
+    static_for<0, NF>([&](auto i) {
+      constexpr int c = i & 1;
+      if constexpr (i + 1 < NF) col_frag(std::integral_constant<int, i + 1>{});
+      constexpr int after = i + 1 < NF ? (WG ? 3 : 2) : 0;
+      if constexpr (WG) wait_col<after>(fb[c], sb[c]);
+      else wait_col<after>(fb[c]);
+      if constexpr (i == 0) {
+        wait_rows<after>(fa, sa);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          ca[j] = WG ? sa[j] : sa[j] * ws0;
+          cb[j] = MODE == FWD1 ? sa[j] * ws1 : 0.f;
+        }
+      }
+      auto add = [&](auto ii, auto j) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float w = WG ? sp[e] * sa[j] : (MODE == FWD1 && ii >= NF / 2 ? cb[j] : ca[j]);
+          acc[ii][j][e] = fmaf(tmp[j][e], w, acc[ii][j][e]);
+        }
+      };
       static_for<0, 4>([&](auto j) {
-        const float c = sa[j] * (i ? ws1 : ws0);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) acc[i][j][q] = fmaf(tmp[i][j][q], c, acc[i][j][q]);
+        if constexpr (i > 0) add(std::integral_constant<int, i - 1>{}, j);
+        tmp[j] = mfma_block(fb[c], fa[j]);
+        __builtin_amdgcn_sched_barrier(0);
       });
+      if constexpr (WG) sp = sb[c];
+      if constexpr (i == NF - 1) static_for<0, 4>([&](auto j) { add(i, j); });
     });
   }
+  const int row0 = t.m0 + 64 * wm;
+  uint16_t* o0 = p.o0;
+  long long out_rows = p.n;
+  if constexpr (WG) {
+    out_rows = t.m_end;
+    o0 = (MODE == WGRAD_GU && t.half ? p.o1 : p.o0) + static_cast<long long>(t.e) * out_rows * N;
+  }
+  if constexpr (BM == 64) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int r = m0 + 16 * j + (lane & 15);
-    if (r >= m_end) continue;
-    const int col = n0 + (MODE == FWD1 ? 16 : 32) * wave + 4 * (lane >> 4);
-    const long long at = static_cast<long long>(r) * N + col;
-    if (col < N) store4<MODE>(p, at, acc[0][j], acc[1][j]);
-    if (MODE != FWD1 && col + 16 < N) store4<MODE>(p, at + 16, acc[1][j], acc[1][j]);
+    for (int j = 0; j < 4; ++j) {
+      const int r = row0 + 16 * j + (lane & 15);
+      if (r >= t.m_end) continue;
+      const int col = t.n0 + (MODE == FWD1 ? 16 : 32) * wn + 4 * (lane >> 4);
+      const long long at = static_cast<long long>(r) * N + col;
+      if (col < N) store4<MODE>(p, at, acc[0][j], acc[1][j]);
+      if (MODE != FWD1 && col + 16 < N) store4<MODE>(p, at + 16, acc[1][j], acc[1][j]);
+    }
+  } else {
+    // staged through 4 KiB per wave of the stages, which every wave is done with
+    using gep::u32x2;
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    const uint32_t stg = base + 4096 * wave;
+    const int rows_valid = t.m_end - row0;
+    if constexpr (MODE == FWD1) {
+      const int col0 = t.n0 + 32 * wn, cv = N - col0;
+      auto store = [&](uint16_t* out, auto&& val) {
+        u32x2 v[4][2];
+        gep::sfor<0, 4>([&](auto j) { gep::sfor<0, 2>([&](auto i) { v[j][i] = val(i, j); }); });
+        gep::stage_out_round<2, 4>(v, std::integral_constant<int, 0>{}, gep::out_rsrc(out, out_rows, N, row0, col0), rows_valid,
+                                   cv, N, stg, lane);
+      };
+      if (p.o0 != nullptr) {
+        store(p.o0, [&](auto i, auto j) { return gep::pack4(acc[i][j]); });
+        store(p.o1, [&](auto i, auto j) { return gep::pack4(acc[i + 2][j]); });
+      }
+      store(p.o2, [&](auto i, auto j) {
+        f32x4 av;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) av[e] = acc[i][j][e] * gep::sigmoid(acc[i][j][e]) * acc[i + 2][j][e];
+        return gep::pack4(av);
+      });
+    } else {
+      const int col0 = t.n0 + 64 * wn, cv = N - col0;
+      auto store = [&](auto q, uint16_t* out, const u32x2 (&v)[2][4]) {
+        gep::stage_out_round<4, 2>(v, q, gep::out_rsrc(out, out_rows, N, row0, col0), rows_valid, cv, N, stg, lane);
+      };
+      if constexpr (MODE == DGRAD1) {
+        // G and U straight into the product's layout (8 bytes of a row per lane), all rows' loads first
+        gep::sfor<0, 2>([&](auto q) {
+          u32x2 gm[2][4], um[2][4];
+          const auto rg = gep::out_rsrc(p.g, p.n, N, row0, col0), ru = gep::out_rsrc(p.u, p.n, N, row0, col0);
+          gep::sfor<0, 2>([&](auto jj) {
+            gep::sfor<0, 4>([&](auto i) {
+              const int rr = 16 * (2 * q + jj) + (lane & 15), cc = 16 * i + 4 * (lane >> 4);
+              const int off = rr < rows_valid && cc < cv ? (rr * N + cc) * 2 : static_cast<int>(gep::OOB);
+              gm[jj][i] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rg, off, 0, 0));
+              um[jj][i] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(ru, off, 0, 0));
+            });
+          });
+          gep::sfor<0, 2>([&](auto jj) {
+            gep::sfor<0, 4>([&](auto i) {
+              const u32x2 g2 = gm[jj][i], u2 = um[jj][i];
+              const float gv[4] = {bf16_lo(g2.x), bf16_hi(g2.x), bf16_lo(g2.y), bf16_hi(g2.y)};
+              const float uv[4] = {bf16_lo(u2.x), bf16_hi(u2.x), bf16_lo(u2.y), bf16_hi(u2.y)};
+              f32x4 dg, du;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float da = acc[i][2 * q + jj][e], sg = gep::sigmoid(gv[e]);
+                dg[e] = da * uv[e] * sg * (1.0f + gv[e] * (1.0f - sg));
+                du[e] = da * gv[e] * sg;
+              }
+              gm[jj][i] = gep::pack4(dg);
+              um[jj][i] = gep::pack4(du);
+            });
+          });
+          store(q, p.o0, gm);
+          store(q, p.o1, um);
+        });
+      } else {
+        gep::sfor<0, 2>([&](auto q) {
+          u32x2 v[2][4];
+          gep::sfor<0, 2>([&](auto jj) { gep::sfor<0, 4>([&](auto i) { v[jj][i] = gep::pack4(acc[i][2 * q + jj]); }); });
+          store(q, o0, v);
+        });
+      }
+    }
   }
 }
 
-template <int MODE, bool TAIL>
-__global__ __launch_bounds__(256, 3) void grouped_mid_fp8b_kernel(Params p) {
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * MID_STAGE];
-  grouped_mid<MODE, TAIL>(p, lds);
+template <int MODE, int BM, bool TAIL>
+__global__ __launch_bounds__(256, Small<BM>::PER_CU) void grouped_small_fp8b_kernel(Params p) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * Small<BM>::STAGE];
+  grouped_small<MODE, BM, TAIL>(p, lds);
 }
 
-template <int MODE>
-int launch_mid(const Params& p, hipStream_t s) {
-  const int K = k_one<MODE>(p.d, p.f), tc = MODE == FWD1 ? 64 : MID_BN;
-  const long long blocks = (static_cast<long long>(p.n / MID_BM) + std::min(p.n, p.E)) * ((n_total<MODE>(p.d, p.f) + tc - 1) / tc);
+template <int MODE, int BM>
+int launch_small(const Params& p, hipStream_t s) {
+  const int K = k_one<MODE>(p.d, p.f), tc = MODE == FWD1 ? SM_BN / 2 : SM_BN;
+  const long long nt = (n_total<MODE>(p.d, p.f) + tc - 1) / tc;
+  const long long blocks =
+      is_wgrad(MODE) ? static_cast<long long>(p.E) * ((m_total<MODE>(p.d, p.f) + BM - 1) / BM) * (MODE == WGRAD_GU ? 2 : 1) * nt
+                     : (static_cast<long long>(p.n / BM) + std::min(p.n, p.E)) * nt;
   MOE_REQUIRE(blocks < (1LL << 31) - 8, MOE_ERR_UNSUPPORTED, "too many tiles");
-  MOE_REQUIRE(static_cast<long long>(K) * MID_BN < 0x7fffffffLL, MOE_ERR_UNSUPPORTED, "rows too long");
+  MOE_REQUIRE((is_wgrad(MODE) ? static_cast<long long>(p.P) : K) * SM_BN < 0x7fffffffLL, MOE_ERR_UNSUPPORTED, "rows too long");
   const unsigned g = static_cast<unsigned>((blocks + 7) / 8 * 8);
-  if (K % BK != 0) grouped_mid_fp8b_kernel<MODE, true><<<g, 256, 0, s>>>(p);
-  else grouped_mid_fp8b_kernel<MODE, false><<<g, 256, 0, s>>>(p);
-  return check_launch("grouped_gemm_fp8b (64-row tiles)");
+  if (!is_wgrad(MODE) && K % BK != 0) grouped_small_fp8b_kernel<MODE, BM, !is_wgrad(MODE)><<<g, 256, 0, s>>>(p);
+  else grouped_small_fp8b_kernel<MODE, BM, false><<<g, 256, 0, s>>>(p);
+  return check_launch("grouped_gemm_fp8b (small tiles)");
 }
 
-// Which form runs a product over rows, from host-visible sizes (the row counts stay on the device).
+// Which form runs a product, from host-visible sizes (the row counts stay on the device).
 //   few rows:  forward products of at most 6 rows per expert on average.  Measured (64 experts, d 2048, f
 //              1024, gate/up + down, us; 64-row tiles in brackets): 1 row 36 + 19 [37 + 18], 4 rows 48 + 29
 //              [56 + 33], 16 rows 73 + 39 [56 + 33]; one token of 8 experts at d 7168, f 2048 43 + 25 [57 + 24].
-//   else whichever of the two tilings the estimate below says is faster: both run a number of rounds of tiles
-//   over the compute units, and a 256-row tile costs more per round than 64-row tiles of the same work but
-//   streams fewer bytes, so few or ragged rounds go to the small tiles.  Per tile, measured over KB = K / 128
-//   steps: 1.9 KB + 10 us (256 rows), 0.4 KB + 1.3 us per 64-row tile of three sharing a unit, and at least
-//   0.65 KB + 3 us for one alone.  Measured on both sides of the choice (gate/up + down, us, 256-row tiles
-//   first): 64 experts, d 7168, f 2048, 64 rows each 519 + 269, 431 + 228; 128 rows 530 + 275, 567 + 291;
-//   16 experts, d 2112, f 1344, 256 rows 74 + 30, 55 + 30; 1024 rows 143 + 74, 165 + 92; one expert, d = f =
-//   4096, 256 rows 54 + 47, 22 + 21.
-// MOE_FP8B_FORM = few, mid or big sets the form (tests run every form on the same cases).
-enum Form { FEW, MID, BIG };
+//   else the tiling with the lowest estimate: rounds of tiles over the compute units, each KB = K / 128 steps
+//   and an epilogue.  Bigger tiles move fewer bytes per product and cost less per output; smaller ones leave
+//   less of the last round empty.  Fitted in us to runs of 1 to 128 experts, d and f 512 to 7168, 64 to 8192
+//   rows per expert, which it reproduces within some 20%: 256 rows 1.9 KB + 10 per tile (25 with the SwiGLU
+//   backward's epilogue, 2.1 KB + 9.7 for weight gradients), 128 rows 0.57 KB + 3.4 (7; 2.8) per tile, 64
+//   rows 0.46 KB + 1.5 (2), and a tile alone on its unit at least 0.7 KB + 4 or 0.65 KB + 3.  Measured on
+//   both sides of the choice (gate/up + down, us, 64- / 128- / 256-row tiles): 64 experts, d 2048, f 1024,
+//   1024 rows each 507 + 301 / 425 + 244 / 371 + 210; 16 experts, d 2112, f 1344, 64 rows 31 + 15 / 28 + 19 /
+//   38 + 26, 512 rows 91 + 50 / 74 + 43 / 75 + 48; one expert, d = f = 4096, 1024 rows 55 + 28 / 43 + 30 /
+//   60 + 52; weight gradients of 16 experts, d 2112, f 1344, 250 rows: 128-row tiles 34 + 62, 256-row 40 + 67.
+// MOE_FP8B_FORM = few, mid, half or big sets the form (tests run every form on the same cases).
+enum Form { FEW, MID, HALF, BIG };
 template <int MODE>
 Form choose_form(const Params& p) {
+  constexpr bool WG = is_wgrad(MODE), FORWARD = MODE == FWD1 || MODE == FWD2;
   if (const char* env = getenv("MOE_FP8B_FORM")) {
-    if (!strcmp(env, "few") && (MODE == FWD1 || MODE == FWD2)) return FEW;
-    if (!strcmp(env, "mid") || !strcmp(env, "few")) return MID;
+    if (!strcmp(env, "few") && FORWARD) return FEW;
+    if (!strcmp(env, "mid") || !strcmp(env, "few")) return WG ? HALF : MID;
+    if (!strcmp(env, "half")) return HALF;
     if (!strcmp(env, "big")) return BIG;
   }
-  if ((MODE == FWD1 || MODE == FWD2) && p.n <= 6LL * p.E) return FEW;
-  const double kb = static_cast<double>(fp8b_blocks(k_one<MODE>(p.d, p.f))) * (MODE == DGRAD2 ? 2 : 1);
+  if (FORWARD && p.n <= 6LL * p.E) return FEW;
   const double busy = std::min(p.n, p.E), mean = p.n / busy;
+  const double kb = WG ? std::ceil(mean / BK) : static_cast<double>(fp8b_blocks(k_one<MODE>(p.d, p.f))) * (MODE == DGRAD2 ? 2 : 1);
   const int N = n_total<MODE>(p.d, p.f), cus = cu_count();
-  auto rounds = [&](int bm, int cols) {            // an expert's last row tile is half full on average
-    const double mt = mean <= 0.84 * bm ? busy : static_cast<double>(p.n) / bm + 0.5 * busy;
+  auto rounds = [&](int bm, int cols) {
+    double mt;
+    if (WG) mt = busy * ((m_total<MODE>(p.d, p.f) + bm - 1) / bm) * (MODE == WGRAD_GU ? 2 : 1);
+    else if (p.E == 1) mt = (p.n + bm - 1) / bm;
+    else mt = mean <= 0.84 * bm ? busy : static_cast<double>(p.n) / bm + 0.5 * busy;   // a last tile half full
     return std::ceil(mt * ((N + cols - 1) / cols) / cus);
   };
-  const double big = rounds(BM, n_tile_width<MODE>()) * (1.9 * kb + 10.0);
-  const double mid = std::max(rounds(MID_BM, MODE == FWD1 ? 64 : MID_BN) * (0.4 * kb + 1.3), 0.65 * kb + 3.0);
-  return mid < big ? MID : BIG;
+  const int cols = MODE == FWD1 ? SM_BN / 2 : SM_BN;
+  const double big = rounds(BM, n_tile_width<MODE>()) * (WG ? 2.1 * kb + 9.7 : 1.9 * kb + (MODE == DGRAD1 ? 25.0 : 10.0));
+  const double half = std::max(rounds(128, cols) * (0.57 * kb + (WG ? 2.8 : MODE == DGRAD1 ? 7.0 : 3.4)), 0.7 * kb + 4.0);
+  const double mid = WG ? half + 1.0 : std::max(rounds(64, cols) * (0.46 * kb + (MODE == DGRAD1 ? 2.0 : 1.5)), 0.65 * kb + 3.0);
+  return mid < half && mid < big ? MID : half < big ? HALF : BIG;
 }
 
 template <int MODE>
@@ -989,7 +1182,11 @@ int launch_rows(const Params& p, hipStream_t s) {
   if constexpr (MODE == FWD1 || MODE == FWD2) {
     if (form == FEW) return launch_skinny<MODE>(p, s);
   }
-  return form == MID ? launch_mid<MODE>(p, s) : launch<MODE>(p, s);
+  if (form == HALF) return launch_small<MODE, 128>(p, s);
+  if constexpr (!is_wgrad(MODE)) {
+    if (form == MID) return launch_small<MODE, 64>(p, s);
+  }
+  return launch<MODE>(p, s);
 }
 
 int check_gemm(int E, int n, int d, int f, const int32_t* offsets) {
@@ -1075,7 +1272,7 @@ extern "C" int moe_grouped_gemm_wgrad_down_fp8b(int E, int n, int d, int f, cons
   p.P = moe_mx_pad_cap(n, E);
   MOE_REQUIRE(p.P > 0, MOE_ERR_UNSUPPORTED, "padded token axis too long");
   p.a0 = dyT; p.a0s = dyTs; p.b0 = aT; p.b0s = aTs; p.o0 = dw_down;
-  return g8b::launch<g8b::WGRAD_DOWN>(p, as_stream(stream));
+  return g8b::launch_rows<g8b::WGRAD_DOWN>(p, as_stream(stream));
 }
 
 extern "C" int moe_grouped_gemm_wgrad_gate_up_fp8b(int E, int n, int d, int f, const int32_t* offsets,
@@ -1091,5 +1288,5 @@ extern "C" int moe_grouped_gemm_wgrad_gate_up_fp8b(int E, int n, int d, int f, c
   p.P = moe_mx_pad_cap(n, E);
   MOE_REQUIRE(p.P > 0, MOE_ERR_UNSUPPORTED, "padded token axis too long");
   p.a0 = dgT; p.a0s = dgTs; p.a1 = duT; p.a1s = duTs; p.b0 = xT; p.b0s = xTs; p.o0 = dw_gate; p.o1 = dw_up;
-  return g8b::launch<g8b::WGRAD_GU>(p, as_stream(stream));
+  return g8b::launch_rows<g8b::WGRAD_GU>(p, as_stream(stream));
 }

@@ -174,9 +174,9 @@ PRODUCTS = [
 IDS = [f"{i}-{d}-{f}" for i, (_, d, f) in enumerate(PRODUCTS)]
 
 
-@pytest.fixture(params=["", "few", "mid", "big"])
+@pytest.fixture(params=["", "few", "mid", "half", "big"])
 def form(request, monkeypatch):
-    """The library's own choice of kernel, and each of the three that it chooses from."""
+    """The library's own choice of kernel, and each of the four that it chooses from."""
     if request.param:
         monkeypatch.setenv("MOE_FP8B_FORM", request.param)
     return request.param
@@ -275,12 +275,12 @@ def test_dgrad_products(counts, d, f, form):
 
 
 @pytest.mark.parametrize("counts,d,f", PRODUCTS, ids=IDS)
-def test_wgrad_products(counts, d, f):
+def test_wgrad_products(counts, d, f, form):
     from expert_ffn_layer_top_amd import ops
     c = Case(counts, d, f, seed=2)
     dy, dyv = c.tokens(d)
     a, av = c.tokens(f)
-    note(f"wgrad_down_fp8b n={c.n} E={c.E} d={d} f={f}")
+    note(f"wgrad_down_fp8b {form} n={c.n} E={c.E} d={d} f={f}")
     dwd = ops.grouped_gemm_wgrad_down_fp8b(*dy, *a, c.offsets, c.offsets_pad, c.n)
     ref, size, lsize = fp8b.grouped_tn(dyv, av, c.off)
     K = max(counts)
@@ -288,7 +288,7 @@ def test_wgrad_products(counts, d, f):
     dg, dgv = c.tokens(f)
     du, duv = c.tokens(f)
     x, xv = c.tokens(d)
-    note(f"wgrad_gate_up_fp8b n={c.n} E={c.E} d={d} f={f}")
+    note(f"wgrad_gate_up_fp8b {form} n={c.n} E={c.E} d={d} f={f}")
     dwg, dwu = ops.grouped_gemm_wgrad_gate_up_fp8b(*dg, *du, *x, c.offsets, c.offsets_pad, c.n)
     for got, left in ((dwg, dgv), (dwu, duv)):
         ref, size, lsize = fp8b.grouped_tn(left, xv, c.off)
