@@ -14,6 +14,9 @@ in both contraction directions; router, combine,
 permute-backward and route-backward stay bf16/fp32.  Its combine backward is the fused producer
 (unpermute_combine_bwd_mx): dYexp leaves as MXFP8 row blocks and per-row gates, and the grouped
 token blocks of dYexp are rebuilt from dy and those gates, so the bf16 dYexp is never written.
+Block-128 E4M3 (fp8b=True: one fp32 scale per block of 128, 128 x 128 for weights) runs the same six
+products; each bf16 tensor that two products need is quantised in both layouts from one read.
+The router is softmax over all experts and top-k, or with `router` the scored one (ScoredRouter).
 
 Every step is a library call on the current stream; this module only sequences them and holds
 the tensors one step passes to the next.  ([news] "Ai2 rebuilds Olmo's training stack ...",
@@ -26,6 +29,18 @@ from dataclasses import dataclass, field
 import torch
 
 from . import ops
+
+
+@dataclass
+class ScoredRouter:
+    """The arguments of ops.route_scored: scores, balance bias, groups of experts, gates."""
+    score: str = "sigmoid"
+    bias: torch.Tensor = None            # [E] fp32, added for the choice alone
+    n_group: int = 1
+    topk_group: int = 1
+    group_top: int = 1
+    renormalize: bool = True
+    scale: float = 1.0
 
 
 @dataclass
@@ -64,6 +79,18 @@ class Weights:
             return self.quantize_mx()
         return self.mx
 
+    def quantize_fp8b(self, transposed=True):
+        """Block-128 copies of the expert weights: (codes, scales) of each, and of each transposed for
+        the backward (`*_t`), from one read.  `forward` takes them as fp8b=; whoever keeps them makes them
+        again after a weight changed."""
+        q = {}
+        for name, w in (("wg", self.w_gate), ("wu", self.w_up), ("wd", self.w_down)):
+            codes, scales, *t = ops.fp8b_quantize_weights(w, want_transposed=transposed)
+            q[name] = codes, scales
+            if transposed:
+                q[name + "_t"] = tuple(t)
+        return q
+
 
 class _Span:
     """Records an optional (start, end) torch.cuda.Event pair on the current stream around one
@@ -93,6 +120,7 @@ RECOMPUTE_CALL = "recompute"
 ROUTER_CALLS = ("router", "router_bwd")
 QUANT_CALLS_FWD = ("quant_a",)
 QUANT_CALLS = ("quant_dg", "quant_du", "quant_dyT", "quant_xT")
+# (block-128: "quant_dy" gives dYexp's row blocks and token blocks from one read, in place of quant_dyT)
 ROW_CALLS = ("route", "permute", "combine", "combine_bwd", "permute_bwd", "route_bwd")
 # MXFP8: each expert's rows start at a multiple of MX_PAD on the padded token axis of the
 # weight-gradient operands.  128 = one K step of those products: every step's 128-byte piece of an
@@ -102,7 +130,7 @@ MX_PAD = 128
 
 
 def forward(x, weights, k, logits=None, mxfp8=False, want_probs=False, events=None, recompute=False,
-            balance_weight=None):
+            balance_weight=None, fp8b=None, router=None, serving=False):
     """Layer forward.  x [T, d] bf16; logits [T, E] fp32 unless weights.w_r is given.
     Returns the context dict that `backward` consumes (all intermediate tensors), with y.
     events: optional {name: (start, end)} of torch.cuda.Event pairs, recorded on the current
@@ -116,20 +144,51 @@ def forward(x, weights, k, logits=None, mxfp8=False, want_probs=False, events=No
     (Weights.mx_current), so an optimizer step between two forwards is always seen.
     balance_weight: also compute the router's load-balancing score and the balance statistics of
     the actual load (ctx["balance"]: p_mean [E], stats [aux, load_max, prob_max, load_cv]), and
-    add the gradient of balance_weight * aux to d_logits in the backward."""
-    ctx = dict(x=x, k=k, mxfp8=mxfp8, balance_weight=balance_weight)
+    add the gradient of balance_weight * aux to d_logits in the backward.
+    fp8b: the expert products run on block-128 E4M3 operands.  True quantises the weights in this
+    forward; the copies of Weights.quantize_fp8b in its place are used as they are (serving, or
+    several micro-batches between two optimizer steps).
+    router: a ScoredRouter to choose and weigh the experts with (without balance_weight and
+    want_probs: its bias balances the load).
+    serving: a forward that no backward follows; block-128 products only, which then write neither
+    G nor U, make no token blocks of A and need no transposed copies of the weights."""
+    if mxfp8 and fp8b:
+        raise ValueError("mxfp8 and fp8b are two formats of the same products: choose one")
+    if serving and (not fp8b or recompute):
+        raise ValueError("serving is a form of the block-128 products (fp8b), without recompute")
+    if router is not None and (balance_weight is not None or want_probs):
+        raise ValueError("balance_weight and want_probs belong to the softmax router, not to a ScoredRouter")
+    ctx = dict(x=x, k=k, mxfp8=mxfp8, balance_weight=balance_weight, router=router, serving=serving)
     want_probs = want_probs or balance_weight is not None
     if logits is None:
         with _Span(events, "router"):
             logits = ops.router_project(x, weights.w_r)
     ctx["logits"] = logits
     with _Span(events, "route"):
-        r = ops.route_topk(logits, k, want_probs=want_probs, pad=MX_PAD if mxfp8 else None)
+        pad = MX_PAD if mxfp8 or fp8b else None
+        if router is None:
+            r = ops.route_topk(logits, k, want_probs=want_probs, pad=pad)
+        else:
+            r = ops.route_scored(logits, k, pad=pad, **vars(router))
     ctx.update(r)
     if balance_weight is not None:
         p_mean, stats = ops.route_balance(r["probs"], r["counts"], k)
         ctx["balance"] = dict(p_mean=p_mean, stats=stats)
-    if not mxfp8:
+    if fp8b:
+        q = weights.quantize_fp8b(transposed=not serving) if fp8b is True else fp8b
+        ctx["fp8b_weights"] = q          # the backward uses the copies this forward used
+        with _Span(events, "permute"):
+            ctx["xq"] = xq = ops.fp8b_quantize_rows(x, dest=r["dest"])
+        with _Span(events, "gate_up"):
+            g, u, a = ops.grouped_gemm_gate_up_fp8b(*xq, r["offsets"], *q["wg"], *q["wu"], want_gu=not (serving or recompute))
+        with _Span(events, "quant_a"):
+            if serving:
+                aq, as_ = ops.fp8b_quantize_rows(a)
+            else:
+                aq, as_, *ctx["aT"] = ops.fp8b_quantize_rows_grouped(a, r["offsets"], r["offsets_pad"])
+        with _Span(events, "down"):
+            yexp = ops.grouped_gemm_down_fp8b(aq, as_, r["offsets"], *q["wd"])
+    elif not mxfp8:
         with _Span(events, "permute"):
             xp = ops.permute(x, r["dest"])
         ctx["xp"] = xp
@@ -175,7 +234,10 @@ def backward(ctx, weights, dy, events=None):
     gradients right after the combine backward, the permute backward right after the product
     that writes dXp), so its input is still in the last-level cache; the arithmetic does not
     depend on the order."""
+    if ctx.get("serving"):
+        raise ValueError("this forward was run for serving: it kept nothing for a backward")
     out = {}
+    fp8b = "fp8b_weights" in ctx
     with _Span(events, "combine_bwd"):
         if not ctx["mxfp8"]:
             dyexp, dgate = ops.unpermute_combine_bwd(dy, ctx["yexp"], ctx["topk_gate"], ctx["dest"])
@@ -189,7 +251,12 @@ def backward(ctx, weights, dy, events=None):
         bal = None
         if ctx.get("balance_weight") is not None:
             bal = (ctx["probs"], ctx["counts"], ctx["balance_weight"])
-        out["d_logits"] = ops.route_topk_bwd(ctx["topk_gate"], ctx["topk_idx"], dgate, E, balance=bal)
+        router = ctx.get("router")
+        if router is None:
+            out["d_logits"] = ops.route_topk_bwd(ctx["topk_gate"], ctx["topk_idx"], dgate, E, balance=bal)
+        else:
+            out["d_logits"] = ops.route_scored_bwd(ctx["logits"], ctx["topk_idx"], dgate, score=router.score,
+                                                   renormalize=router.renormalize, scale=router.scale)
     if weights.w_r is not None:
         with _Span(events, "router_bwd"):
             _, out["dw_r"] = ops.router_project_bwd(ctx["x"], weights.w_r, out["d_logits"], want_dx=False)
@@ -204,13 +271,38 @@ def backward(ctx, weights, dy, events=None):
     if g is None:
         # activation recompute: the forward's gate/up product again (same kernel, same inputs)
         with _Span(events, RECOMPUTE_CALL):
-            if not ctx["mxfp8"]:
+            if fp8b:
+                q = ctx["fp8b_weights"]
+                g, u, a = ops.grouped_gemm_gate_up_fp8b(*ctx["xq"], off, *q["wg"], *q["wu"])
+            elif not ctx["mxfp8"]:
                 g, u, a = ops.grouped_gemm_gate_up(ctx["xp"], off, weights.w_gate, weights.w_up)
             else:
                 q = ctx["mx_weights"]
                 g, u, a = ops.grouped_gemm_gate_up(ctx["xpq"], off, q["wg"], q["wu"],
                                                    scales=(ctx["xps"], q["wg_s"], q["wu_s"]))
-    if not ctx["mxfp8"]:
+    if fp8b:
+        # every operand in blocks of 128 along its product's contraction: rows for the dgrads, tokens of one
+        # expert for the weight gradients, both from one read
+        q, pad, n = ctx["fp8b_weights"], ctx["offsets_pad"], g.shape[0]
+        with _Span(events, "quant_dy"):
+            dyq, dys, dyT, dyTs = ops.fp8b_quantize_rows_grouped(dyexp, off, pad)
+        with _Span(events, "dgrad_down"):
+            dg, du = ops.grouped_gemm_dgrad_down_fp8b(dyq, dys, off, *q["wd_t"], g, u)
+        with _Span(events, "wgrad_down"):
+            dw_down = ops.grouped_gemm_wgrad_down_fp8b(dyT, dyTs, *ctx["aT"], off, pad, n)
+        with _Span(events, "quant_dg"):
+            dgq, dgs, dgT, dgTs = ops.fp8b_quantize_rows_grouped(dg, off, pad)
+        with _Span(events, "quant_du"):
+            duq, dus, duT, duTs = ops.fp8b_quantize_rows_grouped(du, off, pad)
+        with _Span(events, "dgrad_gate_up"):
+            dxp = ops.grouped_gemm_dgrad_gate_up_fp8b(dgq, dgs, duq, dus, off, *q["wg_t"], *q["wu_t"])
+        with _Span(events, "permute_bwd"):
+            out["dx"] = permute_bwd(dxp)
+        with _Span(events, "quant_xT"):
+            _, _, xT, xTs = ops.fp8b_quantize_rows_grouped(ctx["x"], off, pad, row_token=ctx["row_token"], want_rows=False)
+        with _Span(events, "wgrad_gate_up"):
+            dw_gate, dw_up = ops.grouped_gemm_wgrad_gate_up_fp8b(dgT, dgTs, duT, duTs, xT, xTs, off, pad, n)
+    elif not ctx["mxfp8"]:
         with _Span(events, "dgrad_down"):
             dg, du = ops.grouped_gemm_dgrad_down(dyexp, off, weights.w_down, g, u)
         with _Span(events, "wgrad_down"):

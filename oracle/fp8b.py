@@ -124,16 +124,3 @@ def grouped_tn(left, right, offsets):
         size[e] = np.abs(left[r]).T @ np.abs(right[r])
         largest[e] = _largest_by_eight(left[r].T, right[r].T)
     return out, size, largest
-
-
-def layer_forward(x, routed, w_gate, w_up, w_down):
-    """Expert forward of bf16-valued x through block-128 operands; `routed`: dest, offsets, topk_gate."""
-    dest, offsets = routed["dest"], routed["offsets"]
-    xp = moe.permute(x, dest)
-    xd = row_values(*quantize_rows(xp))
-    g, _, _ = grouped_nt(xd, weight_values(*quantize_weights(w_gate)), offsets)
-    u, _, _ = grouped_nt(xd, weight_values(*quantize_weights(w_up)), offsets)
-    a = codecs.bf16_to_f64(codecs.f64_to_bf16(moe.silu(g) * u))
-    yexp, _, _ = grouped_nt(row_values(*quantize_rows(a)), weight_values(*quantize_weights(w_down)), offsets)
-    yexp = codecs.bf16_to_f64(codecs.f64_to_bf16(yexp))
-    return dict(xp=xp, g=g, u=u, a=a, yexp=yexp, y=moe.combine(yexp, routed["topk_gate"], dest))
