@@ -2,11 +2,11 @@
 and gradients to fp32 accuracy.
 
 Tolerances.  Gates are computed in 64 bits and rounded to fp32 once: at most 2^-24 of the value (2^-23
-allows the 64-bit steps).  Only the softmax's sum over all experts, by which its gates are divided when they
+allows the 64-bit steps), or, below 2^-126, where fp32 values are the multiples of 2^-149, half of that step.  Only the softmax's sum over all experts, by which its gates are divided when they
 are not renormalised, is made of fp32 exponentials: one of x = l - max is off by (|x| + 1) 2^-23 of itself
 (its argument is rounded twice, the exponential by a unit), on average over the sum at most (ln E + 1) 2^-23
-since the softmax's mean of |x| is at most its entropy; adding 4 per lane over 6 levels rounds 9 times by
-2^-24; with ln 256 = 5.6 that is less than 12 * 2^-23.  A gradient is g (ds - sum g ds) or s (1 - s) ds in fp32: exponentials are off by
+since the softmax's mean of |x| is at most its entropy; adding 4 per lane over 6 levels, or 16 as
+a tree over 4, rounds at most 9 times by 2^-24; with ln 256 = 5.6 that is less than 12 * 2^-23.  A gradient is g (ds - sum g ds) or s (1 - s) ds in fp32: exponentials are off by
 a few units plus the rounding of their argument (2^-24 of |l - max|, at most 2^-24 * 32 for the logits
 here), sums run over at most 256 terms in a tree of 10 levels, so every term is off by less than 64 * 2^-24
 of the sum of magnitudes that enters it.  The oracle multiplies by a whole Jacobian in 64 bits, whose at
@@ -49,7 +49,7 @@ def _check_forward(logits, k, bias, out, pad=128, **kw):
     assert np.array_equal(host(out["topk_idx"]), idx)
     got = host(out["topk_gate"]).astype(np.float64)
     units = 13 if kw.get("score") == "softmax" and not kw.get("renormalize", True) else 1
-    assert np.all(np.abs(got - gate) <= units * 2.0 ** -23 * np.abs(gate))
+    assert np.all(np.abs(got - gate) <= units * 2.0 ** -23 * np.abs(gate) + 2.0 ** -149)
     meta = moe.route_metadata(idx, E, pad=pad)
     for name, want in zip(("counts", "offsets", "dest", "row_token", "offsets_pad"), meta):
         assert np.array_equal(host(out[name]), want), name
@@ -88,6 +88,48 @@ def test_absent_experts_ties_and_infinities(score):
             note(f"route_scored edges {kw} bias={b is not None}")
             out = ops.route_scored(f32_to_dev(logits), 4, bias=None if b is None else f32_to_dev(b), pad=128, **kw)
             _check_forward(logits, 4, b, out, **kw)
+
+
+# shapes of every form of the choice from fp32 scores (no score output, more than 64 tokens): 4, 8 or 16 experts
+# per lane with whole lanes per group, experts that fill no last lane or no vector load, groups of odd sizes
+FAST = [
+    # E, k, n_group, topk_group, group_top, score, bias
+    (256, 8, 8, 4, 2, "sigmoid", True), (256, 16, 16, 16, 1, "softmax", True), (256, 1, 16, 3, 2, "softmax", False),
+    (200, 11, 1, 1, 1, "sigmoid", True), (130, 16, 1, 1, 1, "softmax", False), (128, 8, 16, 5, 2, "sigmoid", False),
+    (72, 9, 9, 2, 2, "softmax", True), (65, 7, 1, 1, 1, "sigmoid", True), (64, 6, 2, 1, 2, "sigmoid", True),
+    (48, 4, 12, 3, 1, "softmax", True), (33, 16, 1, 1, 1, "softmax", True), (16, 16, 4, 4, 2, "sigmoid", True),
+    (5, 5, 1, 1, 1, "sigmoid", False), (1, 1, 1, 1, 1, "softmax", True),
+    (160, 6, 8, 3, 2, "sigmoid", True), (96, 4, 96, 7, 1, "sigmoid", True), (255, 10, 5, 2, 2, "softmax", True),
+]
+
+
+@pytest.mark.parametrize("E,k,n_group,topk_group,group_top,score,bias", FAST)
+def test_choice_of_many_tokens(E, k, n_group, topk_group, group_top, score, bias):
+    from expert_ffn_layer_top_amd import ops
+    _, logits, b = _inputs(333, E, 7, bias)
+    kw = dict(score=score, n_group=n_group, topk_group=topk_group, group_top=group_top)
+    note(f"route_scored many E={E} k={k} {kw} bias={bias}")
+    out = ops.route_scored(f32_to_dev(logits), k, bias=None if b is None else f32_to_dev(b), pad=128, **kw)
+    assert out["scores"] is None
+    _check_forward(logits, k, b, out, **kw)
+
+
+@pytest.mark.parametrize("E,k,n_group,topk_group,group_top,score,bias", FAST)
+def test_choice_of_many_tokens_with_absent_experts_ties_and_infinities(E, k, n_group, topk_group, group_top, score, bias):
+    from expert_ffn_layer_top_amd import ops
+    rng = np.random.default_rng([13, E])
+    inf, nan, top = np.inf, np.nan, np.finfo(np.float32).max
+    kinds = [np.array(v, np.float32) for v in
+             ([0.0], [-0.0, 0.0], [-inf], [nan], [inf], [-top], [top, -inf], [0.0, -inf, nan], [1.0, 2.0], [1e-40, -1e-40, 0.0],
+              [-200.0, -201.0], [inf, 0.0, -inf], [90.0, -90.0], [nan, 0.5, 0.5, 0.25])]
+    logits = np.stack([rng.choice(kinds[t % len(kinds)], E) for t in range(7 * len(kinds))])
+    logits[::5, E // 2] = -inf
+    some = np.array([0.0, 0.0, 0.0, 1.0, 0.5, -inf, nan, 1e30, inf], np.float32)
+    b = rng.choice(some, E) if bias else None
+    kw = dict(score=score, n_group=n_group, topk_group=topk_group, group_top=group_top)
+    note(f"route_scored many edges E={E} k={k} {kw} bias={bias}")
+    out = ops.route_scored(f32_to_dev(logits), k, bias=None if b is None else f32_to_dev(b), pad=128, **kw)
+    _check_forward(logits, k, b, out, **kw)
 
 
 def test_choice_next_to_ties_is_made_in_64_bits():
