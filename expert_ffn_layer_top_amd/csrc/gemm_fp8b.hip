@@ -277,10 +277,12 @@ __device__ __forceinline__ void read_frag(i32x8& v, uint32_t a0, uint32_t a1) {
 
 // Waits until at most N LDS reads are outstanding and ties the registers that have then landed.
 template <int N>
-__device__ __forceinline__ void wait_rows(i32x8 (&a)[4], float (&sa)[4]) {
-  asm volatile("s_waitcnt lgkmcnt(%8)"
-               : "+v"(a[0]), "+v"(a[1]), "+v"(a[2]), "+v"(a[3]), "+v"(sa[0]), "+v"(sa[1]), "+v"(sa[2]), "+v"(sa[3])
-               : "n"(N));
+__device__ __forceinline__ void wait_first(i32x8& b, i32x8& a) {
+  asm volatile("s_waitcnt lgkmcnt(%2)" : "+v"(b), "+v"(a) : "n"(N));
+}
+template <int N>
+__device__ __forceinline__ void wait_scales(float (&s)[4]) {
+  asm volatile("s_waitcnt lgkmcnt(%4)" : "+v"(s[0]), "+v"(s[1]), "+v"(s[2]), "+v"(s[3]) : "n"(N));
 }
 template <int N>
 __device__ __forceinline__ void wait_col(i32x8& b) {
@@ -293,6 +295,63 @@ __device__ __forceinline__ void wait_col(i32x8& b, f32x4& sb) {
 
 __device__ __forceinline__ f32x4 mfma_block(const i32x8& x, const i32x8& y) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+}
+
+// One K step of a wave: 64 rows (four fragments at a0, a1) by NF column fragments (at b0, b1; FWD1: the first
+// half are the gate's, the others the up matrix's, from fragment UP on), its scaled block sums added to acc.
+// `next` issues all loads of the step after, behind the first MFMAs (spread over the step, 5% more time: the
+// last of them had an eighth of it to arrive).
+template <int MODE, int NF, int UP, class F>
+__device__ __forceinline__ void multiply_step(f32x4 (&acc)[NF][4], uint32_t a0, uint32_t a1, uint32_t b0, uint32_t b1,
+                                              uint32_t sa_at, uint32_t sb_at, float ws0, float ws1, F&& next) {
+  constexpr bool WG = is_wgrad(MODE);
+  i32x8 fa[4], fb[2];
+  float sa[4], ca[4], cb[4];
+  f32x4 sb[3], tmp[4];               // sb: column scales of the fragments i - 1 (whose sums are in tmp), i and i + 1
+  auto col_frag = [&](auto i) {
+    constexpr int q = MODE == FWD1 && i >= NF / 2 ? i - NF / 2 + UP : i;
+    read_frag<q>(fb[i & 1], b0, b1);
+    if constexpr (WG && i > 0) ds_f128<64 * i>(sb[i % 3], sb_at);
+  };
+  // reads return in order: the first MFMA starts on the first two fragments, the others follow as they come
+  col_frag(std::integral_constant<int, 0>{});
+  static_for<0, 4>([&](auto j) { read_frag<j>(fa[j], a0, a1); });
+  static_for<0, 4>([&](auto j) { ds_f32<64 * j>(sa[j], sa_at); });
+  if constexpr (WG) ds_f128<0>(sb[0], sb_at);
+  static_for<0, NF>([&](auto i) {
+    constexpr int after = i + 1 < NF ? (WG ? 3 : 2) : 0;     // reads of the next fragment
+    if constexpr (i + 1 < NF) col_frag(std::integral_constant<int, i + 1>{});
+    if constexpr (i > 0) {
+      if constexpr (WG) wait_col<after>(fb[i & 1], sb[i % 3]);
+      else wait_col<after>(fb[i & 1]);
+    }
+    if constexpr (i == 1) {
+      wait_scales<after>(sa);
+      if constexpr (WG) asm volatile("" : "+v"(sb[0]));       // has landed with them
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        ca[j] = WG ? sa[j] : sa[j] * ws0;
+        cb[j] = MODE == FWD1 ? sa[j] * ws1 : 0.f;
+      }
+    }
+    // a block sum enters the running sum just before its register takes the next fragment's, three MFMAs after
+    // its own was issued
+    auto add = [&](auto ii, auto j) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float w = WG ? sb[ii % 3][e] * sa[j] : (MODE == FWD1 && ii >= NF / 2 ? cb[j] : ca[j]);
+        acc[ii][j][e] = fmaf(tmp[j][e], w, acc[ii][j][e]);
+      }
+    };
+    static_for<0, 4>([&](auto j) {
+      if constexpr (i > 0) add(std::integral_constant<int, i - 1>{}, j);
+      if constexpr (i == 0) wait_first<after + (WG ? 5 : 4) + 2 * (3 - j)>(fb[0], fa[j]);
+      tmp[j] = mfma_block(fb[i & 1], fa[j]);
+      __builtin_amdgcn_sched_barrier(0);   // the compiler would pull the FMAs up to their MFMA and wait there
+      if constexpr (i == 0 && j == 3) { next(); __builtin_amdgcn_sched_barrier(0); }
+    });
+    if constexpr (i == NF - 1) static_for<0, 4>([&](auto j) { add(i, j); });
+  });
 }
 
 // Writes the tile's results, staged through this wave's 8 KiB of the stage just consumed.
@@ -519,55 +578,9 @@ __device__ __forceinline__ void grouped_gemm(const Params& p) {
       const uint32_t so = ring + st * OP_BYTES, sso = ring + st * SC_BYTES;
       const uint32_t fa0 = so + a_off + kc0, fa1 = so + a_off + kc1, fb0 = so + b_off + kc0, fb1 = so + b_off + kc1;
       uint8_t* const dst = dst0 + (st ^ 1) * OP_BYTES;
-      i32x8 fa[4], fb[2];
-      float sa[4], ca[4], cb[4];
-      f32x4 sb[2], tmp[4];
-      f32x4 sp = {0.f, 0.f, 0.f, 0.f};   // column scales of the fragment whose sums are in tmp
-      // FWD1: column fragments 0-3 are the gate's rows of this wave, 4-7 the up matrix's (128 rows on)
-      auto bq = [](auto i) { return std::integral_constant<int, MODE == FWD1 && i >= 4 ? i + 4 : i>{}; };
-      static_for<0, 4>([&](auto j) {
-        read_frag<j>(fa[j], fa0, fa1);
-        ds_f32<64 * j>(sa[j], sso + sa_off);
-      });
-      read_frag<0>(fb[0], fb0, fb1);
-      if constexpr (WG) ds_f128<0>(sb[0], sso + sb_off);
-      static_for<0, 8>([&](auto i) {
-        constexpr int c = i & 1;
-        if constexpr (i == 0) {
-          if (WG || !role_b) issue_scales(ns, sdst0 + (st ^ 1) * SC_BYTES);
-        }
-        issue(i, ns, dst);
-        if constexpr (i < 7) {
-          read_frag<bq(std::integral_constant<int, i + 1>{}).value>(fb[c ^ 1], fb0, fb1);
-          if constexpr (WG) ds_f128<64 * (i + 1)>(sb[c ^ 1], sso + sb_off);
-        }
-        constexpr int after = i < 7 ? (WG ? 3 : 2) : 0;
-        if constexpr (WG) wait_col<after>(fb[c], sb[c]);
-        else wait_col<after>(fb[c]);
-        if constexpr (i == 0) {
-          wait_rows<after>(fa, sa);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            ca[j] = WG ? sa[j] : sa[j] * ws0;
-            cb[j] = MODE == FWD1 ? sa[j] * ws1 : 0.f;
-          }
-        }
-        // a block sum enters the running sum just before its register takes the next fragment's, three
-        // MFMAs after its own was issued
-        auto add = [&](auto ii, auto j) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float w = WG ? sp[e] * sa[j] : (MODE == FWD1 && ii >= 4 ? cb[j] : ca[j]);
-            acc[ii][j][e] = fmaf(tmp[j][e], w, acc[ii][j][e]);
-          }
-        };
-        static_for<0, 4>([&](auto j) {
-          if constexpr (i > 0) add(std::integral_constant<int, i - 1>{}, j);
-          tmp[j] = mfma_block(fb[c], fa[j]);
-          __builtin_amdgcn_sched_barrier(0);   // the compiler would pull the FMAs up to their MFMA and wait there
-        });
-        if constexpr (WG) sp = sb[c];
-        if constexpr (i == 7) static_for<0, 4>([&](auto j) { add(i, j); });
+      multiply_step<MODE, 8, 8>(acc, fa0, fa1, fb0, fb1, sso + sa_off, sso + sb_off, ws0, ws1, [&]() {
+        if (WG || !role_b) issue_scales(ns, sdst0 + (st ^ 1) * SC_BYTES);
+        static_for<0, 8>([&](auto i) { issue(i, ns, dst); });
       });
       st ^= 1;
       ++kt;
@@ -977,51 +990,11 @@ __device__ __forceinline__ void grouped_small(const Params& p, uint8_t* lds) {
       if constexpr (MODE == FWD1) ws1 = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(w1), kb & 63));
     }
     asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
-    if (k + 1 < nk) issue(k + 1, (k + 1) & 1);
     const uint32_t so = base + (k & 1) * S::STAGE;
-    i32x8 fa[4], fb[2];
-    float sa[4], ca[4], cb[4];
-    f32x4 sb[2], sp = {0.f, 0.f, 0.f, 0.f}, tmp[4];
-    static_for<0, 4>([&](auto j) {
-      read_frag<j>(fa[j], so + a_off + kc0, so + a_off + kc1);
-      ds_f32<64 * j>(sa[j], so + sa_off);
-    });
-    // FWD1: fragments below NF / 2 are the gate's, the others the up matrix's (64 rows on)
-    auto col_frag = [&](auto i) {
-      constexpr int q = MODE == FWD1 && i >= NF / 2 ? i - NF / 2 + 4 : i;
-      read_frag<q>(fb[i & 1], so + b_off + kc0, so + b_off + kc1);
-      if constexpr (WG) ds_f128<64 * i>(sb[i & 1], so + sb_off);
-    };
-    col_frag(std::integral_constant<int, 0>{});
-    static_for<0, NF>([&](auto i) {
-      constexpr int c = i & 1;
-      if constexpr (i + 1 < NF) col_frag(std::integral_constant<int, i + 1>{});
-      constexpr int after = i + 1 < NF ? (WG ? 3 : 2) : 0;
-      if constexpr (WG) wait_col<after>(fb[c], sb[c]);
-      else wait_col<after>(fb[c]);
-      if constexpr (i == 0) {
-        wait_rows<after>(fa, sa);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          ca[j] = WG ? sa[j] : sa[j] * ws0;
-          cb[j] = MODE == FWD1 ? sa[j] * ws1 : 0.f;
-        }
-      }
-      auto add = [&](auto ii, auto j) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float w = WG ? sp[e] * sa[j] : (MODE == FWD1 && ii >= NF / 2 ? cb[j] : ca[j]);
-          acc[ii][j][e] = fmaf(tmp[j][e], w, acc[ii][j][e]);
-        }
-      };
-      static_for<0, 4>([&](auto j) {
-        if constexpr (i > 0) add(std::integral_constant<int, i - 1>{}, j);
-        tmp[j] = mfma_block(fb[c], fa[j]);
-        __builtin_amdgcn_sched_barrier(0);
-      });
-      if constexpr (WG) sp = sb[c];
-      if constexpr (i == NF - 1) static_for<0, 4>([&](auto j) { add(i, j); });
-    });
+    multiply_step<MODE, NF, 4>(acc, so + a_off + kc0, so + a_off + kc1, so + b_off + kc0, so + b_off + kc1, so + sa_off,
+                               so + sb_off, ws0, ws1, [&]() {
+                                 if (k + 1 < nk) issue(k + 1, (k + 1) & 1);
+                               });
   }
   const int row0 = t.m0 + 64 * wm;
   uint16_t* o0 = p.o0;
@@ -1139,14 +1112,16 @@ int launch_small(const Params& p, hipStream_t s) {
 //              [56 + 33], 16 rows 73 + 39 [56 + 33]; one token of 8 experts at d 7168, f 2048 43 + 25 [57 + 24].
 //   else the tiling with the lowest estimate: rounds of tiles over the compute units, each KB = K / 128 steps
 //   and an epilogue.  Bigger tiles move fewer bytes per product and cost less per output; smaller ones leave
-//   less of the last round empty.  Fitted in us to runs of 1 to 128 experts, d and f 512 to 7168, 64 to 8192
-//   rows per expert, which it reproduces within some 20%: 256 rows 1.9 KB + 10 per tile (25 with the SwiGLU
-//   backward's epilogue, 2.1 KB + 9.7 for weight gradients), 128 rows 0.57 KB + 3.4 (7; 2.8) per tile, 64
-//   rows 0.46 KB + 1.5 (2), and a tile alone on its unit at least 0.7 KB + 4 or 0.65 KB + 3.  Measured on
-//   both sides of the choice (gate/up + down, us, 64- / 128- / 256-row tiles): 64 experts, d 2048, f 1024,
-//   1024 rows each 507 + 301 / 425 + 244 / 371 + 210; 16 experts, d 2112, f 1344, 64 rows 31 + 15 / 28 + 19 /
-//   38 + 26, 512 rows 91 + 50 / 74 + 43 / 75 + 48; one expert, d = f = 4096, 1024 rows 55 + 28 / 43 + 30 /
-//   60 + 52; weight gradients of 16 experts, d 2112, f 1344, 250 rows: 128-row tiles 34 + 62, 256-row 40 + 67.
+//   less of the last round empty.  A tile of K blocks takes, in us: 256 rows 1.5 K + 6.5 (23 with the SwiGLU
+//   backward's epilogue, 1.75 K + 6 for weight gradients), 128 rows 0.64 K + 3 (7.6; 0.72 K + 2.6), 64 rows
+//   0.4 K + 2 (4); a unit's share of the tiles counts as whole rounds, and half a round more than the share
+//   for the persistent 256-row kernel, whose units drift apart.  Fitted to 1 to 128 experts, d and f 512 to
+//   7168, 64 to 8192 rows per expert, where the choice costs 1% over the best form on average, 20% at worst.
+//   Both sides of it (gate/up + down, us, 64- / 128- / 256-row tiles): 64 experts, d 2048, f 1024, 128 rows
+//   each 101 + 47 / 109 + 55 / 86 + 44, 1024 rows 531 + 314 / 438 + 253 / 348 + 191; 16 experts, d 2112, f 1344,
+//   64 rows 31 + 15 / 27 + 18 / 37 + 24, 250 rows 52 + 30 / 48 + 29 / 41 + 26; one expert, d = f = 4096, 1024
+//   rows 60 + 30 / 43 + 30 / 59 + 50, 4096 rows 203 + 97 / 160 + 79 / 122 + 61; weight gradients of 16 experts,
+//   d 2112, f 1344, 64 rows 128-row tiles 28 + 52, 256-row 27 + 41.
 // MOE_FP8B_FORM = few, mid, half or big sets the form (tests run every form on the same cases).
 enum Form { FEW, MID, HALF, BIG };
 template <int MODE>
@@ -1162,17 +1137,19 @@ Form choose_form(const Params& p) {
   const double busy = std::min(p.n, p.E), mean = p.n / busy;
   const double kb = WG ? std::ceil(mean / BK) : static_cast<double>(fp8b_blocks(k_one<MODE>(p.d, p.f))) * (MODE == DGRAD2 ? 2 : 1);
   const int N = n_total<MODE>(p.d, p.f), cus = cu_count();
-  auto rounds = [&](int bm, int cols) {
+  auto tiles = [&](int bm, int cols) {           // per unit
     double mt;
     if (WG) mt = busy * ((m_total<MODE>(p.d, p.f) + bm - 1) / bm) * (MODE == WGRAD_GU ? 2 : 1);
     else if (p.E == 1) mt = (p.n + bm - 1) / bm;
     else mt = mean <= 0.84 * bm ? busy : static_cast<double>(p.n) / bm + 0.5 * busy;   // a last tile half full
-    return std::ceil(mt * ((N + cols - 1) / cols) / cus);
+    return mt * ((N + cols - 1) / cols) / cus;
   };
   const int cols = MODE == FWD1 ? SM_BN / 2 : SM_BN;
-  const double big = rounds(BM, n_tile_width<MODE>()) * (WG ? 2.1 * kb + 9.7 : 1.9 * kb + (MODE == DGRAD1 ? 25.0 : 10.0));
-  const double half = std::max(rounds(128, cols) * (0.57 * kb + (WG ? 2.8 : MODE == DGRAD1 ? 7.0 : 3.4)), 0.7 * kb + 4.0);
-  const double mid = WG ? half + 1.0 : std::max(rounds(64, cols) * (0.46 * kb + (MODE == DGRAD1 ? 2.0 : 1.5)), 0.65 * kb + 3.0);
+  const double tb = tiles(BM, n_tile_width<MODE>());
+  const double big = (tb <= 1.0 ? 1.0 : tb + 0.5) * (WG ? 1.75 * kb + 6.0 : 1.5 * kb + (MODE == DGRAD1 ? 23.0 : 6.5));
+  const double half = std::ceil(tiles(128, cols)) * (WG ? 0.72 * kb + 2.6 : 0.64 * kb + (MODE == DGRAD1 ? 7.6 : 3.0)) - 1.5;
+  if (WG) return half < big ? HALF : BIG;
+  const double mid = std::ceil(tiles(64, cols)) * (0.4 * kb + (MODE == DGRAD1 ? 4.0 : 2.0)) + 2.5;
   return mid < half && mid < big ? MID : half < big ? HALF : BIG;
 }
 
