@@ -297,11 +297,32 @@ __device__ __forceinline__ f32x4 mfma_block(const i32x8& x, const i32x8& y) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
 }
 
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+// 8 codes of a fragment (dwords 2 I and 2 I + 1) as bf16.
+template <int I>
+__device__ __forceinline__ bf16x8 codes_bf16(const i32x8& v) {
+  const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[2 * I], 1.0f, false);
+  const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[2 * I], 1.0f, true);
+  const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[2 * I + 1], 1.0f, false);
+  const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[2 * I + 1], 1.0f, true);
+  return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// The same block sums, exact to fp32: every E4M3 value is a bf16 one, and the bf16 matrix core keeps what the fp8
+// one cuts off beside a larger product (rms error of a sum 2^-27 of its size instead of 2^-16).
+__device__ __forceinline__ f32x4 exact_block(const i32x8& x, const i32x8& y) {
+  f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+  static_for<0, 4>([&](auto h) { sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes_bf16<h>(x), codes_bf16<h>(y), sum, 0, 0, 0); });
+  return sum;
+}
+
 // One K step of a wave: 64 rows (four fragments at a0, a1) by NF column fragments (at b0, b1; FWD1: the first
 // half are the gate's, the others the up matrix's, from fragment UP on), its scaled block sums added to acc.
 // `next` issues all loads of the step after, behind the first MFMAs (spread over the step, 5% more time: the
 // last of them had an eighth of it to arrive).
-template <int MODE, int NF, int UP, class F>
+template <int MODE, int NF, int UP, bool EXACT, class F>
 __device__ __forceinline__ void multiply_step(f32x4 (&acc)[NF][4], uint32_t a0, uint32_t a1, uint32_t b0, uint32_t b1,
                                               uint32_t sa_at, uint32_t sb_at, float ws0, float ws1, F&& next) {
   constexpr bool WG = is_wgrad(MODE);
@@ -346,7 +367,7 @@ __device__ __forceinline__ void multiply_step(f32x4 (&acc)[NF][4], uint32_t a0, 
     static_for<0, 4>([&](auto j) {
       if constexpr (i > 0) add(std::integral_constant<int, i - 1>{}, j);
       if constexpr (i == 0) wait_first<after + (WG ? 5 : 4) + 2 * (3 - j)>(fb[0], fa[j]);
-      tmp[j] = mfma_block(fb[i & 1], fa[j]);
+      tmp[j] = EXACT ? exact_block(fb[i & 1], fa[j]) : mfma_block(fb[i & 1], fa[j]);
       __builtin_amdgcn_sched_barrier(0);   // the compiler would pull the FMAs up to their MFMA and wait there
       if constexpr (i == 0 && j == 3) { next(); __builtin_amdgcn_sched_barrier(0); }
     });
@@ -578,7 +599,7 @@ __device__ __forceinline__ void grouped_gemm(const Params& p) {
       const uint32_t so = ring + st * OP_BYTES, sso = ring + st * SC_BYTES;
       const uint32_t fa0 = so + a_off + kc0, fa1 = so + a_off + kc1, fb0 = so + b_off + kc0, fb1 = so + b_off + kc1;
       uint8_t* const dst = dst0 + (st ^ 1) * OP_BYTES;
-      multiply_step<MODE, 8, 8>(acc, fa0, fa1, fb0, fb1, sso + sa_off, sso + sb_off, ws0, ws1, [&]() {
+      multiply_step<MODE, 8, 8, false>(acc, fa0, fa1, fb0, fb1, sso + sa_off, sso + sb_off, ws0, ws1, [&]() {
         if (WG || !role_b) issue_scales(ns, sdst0 + (st ^ 1) * SC_BYTES);
         static_for<0, 8>([&](auto i) { issue(i, ns, dst); });
       });
@@ -720,6 +741,7 @@ __device__ __forceinline__ bool find_group(const int32_t* __restrict__ offsets, 
 // wave only), D K steps ahead and together with the rows' codes and scales (loads return in order, so what
 // is used together is loaded together).  The 4 waves of a workgroup split the contraction KS ways, summed in
 // wave order through LDS, where the columns alone make too few waves.
+// It has time to spare (4% of it), so its block sums are the exact ones, for the reason given at exact_rows.
 constexpr int SKINNY_ROWS = 16;
 
 struct SkinnyStep {
@@ -787,7 +809,7 @@ __device__ __forceinline__ void grouped_skinny(const Params& p) {
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
               const float sw = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(w ? ws1 : ws0), kb - base));
-              const f32x4 t = mfma_block(s[i].w[w], s[i].x);
+              const f32x4 t = exact_block(s[i].w[w], s[i].x);
               const float c = sw * s[i].sx;
 #pragma unroll
               for (int q = 0; q < 4; ++q) acc[w][q] = fmaf(t[q], c, acc[w][q]);
@@ -858,7 +880,7 @@ struct Small {
   static constexpr int PER_CU = BM == 64 ? 3 : 2;
 };
 
-template <int MODE, int BM, bool TAIL>
+template <int MODE, int BM, bool TAIL, bool EXACT>
 __device__ __forceinline__ void grouped_small(const Params& p, uint8_t* lds) {
   constexpr bool WG = is_wgrad(MODE);
   using S = Small<BM>;
@@ -991,7 +1013,7 @@ __device__ __forceinline__ void grouped_small(const Params& p, uint8_t* lds) {
     }
     asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
     const uint32_t so = base + (k & 1) * S::STAGE;
-    multiply_step<MODE, NF, 4>(acc, so + a_off + kc0, so + a_off + kc1, so + b_off + kc0, so + b_off + kc1, so + sa_off,
+    multiply_step<MODE, NF, 4, EXACT>(acc, so + a_off + kc0, so + a_off + kc1, so + b_off + kc0, so + b_off + kc1, so + sa_off,
                                so + sb_off, ws0, ws1, [&]() {
                                  if (k + 1 < nk) issue(k + 1, (k + 1) & 1);
                                });
@@ -1085,13 +1107,13 @@ __device__ __forceinline__ void grouped_small(const Params& p, uint8_t* lds) {
   }
 }
 
-template <int MODE, int BM, bool TAIL>
+template <int MODE, int BM, bool TAIL, bool EXACT>
 __global__ __launch_bounds__(256, Small<BM>::PER_CU) void grouped_small_fp8b_kernel(Params p) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * Small<BM>::STAGE];
-  grouped_small<MODE, BM, TAIL>(p, lds);
+  grouped_small<MODE, BM, TAIL, EXACT>(p, lds);
 }
 
-template <int MODE, int BM>
+template <int MODE, int BM, bool EXACT = false>
 int launch_small(const Params& p, hipStream_t s) {
   const int K = k_one<MODE>(p.d, p.f), tc = MODE == FWD1 ? SM_BN / 2 : SM_BN;
   const long long nt = (n_total<MODE>(p.d, p.f) + tc - 1) / tc;
@@ -1101,8 +1123,8 @@ int launch_small(const Params& p, hipStream_t s) {
   MOE_REQUIRE(blocks < (1LL << 31) - 8, MOE_ERR_UNSUPPORTED, "too many tiles");
   MOE_REQUIRE((is_wgrad(MODE) ? static_cast<long long>(p.P) : K) * SM_BN < 0x7fffffffLL, MOE_ERR_UNSUPPORTED, "rows too long");
   const unsigned g = static_cast<unsigned>((blocks + 7) / 8 * 8);
-  if (!is_wgrad(MODE) && K % BK != 0) grouped_small_fp8b_kernel<MODE, BM, !is_wgrad(MODE)><<<g, 256, 0, s>>>(p);
-  else grouped_small_fp8b_kernel<MODE, BM, false><<<g, 256, 0, s>>>(p);
+  if (!is_wgrad(MODE) && K % BK != 0) grouped_small_fp8b_kernel<MODE, BM, !is_wgrad(MODE), EXACT><<<g, 256, 0, s>>>(p);
+  else grouped_small_fp8b_kernel<MODE, BM, false, EXACT><<<g, 256, 0, s>>>(p);
   return check_launch("grouped_gemm_fp8b (small tiles)");
 }
 
@@ -1153,11 +1175,32 @@ Form choose_form(const Params& p) {
   return mid < half && mid < big ? MID : half < big ? HALF : BIG;
 }
 
+// A, dG and dU are quantised again by whoever uses them.  Where one is rounded to bf16 the other way at the
+// largest value of a block, the block's scale moves by 2^-8 and some 5% of its codes by a step, 2% of its sum; the
+// fp8 matrix core's cut does that to one block in 200.  Among many blocks it takes y from 0.17% (its own rounding)
+// to 0.21% off, but one such block in 32 to 0.4%.  So a product of fewer than 2048 blocks has exact block sums:
+// above, twice the expected number of moved blocks still leaves y within one and a half times its rounding.
+// They cost (gate/up, us, 64-row tiles of the two kinds and the kernel of few rows): 16 experts, d 2112, f 1344, 16
+// rows each 17 / 28 / 18; one expert, d = f = 4096, 16 rows 18 / 29 / 13, 64 rows 19 / 31 / 26; 8 experts, d 7168,
+// f 2048, 16 rows 41 / 57 / 41, 30 rows 41 / 58 / 79.
+template <int MODE>
+bool exact_rows(const Params& p) {
+  return (MODE == FWD1 || MODE == DGRAD1) && p.n * static_cast<long long>(fp8b_blocks(p.f)) < 2048 &&
+         getenv("MOE_FP8B_FORM") == nullptr;
+}
+
 template <int MODE>
 int launch_rows(const Params& p, hipStream_t s) {
   const Form form = choose_form<MODE>(p);
   if constexpr (MODE == FWD1 || MODE == FWD2) {
     if (form == FEW) return launch_skinny<MODE>(p, s);
+  }
+  if constexpr (MODE == FWD1 || MODE == DGRAD1) {
+    if (exact_rows<MODE>(p)) {
+      if constexpr (MODE == FWD1)
+        if (p.n <= 16LL * p.E) return launch_skinny<MODE>(p, s);
+      return launch_small<MODE, 64, true>(p, s);
+    }
   }
   if (form == HALF) return launch_small<MODE, 128>(p, s);
   if constexpr (!is_wgrad(MODE)) {

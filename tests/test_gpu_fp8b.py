@@ -402,3 +402,27 @@ def test_streams_and_replayed_graph(form):
         torch.cuda.synchronize()
         for p, q, r in zip(want, captured, again):
             assert torch.equal(p, q) and torch.equal(p, r), replay
+
+
+@pytest.mark.parametrize("counts,d,f", PRODUCTS[:6] + [([30, 20], 256, 320)], ids=IDS[:6] + ["30-20"])
+def test_few_rows_have_exact_block_sums(counts, d, f):
+    """Products of few rows whose results are quantised again lose nothing in the matrix core: no `largest`."""
+    from expert_ffn_layer_top_amd import ops
+    c = Case(counts, d, f, seed=5)
+    x, xv = c.rows(d)
+    (wg, wgv), (wu, wuv) = c.weight(f, d), c.weight(f, d)
+    note(f"exact gate_up and dgrad_down n={c.n} E={c.E} d={d} f={f}")
+    g, u, a = ops.grouped_gemm_gate_up_fp8b(*x, c.offsets, *wg, *wu)
+    gr, gs, _ = fp8b.grouped_nt(xv, wgv, c.off)
+    ur, us, _ = fp8b.grouped_nt(xv, wuv, c.off)
+    eg, eu = sum_tol(gs, 0.0, d), sum_tol(us, 0.0, d)
+    assert_bf16(g, gr, eg, "g")
+    assert_bf16(u, ur, eu, "u")
+    assert_bf16(a, moe.silu(gr) * ur, silu_slack(gr, ur, eg, eu), "a")
+    gb, gv = c.bf16(f)
+    ub, uv = c.bf16(f)
+    dg, du = ops.grouped_gemm_dgrad_down_fp8b(*x, c.offsets, *wg, gb, ub)
+    off, s = sum_tol(gs, 0.0, d), 1 / (1 + np.exp(-gv))
+    kg, ku = uv * s * (1 + gv * (1 - s)), gv * s
+    assert_bf16(dg, gr * kg, off * np.abs(kg) + 16 * 2.0 ** -24 * np.abs(gr * uv) * (1 + np.abs(gv)), "dg")
+    assert_bf16(du, gr * ku, off * np.abs(ku) + 16 * 2.0 ** -24 * np.abs(gr * gv), "du")
