@@ -1,6 +1,6 @@
 // Device-scheduled grouped GEMMs of the SwiGLU expert FFN on E4M3 codes with one fp32 scale per block
 // of 128 along the contraction dimension, forward and backward, on the fp8 matrix cores
-// (v_mfma_f32_16x16x128_f8f6f4: one instruction contracts exactly one block).
+// (v_mfma_f32_16x16x128_f8f6f4: one instruction contracts exactly one block), or, for few rows, on the bf16 ones.
 //
 //   out[r][c] = sum over blocks b of  sa[b][r] * sb * sum over k in b of qa[r][k] qb[c][k]
 //
@@ -29,6 +29,13 @@
 // 64 + 16 (l / 16) .. + 15 of the step (any order serves, being the same for both operands); the product
 // takes columns from the first operand, so a lane ends with 4 consecutive columns of one row and
 // needs one row scale per 16 x 16 tile.
+//
+// Measured, 131072 rows of 64 experts, d 7168, f 2048: gate/up 4.0 ms, down 2.04 ms, 1.9 PFLOP/s each (a large
+// library fp8 product with one scale for all: 2.7 to 3.1).  What bounds it: the matrix core is busy 57% of the cycles
+// (a step takes some 3400 of them for 2048 of MFMAs; epilogues take 7% and 12% of the two products), and with random codes
+// power holds the clock near 1.7 GHz; with all codes zero gate/up takes 2.85 ms.  Taking out single parts of the work:
+// no epilogue 3.3, no FMAs 3.1, loads that always hit the first-level cache 3.0 ms.  Tried without gain: other cell
+// shapes (+-2%), a load that touches the lines of the step after next (10% slower), waiting fragment by fragment.
 #include <algorithm>
 #include <cmath>
 #include <cstdlib>
@@ -1129,9 +1136,10 @@ int launch_small(const Params& p, hipStream_t s) {
 }
 
 // Which form runs a product, from host-visible sizes (the row counts stay on the device).
-//   few rows:  forward products of at most 6 rows per expert on average.  Measured (64 experts, d 2048, f
-//              1024, gate/up + down, us; 64-row tiles in brackets): 1 row 36 + 19 [37 + 18], 4 rows 48 + 29
-//              [56 + 33], 16 rows 73 + 39 [56 + 33]; one token of 8 experts at d 7168, f 2048 43 + 25 [57 + 24].
+//   few rows:  forward products of at most 6 rows per expert on average.  Measured (gate/up + down with their
+//              quantisers and combine, weights not in the last-level cache, us; 64-row tiles in brackets): 64
+//              experts, d 2048, f 1024, 4 rows each 88 [101]; one token of 8 experts, d 4096, f 768 41 [51]; the
+//              first with 16 rows each, products alone, weights cached: 47 + 27 [34 + 26].
 //   else the tiling with the lowest estimate: rounds of tiles over the compute units, each KB = K / 128 steps
 //   and an epilogue.  Bigger tiles move fewer bytes per product and cost less per output; smaller ones leave
 //   less of the last round empty.  A tile of K blocks takes, in us: 256 rows 1.5 K + 6.5 (23 with the SwiGLU

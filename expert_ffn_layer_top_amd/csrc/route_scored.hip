@@ -15,7 +15,8 @@
 // us for 32768 tokens of 256 experts).  So a token is chosen from fp32 scores with a bound on their error,
 // and the few tokens (about 1 in 700 there) where two values that the choice separates are closer than the
 // bound are chosen again from 64-bit ones.  A gate is computed from its logit in 64 bits always, all of a
-// block's gates together.
+// block's gates together.  Measured for that batch, us: choice 21, gates and ranks 18, scan 4, rows 6; one token in
+// one launch 7.5; the gradient of 16384 tokens of 128 experts (softmax, not renormalised) 10.
 #include <algorithm>
 #include <cmath>
 
