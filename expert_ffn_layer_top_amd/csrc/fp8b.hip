@@ -42,6 +42,7 @@ __global__ __launch_bounds__(kRowThreads) void fp8b_rows_kernel(const uint16_t* 
   const int copies = PERMUTE ? k : 1;
   for (int j = 0; j < copies; ++j) {
     const long long r = PERMUTE ? dest[t * k + j] : t;
+    if (PERMUTE && static_cast<unsigned long long>(r) >= static_cast<unsigned long long>(n)) continue;   // no row of the buffers
     *reinterpret_cast<uint2*>(q + r * C + 8 * c) = o;
     if ((c & 15) == 0) s[(c >> 4) * n + r] = f.scale;
   }

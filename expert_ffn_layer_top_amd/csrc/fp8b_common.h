@@ -1,7 +1,8 @@
 // Block-128 E4M3 helpers (device).  A block's largest magnitude amax counts as at least 2^-100 (so an
 // all-zero block has finite factors), its codes are E4M3(v * inv) rounded to nearest even with
 // inv = 448 / amax rounded to fp32 (448: the largest E4M3 value), and its scale is amax * (1/448)
-// rounded to fp32; the value a code stands for is code * scale.
+// rounded to fp32; the value a code stands for is code * scale.  A block that holds an infinity (inv 0, scale
+// inf) or a NaN is NaN throughout.
 //
 // The product with inv is rounded to fp32 before it is rounded to E4M3's 4 significant bits; the first
 // rounding is off by at most 2^-24 of the value, so it moves only values that close to a border.
@@ -22,7 +23,8 @@ struct Fp8bScale {
 
 // From the magnitude bits of a block's bf16 amax.
 __device__ __forceinline__ Fp8bScale fp8b_scale(uint32_t amax_bits) {
-  const float amax = fmaxf(__uint_as_float(amax_bits << 16), 0x1p-100f);
+  float amax = __uint_as_float(amax_bits << 16);
+  amax = amax < 0x1p-100f ? 0x1p-100f : amax;      // (a NaN stays)
   return {448.0f / amax, amax * (1.0f / 448.0f)};
 }
 

@@ -152,6 +152,13 @@ def forward(x, weights, k, logits=None, mxfp8=False, want_probs=False, events=No
     want_probs: its bias balances the load).
     serving: a forward that no backward follows; block-128 products only, which then write neither
     G nor U, make no token blocks of A and need no transposed copies of the weights."""
+    if not (fp8b is None or fp8b is True or fp8b is False or isinstance(fp8b, dict)):
+        raise ValueError("fp8b must be True or the copies that Weights.quantize_fp8b returns")
+    fp8b = True if fp8b is True else fp8b if isinstance(fp8b, dict) else None
+    if fp8b is not None and fp8b is not True:
+        need = ("wg", "wu", "wd") if serving else ("wg", "wu", "wd", "wg_t", "wu_t", "wd_t")
+        if any(name not in fp8b for name in need):
+            raise ValueError(f"fp8b copies must hold {need} (without serving, quantize_fp8b(transposed=True))")
     if mxfp8 and fp8b:
         raise ValueError("mxfp8 and fp8b are two formats of the same products: choose one")
     if serving and (not fp8b or recompute):

@@ -158,6 +158,55 @@ def test_quantize_weights(E, R, C):
 
 # --------------------------------------------------------------------------------------- products
 
+def test_blocks_with_infinities_and_nans_are_nan():
+    """... throughout, in every layout, and no other block changes."""
+    from expert_ffn_layer_top_amd import ops
+    rng = np.random.default_rng(9)
+    counts, C = [130, 20], 192
+    off, offp = groups(counts)
+    _, v = rand_bf16(rng, 150, C)
+    bad = v.copy()
+    bad[3, 5], bad[140, 150], bad[129, 191] = np.nan, np.inf, -np.inf
+    x, y = (bf16_to_dev(codecs.f64_to_bf16(t)) for t in (v, bad))
+    o, op = i32_to_dev(off), i32_to_dev(offp)
+    note("fp8b infinities and nans")
+    rows = np.zeros((150, C), bool)
+    rows[3, :128] = rows[140, 128:] = rows[129, 128:] = True
+    for (q, s), (q0, s0) in ((ops.fp8b_quantize_rows(y), ops.fp8b_quantize_rows(x)),
+                             (ops.fp8b_quantize_rows_grouped(y, o, op)[:2], ops.fp8b_quantize_rows_grouped(x, o, op)[:2])):
+        with np.errstate(invalid="ignore"):
+            got = fp8b.row_values(host(q), host(s))
+        assert np.array_equal(np.isnan(got), rows)
+        assert np.array_equal(got[~rows], fp8b.row_values(host(q0), host(s0))[~rows])
+    _, _, qT, sT = ops.fp8b_quantize_rows_grouped(y, o, op)
+    _, _, q0, s0 = ops.fp8b_quantize_rows_grouped(x, o, op)
+    cols = np.zeros((150, C), bool)
+    cols[:128, 5] = cols[130:, 150] = cols[128:130, 191] = True
+    with np.errstate(invalid="ignore"):
+        got = fp8b.token_values(host(qT), host(sT), off, offp)
+    assert np.array_equal(np.isnan(got), cols)
+    assert np.array_equal(got[~cols], fp8b.token_values(host(q0), host(s0), off, offp)[~cols])
+    w = y[:128].reshape(1, 128, C).contiguous()
+    q, s, qT, sT = ops.fp8b_quantize_weights(w)
+    with np.errstate(invalid="ignore"):
+        got = fp8b.weight_values(host(q), host(s))[0]
+        got_t = fp8b.weight_values(host(qT), host(sT))[0]
+    assert np.isnan(got[:, :128]).all() and not np.isnan(got[:, 128:]).any() and np.array_equal(got, got_t.T, equal_nan=True)
+
+
+def test_destinations_outside_the_buffers_are_skipped():
+    from expert_ffn_layer_top_amd._lib import call
+    x = bf16_to_dev(rand_bf16(np.random.default_rng(1), 2, 64)[0])
+    dest = i32_to_dev([[1, -1], [4, 2]])
+    q = torch.full((4, 64), 77, dtype=torch.uint8, device=dev())
+    s = torch.full((1, 4), 7.0, dtype=torch.float32, device=dev())
+    note("fp8b destinations outside")
+    call("moe_fp8b_quantize_rows", x.data_ptr(), dest.data_ptr(), 2, 64, 2, q.data_ptr(), s.data_ptr(),
+         torch.cuda.current_stream().cuda_stream)
+    q, s = host(q), host(s)
+    assert (q[[0, 3]] == 77).all() and (s[0, [0, 3]] == 7.0).all() and (s[0, [1, 2]] != 7.0).all()
+
+
 PRODUCTS = [
     # counts per expert, d, f
     ([1], 128, 128),

@@ -16,6 +16,9 @@ def _args():
     (dict(serving=True), "serving"),
     (dict(serving=True, mxfp8=True), "serving"),
     (dict(serving=True, fp8b=True, recompute=True), "serving"),
+    (dict(fp8b="yes"), "quantize_fp8b"),
+    (dict(fp8b={}), "must hold"),
+    (dict(fp8b=dict(wg=0, wu=0, wd=0)), "transposed"),
     (dict(router=layer.ScoredRouter(), balance_weight=0.1), "balance_weight"),
     (dict(router=layer.ScoredRouter(), want_probs=True), "want_probs"),
 ], ids=str)
