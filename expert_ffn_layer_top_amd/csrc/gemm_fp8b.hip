@@ -415,13 +415,17 @@ __device__ __forceinline__ void epilogue(const Params& p, const Tile& t, f32x4 (
     const auto rg = gep::out_rsrc(p.g, p.n, p.f, row0, col0), ru = gep::out_rsrc(p.u, p.n, p.f, row0, col0);
     const auto rdg = gep::out_rsrc(p.o0, p.n, p.f, row0, col0), rdu = gep::out_rsrc(p.o1, p.n, p.f, row0, col0);
     // (8-byte loads straight into the product's layout, a round ahead, ran the product 13% slower)
+    u32x4 gl[4], ul[4];
+    gep::load_rows<1>(rg, std::integral_constant<int, 0>{}, rows_valid, cv, p.f, lane, gl);
+    gep::load_rows<1>(ru, std::integral_constant<int, 0>{}, rows_valid, cv, p.f, lane, ul);
     gep::sfor<0, 4>([&](auto q) {
       u32x2 gm[1][8], um[1][8];
-      u32x4 gl[4], ul[4];
-      gep::load_rows<1>(rg, q, rows_valid, cv, p.f, lane, gl);
-      gep::load_rows<1>(ru, q, rows_valid, cv, p.f, lane, ul);
       gep::stage_in_round<1>(gl, gm, stg, lane);
       gep::stage_in_round<1>(ul, um, stg, lane);
+      if constexpr (q < 3) {                     // the next round's, on their way while this one's are used
+        gep::load_rows<1>(rg, std::integral_constant<int, q + 1>{}, rows_valid, cv, p.f, lane, gl);
+        gep::load_rows<1>(ru, std::integral_constant<int, q + 1>{}, rows_valid, cv, p.f, lane, ul);
+      }
       gep::sfor<0, 8>([&](auto i) {
         const u32x2 g2 = gm[0][i], u2 = um[0][i];
         const float gv[4] = {bf16_lo(g2.x), bf16_hi(g2.x), bf16_lo(g2.y), bf16_hi(g2.y)};

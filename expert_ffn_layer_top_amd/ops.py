@@ -74,6 +74,13 @@ def _is(t, dtype, shape, name):
         _check(t, dtype, name, shape)
 
 
+def _dims(t, dtype, ndim, name):
+    """_check for a known number of dims, likewise."""
+    if not (type(t) is torch.Tensor and t.dtype is dtype and t.dim() == ndim and t.is_contiguous()):
+        _check(t, dtype, name, ndim=ndim)
+    return t.shape
+
+
 def _device_of(*ts):
     """The index of the GPU that every tensor (or None) is on."""
     d = ts[0].get_device()
@@ -101,7 +108,7 @@ _devices = [torch.device("cuda", i) for i in range(64)]
 
 def _call_on(device, name, *args):
     """Calls `name` with GPU `device` current, on that device's current stream (the last argument)."""
-    if torch.cuda.current_device() == device:
+    if torch._C._cuda_getDevice() == device:
         call(name, *args, torch._C._cuda_getCurrentRawStream(device))
     else:
         with torch.cuda.device(device):
@@ -229,8 +236,7 @@ def route_scored(logits, k, score="sigmoid", bias=None, n_group=1, topk_group=1,
     scores [T,E] fp32 (or None) for probs.  A logit of -inf or NaN, or a bias of -inf, marks an expert that
     is not there: it is chosen after every other one of the kept groups, and with a gate of 0 (a bias alone
     leaves its gate)."""
-    _check(logits, torch.float32, "logits", ndim=2)
-    T, E = logits.shape
+    T, E = _dims(logits, torch.float32, 2, "logits")
     score = _score(score)
     if not (T >= 1 and 1 <= E <= 256):
         raise ValueError(f"logits: need T >= 1 and 1 <= E <= 256, got {list(logits.shape)}")
@@ -269,10 +275,10 @@ def route_scored(logits, k, score="sigmoid", bias=None, n_group=1, topk_group=1,
 
 def route_scored_bwd(logits, topk_idx, d_gate, score="sigmoid", renormalize=True, scale=1.0):
     """d_logits [T,E] fp32: the gradient of route_scored's gates with the choice held fixed."""
-    _check(logits, torch.float32, "logits", ndim=2)
-    T, E = logits.shape
+    T, E = _dims(logits, torch.float32, 2, "logits")
     score = _score(score)
-    _check(topk_idx, torch.int32, "topk_idx", (T, None))
+    if _dims(topk_idx, torch.int32, 2, "topk_idx")[0] != T:
+        _check(topk_idx, torch.int32, "topk_idx", (T, None))
     k = topk_idx.shape[1]
     _is(d_gate, torch.float32, (T, k), "d_gate")
     dev = _device_of(logits, topk_idx, d_gate)
@@ -825,13 +831,13 @@ def _blocks(x):
 def fp8b_quantize_rows(x, dest=None):
     """(q [n, C] E4M3 bytes, s [ceil(C/128), n] fp32): blocks of 128 along each row of x [T, C] bf16, in x's
     order or, with dest [T, k], each row written to its k rows of the expert buffers (n = T k)."""
-    _check(x, torch.bfloat16, "x", ndim=2)
-    T, C = x.shape
+    T, C = _dims(x, torch.bfloat16, 2, "x")
     if T < 1 or C < 64 or C % 64:
         raise ValueError(f"x: need T >= 1 and C a multiple of 64, got {list(x.shape)}")
     k = 1
     if dest is not None:
-        _check(dest, torch.int32, "dest", (T, None))
+        if _dims(dest, torch.int32, 2, "dest")[0] != T:
+            _check(dest, torch.int32, "dest", (T, None))
         k = dest.shape[1]
         if not 1 <= k <= 16:
             raise ValueError(f"dest: k = {k} must be in [1, 16]")
@@ -892,8 +898,9 @@ def fp8b_quantize_weights(w, want_transposed=True):
 def _fp8b_rows(q, s, name, n, C):
     """Row codes [n, C] (n None: any) and their scales; returns n."""
     if n is None:
-        _check(q, torch.uint8, name, (None, C))
-        n = q.shape[0]
+        n, width = _dims(q, torch.uint8, 2, name)
+        if width != C:
+            _check(q, torch.uint8, name, (None, C))
     else:
         _is(q, torch.uint8, (n, C), name)
     _is(s, torch.float32, (-(-C // 128), n), name + "_s")
@@ -902,8 +909,7 @@ def _fp8b_rows(q, s, name, n, C):
 
 def _fp8b_weight(q, s, name, shape=None):
     if shape is None:
-        _check(q, torch.uint8, name, ndim=3)
-        shape = q.shape
+        shape = _dims(q, torch.uint8, 3, name)
     else:
         _is(q, torch.uint8, shape, name)
     E, R, C = shape
@@ -953,8 +959,8 @@ def grouped_gemm_dgrad_down_fp8b(dyq, dyq_s, offsets, w_down_t, w_down_t_s, g, u
     scales are fp8b_quantize_weights' qT, sT."""
     E, f, d = _fp8b_weight(w_down_t, w_down_t_s, "w_down_t")
     n = _fp8b_rows(dyq, dyq_s, "dyq", None, d)
-    _check(g, torch.bfloat16, "g", (n, f))
-    _check(u, torch.bfloat16, "u", (n, f))
+    _is(g, torch.bfloat16, (n, f), "g")
+    _is(u, torch.bfloat16, (n, f), "u")
     _fp8b_sizes(offsets, E, n, d, f)
     dev = _device_of(dyq, dyq_s, offsets, w_down_t, w_down_t_s, g, u)
     dg = _new((n, f), torch.bfloat16, dev)
