@@ -193,8 +193,8 @@ int moe_route_topk_bwd_balance(const float* topk_gate, const int32_t* topk_idx, 
  *   descending; ties go to the lower index, for groups and for experts;
  *   topk_gate = scale * s, divided by the sum of the k chosen s where `renormalize` is nonzero (all 0
  *   where every chosen expert is absent, or every sigmoid below the smallest double).
- * Scores and choice are computed in 64 bits, so the chosen experts do not depend on how fp32 rounds an
- * exponential.  A logit of -inf or NaN marks an absent expert (score 0, never counted in a group's
+ * The choice is the one that 64-bit scores make, so the chosen experts do not depend on how fp32 rounds an
+ * exponential; gates are rounded to fp32 once (softmax gates that are not renormalised: over a sum in fp32).  A logit of -inf or NaN marks an absent expert (score 0, never counted in a group's
  * value, chosen only after every present expert of the kept groups); a bias of -inf excludes an expert
  * in the same way, and NaN biases count as -inf; a logit of +inf counts as the largest finite float.
  *   in   logits [T,E] fp32;  out  as moe_route_topk; scores_or_null [T,E] fp32: every s.
@@ -490,13 +490,14 @@ int moe_grouped_gemm_wgrad_gate_up(int dtype, int E, int n, int d, int f, const 
  * larger blocks and fp32 scales, the form of weights that were trained or stored that way).
  * Arithmetic of a block: amax = max(2^-100, largest |v|); inv = 448 / amax rounded to fp32;
  * code = E4M3 of v * inv (fp32 product, round to nearest even); scale = amax * (1/448), both rounded to
- * fp32.  A code stands for code * scale.  Non-finite inputs are unsupported.
+ * fp32.  A code stands for code * scale.  A block that holds an infinity or a NaN is NaN throughout.
  * Blocks start at multiples of 128; the last one of an axis may be partial (sizes are multiples of 64).
  * Scales of rows are block-major: [ceil(K/128)][rows].  Scales of a weight matrix [R][C] are one per
  * 128 x 128 block: [ceil(R/128)][ceil(C/128)]. */
 
 /* Row blocks of x [T][C] bf16: without dest (k = 1) q [T][C], s [ceil(C/128)][T]; with dest [T][k] each
- * row goes to its k rows of the expert buffers: q [T*k][C], s [ceil(C/128)][T*k].  C a multiple of 64,
+ * row goes to its k rows of the expert buffers (a destination outside them is skipped): q [T*k][C],
+ * s [ceil(C/128)][T*k].  C a multiple of 64,
  * 1 <= k <= 16, all pointers 16-byte aligned. */
 int moe_fp8b_quantize_rows(const uint16_t* x, const int32_t* dest_or_null, int T, int C, int k, uint8_t* q,
                            float* s, void* stream);
