@@ -475,3 +475,44 @@ def test_few_rows_have_exact_block_sums(counts, d, f):
     kg, ku = uv * s * (1 + gv * (1 - s)), gv * s
     assert_bf16(dg, gr * kg, off * np.abs(kg) + 16 * 2.0 ** -24 * np.abs(gr * uv) * (1 + np.abs(gv)), "dg")
     assert_bf16(du, gr * ku, off * np.abs(ku) + 16 * 2.0 ** -24 * np.abs(gr * gv), "du")
+
+
+def test_tensors_past_32_bits():
+    """The last expert's rows, behind more than 2^32 codes, give the bits that they give alone."""
+    from expert_ffn_layer_top_amd import ops
+    n, d, f, last = 620000, 7168, 192, 1500
+    gen = torch.Generator(device=dev()).manual_seed(0)
+
+    def offsets(*values):
+        return torch.tensor(values, dtype=torch.int32, device=dev())
+    first, pad_last = n - last, -(-last // 128) * 128
+    pad_first = -(-first // 128) * 128
+    both = offsets(0, first, first, n), offsets(0, pad_first, pad_first, pad_first + pad_last)
+    alone = offsets(0, 0, 0, last), offsets(0, 0, 0, pad_last)
+    note(f"fp8b past 32 bits n={n} d={d} f={f}")
+    x = torch.randn(1000, d, device=dev(), generator=gen).bfloat16().repeat(n // 1000, 1)
+    x[first:] = torch.randn(last, d, device=dev(), generator=gen).bfloat16()
+    tail = x[first:].clone()
+    wg = ops.fp8b_quantize_weights(torch.randn(3, f, d, device=dev(), generator=gen).bfloat16())
+    wd = ops.fp8b_quantize_weights(torch.randn(3, d, f, device=dev(), generator=gen).bfloat16())
+    q, s, qT, sT = ops.fp8b_quantize_rows_grouped(x, *both)
+    r, t, rT, tT = ops.fp8b_quantize_rows_grouped(tail, *alone)
+    del x
+    assert torch.equal(q[first:], r) and torch.equal(s[:, first:], t)
+    assert torch.equal(qT[:, pad_first:pad_first + pad_last], rT[:, :pad_last])
+    assert torch.equal(sT[pad_first // 128:(pad_first + pad_last) // 128], tT[:pad_last // 128])
+    for form in ("mid", "half", "big"):
+        with pytest.MonkeyPatch.context() as m:
+            m.setenv("MOE_FP8B_FORM", form)
+
+            def run(codes, scales, tokens, off, pad, rows):
+                g, u, a = ops.grouped_gemm_gate_up_fp8b(codes, scales, off, *wg[:2], *wg[:2])
+                aq, as_, aT, aTs = ops.fp8b_quantize_rows_grouped(a, off, pad)
+                dg, du = ops.grouped_gemm_dgrad_down_fp8b(codes, scales, off, *wd[2:], g, u)
+                return (g, u, a, ops.grouped_gemm_down_fp8b(aq, as_, off, *wd[:2]), dg, du,
+                        ops.grouped_gemm_dgrad_gate_up_fp8b(aq, as_, aq, as_, off, *wg[2:], *wg[2:]),
+                        ops.grouped_gemm_wgrad_down_fp8b(*tokens, aT, aTs, off, pad, rows))
+            many, few = run(q, s, (qT, sT), *both, n), run(r, t, (rT, tT), *alone, last)
+            for i, (a, b) in enumerate(zip(many[:-1], few[:-1])):
+                assert torch.equal(a[first:], b), (form, i)
+            assert torch.equal(many[-1][2], few[-1][2]), form
