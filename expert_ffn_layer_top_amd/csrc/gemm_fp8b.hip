@@ -35,7 +35,8 @@
 // (a step takes some 3400 of them for 2048 of MFMAs; epilogues take 7% and 12% of the two products), and with random codes
 // power holds the clock near 1.7 GHz; with all codes zero gate/up takes 2.85 ms.  Taking out single parts of the work:
 // no epilogue 3.3, no FMAs 3.1, loads that always hit the first-level cache 3.0 ms.  Tried without gain: other cell
-// shapes (+-2%), a load that touches the lines of the step after next (10% slower), waiting fragment by fragment.
+// shapes (+-2%), a load that touches the lines of the step after next (10% slower), a
+// higher priority for half of the waves or for the MFMAs, stores left in flight over the next tile's first step.
 #include <algorithm>
 #include <cmath>
 #include <cstdlib>
