@@ -187,11 +187,28 @@ __device__ __forceinline__ int choose_exact(const ScoredArgs& a, const float (&l
   return my_e;
 }
 
+// Where a group's value lies in 64 bits, from the fp32 values b0 >= b1 of its best two experts (-inf: absent).
+// Each of them is off by its score's error (less than 2^-22, see choose_fast) and by 2^-24 of itself, to which adding
+// the bias rounds it; their sum by 2^-24 of the sum, and the bounds by as much again.  The two may cancel (biases of
+// either sign), so the margin counts their magnitudes, not the sum's.  Not `known` where those leave fp32.
+struct GroupRange {
+  float lo, hi;
+  bool known;
+};
+__device__ __forceinline__ GroupRange group_range(const ScoredArgs& a, float b0, float b1) {
+  const bool two = a.group_top == 2 && b1 != -INFINITY;
+  const float v = two ? b0 + b1 : b0, size = two ? fabsf(b0) + fabsf(b1) : fabsf(b0);
+  const bool absent = b0 == -INFINITY;
+  const float tol = absent ? 0.f : 0x1p-20f + 0x1p-22f * size;
+  return {v - tol, v + tol, absent || size < INFINITY};
+}
+
 // The same choice from fp32 scores, with my_e valid where the result is true: whether every comparison
 // that the choice rests on is wider than the scores' error.  A score is off by less than 2^-22: the
 // argument of the exponential by |l| 2^-24 of the result (l e^-|l| < 0.37), exponential and reciprocal by a
 // unit each (2^-23), sums by less than that; adding the bias rounds to 2^-24 of the sum.  Two values
-// further apart than 2^-20 + 2^-22 |value| are in the same order in 64 bits.  Logits compare exactly.
+// further apart than 2^-20 + 2^-22 |value| are in the same order in 64 bits (groups: group_range).  Logits
+// compare exactly.
 // m_out, sum_out: the softmax's maximum and sum.
 __device__ __forceinline__ bool choose_fast(const ScoredArgs& a, const float (&l)[kQ], const float (&bias)[kQ], int lane,
                                             float* s_choice, int& my_e, float& m_out, float& sum_out) {
@@ -264,19 +281,19 @@ __device__ __forceinline__ bool choose_fast(const ScoredArgs& a, const float (&l
       }
       wave_lds_sync();
     }
-    const float v = a.group_top == 1 || b1 == -INFINITY ? b0 : b0 + b1;
-    // kept: at most topk_group groups (itself among them) are as large within the margin; dropped: at
-    // least that many are larger beyond it; neither: not sure
-    const float tol = v > -INFINITY ? 0x1p-19f + 0x1p-21f * fabsf(v) : 0.f;
+    const GroupRange v = group_range(a, b0, b1);
+    // kept: at most topk_group groups (itself among them) may be as large; dropped: at least that many are
+    // larger for certain; neither: not sure
     int maybe = 0, above = 0;
     for (int i = 0; i < a.n_group; ++i) {
-      const float w = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), i * stride));
-      maybe += w >= v - tol ? 1 : 0;
-      above += w > v + tol ? 1 : 0;
+      const float lo = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v.lo), i * stride));
+      const float hi = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v.hi), i * stride));
+      maybe += hi >= v.lo ? 1 : 0;
+      above += lo > v.hi ? 1 : 0;
     }
     const bool in = maybe <= a.topk_group;
     const bool counts = lane < a.n_group * stride;       // lanes that hold a group
-    if (__ballot(counts && ((!in && above < a.topk_group) || v == INFINITY)) != 0ull) return false;
+    if (__ballot(counts && ((!in && above < a.topk_group) || !v.known)) != 0ull) return false;
     const unsigned long long kept = __ballot(counts && in);
 #pragma unroll
     for (int q = 0; q < kQ; ++q) {
@@ -564,16 +581,15 @@ __global__ __launch_bounds__(64 * kQuadWaves) void route_scored_choose_quad(Scor
       b1 = fmaxf(fminf(b0, p0), fmaxf(b1, p1));
       b0 = fmaxf(b0, p0);
     }
-    const float v = a.group_top == 1 || b1 == -INFINITY ? b0 : b0 + b1;
-    const float tol = v > -INFINITY ? 0x1p-19f + 0x1p-21f * fabsf(v) : 0.f;
+    const GroupRange v = group_range(a, b0, b1);
     int maybe = 0, above = 0;
     for (int i = 0; i < a.n_group; ++i) {
-      const float w = __shfl(v, row + i * lanes, 64);
-      maybe += w >= v - tol ? 1 : 0;
-      above += w > v + tol ? 1 : 0;
+      const float lo = __shfl(v.lo, row + i * lanes, 64), hi = __shfl(v.hi, row + i * lanes, 64);
+      maybe += hi >= v.lo ? 1 : 0;
+      above += lo > v.hi ? 1 : 0;
     }
     in = maybe <= a.topk_group;
-    if (e0 < a.E) sure = (in || above >= a.topk_group) && v != INFINITY;
+    if (e0 < a.E) sure = (in || above >= a.topk_group) && v.known;
   }
   double key[PL];
 #pragma unroll
