@@ -107,7 +107,8 @@ __device__ __forceinline__ long long run_item(long long id, long long total) {
 
 // Grouped rows: padded position p of expert e holds grouped row r = offsets[e] + p - offsets_pad[e] while
 // that is below offsets[e + 1]; its data is in[row_token ? row_token[r] : r], times row_gate[r] rounded
-// to bf16 where given.  ROWS: also the real rows' row layout, q [n][C] and s [ceil(C/128)][n].
+// to bf16 where given.  ROWS: also the real rows' row layout, q [n][C] and s [ceil(C/128)][n].  Offsets that are not
+// whole blocks of the axis (of another pad than 128) would leave rows out: they make every scale NaN instead.
 // A division per block: lane i of a row's 16 makes the factors of the thread group's row i, and one thread
 // those of each column.  One tile per workgroup: walking four or eight along the band, as the MX quantisers
 // do, measured level in time (81-88 us for 65536 rows of 1536, k = 4) and took 50 registers more.  Bound by
@@ -127,17 +128,28 @@ __global__ __launch_bounds__(kTileThreads, 6) void fp8b_grouped_kernel(
   // the band's expert: the last one that starts at or before it (every wave counts for itself: one round
   // of loads, where a search would wait for each of eight)
   int before = 0;
+  const int end = offsets_pad[E];
+  bool odd = end < 0 || end > P || (end & (kTile - 1)) != 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int e = 64 * i + (tid & 63);
-    const bool here = e < E && offsets_pad[min(e, E)] <= p0;
-    before += __popcll(__ballot(here));
+    const int start = e < E ? offsets_pad[e] : end;
+    before += __popcll(__ballot(e < E && start <= p0));
+    odd |= (start & (kTile - 1)) != 0 || start < 0 || start > end || (e == 0 && start != 0);
+  }
+  if (__ballot(odd) != 0ull) {                             // (the same in every workgroup)
+    const float nan = __builtin_nanf("");
+    if (tid < kTile) {
+      if (ROWS && p0 + tid < n) s[ct * n + p0 + tid] = nan;
+      if (c0 + tid < C) sT[(p0 / kTile) * C + c0 + tid] = nan;
+    }
+    return;
   }
   const int e = max(before - 1, 0);
   const int first = offsets[e];
   // the thread's eight positions: consecutive rows row0 .. of that expert, as far as it has them
   const int row0 = static_cast<int>(first + (p0 - offsets_pad[e]) + 8 * pg);
-  const int rows = p0 < offsets_pad[E] ? min(max(static_cast<int>(min(static_cast<long long>(offsets[e + 1]), n)) - row0, 0), 8) : 0;
+  const int rows = p0 < end ? min(max(static_cast<int>(min(static_cast<long long>(offsets[e + 1]), n)) - row0, 0), 8) : 0;
   const unsigned live = (1u << rows) - 1u;
   int src[8];
 #pragma unroll

@@ -17,7 +17,7 @@
 //   WGRAD_DOWN  dy^T [d][P]    x  a^T [f][P]                        -> dW_down[e]
 //   WGRAD_GU    dg^T | du^T [f][P]  x  x^T [d][P]                   -> dW_gate[e], dW_up[e]
 // where P is the padded token axis: expert e owns positions [offsets_pad[e], offsets_pad[e + 1]), whole
-// blocks of 128.
+// blocks of 128 inside it.  An expert whose offsets say otherwise (another pad) has NaN gradients.
 //
 // Tile: 256 x 256 outputs per workgroup of eight waves, 64 rows x 128 columns each (two waves per
 // SIMD).  The running sums must be plain vector registers, since vector instructions cannot use
@@ -112,7 +112,7 @@ __device__ __forceinline__ int kc_off(int r, int c) { return r * 128 + ((c ^ ((r
 struct Tile {
   int e, m0, m_end, n0, half;
   int k_begin;   // WGRAD: first padded token position of the expert
-  int k_len;     // WGRAD: its padded tokens
+  int k_len;     // WGRAD: its padded tokens (-1: no whole blocks of the axis)
 };
 
 template <int MODE>
@@ -148,6 +148,21 @@ __device__ __forceinline__ int map_find(int mt, int& first) {
   return count - 1;
 }
 
+// Expert t.e's range of the padded token axis.  Offsets of a pad that the axis has no room for, or that splits
+// blocks, can only be seen here, on the device; nothing is read through them.
+__device__ __forceinline__ void token_range(const Params& p, Tile& t) {
+  const int begin = p.offsets_pad[t.e], end = p.offsets_pad[t.e + 1];
+  const bool whole = ((begin | end) & (BK - 1)) == 0 && 0 <= begin && begin <= end && end <= p.P;
+  t.k_begin = __builtin_amdgcn_readfirstlane(whole ? begin : 0);
+  t.k_len = __builtin_amdgcn_readfirstlane(whole ? end - begin : -1);
+}
+
+// What a tile's sums start from.
+template <int MODE>
+__device__ __forceinline__ float start_value(const Tile& t) {
+  return is_wgrad(MODE) && t.k_len < 0 ? __builtin_nanf("") : 0.f;
+}
+
 // The tile with linear id `lid`: each expert owns a contiguous run of ids, its tiles in cell order.
 template <int MODE>
 __device__ __forceinline__ Tile tile_at(const Params& p, int ntiles_n, int lid) {
@@ -170,8 +185,7 @@ __device__ __forceinline__ Tile tile_at(const Params& p, int ntiles_n, int lid) 
     t.half = mi >= mt ? 1 : 0;
     t.m0 = (mi - t.half * mt) * BM;
     t.m_end = Mtot;
-    t.k_begin = p.offsets_pad[t.e];
-    t.k_len = p.offsets_pad[t.e + 1] - t.k_begin;
+    token_range(p, t);
   }
   t.n0 = nt * n_tile_width<MODE>();
   t.e = __builtin_amdgcn_readfirstlane(t.e);
@@ -179,8 +193,6 @@ __device__ __forceinline__ Tile tile_at(const Params& p, int ntiles_n, int lid) 
   t.m_end = __builtin_amdgcn_readfirstlane(t.m_end);
   t.n0 = __builtin_amdgcn_readfirstlane(t.n0);
   t.half = __builtin_amdgcn_readfirstlane(t.half);
-  t.k_begin = __builtin_amdgcn_readfirstlane(t.k_begin);
-  t.k_len = __builtin_amdgcn_readfirstlane(t.k_len);
   return t;
 }
 
@@ -210,7 +222,7 @@ __device__ __forceinline__ TileSrc tile_src(const Params& p, const Tile& t, bool
   TileSrc s{};
   const int Kone = k_one<MODE>(p.d, p.f);
   if constexpr (is_wgrad(MODE)) {
-    s.nk = (t.k_len + BK - 1) / BK;
+    s.nk = max(t.k_len, 0) / BK;
     const int C = role_b ? n_total<MODE>(p.d, p.f) : m_total<MODE>(p.d, p.f);
     const int c0 = role_b ? t.n0 : t.m0;
     const uint8_t* base = role_b ? p.b0 : (MODE == WGRAD_GU && t.half ? p.a1 : p.a0);
@@ -573,13 +585,14 @@ __device__ __forceinline__ void grouped_gemm(const Params& p) {
   const uint32_t sb_off = SB_RING + 4 * (128 * wn + 4 * (lane >> 4));
 
   f32x4 acc[8][4];
-  auto zero_acc = [&]() {
+  auto start_acc = [&]() {
+    const float v = start_value<MODE>(t);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{v, v, v, v};
   };
-  zero_acc();
+  start_acc();
   int st = 0, kt = 0;
   bool ready = false;
   for (;;) {
@@ -623,9 +636,9 @@ __device__ __forceinline__ void grouped_gemm(const Params& p) {
     const uint32_t spent = ring + (st ^ 1) * OP_BYTES + (wave < 4 ? A_RING : B_RING) + (wave & 3) * STG_BYTES;
     epilogue<MODE>(p, t, acc, wm, wn, lane, spent);
     if (lid_n >= lend) break;
-    zero_acc();
     ready = next_ready;
     t = tn;
+    start_acc();
     cur = nxt;
     w0 = w0n;
     w1 = w1n;
@@ -928,8 +941,8 @@ __device__ __forceinline__ void grouped_small(const Params& p, uint8_t* lds) {
     t.half = __builtin_amdgcn_readfirstlane(mi >= mt ? 1 : 0);
     t.m0 = __builtin_amdgcn_readfirstlane((mi - t.half * mt) * BM);
     t.m_end = Mtot;
-    t.k_begin = __builtin_amdgcn_readfirstlane(p.offsets_pad[t.e]);
-    nk = __builtin_amdgcn_readfirstlane((p.offsets_pad[t.e + 1] - t.k_begin) / BK);
+    token_range(p, t);
+    nk = max(t.k_len, 0) / BK;
   } else {
     int e, first;
     gsched::mtile_find(mts, lid / nt, e, first);
@@ -1002,10 +1015,11 @@ __device__ __forceinline__ void grouped_small(const Params& p, uint8_t* lds) {
   };
   float w0 = 0.f, w1 = 0.f;                        // weight scales: lane l holds K block l's
   f32x4 acc[NF][4];
+  const float start = start_value<MODE>(t);
 #pragma unroll
   for (int i = 0; i < NF; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{start, start, start, start};
   if (nk > 0) issue(0, 0);
   const uint32_t base = lds_addr(lds);
   const uint32_t kc0 = kc_off(lane & 15, lane >> 4), kc1 = kc_off(lane & 15, 4 + (lane >> 4));

@@ -852,7 +852,8 @@ def fp8b_quantize_rows_grouped(x, offsets, offsets_pad, row_token=None, row_gate
     """Both layouts of a grouped bf16 tensor from one read: the row blocks (q [n, C], s [ceil(C/128), n]; None,
     None without want_rows) and the blocks of 128 tokens of one expert, transposed (qT [C, P], sT [P/128, C],
     P = mx_pad_cap(n, E)).  Grouped row r is x[r], or x[row_token[r]], times row_gate[r] where given.
-    offsets_pad: a router's padded offsets with pad = 128 (or a multiple)."""
+    offsets_pad: a router's padded offsets with pad = 128 (others, which only the device can see, make every
+    scale NaN where they split blocks of 128 or run past P)."""
     _check(offsets, torch.int32, "offsets", ndim=1)
     E = offsets.shape[0] - 1
     _need(1 <= E <= 256, f"offsets must hold E + 1 entries with 1 <= E <= 256, got {E + 1}")

@@ -506,7 +506,9 @@ int moe_fp8b_quantize_rows(const uint16_t* x, const int32_t* dest_or_null, int T
  * the same rows from one read: grouped row r is in[r], or in[row_token[r]] where row_token is given, times
  * row_gate[r] (fp32 product rounded to bf16) where that is given.  Expert e's row i sits at position
  * offsets_pad[e] + i of the padded token axis of length P = moe_mx_pad_cap(n, E); offsets_pad must be a
- * router's padded offsets with pad a multiple of 128.
+ * router's padded offsets with pad 128 (whole blocks, and offsets_pad[E] <= P).  Offsets of another pad are seen on
+ * the device only: where they split blocks or run past P, every scale here is NaN, and so are the
+ * weight gradients of the experts that they misplace.
  *   out  qT [C][P], sT [P/128][C] (zeros and their scale 2^-100 / 448 at every other position);
  *        q_or_null [n][C] and s_or_null [ceil(C/128)][n]: the row blocks, rows from offsets[E] on left as
  *        they were.  C a multiple of 64, 1 <= E <= 256. */
@@ -531,8 +533,8 @@ int moe_fp8b_quantize_weights(const uint16_t* w, int E, int R, int C, uint8_t* q
  * dgrad_down: dyq [n][d], dys; w_down_t [E][f][d] (moe_fp8b_quantize_weights' qT, sT); dg, du [n][f]
  *   through the SwiGLU backward of (g, u).
  * dgrad_gate_up: dgq, duq [n][f] and scales; w_gate_t, w_up_t [E][d][f]; dxp [n][d].
- * wgrad_down, wgrad_gate_up: moe_fp8b_quantize_rows_grouped's qT, sT of dyexp, a, dg, du, xp;
- *   dw_down [E][d][f], dw_gate, dw_up [E][f][d], zeros for experts without rows. */
+ * wgrad_down, wgrad_gate_up: moe_fp8b_quantize_rows_grouped's qT, sT of dyexp, a, dg, du, xp and the same
+ *   offsets_pad (pad 128); dw_down [E][d][f], dw_gate, dw_up [E][f][d], zeros for experts without rows. */
 int moe_grouped_gemm_gate_up_fp8b(int E, int n, int d, int f, const int32_t* offsets, const uint8_t* xq,
                                   const float* xs, const uint8_t* w_gate, const float* w_gate_s,
                                   const uint8_t* w_up, const float* w_up_s, uint16_t* g_or_null,
