@@ -187,8 +187,23 @@ __device__ __forceinline__ int choose_exact(const ScoredArgs& a, const float (&l
   return my_e;
 }
 
+// How far apart two values of fp32 scores have to be (beside 2^-22 of the value: adding a bias rounds to 2^-24 of the
+// result) to be in the same order in 64 bits.  With u = 2^-24, an exponential of x is off by 2.3 u |x| (x, log2 e and
+// their product are rounded) + 2 u (a unit of the instruction) of itself.
+//   sigmoid  x = -l is exact, which leaves s (1 - s) (1.3 u |l| + 2 u) < 0.8 u; rounding 1 + exp(-l) adds u, the
+//            reciprocal 2 u: less than 2^-22 each, 2^-21 for two.
+//   softmax  p = e^x / sum: 2.3 u |x| + 2 u of its own, and the mean of that over all experts for the sum, with 9 u
+//            for at most 9 levels of additions, and u each for 1 / sum and the product; together
+//            p (15 u + 2.3 u (|x| + mean |x|)).  The p add up to 1, and where one is near it the mean of |x| is small (256
+//            experts: 15.2 u at p = 0.95 is the most that one or two can be off), so the difference of two experts'
+//            scores is off by less than 15.2 u, that of two groups' sums by less than 17 u.
+// Twice that is taken.
+__device__ __forceinline__ float score_margin(const ScoredArgs& a) {
+  return a.score == MOE_SCORE_SIGMOID ? 0x1p-20f : 0x1p-19f;
+}
+
 // Where a group's value lies in 64 bits, from the fp32 values b0 >= b1 of its best two experts (-inf: absent).
-// Each of them is off by its score's error (less than 2^-22, see choose_fast) and by 2^-24 of itself, to which adding
+// Each of them is off by its score's error and by 2^-24 of itself, to which adding
 // the bias rounds it; their sum by 2^-24 of the sum, and the bounds by as much again.  The two may cancel (biases of
 // either sign), so the margin counts their magnitudes, not the sum's.  Not `known` where those leave fp32.
 struct GroupRange {
@@ -199,16 +214,12 @@ __device__ __forceinline__ GroupRange group_range(const ScoredArgs& a, float b0,
   const bool two = a.group_top == 2 && b1 != -INFINITY;
   const float v = two ? b0 + b1 : b0, size = two ? fabsf(b0) + fabsf(b1) : fabsf(b0);
   const bool absent = b0 == -INFINITY;
-  const float tol = absent ? 0.f : 0x1p-20f + 0x1p-22f * size;
+  const float tol = absent ? 0.f : score_margin(a) + 0x1p-22f * size;
   return {v - tol, v + tol, absent || size < INFINITY};
 }
 
 // The same choice from fp32 scores, with my_e valid where the result is true: whether every comparison
-// that the choice rests on is wider than the scores' error.  A score is off by less than 2^-22: the
-// argument of the exponential by |l| 2^-24 of the result (l e^-|l| < 0.37), exponential and reciprocal by a
-// unit each (2^-23), sums by less than that; adding the bias rounds to 2^-24 of the sum.  Two values
-// further apart than 2^-20 + 2^-22 |value| are in the same order in 64 bits (groups: group_range).  Logits
-// compare exactly.
+// that the choice rests on is wider than the scores' error (score_margin, group_range).  Logits compare exactly.
 // m_out, sum_out: the softmax's maximum and sum.
 __device__ __forceinline__ bool choose_fast(const ScoredArgs& a, const float (&l)[kQ], const float (&bias)[kQ], int lane,
                                             float* s_choice, int& my_e, float& m_out, float& sum_out) {
@@ -319,11 +330,12 @@ __device__ __forceinline__ bool choose_fast(const ScoredArgs& a, const float (&l
   my_e = 0;
   float last = 0.f;
   const int rounds = a.k + (a.bias != nullptr ? 1 : 0);
+  const float margin = score_margin(a);
   for (int j = 0; j < rounds; ++j) {
     const int m = wave_max_key(key[0]);
     if (a.bias != nullptr) {
       const float v = key_float(m);
-      if (j > 0 && m != kOut) sure = sure && last - v > 0x1p-20f + 0x1p-22f * fabsf(last);
+      if (j > 0 && m != kOut) sure = sure && last - v > margin + 0x1p-22f * fabsf(last);
       if (j > 0 && m == kOut) sure = sure && last > -INFINITY;
       last = v;
     }
@@ -608,10 +620,11 @@ __global__ __launch_bounds__(64 * kQuadWaves) void route_scored_choose_quad(Scor
   float last = 3.4028234663852886e38f;
   double mine = kGone;
   const int rounds = a.k + (biased ? 1 : 0);
+  const float margin = score_margin(a);
   for (int i = 0; i < rounds; ++i) {              // (the last round of a biased choice only compares)
     const double m = row_max(head);
     const float v = static_cast<float>(m);        // -inf for kGone
-    sure = sure & (!biased | (last - v > 0x1p-20f + 0x1p-22f * fabsf(last)));
+    sure = sure & (!biased | (last - v > margin + 0x1p-22f * fabsf(last)));
     last = v;
     mine = j == i ? m : mine;
     const bool pop = head == m;

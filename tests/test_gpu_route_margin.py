@@ -78,3 +78,28 @@ def test_group_values_past_the_largest_float(E, n_group):
         note(f"route_scored huge biases E={E} n_group={n_group} group_top={group_top}")
         out = ops.route_scored(f32_to_dev(logits), 4, bias=f32_to_dev(bias), **kw)
         assert np.array_equal(host(out["topk_idx"]), idx)
+
+
+@pytest.mark.parametrize("beta", [0.9, 0.5, 0.05])
+@pytest.mark.parametrize("E", [256, 100, 64, 5])
+@pytest.mark.parametrize("T", [64, 900])
+def test_softmax_scores_next_to_a_biased_one(T, E, beta):
+    """One expert's softmax score and a small one with a bias of `beta`, some 2^-20 apart in 64 bits: as close as
+    the errors of their fp32 values, which share the error of one sum."""
+    from expert_ffn_layer_top_amd import ops
+    rng = np.random.default_rng([T, E])
+    logits = rng.uniform(-4.0, 0.0, (T, E))
+    rest = np.exp(logits[:, 2:]).sum(axis=1)
+    small = 10.0 ** rng.uniform(-5, -2, T)
+    gap = rng.choice([-1.0, 1.0], T) * rng.uniform(0.5e-6, 2.5e-6, T)
+    a, b = beta + small + gap, small
+    total = rest / (1 - a - b)
+    logits[:, 0], logits[:, 1] = np.log(a * total), np.log(b * total)
+    logits = logits.astype(np.float32)
+    bias = np.full(E, -4.0, np.float32)
+    bias[0], bias[1] = 0.0, beta
+    idx, _, _ = scored.route(logits, 2, score="softmax", bias=bias)
+    assert (idx[:, 0] == 0).any() and (idx[:, 0] == 1).any() and idx.max() == 1
+    note(f"route_scored softmax pairs T={T} E={E} beta={beta}")
+    out = ops.route_scored(f32_to_dev(logits), 2, score="softmax", bias=f32_to_dev(bias))
+    assert np.array_equal(host(out["topk_idx"]), idx)
