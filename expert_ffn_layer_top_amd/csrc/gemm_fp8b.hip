@@ -1196,10 +1196,12 @@ Form choose_form(const Params& p) {
   const int cols = MODE == FWD1 ? SM_BN / 2 : SM_BN;
   const double tb = tiles(BM, n_tile_width<MODE>());
   const double big = (tb <= 1.0 ? 1.0 : tb + 0.5) * (WG ? 1.75 * kb + 6.0 : 1.5 * kb + (MODE == DGRAD1 ? 23.0 : 6.5));
+  // (the 256-row kernel's 32-bit offsets span 256 rows of codes, the others' 128)
+  const bool fits = (WG ? static_cast<long long>(p.P) : k_one<MODE>(p.d, p.f)) * BM < 0x7fffffffLL;
   const double half = std::ceil(tiles(128, cols)) * (WG ? 0.72 * kb + 2.6 : 0.64 * kb + (MODE == DGRAD1 ? 7.6 : 3.0)) - 1.5;
-  if (WG) return half < big ? HALF : BIG;
+  if (WG) return half < big || !fits ? HALF : BIG;
   const double mid = std::ceil(tiles(64, cols)) * (0.4 * kb + (MODE == DGRAD1 ? 4.0 : 2.0)) + 2.5;
-  return mid < half && mid < big ? MID : half < big ? HALF : BIG;
+  return mid < half && (mid < big || !fits) ? MID : half < big || !fits ? HALF : BIG;
 }
 
 // A, dG and dU are quantised again by whoever uses them.  Where one is rounded to bf16 the other way at the
