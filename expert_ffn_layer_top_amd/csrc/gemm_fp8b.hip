@@ -1171,16 +1171,20 @@ int launch_small(const Params& p, hipStream_t s) {
 //   64 rows 31 + 15 / 27 + 18 / 37 + 24, 250 rows 52 + 30 / 48 + 29 / 41 + 26; one expert, d = f = 4096, 1024
 //   rows 60 + 30 / 43 + 30 / 59 + 50, 4096 rows 203 + 97 / 160 + 79 / 122 + 61; weight gradients of 16 experts,
 //   d 2112, f 1344, 64 rows 128-row tiles 28 + 52, 256-row 27 + 41.
-// MOE_FP8B_FORM = few, mid, half or big sets the form (tests run every form on the same cases).
-enum Form { FEW, MID, HALF, BIG };
+// MOE_FP8B_FORM = few, mid, half or big sets the form (tests run every form on the same cases; a product without it
+// takes the next).  It chooses a kernel, not a precision: see exact_rows for the one exception.
+enum Form { FEW, MID, HALF, BIG, NONE, UNKNOWN };
+Form forced_form() {
+  const char* env = getenv("MOE_FP8B_FORM");
+  if (env == nullptr || env[0] == '\0') return NONE;
+  return !strcmp(env, "few") ? FEW : !strcmp(env, "mid") ? MID : !strcmp(env, "half") ? HALF : !strcmp(env, "big") ? BIG : UNKNOWN;
+}
 template <int MODE>
-Form choose_form(const Params& p) {
+Form choose_form(const Params& p, Form forced) {
   constexpr bool WG = is_wgrad(MODE), FORWARD = MODE == FWD1 || MODE == FWD2;
-  if (const char* env = getenv("MOE_FP8B_FORM")) {
-    if (!strcmp(env, "few") && FORWARD) return FEW;
-    if (!strcmp(env, "mid") || !strcmp(env, "few")) return WG ? HALF : MID;
-    if (!strcmp(env, "half")) return HALF;
-    if (!strcmp(env, "big")) return BIG;
+  if (forced != NONE) {
+    if (forced == FEW && !FORWARD) forced = MID;
+    return forced == MID && WG ? HALF : forced;
   }
   if (FORWARD && p.n <= 6LL * p.E) return FEW;
   const double busy = std::min(p.n, p.E), mean = p.n / busy;
@@ -1212,22 +1216,25 @@ Form choose_form(const Params& p) {
 // They cost (gate/up, us, 64-row tiles of the two kinds and the kernel of few rows): 16 experts, d 2112, f 1344, 16
 // rows each 17 / 28 / 18; one expert, d = f = 4096, 16 rows 18 / 29 / 13, 64 rows 19 / 31 / 26; 8 experts, d 7168,
 // f 2048, 16 rows 41 / 57 / 41, 30 rows 41 / 58 / 79.
+// (128- and 256-row tiles have no exact form: where one of them is set by hand, its sums are the fp8 core's.)
 template <int MODE>
-bool exact_rows(const Params& p) {
-  return (MODE == FWD1 || MODE == DGRAD1) && p.n * static_cast<long long>(fp8b_blocks(p.f)) < 2048 &&
-         getenv("MOE_FP8B_FORM") == nullptr;
+bool exact_rows(const Params& p, Form forced) {
+  return (MODE == FWD1 || MODE == DGRAD1) && p.n * static_cast<long long>(fp8b_blocks(p.f)) < 2048 && forced != HALF &&
+         forced != BIG;
 }
 
 template <int MODE>
 int launch_rows(const Params& p, hipStream_t s) {
-  const Form form = choose_form<MODE>(p);
+  const Form forced = forced_form();
+  MOE_REQUIRE(forced != UNKNOWN, MOE_ERR_INVALID_ARG, "MOE_FP8B_FORM must be few, mid, half or big");
+  const Form form = choose_form<MODE>(p, forced);
   if constexpr (MODE == FWD1 || MODE == FWD2) {
     if (form == FEW) return launch_skinny<MODE>(p, s);
   }
   if constexpr (MODE == FWD1 || MODE == DGRAD1) {
-    if (exact_rows<MODE>(p)) {
+    if (exact_rows<MODE>(p, forced)) {
       if constexpr (MODE == FWD1)
-        if (p.n <= 16LL * p.E) return launch_skinny<MODE>(p, s);
+        if (forced == NONE && p.n <= 16LL * p.E) return launch_skinny<MODE>(p, s);
       return launch_small<MODE, 64, true>(p, s);
     }
   }
