@@ -791,6 +791,8 @@ __device__ __forceinline__ void grouped_skinny(const Params& p) {
   const int cb = (blockIdx.x - mu * groups) * CBW + wave / KS;
   int e, r0, r1;
   if (!find_group<SKINNY_ROWS>(p.offsets, p.E, mu, e, r0, r1)) return;
+  r1 = min(r1, p.n);                               // (as the other forms' descriptors: no row past the buffers)
+  if (r0 >= r1) return;
   const int rows = min(SKINNY_ROWS, r1 - r0);
   const bool active = cb * WC < N;
   const int n0 = active ? cb * WC : 0;
@@ -951,7 +953,7 @@ __device__ __forceinline__ void grouped_small(const Params& p, uint8_t* lds) {
     const int r0 = p.offsets[t.e], r1 = p.offsets[t.e + 1];
     gsched::cell_order(lid - first * nt, (r1 - r0 + BM - 1) / BM, nt, 1 << 20, 1, mi, ni);
     t.m0 = __builtin_amdgcn_readfirstlane(r0 + mi * BM);
-    t.m_end = __builtin_amdgcn_readfirstlane(r1);
+    t.m_end = __builtin_amdgcn_readfirstlane(min(r1, p.n));
   }
   t.n0 = __builtin_amdgcn_readfirstlane(ni * TC);
 

@@ -3,7 +3,7 @@
 import pytest
 import torch
 
-from gpu_util import dev, note
+from gpu_util import dev, i32_to_dev, note
 
 pytestmark = pytest.mark.gpu
 
@@ -40,3 +40,31 @@ def test_weight_gradients_of_a_token_axis_past_the_256_row_kernels_offsets(monke
     monkeypatch.setenv("MOE_FP8B_FORM", "half")
     want = ops.grouped_gemm_wgrad_down_fp8b(*dy, *a, *small, m)
     assert torch.equal(got, want) and want.abs().max() > 0
+
+
+@pytest.mark.parametrize("form", ["", "few", "mid", "half", "big"])
+def test_offsets_past_the_rows_of_a_call(form, monkeypatch):
+    """Offsets that name more rows than the call's n are a caller's mistake: whatever the rows below n hold then,
+    nothing is written behind them, in any form."""
+    from expert_ffn_layer_top_amd._lib import call
+    from test_gpu_fp8b import Case
+    if form:
+        monkeypatch.setenv("MOE_FP8B_FORM", form)
+    held, n, d, f = 200, 20, 192, 320
+    c = Case([held], d, f, seed=12)
+    (xq, xs), _ = c.rows(d)
+    c.E = 3
+    wg, wu = c.weight(f, d)[0], c.weight(f, d)[0]
+    g, u = c.bf16(f)[0], c.bf16(f)[0]
+    xs = xs[:, :n].contiguous()
+    stream = torch.cuda.current_stream().cuda_stream
+
+    note(f"fp8b offsets past n {form}")
+    for offsets in ([0, 3, 90, 200], [0, 20, 21, 140]):
+        off = i32_to_dev(offsets)
+        out = [torch.full((held, f), 7.0, device=dev()).bfloat16() for _ in range(5)]
+        call("moe_grouped_gemm_gate_up_fp8b", 3, n, d, f, *(t.data_ptr() for t in (off, xq, xs, *wg, *wu, *out[:3])), stream)
+        call("moe_grouped_gemm_dgrad_down_fp8b", 3, n, d, f,
+             *(t.data_ptr() for t in (off, xq, xs, *wg, g, u, *out[3:])), stream)
+        for t in out:
+            assert (t[n:] == 7.0).all()
