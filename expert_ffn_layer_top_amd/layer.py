@@ -24,7 +24,7 @@ the tensors one step passes to the next.  ([news] "Ai2 rebuilds Olmo's training 
 the whole step without waiting.)
 """
 
-from dataclasses import dataclass, field
+from dataclasses import dataclass, field, replace
 
 import torch
 
@@ -165,6 +165,8 @@ def forward(x, weights, k, logits=None, mxfp8=False, want_probs=False, events=No
         raise ValueError("serving is a form of the block-128 products (fp8b), without recompute")
     if router is not None and (balance_weight is not None or want_probs):
         raise ValueError("balance_weight and want_probs belong to the softmax router, not to a ScoredRouter")
+    if router is not None:
+        router = replace(router)         # the backward uses the settings this forward used
     ctx = dict(x=x, k=k, mxfp8=mxfp8, balance_weight=balance_weight, router=router, serving=serving)
     want_probs = want_probs or balance_weight is not None
     if logits is None:
