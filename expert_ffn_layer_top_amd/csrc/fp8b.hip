@@ -296,7 +296,7 @@ extern "C" int moe_fp8b_quantize_rows(const uint16_t* x, const int32_t* dest, in
   const long long n = static_cast<long long>(T) * k;
   MOE_REQUIRE(n < (1LL << 31), MOE_ERR_UNSUPPORTED, "T*k must be < 2^31");
   const long long blocks = (static_cast<long long>(T) * fp8b_blocks(C) * 16 + kRowThreads - 1) / kRowThreads;
-  MOE_REQUIRE(blocks <= 0x7fffffffLL, MOE_ERR_UNSUPPORTED, "tensor too large");
+  MOE_REQUIRE(blocks * kRowThreads < (1LL << 32), MOE_ERR_UNSUPPORTED, "tensor too large (a launch has fewer than 2^32 threads)");
   if (dest)
     fp8b_rows_kernel<true><<<static_cast<unsigned>(blocks), kRowThreads, 0, as_stream(stream)>>>(x, dest, T, C, k, n, q, s);
   else

@@ -930,6 +930,8 @@ size_t hist_bytes(int T, int E) {
 
 int check_scored(int T, int E, int k, int score, float scale) {
   if (int st = check_layer_shape(T, E, k)) return st;
+  // 16 lanes per token, in launches of fewer than 2^32 threads
+  MOE_REQUIRE(T <= (1 << 28) - 64, MOE_ERR_UNSUPPORTED, "T must be at most 2^28 - 64 (got %d)", T);
   MOE_REQUIRE(score == MOE_SCORE_SIGMOID || score == MOE_SCORE_SOFTMAX, MOE_ERR_INVALID_ARG,
               "score must be MOE_SCORE_SIGMOID or MOE_SCORE_SOFTMAX (got %d)", score);
   MOE_REQUIRE(std::isfinite(scale), MOE_ERR_INVALID_ARG, "the gates' scale must be finite");

@@ -198,7 +198,7 @@ int moe_route_topk_bwd_balance(const float* topk_gate, const int32_t* topk_idx, 
  * value, chosen only after every present expert of the kept groups); a bias of -inf excludes an expert
  * in the same way, and NaN biases count as -inf; a logit of +inf counts as the largest finite float.
  *   in   logits [T,E] fp32;  out  as moe_route_topk; scores_or_null [T,E] fp32: every s.
- * Needs n_group dividing E, 1 <= topk_group <= n_group, k <= topk_group * E / n_group, finite scale;
+ * Needs n_group dividing E, 1 <= topk_group <= n_group, k <= topk_group * E / n_group, T <= 2^28 - 64, finite scale;
  * workspace moe_route_scored_workspace_bytes(T, E, k): none (NULL) up to 64 tokens. */
 size_t moe_route_scored_workspace_bytes(int T, int E, int k);
 int moe_route_scored(const float* logits, const float* bias_or_null, int T, int E, int k, int score,
@@ -498,7 +498,7 @@ int moe_grouped_gemm_wgrad_gate_up(int dtype, int E, int n, int d, int f, const 
 /* Row blocks of x [T][C] bf16: without dest (k = 1) q [T][C], s [ceil(C/128)][T]; with dest [T][k] each
  * row goes to its k rows of the expert buffers (a destination outside them is skipped): q [T*k][C],
  * s [ceil(C/128)][T*k].  C a multiple of 64,
- * 1 <= k <= 16, all pointers 16-byte aligned. */
+ * 1 <= k <= 16, T ceil(C/128) 16 below 2^32 - 256, all pointers 16-byte aligned. */
 int moe_fp8b_quantize_rows(const uint16_t* x, const int32_t* dest_or_null, int T, int C, int k, uint8_t* q,
                            float* s, void* stream);
 
