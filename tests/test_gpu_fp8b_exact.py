@@ -72,8 +72,8 @@ def test_an_unknown_form_is_refused(monkeypatch):
     from expert_ffn_layer_top_amd import _lib, ops
     monkeypatch.setenv("MOE_FP8B_FORM", "small")
     z = torch.zeros(4, 64, dtype=torch.uint8, device=dev())
-    s = torch.ones(1, 4, device=dev())
-    w, ws = torch.zeros(1, 64, 64, dtype=torch.uint8, device=dev()), torch.ones(1, 1, 1, device=dev())
+    s = f32_to_dev(np.ones((1, 4)))
+    w, ws = torch.zeros(1, 64, 64, dtype=torch.uint8, device=dev()), f32_to_dev(np.ones((1, 1, 1)))
     with pytest.raises(_lib.MoeError, match="MOE_FP8B_FORM"):
         ops.grouped_gemm_down_fp8b(z, s, i32_to_dev([0, 4]), w, ws)
 

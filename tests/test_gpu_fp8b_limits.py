@@ -29,7 +29,7 @@ def test_weight_gradients_of_a_token_axis_past_the_256_row_kernels_offsets(monke
         x = torch.randn(m, C, device=dev(), generator=gen).bfloat16()
         _, _, q, s = ops.fp8b_quantize_rows_grouped(x, *small)
         codes = torch.zeros(C, P, dtype=torch.uint8, device=dev())
-        scales = torch.ones(P // 128, C, device=dev())
+        scales = torch.ones(P // 128, C, dtype=torch.float32, device=dev())
         for i, b in enumerate(at):
             codes[:, 128 * b:128 * (b + 1)] = q[:, 128 * i:128 * (i + 1)]
             scales[b] = s[i]
