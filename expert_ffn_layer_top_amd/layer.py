@@ -137,7 +137,8 @@ def forward(x, weights, k, logits=None, mxfp8=False, want_probs=False, events=No
     stream around the calls named in GEMM_CALLS and ROW_CALLS.
     recompute: keep neither G, U nor A (3 n f bf16 values) for the backward, which then runs the
     gate/up product again on the kept permuted input (per-layer activation recompute, [card]
-    "Supercharging Olmo-core ...": used at the largest scale).  The kernels are deterministic,
+    "Supercharging Olmo-core ...": used at the largest scale).  The 8-bit formats still keep A's token
+    blocks for the down weight gradient.  The kernels are deterministic,
     so the backward's results are bit-identical either way.
     mxfp8: the expert products run on MXFP8 operands; the weights' MXFP8 copies are made on the
     first such forward and again whenever a bf16 weight was replaced or changed in place

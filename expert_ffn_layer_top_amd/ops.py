@@ -233,7 +233,8 @@ def route_scored(logits, k, score="sigmoid", bias=None, n_group=1, topk_group=1,
     fp32 added for the choice alone, and groups: of n_group groups of E / n_group experts, the topk_group
     with the largest sum of their group_top best (score + bias); of their experts the k best.  Gates are
     scale * score, over the chosen scores' sum with renormalize.  Returns the same dict as route_topk, with
-    scores [T,E] fp32 (or None) for probs.  A logit of -inf or NaN, or a bias of -inf, marks an expert that
+    scores [T,E] fp32 (or None) for probs; they come from a pass over every logit in 64 bits (32768 tokens of 256
+    experts: 150 us, 46 without).  A logit of -inf or NaN, or a bias of -inf, marks an expert that
     is not there: it is chosen after every other one of the kept groups, and with a gate of 0 (a bias alone
     leaves its gate)."""
     T, E = _dims(logits, torch.float32, 2, "logits")

@@ -194,10 +194,12 @@ int moe_route_topk_bwd_balance(const float* topk_gate, const int32_t* topk_idx, 
  *   topk_gate = scale * s, divided by the sum of the k chosen s where `renormalize` is nonzero (all 0
  *   where every chosen expert is absent, or every sigmoid below the smallest double).
  * The choice is the one that 64-bit scores make, so the chosen experts do not depend on how fp32 rounds an
- * exponential; gates are rounded to fp32 once (softmax gates that are not renormalised: over a sum in fp32).  A logit of -inf or NaN marks an absent expert (score 0, never counted in a group's
+ * exponential; gates are rounded to fp32 once (softmax gates that are not renormalised: over a sum in fp32).
+ * A logit of -inf or NaN marks an absent expert (score 0, never counted in a group's
  * value, chosen only after every present expert of the kept groups); a bias of -inf excludes an expert
  * in the same way, and NaN biases count as -inf; a logit of +inf counts as the largest finite float.
- *   in   logits [T,E] fp32;  out  as moe_route_topk; scores_or_null [T,E] fp32: every s.
+ *   in   logits [T,E] fp32;  out  as moe_route_topk; scores_or_null [T,E] fp32: every s, from a 64-bit pass
+ *        over all logits that otherwise only undecided tokens take (32768 tokens of 256 experts: 150 us, 46 without).
  * Needs n_group dividing E, 1 <= topk_group <= n_group, k <= topk_group * E / n_group, T <= 2^28 - 64, finite scale;
  * workspace moe_route_scored_workspace_bytes(T, E, k): none (NULL) up to 64 tokens. */
 size_t moe_route_scored_workspace_bytes(int T, int E, int k);
@@ -524,8 +526,12 @@ int moe_fp8b_quantize_weights(const uint16_t* w, int E, int R, int C, uint8_t* q
                               uint8_t* qT_or_null, float* sT_or_null, void* stream);
 
 /* The grouped products of moe_grouped_gemm_swiglu and its backward on block-128 E4M3 operands, one
- * kernel per call, fp32 accumulation, bf16 outputs; the expert row ranges are read from `offsets` on the
- * device, and output rows from offsets[E] on are left as they were.  d and f multiples of 64 (all of a
+ * kernel per call, block sums scaled and added in fp32, bf16 outputs; the expert row ranges are read from
+ * `offsets` on the device, and output rows from offsets[E] on are left as they were.  A block's sum is the fp8 matrix
+ * core's, which cuts products beside larger ones of the same 8 along K (rms error 2^-16 of the sum); gate_up and
+ * dgrad_down of fewer than 2048 result blocks (n ceil(f/128)), whose results are quantised again, and the kernel
+ * for few rows per expert have exact ones, so the last bits of a row may differ with the number of rows in
+ * the call.  d and f multiples of 64 (all of a
  * weight's and an activation's blocks along them start at multiples of 128).
  * gate_up: xq [n][d], xs [ceil(d/128)][n]; w_gate, w_up [E][f][d] with their block scales;
  *   a = silu(g) * u, and g, u where both are given (NULL: a serving pass that needs only a).
