@@ -12,6 +12,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoe_mi35
 _i = ctypes.c_int
 _sz = ctypes.c_size_t
 _p = ctypes.c_void_p
+_f = ctypes.c_float
 
 # name -> (restype, argtypes); the order and meaning of arguments follow include/moe_mi355x.h
 SIGNATURES = {
@@ -71,6 +72,16 @@ SIGNATURES = {
     "moe_grouped_gemm_dgrad_gate_up_fp8b": (_i, [_i] * 4 + [_p] * 11),
     "moe_grouped_gemm_wgrad_down_fp8b": (_i, [_i] * 4 + [_p] * 8),
     "moe_grouped_gemm_wgrad_gate_up_fp8b": (_i, [_i] * 4 + [_p] * 11),
+    "moe_dropout": (_i, [_p, _p, _p, _f, _i, _i, _i, _p, _p]),
+    "moe_unpermute_combine_dropout": (_i, [_p, _p, _p, _p, _p, _f, _i, _i, _i, _i, _p, _p]),
+    "moe_unpermute_combine_dropout_bwd": (_i, [_p, _p, _p, _p, _p, _f, _i, _i, _i, _i, _p, _p, _p]),
+    "moe_adapter_plan_bytes": (_sz, [_i, _i, _i]),
+    "moe_adapter_plan": (_i, [_p] * 3 + [_i] * 4 + [_p, _sz, _p]),
+    "moe_adapter_workspace_bytes": (_sz, [_i] * 6),
+    "moe_adapter_gate_up": (_i, [_p] * 5 + [_i] * 7 + [_p] * 5 + [_f, _i] + [_p] * 8 + [_sz, _p]),
+    "moe_adapter_down": (_i, [_p] * 5 + [_i] * 7 + [_p] * 4 + [_f, _i] + [_p] * 4 + [_sz, _p]),
+    "moe_adapter_down_bwd": (_i, [_p] * 7 + [_i] * 7 + [_p] * 4 + [_f, _i] + [_p] * 9 + [_sz, _p]),
+    "moe_adapter_gate_up_bwd": (_i, [_p] * 8 + [_i] * 7 + [_p] * 5 + [_f, _i] + [_p] * 6 + [_sz, _p]),
 }
 
 

@@ -1,0 +1,1077 @@
+// Low-rank adapters of many requests beside the experts' products: every routed row may have an adapter of
+// its own (its token's), and of each adapter the matrices of its expert take part.
+//
+// [news] "Ai2 rebuilds Olmo's training stack for trillion-parameter MoEs", lead paragraphs: a router sends each
+// token to a small selection of experts; "Routing work stays on the GPU": rows lie by expert in the expert
+// buffers, and what is known about them stays on the device.
+//
+// Three products make up the forward and the backward.  With W [R][C] the matrix of one adapter and expert:
+//   shrink   v[row][R]   = x[row][C] W^T       contracts over a long axis:  A x, and B^T dy, B^T dg in the backward
+//   expand   y[row][C]  += s v[row][R] W       contracts over the rank:     B v, and A^T dv in the backward
+//   wgrad    dW[R][C]    = v^T y               contracts over the rows of one adapter and expert
+// B is stored by rank like A ([R][out]), so each of them serves A and B.  All three move far more bytes than
+// the matrix cores need time for (R operations per byte of x or y), so they are built as streams: operands go
+// straight from memory into the fragments of v_mfma_f32_16x16x32_bf16, without LDS, and what the fragments would
+// have transposed is permuted in registers (expand, wgrad: a lane loads 16 bytes of each of 8 rows along the
+// contraction; the 8 columns that it holds become 8 column tiles, of which tile i takes column 8 c + i from lane
+// c, so its accumulators hold 8 neighbouring columns and leave as 16-byte stores).
+//
+// Rows are taken in tiles of up to 64 rows of one expert and adapter, from a list that adapter_plan makes on the
+// device by a stable sort of each expert's rows by adapter, so sums run in a fixed order.  For few rows there is no
+// list: every row is a tile.
+#include <hip/hip_runtime.h>
+
+#include "common.h"
+#include "dropout.h"
+
+namespace moe {
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kTileRows = 64;      // rows of a tile
+constexpr int kPlanChunk = 512;    // rows of one expert that a workgroup of the sort takes
+constexpr int kMaxRank = 64;
+constexpr int kMaxAdapters = 256;
+
+__device__ __forceinline__ f32x4 mfma(uint4 a, uint4 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+// ---------------------------------------------------------------- the plan
+
+// Rows of one piece of a group's contraction in the weight gradients: pieces enough for the chip where few
+// groups hold the rows, long enough that their fp32 partial sums (2 R C 4 bytes each) stay a fraction of the
+// rows' own bytes.
+__host__ __device__ inline int piece_rows(int n) {
+  const int want = (n + 63) / 64;
+  return want <= 512 ? 512 : want >= 2048 ? 2048 : (want + 31) / 32 * 32;
+}
+
+struct Tile {
+  int pos, count, e, l;   // rows [pos, pos + count) of the sorted list
+};
+
+// The plan's parts, as offsets in 4-byte words of its buffer.
+struct PlanLayout {
+  int chunks, pairs, tiles_cap, items_cap, multi_cap;
+  long long rows, goff, tile0, tiles, items, multi, hist, words;
+};
+
+constexpr int kHeadTiles = 0, kHeadItems = 1, kHeadMulti = 2, kHeadWords = 16;
+
+__host__ __device__ inline PlanLayout plan_layout(int n, int E, int L) {
+  PlanLayout p;
+  p.chunks = n / kPlanChunk + E;
+  p.pairs = E * (L + 1);
+  const int groups = n < p.pairs ? n : p.pairs;
+  p.tiles_cap = n / kTileRows + groups;
+  p.items_cap = n / piece_rows(n) + E * L;
+  p.multi_cap = n / piece_rows(n) + 1;
+  long long at = kHeadWords;
+  auto take = [&](long long words) {
+    const long long here = at;
+    at += (words + 3) / 4 * 4;
+    return here;
+  };
+  p.rows = take(n);
+  p.goff = take(p.pairs + 1);
+  p.tile0 = take(p.pairs);
+  p.tiles = take(4LL * p.tiles_cap);
+  p.items = take(4LL * p.items_cap);
+  p.multi = take(p.multi_cap);
+  p.hist = take(static_cast<long long>(p.chunks) * (L + 1));
+  p.words = at;
+  return p;
+}
+
+// Expert e's rows, whatever the offsets hold: within [0, n) and not negative in number.
+__device__ __forceinline__ int row_begin(const int32_t* offsets, int e, int n) {
+  const int o = offsets[e];
+  return o < 0 ? 0 : o > n ? n : o;
+}
+
+__device__ __forceinline__ int adapter_of(const int32_t* ids, const int32_t* row_token, int row, int T, int L) {
+  const int t = row_token != nullptr ? row_token[row] : row;
+  if (t < 0 || t >= T) return L;
+  const int l = ids[t];
+  return l >= 0 && l < L ? l : L;   // L: none
+}
+
+struct Chunk {
+  int e, begin, end, index;   // index < 0: there is none
+};
+
+// The rows that chunk `want` holds: chunks are counted expert by expert, each of up to kPlanChunk rows of one.
+// All 256 threads call it (E <= 256: thread e looks at expert e).
+__device__ __forceinline__ Chunk find_chunk(const int32_t* offsets, int E, int n, int want) {
+  __shared__ int sums[4], found[3];
+  const int e = threadIdx.x, lane = e & 63, wave = e >> 6;
+  int lo = 0, hi = 0;
+  if (e < E) {
+    lo = row_begin(offsets, e, n);
+    hi = row_begin(offsets, e + 1, n);
+  }
+  const int mine = hi > lo ? (hi - lo + kPlanChunk - 1) / kPlanChunk : 0;
+  int run = mine;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int v = __shfl_up(run, o, 64);
+    if (lane >= o) run += v;
+  }
+  if (lane == 63) sums[wave] = run;
+  if (e == 0) found[0] = -1;
+  __syncthreads();
+  int base = run - mine;
+  for (int w = 0; w < wave; ++w) base += sums[w];
+  if (want >= base && want < base + mine) {
+    found[0] = e;
+    found[1] = lo + (want - base) * kPlanChunk;
+    found[2] = hi;
+  }
+  __syncthreads();
+  Chunk c;
+  c.e = found[0];
+  c.index = c.e < 0 ? -1 : want;
+  c.begin = found[1];
+  c.end = min(found[2], found[1] + kPlanChunk);
+  return c;
+}
+
+// Rows of each adapter in every chunk.
+__global__ __launch_bounds__(256) void plan_count_kernel(const int32_t* __restrict__ ids, const int32_t* __restrict__ row_token,
+                                                         const int32_t* __restrict__ offsets, int T, int n, int E, int L,
+                                                         int32_t* __restrict__ plan) {
+  __shared__ int count[kMaxAdapters + 1];
+  const PlanLayout p = plan_layout(n, E, L);
+  const Chunk c = find_chunk(offsets, E, n, blockIdx.x);
+  if (c.index < 0) return;
+  for (int l = threadIdx.x; l <= L; l += 256) count[l] = 0;
+  __syncthreads();
+  for (int r = c.begin + threadIdx.x; r < c.end; r += 256) atomicAdd(&count[adapter_of(ids, row_token, r, T, L)], 1);
+  __syncthreads();
+  int32_t* hist = plan + p.hist + static_cast<long long>(blockIdx.x) * (L + 1);
+  for (int l = threadIdx.x; l <= L; l += 256) hist[l] = count[l];
+}
+
+// Exclusive sums over 1024 threads of four counts; `total` gets the sums over all.
+__device__ __forceinline__ int4 scan4(int4 v, int4* total) {
+  __shared__ int4 sums[16];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int4 run = v;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int4 u = make_int4(__shfl_up(run.x, o, 64), __shfl_up(run.y, o, 64), __shfl_up(run.z, o, 64), __shfl_up(run.w, o, 64));
+    if (lane >= o) run = make_int4(run.x + u.x, run.y + u.y, run.z + u.z, run.w + u.w);
+  }
+  if (lane == 63) sums[wave] = run;
+  __syncthreads();
+  int4 base = make_int4(0, 0, 0, 0), all = base;
+  for (int w = 0; w < 16; ++w) {
+    const int4 s = sums[w];
+    if (w < wave) base = make_int4(base.x + s.x, base.y + s.y, base.z + s.z, base.w + s.w);
+    all = make_int4(all.x + s.x, all.y + s.y, all.z + s.z, all.w + s.w);
+  }
+  *total = all;
+  return make_int4(base.x + run.x - v.x, base.y + run.y - v.y, base.z + run.z - v.z, base.w + run.w - v.w);
+}
+
+// Positions: of every (expert, adapter) in the sorted list, of its tiles, its pieces for the weight gradients and
+// of every chunk's rows of it.  One workgroup; a thread takes consecutive pairs (their number is E (L + 1)).
+__global__ __launch_bounds__(1024) void plan_scan_kernel(const int32_t* __restrict__ offsets, int n, int E, int L,
+                                                         int32_t* __restrict__ plan) {
+  __shared__ int chunk0[257];
+  const PlanLayout p = plan_layout(n, E, L);
+  int4 total;
+  {
+    int mine = 0;
+    if (threadIdx.x < static_cast<unsigned>(E)) {
+      const int lo = row_begin(offsets, threadIdx.x, n), hi = row_begin(offsets, threadIdx.x + 1, n);
+      mine = hi > lo ? (hi - lo + kPlanChunk - 1) / kPlanChunk : 0;
+    }
+    const int4 at = scan4(make_int4(mine, 0, 0, 0), &total);
+    if (threadIdx.x < static_cast<unsigned>(E)) chunk0[threadIdx.x] = at.x;
+    if (threadIdx.x == 0) chunk0[E] = total.x;
+    __syncthreads();
+  }
+  const int per = (p.pairs + 1023) / 1024, first = threadIdx.x * per, last = min(first + per, p.pairs);
+  const int piece = piece_rows(n);
+  int32_t* hist = plan + p.hist;
+  int32_t* goff = plan + p.goff;
+  int4 sum = make_int4(0, 0, 0, 0);   // rows, tiles, pieces, groups of several pieces
+  for (int q = first; q < last; ++q) {
+    const int e = q / (L + 1), l = q - e * (L + 1);
+    int rows = 0;
+    for (int c = chunk0[e]; c < chunk0[e + 1]; ++c) rows += hist[static_cast<long long>(c) * (L + 1) + l];
+    goff[q] = rows;
+    sum.x += rows;
+    sum.y += (rows + kTileRows - 1) / kTileRows;
+    if (l < L) {
+      sum.z += rows > piece ? (rows + piece - 1) / piece : 1;
+      sum.w += rows > piece;
+    }
+  }
+  int4 at = scan4(sum, &total);
+  Tile* items = reinterpret_cast<Tile*>(plan + p.items);
+  for (int q = first; q < last; ++q) {
+    const int e = q / (L + 1), l = q - e * (L + 1), rows = goff[q];
+    goff[q] = at.x;
+    plan[p.tile0 + q] = at.y;
+    int pos = at.x;
+    for (int c = chunk0[e]; c < chunk0[e + 1]; ++c) {
+      int32_t* h = &hist[static_cast<long long>(c) * (L + 1) + l];
+      const int here = *h;
+      *h = pos;
+      pos += here;
+    }
+    if (l < L) {
+      const int pieces = rows > piece ? (rows + piece - 1) / piece : 1;
+      for (int i = 0; i < pieces; ++i) items[at.z + i] = {at.x + i * piece, min(piece, rows - i * piece), e, l};
+      if (rows > piece) plan[p.multi + at.w] = q;
+      at.z += pieces;
+      at.w += rows > piece;
+    }
+    at.x += rows;
+    at.y += (rows + kTileRows - 1) / kTileRows;
+  }
+  if (threadIdx.x == 0) {
+    goff[p.pairs] = total.x;
+    plan[kHeadTiles] = total.y;
+    plan[kHeadItems] = total.z;
+    plan[kHeadMulti] = total.w;
+  }
+}
+
+// The sorted list and the tiles.  A row's rank among those of its adapter is its position's count of equal
+// adapters in the wave (ballots over the bits of the number), plus those of the chunk's earlier groups of 64.
+__global__ __launch_bounds__(256) void plan_place_kernel(const int32_t* __restrict__ ids, const int32_t* __restrict__ row_token,
+                                                         const int32_t* __restrict__ offsets, int T, int n, int E, int L,
+                                                         int32_t* __restrict__ plan) {
+  constexpr int kGroups = kPlanChunk / 64;
+  __shared__ int before[kGroups][kMaxAdapters + 1];
+  const PlanLayout p = plan_layout(n, E, L);
+  const Chunk c = find_chunk(offsets, E, n, blockIdx.x);
+  if (c.index < 0) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  for (int i = threadIdx.x; i < kGroups * (kMaxAdapters + 1); i += 256) (&before[0][0])[i] = 0;
+  __syncthreads();
+  int l[kGroups / 4], rank[kGroups / 4];
+#pragma unroll
+  for (int i = 0; i < kGroups / 4; ++i) {
+    const int g = i * 4 + wave, r = c.begin + g * 64 + lane;
+    const bool live = r < c.end;
+    l[i] = live ? adapter_of(ids, row_token, r, T, L) : -1;
+    unsigned long long same = __ballot(live);
+    for (int b = 0; b < 9; ++b) {
+      const unsigned long long set = __ballot((l[i] >> b) & 1);
+      same &= ((l[i] >> b) & 1) ? set : ~set;
+    }
+    rank[i] = __popcll(same & ((1ull << lane) - 1));
+    if (live && rank[i] == 0) before[g][l[i]] = __popcll(same);
+  }
+  __syncthreads();
+  for (int a = threadIdx.x; a <= L; a += 256) {
+    int run = plan[p.hist + static_cast<long long>(blockIdx.x) * (L + 1) + a];
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      const int here = before[g][a];
+      before[g][a] = run;
+      run += here;
+    }
+  }
+  __syncthreads();
+  Tile* tiles = reinterpret_cast<Tile*>(plan + p.tiles);
+#pragma unroll
+  for (int i = 0; i < kGroups / 4; ++i) {
+    const int g = i * 4 + wave, r = c.begin + g * 64 + lane;
+    if (r >= c.end) continue;
+    const int pos = before[g][l[i]] + rank[i], q = c.e * (L + 1) + l[i];
+    plan[p.rows + pos] = r;
+    const int in = pos - plan[p.goff + q];
+    if (in % kTileRows == 0)
+      tiles[plan[p.tile0 + q] + in / kTileRows] = {pos, min(kTileRows, plan[p.goff + q + 1] - pos), c.e, l[i]};
+  }
+}
+
+// ---------------------------------------------------------------- the rows of a call
+
+struct Rows {
+  const int32_t* plan;        // null: every row is a tile
+  const int32_t* ids;
+  const int32_t* row_token;   // null: row r is token r
+  const int32_t* offsets;
+  int T, n, E, L;
+};
+
+// Tile `i`'s place; count 0: there is none (past the list, or a row behind the last expert's).
+// Called with i uniform in the wave, all lanes.
+__device__ __forceinline__ Tile tile_at(const Rows& rows, const PlanLayout& p, int i) {
+  if (rows.plan != nullptr) return reinterpret_cast<const Tile*>(rows.plan + p.tiles)[i];
+  int e = 0;
+  for (int b = 0; b < rows.E; b += 64) {
+    const int at = b + (threadIdx.x & 63);
+    e += __popcll(__ballot(at < rows.E && rows.offsets[at + 1] <= i));
+  }
+  if (e >= rows.E || i < rows.offsets[0]) return {i, 0, 0, rows.L};
+  return {i, 1, e, __builtin_amdgcn_readfirstlane(adapter_of(rows.ids, rows.row_token, i, rows.T, rows.L))};
+}
+
+__device__ __forceinline__ int n_tiles(const Rows& rows) { return rows.plan != nullptr ? rows.plan[kHeadTiles] : rows.n; }
+
+// Row at sorted position pos (clamped by the caller to the tile).
+__device__ __forceinline__ int row_at(const Rows& rows, const PlanLayout& p, int pos) {
+  return rows.plan != nullptr ? rows.plan[p.rows + pos] : pos;
+}
+
+// ---------------------------------------------------------------- shrink
+
+struct ShrinkArgs {
+  Rows rows;
+  const uint16_t* x[2];    // up to two products in a launch (blockIdx.y): dg and du
+  const uint16_t* w[2];
+  int v0[2];               // their first columns in v
+  int gather;              // x by token (through row_token)
+  int K, R, ldv, S;        // S > 1: slices of K whose fp32 sums go to part [S][n][ldv]
+  const float* scale;      // null, or [L]: factor of v
+  uint16_t* v;
+  float* part;
+  DropArgs drop;
+};
+
+// One tile (NB blocks of 16 rows) times RT tiles of 16 ranks over K's units of 64 elements u0, u0 + 4, ...
+// A lane holds the rows 16 b + c and the ranks 16 t + c; rows past the tile and ranks past R are copies of the last
+// one, which nobody stores.
+template <int NB, int RT, bool DROP>
+__device__ __forceinline__ void shrink_tile(const ShrinkArgs& a, const Tile& t, const PlanLayout& p, const uint16_t* x,
+                                            const uint16_t* w, int u0, int u1, f32x4 (&acc)[NB][RT]) {
+  const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4;
+  const uint16_t* xp[NB];
+  const uint16_t* wp[RT];
+  uint32_t row[NB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    const int r = row_at(a.rows, p, t.pos + min(16 * b + c, t.count - 1));
+    int src = r;
+    if (a.gather && a.rows.row_token != nullptr) src = min(max(a.rows.row_token[r], 0), a.rows.T - 1);
+    row[b] = static_cast<uint32_t>(r);
+    xp[b] = x + static_cast<long long>(src) * a.K + 8 * q;
+#pragma unroll
+    for (int i = 0; i < RT; ++i) acc[b][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+#pragma unroll
+  for (int i = 0; i < RT; ++i) wp[i] = w + static_cast<long long>(min(16 * i + c, a.R - 1)) * a.K + 8 * q;
+  DropKey key;
+  if (DROP) key = drop_key(a.drop);
+  uint4 xf[NB][2], wf[RT][2];
+  auto load = [&](int u) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int b = 0; b < NB; ++b) xf[b][h] = *reinterpret_cast<const uint4*>(xp[b] + 64 * u + 32 * h);
+#pragma unroll
+      for (int i = 0; i < RT; ++i) wf[i][h] = *reinterpret_cast<const uint4*>(wp[i] + 64 * u + 32 * h);
+    }
+  };
+  if (u0 >= u1) return;
+  load(u0);
+  for (int u = u0; u < u1; u += 4) {
+    uint4 xc[NB][2], wc[RT][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int b = 0; b < NB; ++b) xc[b][h] = xf[b][h];
+#pragma unroll
+      for (int i = 0; i < RT; ++i) wc[i][h] = wf[i][h];
+    }
+    load(u + 4 < u1 ? u + 4 : u);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        if (DROP) xc[b][h] = drop_zero(key, row[b], 8 * u + 4 * h + q, xc[b][h]);
+#pragma unroll
+        for (int i = 0; i < RT; ++i) acc[b][i] = mfma(xc[b][h], wc[i][h], acc[b][i]);
+      }
+    }
+  }
+}
+
+// The four waves' sums joined through LDS, two tiles of ranks at a time, and stored.
+template <int NB, int RT, bool DROP>
+__device__ __forceinline__ void shrink_run(const ShrinkArgs& a, const Tile& t, const PlanLayout& p, int which, int slice,
+                                           f32x4* lds) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int units = a.K / 64;
+  const int s0 = static_cast<int>(static_cast<long long>(units) * slice / a.S);
+  const int s1 = static_cast<int>(static_cast<long long>(units) * (slice + 1) / a.S);
+  const uint16_t* w = a.w[which] + (static_cast<long long>(t.l) * a.rows.E + t.e) * a.R * a.K;
+  f32x4 acc[NB][RT];
+  shrink_tile<NB, RT, DROP>(a, t, p, a.x[which], w, s0 + wave, s1, acc);
+  float f = a.scale != nullptr ? a.scale[t.l] : 1.f;
+  if (DROP) f *= drop_scale(a.drop.drop);
+  constexpr int G = RT < 2 ? RT : 2;
+#pragma unroll
+  for (int i0 = 0; i0 < RT; i0 += G) {
+    __syncthreads();
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int i = 0; i < G; ++i) lds[((wave * NB + b) * G + i) * 64 + lane] = acc[b][i0 + i];
+    __syncthreads();
+    for (int at = threadIdx.x; at < NB * G * 64; at += 256) {
+      f32x4 s = lds[at];
+#pragma unroll
+      for (int o = 1; o < 4; ++o) s += lds[o * NB * G * 64 + at];
+      const int b = at / (G * 64), rank = 16 * (i0 + at / 64 % G) + (at & 15), m = 16 * b + 4 * (at >> 4 & 3);
+      if (rank >= a.R) continue;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (m + j >= t.count) break;
+        const long long r = row_at(a.rows, p, t.pos + m + j);
+        if (a.S > 1)
+          a.part[(static_cast<long long>(slice) * a.rows.n + r) * a.ldv + a.v0[which] + rank] = f * s[j];
+        else
+          a.v[r * a.ldv + a.v0[which] + rank] = f32_to_bf16(f * s[j]);
+      }
+    }
+  }
+}
+
+template <int RT, bool DROP>
+__global__ __launch_bounds__(256) void adapter_shrink_kernel(ShrinkArgs a) {
+  __shared__ f32x4 lds[4 * 4 * (RT < 2 ? RT : 2) * 64];
+  const PlanLayout p = plan_layout(a.rows.n, a.rows.E, a.rows.L);
+  const long long items = static_cast<long long>(n_tiles(a.rows)) * a.S;
+  const int which = blockIdx.y;
+  for (long long i = blockIdx.x; i < items; i += gridDim.x) {
+    const Tile t = tile_at(a.rows, p, static_cast<int>(i / a.S));
+    const int slice = static_cast<int>(i % a.S);
+    if (t.count == 0) continue;
+    if (t.l >= a.rows.L) {   // no adapter: v is 0 (with slices, expand writes that)
+      if (a.S == 1)
+        for (int at = threadIdx.x; at < t.count * a.R; at += 256)
+          a.v[static_cast<long long>(row_at(a.rows, p, t.pos + at / a.R)) * a.ldv + a.v0[which] + at % a.R] = 0;
+      continue;
+    }
+    const int nb = (t.count + 15) / 16;
+    if (nb == 1) shrink_run<1, RT, DROP>(a, t, p, which, slice, lds);
+    else if (nb == 2) shrink_run<2, RT, DROP>(a, t, p, which, slice, lds);
+    else if (nb == 3) shrink_run<3, RT, DROP>(a, t, p, which, slice, lds);
+    else shrink_run<4, RT, DROP>(a, t, p, which, slice, lds);
+  }
+}
+
+// ---------------------------------------------------------------- expand
+
+enum { kAdd = 0, kSwiglu = 1, kSwigluBwd = 2 };
+
+struct ExpandArgs {
+  Rows rows;
+  const uint16_t* v;        // [n][ldv], or part [S][n][ldv]
+  const float* part;
+  int ldv, S, R, N;         // R: ranks of one product
+  const uint16_t* w[2];     // kSwiglu: gate and up (v's columns [0, R) and [R, 2 R))
+  const float* scale;       // null, or [L]
+  const uint16_t* in[4];    // kAdd: y; kSwiglu: g, u, a; kSwigluBwd: g, u, dg, du
+  uint16_t* out[3];         // kAdd: y; kSwiglu: g, u (or null), a; kSwigluBwd: dg, du
+  uint16_t* v_out;          // with slices: v, where it is wanted
+  DropArgs drop;
+};
+
+// Logistic function with the hardware reciprocal (about 1 ulp), as the experts' products have it.
+__device__ __forceinline__ float logistic(float x) { return __builtin_amdgcn_rcpf(1.0f + __expf(-x)); }
+
+__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
+  f[0] = bf16_lo(v.x); f[1] = bf16_hi(v.x); f[2] = bf16_lo(v.y); f[3] = bf16_hi(v.y);
+  f[4] = bf16_lo(v.z); f[5] = bf16_hi(v.z); f[6] = bf16_lo(v.w); f[7] = bf16_hi(v.w);
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+}
+
+// 8 rows (the contraction) of 8 columns -> for each column its 8 rows: tile i's fragment is o[i].
+__device__ __forceinline__ void transpose8(const uint4 (&r)[8], uint4 (&o)[8]) {
+  const uint32_t* in = reinterpret_cast<const uint32_t*>(r);
+  uint32_t* out = reinterpret_cast<uint32_t*>(o);
+#pragma unroll
+  for (int j = 0; j < 4; ++j)        // rows 2 j, 2 j + 1
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {    // columns 2 h, 2 h + 1
+      const uint32_t lo = in[(2 * j) * 4 + h], hi = in[(2 * j + 1) * 4 + h];
+      out[(2 * h) * 4 + j] = __builtin_amdgcn_perm(hi, lo, 0x05040100u);
+      out[(2 * h + 1) * 4 + j] = __builtin_amdgcn_perm(hi, lo, 0x07060302u);
+    }
+}
+
+// w's fragments for 128 columns: ranks 32 k + 8 q .. + 7 of the columns that the lane holds, 0 past R.
+template <int KS>
+__device__ __forceinline__ void load_w(const uint16_t* w, int R, int N, int col, uint4 (&f)[KS][8]) {
+  const int q = (threadIdx.x & 63) >> 4;
+#pragma unroll
+  for (int k = 0; k < KS; ++k) {
+    uint4 r[8];
+    const bool live = 32 * k + 8 * q < R;
+    const uint16_t* at = w + static_cast<long long>(live ? 32 * k + 8 * q : 0) * N + col;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      r[j] = *reinterpret_cast<const uint4*>(at + static_cast<long long>(j) * N);
+      if (!live) r[j] = make_uint4(0, 0, 0, 0);
+    }
+    transpose8(r, f[k]);
+  }
+}
+
+// 8 ranks of one row of v, 0 past R; from slices: their fp32 sums in slice order, rounded once.
+__device__ __forceinline__ uint4 load_v(const ExpandArgs& a, long long row, int col) {
+  if (a.S == 1) return *reinterpret_cast<const uint4*>(a.v + row * a.ldv + col);
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = 0.f;
+  for (int s = 0; s < a.S; ++s) {
+    const float4* at = reinterpret_cast<const float4*>(a.part + (static_cast<long long>(s) * a.rows.n + row) * a.ldv + col);
+    const float4 lo = at[0], hi = at[1];
+    f[0] += lo.x; f[1] += lo.y; f[2] += lo.z; f[3] += lo.w;
+    f[4] += hi.x; f[5] += hi.y; f[6] += hi.z; f[7] += hi.w;
+  }
+  return pack8(f);
+}
+
+template <int KS, int MODE, bool DROP>
+__global__ __launch_bounds__(256) void adapter_expand_kernel(ExpandArgs a) {
+  constexpr int NW = MODE == kSwiglu ? 2 : 1;
+  constexpr int NOUT = MODE == kAdd ? 1 : MODE == kSwiglu ? 3 : 2;
+  const PlanLayout p = plan_layout(a.rows.n, a.rows.E, a.rows.L);
+  const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4;
+  const int stripes = (a.N + 127) / 128;
+  const long long items = static_cast<long long>(n_tiles(a.rows)) * stripes, step = gridDim.x * 4LL;
+  DropKey key;
+  if (DROP) key = drop_key(a.drop);
+  for (long long i = blockIdx.x * 4LL + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); i < items; i += step) {
+    const Tile t = tile_at(a.rows, p, static_cast<int>(i / stripes));
+    const int stripe = static_cast<int>(i % stripes);
+    if (t.count == 0) continue;
+    const int col = 128 * stripe + 8 * c;
+    const bool live = col < a.N;        // the last stripe may be half
+    const int cc = live ? col : 0;
+    if (t.l >= a.rows.L) {              // no adapter: copies
+      if (a.v_out != nullptr && stripe == 0)
+        for (int at = lane; at < t.count * a.ldv; at += 64)
+          a.v_out[static_cast<long long>(row_at(a.rows, p, t.pos + at / a.ldv)) * a.ldv + at % a.ldv] = 0;
+      for (int m = q; m < t.count; m += 4) {
+        const long long at = static_cast<long long>(row_at(a.rows, p, t.pos + m)) * a.N + cc;
+#pragma unroll
+        for (int o = 0; o < NOUT; ++o)
+          if (live && a.out[o] != nullptr)
+            *reinterpret_cast<uint4*>(a.out[o] + at) = *reinterpret_cast<const uint4*>(a.in[MODE == kSwigluBwd ? o + 2 : o] + at);
+      }
+      continue;
+    }
+    uint4 wf[NW][KS][8];
+    const long long g = (static_cast<long long>(t.l) * a.rows.E + t.e) * a.R * a.N;
+#pragma unroll
+    for (int m = 0; m < NW; ++m) load_w<KS>(a.w[m] + g, a.R, a.N, cc, wf[m]);
+    float f = a.scale != nullptr ? a.scale[t.l] : 1.f;
+    if (DROP) f *= drop_scale(a.drop.drop);
+    const int nb = (t.count + 15) / 16;
+    for (int b = 0; b < nb; ++b) {
+      const int mine = row_at(a.rows, p, t.pos + min(16 * b + c, t.count - 1));
+      int row[4];
+      uint4 in[4][MODE == kAdd ? 1 : MODE == kSwiglu ? 2 : 4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        row[j] = __shfl(mine, 4 * q + j, 64);
+        const long long at = static_cast<long long>(row[j]) * a.N + cc;
+#pragma unroll
+        for (int o = 0; o < (MODE == kAdd ? 1 : MODE == kSwiglu ? 2 : 4); ++o)
+          in[j][o] = *reinterpret_cast<const uint4*>(a.in[o] + at);
+      }
+      f32x4 acc[NW][8];
+#pragma unroll
+      for (int m = 0; m < NW; ++m) {
+#pragma unroll
+        for (int o = 0; o < 8; ++o) acc[m][o] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          const int rank = 32 * k + 8 * q;
+          uint4 vf = make_uint4(0, 0, 0, 0);
+          if (rank < a.R) {
+            vf = load_v(a, mine, m * a.R + rank);
+            if (a.v_out != nullptr && stripe == 0 && 16 * b + c < t.count)
+              *reinterpret_cast<uint4*>(a.v_out + static_cast<long long>(mine) * a.ldv + m * a.R + rank) = vf;
+          }
+#pragma unroll
+          for (int o = 0; o < 8; ++o) acc[m][o] = mfma(vf, wf[m][k][o], acc[m][o]);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (16 * b + 4 * q + j >= t.count || !live) continue;
+        const long long at = static_cast<long long>(row[j]) * a.N + col;
+        float x0[8], x1[8];
+        unpack8(in[j][0], x0);
+        if constexpr (MODE == kAdd) {
+          float delta[8];
+#pragma unroll
+          for (int o = 0; o < 8; ++o) delta[o] = acc[0][o][j];
+          if (DROP) drop_apply(key, row[j], col >> 3, 1.f, delta);
+#pragma unroll
+          for (int o = 0; o < 8; ++o) x0[o] = fmaf(f, delta[o], x0[o]);
+          *reinterpret_cast<uint4*>(a.out[0] + at) = pack8(x0);
+        } else if constexpr (MODE == kSwiglu) {
+          float y[8];
+          unpack8(in[j][1], x1);
+#pragma unroll
+          for (int o = 0; o < 8; ++o) {
+            x0[o] = fmaf(f, acc[0][o][j], x0[o]);
+            x1[o] = fmaf(f, acc[NW - 1][o][j], x1[o]);
+            y[o] = x0[o] * logistic(x0[o]) * x1[o];
+          }
+          if (a.out[0] != nullptr) {
+            *reinterpret_cast<uint4*>(a.out[0] + at) = pack8(x0);
+            *reinterpret_cast<uint4*>(a.out[1] + at) = pack8(x1);
+          }
+          *reinterpret_cast<uint4*>(a.out[2] + at) = pack8(y);
+        } else {
+          float dg[8], du[8], delta[8];
+          unpack8(in[j][1], x1);
+          unpack8(in[j][2], dg);
+          unpack8(in[j][3], du);
+#pragma unroll
+          for (int o = 0; o < 8; ++o) delta[o] = acc[0][o][j];
+          if (DROP) drop_apply(key, row[j], col >> 3, 1.f, delta);
+#pragma unroll
+          for (int o = 0; o < 8; ++o) {
+            const float s = logistic(x0[o]), da = f * delta[o];
+            dg[o] = fmaf(da * x1[o], s * fmaf(x0[o], 1.f - s, 1.f), dg[o]);
+            du[o] = fmaf(da, x0[o] * s, du[o]);
+          }
+          *reinterpret_cast<uint4*>(a.out[0] + at) = pack8(dg);
+          *reinterpret_cast<uint4*>(a.out[1] + at) = pack8(du);
+        }
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- wgrad
+
+struct WgradArgs {
+  Rows rows;
+  const uint16_t* v;        // [n][ldv]
+  int v0[2];                // first columns of up to two products (blockIdx.y): gate and up
+  const uint16_t* y[2];
+  int gather;               // y by token
+  int ldv, R, C;
+  const float* scale;       // null, or [L]
+  uint16_t* out[2];         // [L][E][R][C]
+  float* part;              // [2 products][2 (n / piece + 1)][R][C]: sums of pieces of groups that have several
+  DropArgs drop;
+};
+
+// Slot of a piece that starts at `pos`: pieces of one group start `piece` apart, and a group's first one never lies in the same
+// `piece` positions as another group's first, nor a later one as another's later one (groups of several
+// pieces are longer than that), so a bit for the first keeps all apart.
+__device__ __forceinline__ long long piece_slot(int pos, int piece, bool first) { return 2LL * (pos / piece) + first; }
+
+// RT tiles of 16 ranks (from rank r0) x 128 columns over the rows of one piece, 32 rows a step.
+template <int RT, bool DROP>
+__global__ __launch_bounds__(256) void adapter_wgrad_kernel(WgradArgs a) {
+  const PlanLayout p = plan_layout(a.rows.n, a.rows.E, a.rows.L);
+  const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4;
+  const int stripes = (a.C + 127) / 128, parts = (a.R + 16 * RT - 1) / (16 * RT), which = blockIdx.y;
+  const int piece = piece_rows(a.rows.n);
+  const long long items = static_cast<long long>(a.rows.plan[kHeadItems]) * parts * stripes, step = gridDim.x * 4LL;
+  const uint16_t* y = a.y[which];
+  DropKey key;
+  if (DROP) key = drop_key(a.drop);
+  for (long long i = blockIdx.x * 4LL + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); i < items; i += step) {
+    const Tile t = reinterpret_cast<const Tile*>(a.rows.plan + p.items)[i / (parts * stripes)];
+    const int stripe = static_cast<int>(i % stripes), r0 = static_cast<int>(i / stripes % parts) * 16 * RT;
+    const int col = 128 * stripe + 8 * c, cc = col < a.C ? col : 0;
+    f32x4 acc[RT][8];
+#pragma unroll
+    for (int m = 0; m < RT; ++m)
+#pragma unroll
+      for (int o = 0; o < 8; ++o) acc[m][o] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const uint16_t* v = a.v + a.v0[which];
+    for (int s = 0; s < t.count; s += 32) {
+      const int left = t.count - s;
+      const int mine = a.rows.plan[p.rows + t.pos + s + min(lane & 31, left - 1)];
+      int src = mine;
+      if (a.gather && a.rows.row_token != nullptr) src = min(max(a.rows.row_token[mine], 0), a.rows.T - 1);
+      uint4 yr[8];
+      int row[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        row[j] = __shfl(mine, 8 * q + j, 64);
+        yr[j] = *reinterpret_cast<const uint4*>(y + static_cast<long long>(__shfl(src, 8 * q + j, 64)) * a.C + cc);
+      }
+      uint4 vf[RT];
+      if constexpr (RT == 1) {
+        // ranks r0 + c: 8 rows' values of one rank each
+        const int rank = min(r0 + c, a.R - 1);
+        uint32_t w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = 8 * q + j < left ? v[static_cast<long long>(row[j]) * a.ldv + rank] : 0u;
+        vf[0] = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+      } else {
+        // two tiles at a time take the even and the odd ones of 32 ranks: 4 bytes of 8 rows
+#pragma unroll
+        for (int m = 0; m < RT; m += 2) {
+          const int rank = min(r0 + 16 * m + 2 * c, a.R - 2);
+          uint32_t w[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            w[j] = 8 * q + j < left ? *reinterpret_cast<const uint32_t*>(v + static_cast<long long>(row[j]) * a.ldv + rank) : 0u;
+          uint32_t lo[4], hi[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            lo[j] = __builtin_amdgcn_perm(w[2 * j + 1], w[2 * j], 0x05040100u);
+            hi[j] = __builtin_amdgcn_perm(w[2 * j + 1], w[2 * j], 0x07060302u);
+          }
+          vf[m] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          vf[m + 1] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        }
+      }
+      if (DROP) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) yr[j] = drop_zero(key, row[j], cc >> 3, yr[j]);
+      }
+      if (left < 32) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (8 * q + j >= left) yr[j] = make_uint4(0, 0, 0, 0);
+      }
+      uint4 yf[8];
+      transpose8(yr, yf);
+#pragma unroll
+      for (int m = 0; m < RT; ++m)
+#pragma unroll
+        for (int o = 0; o < 8; ++o) acc[m][o] = mfma(vf[m], yf[o], acc[m][o]);
+    }
+    float f = a.scale != nullptr ? a.scale[t.l] : 1.f;
+    if (DROP) f *= drop_scale(a.drop.drop);
+    const int32_t* goff = a.rows.plan + p.goff + t.e * (a.rows.L + 1) + t.l;
+    const bool several = goff[1] - goff[0] > piece;
+    uint16_t* out = a.out[which] + (static_cast<long long>(t.l) * a.rows.E + t.e) * a.R * a.C;
+    float* part = a.part + ((which * 2LL * (a.rows.n / piece + 1)) + piece_slot(t.pos, piece, t.pos == goff[0])) * a.R * a.C;
+#pragma unroll
+    for (int m = 0; m < RT; ++m) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        // accumulator row 4 q + j of tile m
+        const int rank = RT == 1 ? r0 + 4 * q + j : r0 + 16 * (m & ~1) + 2 * (4 * q + j) + (m & 1);
+        if (rank >= a.R || col >= a.C) continue;
+        const long long at = static_cast<long long>(rank) * a.C + col;
+        float x[8];
+#pragma unroll
+        for (int o = 0; o < 8; ++o) x[o] = f * acc[m][o][j];
+        if (several) {
+          *reinterpret_cast<float4*>(part + at) = make_float4(x[0], x[1], x[2], x[3]);
+          *reinterpret_cast<float4*>(part + at + 4) = make_float4(x[4], x[5], x[6], x[7]);
+        } else {
+          *reinterpret_cast<uint4*>(out + at) = pack8(x);
+        }
+      }
+    }
+  }
+}
+
+// Groups of several pieces: their sums in the order of the pieces.  gridDim.x workgroups to a group.
+__global__ __launch_bounds__(256) void adapter_join_kernel(WgradArgs a) {
+  const PlanLayout p = plan_layout(a.rows.n, a.rows.E, a.rows.L);
+  const int which = blockIdx.z, piece = piece_rows(a.rows.n);
+  if (static_cast<int>(blockIdx.y) >= a.rows.plan[kHeadMulti]) return;
+  const int pair = a.rows.plan[p.multi + blockIdx.y], e = pair / (a.rows.L + 1), l = pair - e * (a.rows.L + 1);
+  const int begin = a.rows.plan[p.goff + pair], end = a.rows.plan[p.goff + pair + 1];
+  const long long size = static_cast<long long>(a.R) * a.C;
+  const float* part = a.part + which * 2LL * (a.rows.n / piece + 1) * size;
+  uint16_t* out = a.out[which] + (static_cast<long long>(l) * a.rows.E + e) * size;
+  for (long long i = (blockIdx.x * 256LL + threadIdx.x) * 8; i < size; i += gridDim.x * 2048LL) {
+    float x[8];
+#pragma unroll
+    for (int o = 0; o < 8; ++o) x[o] = 0.f;
+    for (int pos = begin; pos < end; pos += piece) {
+      const float4* at = reinterpret_cast<const float4*>(part + piece_slot(pos, piece, pos == begin) * size + i);
+      const float4 lo = at[0], hi = at[1];
+      x[0] += lo.x; x[1] += lo.y; x[2] += lo.z; x[3] += lo.w;
+      x[4] += hi.x; x[5] += hi.y; x[6] += hi.z; x[7] += hi.w;
+    }
+    *reinterpret_cast<uint4*>(out + i) = pack8(x);
+  }
+}
+
+// ---------------------------------------------------------------- host side
+
+constexpr int kGridCap = 8192;   // workgroups of a launch; more tiles are taken in turn
+
+int tiles_cap(const Rows& r) { return r.plan != nullptr ? plan_layout(r.n, r.E, r.L).tiles_cap : r.n; }
+
+// Slices of K: enough workgroups for the chip where there are few tiles, each with a unit for every wave.
+int slices(bool planned, int n, int K) {
+  const long long tiles = planned ? (n + kTileRows - 1) / kTileRows : n;
+  const int most = (K / 64 + 3) / 4;
+  const long long want = 512 / tiles;
+  const int s = want < 1 ? 1 : want > 16 ? 16 : static_cast<int>(want);
+  return s < most ? s : most;
+}
+
+unsigned grid_of(long long workgroups) { return static_cast<unsigned>(workgroups < kGridCap ? workgroups : kGridCap); }
+
+template <bool DROP>
+void launch_shrink(const ShrinkArgs& a, int products, hipStream_t st) {
+  const dim3 grid(grid_of(static_cast<long long>(tiles_cap(a.rows)) * a.S), products);
+  if (a.R <= 16) adapter_shrink_kernel<1, DROP><<<grid, 256, 0, st>>>(a);
+  else if (a.R <= 32) adapter_shrink_kernel<2, DROP><<<grid, 256, 0, st>>>(a);
+  else if (a.R <= 64) adapter_shrink_kernel<4, DROP><<<grid, 256, 0, st>>>(a);
+  else adapter_shrink_kernel<8, DROP><<<grid, 256, 0, st>>>(a);
+}
+
+template <int MODE, bool DROP>
+void launch_expand(const ExpandArgs& a, hipStream_t st) {
+  const unsigned grid = grid_of((static_cast<long long>(tiles_cap(a.rows)) * ((a.N + 127) / 128) + 3) / 4);
+  if (a.R <= 32) adapter_expand_kernel<1, MODE, DROP><<<grid, 256, 0, st>>>(a);
+  else if (a.R <= 64) adapter_expand_kernel<2, MODE, DROP><<<grid, 256, 0, st>>>(a);
+  else if constexpr (MODE == kAdd) adapter_expand_kernel<4, MODE, DROP><<<grid, 256, 0, st>>>(a);
+}
+
+template <bool DROP>
+void launch_wgrad(const WgradArgs& a, int products, hipStream_t st) {
+  const PlanLayout p = plan_layout(a.rows.n, a.rows.E, a.rows.L);
+  const int rt = a.R <= 16 ? 1 : a.R <= 32 ? 2 : 4;
+  const long long waves = static_cast<long long>(p.items_cap) * ((a.R + 16 * rt - 1) / (16 * rt)) * ((a.C + 127) / 128);
+  const dim3 grid(grid_of((waves + 3) / 4), products);
+  if (rt == 1) adapter_wgrad_kernel<1, DROP><<<grid, 256, 0, st>>>(a);
+  else if (rt == 2) adapter_wgrad_kernel<2, DROP><<<grid, 256, 0, st>>>(a);
+  else adapter_wgrad_kernel<4, DROP><<<grid, 256, 0, st>>>(a);
+  const int piece = piece_rows(a.rows.n);
+  if (a.rows.n > piece) {
+    const long long blocks = (static_cast<long long>(a.R) * a.C + 2047) / 2048;
+    adapter_join_kernel<<<dim3(static_cast<unsigned>(blocks < 64 ? blocks : 64), p.multi_cap, products), 256, 0, st>>>(a);
+  }
+}
+
+int check_sizes(int T, int n, int E, int L) {
+  MOE_REQUIRE(T >= 1 && n >= 1, MOE_ERR_UNSUPPORTED, "T and n must be >= 1 (got %d, %d)", T, n);
+  MOE_REQUIRE(E >= 1 && E <= 256, MOE_ERR_UNSUPPORTED, "E must be in [1, 256] (got %d)", E);
+  MOE_REQUIRE(L >= 1 && L <= kMaxAdapters, MOE_ERR_UNSUPPORTED, "adapters must be 1 to %d in number (got %d)", kMaxAdapters, L);
+  MOE_REQUIRE(n <= 1 << 26, MOE_ERR_UNSUPPORTED, "n must be at most 2^26 (got %d)", n);
+  return MOE_OK;
+}
+
+int check_rows(const Rows& r) {
+  if (int st = check_sizes(r.T, r.n, r.E, r.L)) return st;
+  MOE_CHECK_PTR(r.ids); MOE_CHECK_PTR(r.offsets);
+  MOE_REQUIRE(r.row_token != nullptr || r.T == r.n, MOE_ERR_INVALID_ARG, "without row_token n = %d must be T = %d", r.n, r.T);
+  if (r.plan) MOE_CHECK_ALIGN(r.plan);
+  return MOE_OK;
+}
+
+int check_dims(int d, int f, int r) {
+  MOE_REQUIRE(d >= 64 && d % 64 == 0, MOE_ERR_UNSUPPORTED, "d must be a positive multiple of 64 (got %d)", d);
+  MOE_REQUIRE(f >= 64 && f % 64 == 0, MOE_ERR_UNSUPPORTED, "f must be a positive multiple of 64 (got %d)", f);
+  MOE_REQUIRE(r >= 8 && r <= kMaxRank && r % 8 == 0, MOE_ERR_UNSUPPORTED, "r must be a multiple of 8 in [8, %d] (got %d)",
+              kMaxRank, r);
+  return MOE_OK;
+}
+
+long long align256(long long b) { return (b + 255) / 256 * 256; }
+
+// Bytes of v (bf16), of its slices and of the weight gradients' pieces for a product pair of widths K -> R.
+long long v_bytes(int n, int R) { return align256(2LL * n * R); }
+long long part_bytes(bool planned, int n, int R, int K) {
+  const int s = slices(planned, n, K);
+  return s > 1 ? align256(4LL * s * n * R) : 0;
+}
+long long piece_bytes(int n, int products, int R, int C) {
+  const int piece = piece_rows(n);
+  return n > piece ? align256(4LL * products * 2 * (n / piece + 1) * R * C) : 0;
+}
+
+long long forward_bytes(bool planned, int n, int R, int K) { return v_bytes(n, R) + part_bytes(planned, n, R, K); }
+
+long long max_ll(long long a, long long b) { return a > b ? a : b; }
+
+long long down_bwd_bytes(int n, int d, int f, int r) {
+  return v_bytes(n, r) + max_ll(part_bytes(true, n, r, d), max_ll(piece_bytes(n, 1, r, d), piece_bytes(n, 1, r, f)));
+}
+long long gate_up_bwd_bytes(int n, int d, int f, int r) {
+  return v_bytes(n, 2 * r) +
+         max_ll(part_bytes(true, n, 2 * r, f), max_ll(piece_bytes(n, 2, r, f), piece_bytes(n, 1, 2 * r, d)));
+}
+
+#define MOE_CHECK_WS(need)                                                                                     \
+  do {                                                                                                         \
+    MOE_REQUIRE(ws != nullptr && ws_bytes >= static_cast<size_t>(need), MOE_ERR_WORKSPACE,                     \
+                "workspace of %lld bytes needed", static_cast<long long>(need));                               \
+    MOE_CHECK_ALIGN(ws);                                                                                       \
+  } while (0)
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" size_t moe_adapter_plan_bytes(int n, int E, int L) {
+  if (check_sizes(1, n, E, L)) return 0;
+  return static_cast<size_t>(plan_layout(n, E, L).words) * 4;
+}
+
+extern "C" int moe_adapter_plan(const int32_t* ids, const int32_t* row_token, const int32_t* offsets, int T, int n,
+                                int E, int L, void* plan, size_t plan_bytes, void* stream) {
+  const Rows rows = {nullptr, ids, row_token, offsets, T, n, E, L};
+  if (int st = check_rows(rows)) return st;
+  const PlanLayout p = plan_layout(n, E, L);
+  MOE_REQUIRE(plan != nullptr && plan_bytes >= static_cast<size_t>(p.words) * 4, MOE_ERR_WORKSPACE,
+              "plan buffer of %lld bytes needed", p.words * 4);
+  MOE_CHECK_ALIGN(plan);
+  hipStream_t st = as_stream(stream);
+  int32_t* buf = static_cast<int32_t*>(plan);
+  plan_count_kernel<<<p.chunks, 256, 0, st>>>(ids, row_token, offsets, T, n, E, L, buf);
+  plan_scan_kernel<<<1, 1024, 0, st>>>(offsets, n, E, L, buf);
+  plan_place_kernel<<<p.chunks, 256, 0, st>>>(ids, row_token, offsets, T, n, E, L, buf);
+  return check_launch("adapter_plan");
+}
+
+extern "C" size_t moe_adapter_workspace_bytes(int n, int d, int f, int r, int planned, int backward) {
+  if (check_sizes(1, n, 1, 1) || check_dims(d, f, r)) return 0;
+  const bool p = planned != 0;
+  if (backward) return static_cast<size_t>(max_ll(down_bwd_bytes(n, d, f, r), gate_up_bwd_bytes(n, d, f, r)));
+  return static_cast<size_t>(max_ll(forward_bytes(p, n, 2 * r, d), forward_bytes(p, n, r, f)));
+}
+
+extern "C" int moe_adapter_gate_up(const uint16_t* x, const int32_t* ids, const int32_t* row_token, const int32_t* offsets,
+                                   const void* plan, int T, int n, int E, int L, int d, int f, int r,
+                                   const uint16_t* a_gu, const uint16_t* b_gate, const uint16_t* b_up, const float* scale,
+                                   const int64_t* rng, float p, int site, const uint16_t* g, const uint16_t* u,
+                                   const uint16_t* a, uint16_t* v, uint16_t* g_out, uint16_t* u_out, uint16_t* a_out,
+                                   void* ws, size_t ws_bytes, void* stream) {
+  const Rows rows = {static_cast<const int32_t*>(plan), ids, row_token, offsets, T, n, E, L};
+  if (int st = check_rows(rows)) return st;
+  if (int st = check_dims(d, f, r)) return st;
+  MOE_CHECK_PTR(x); MOE_CHECK_PTR(a_gu); MOE_CHECK_PTR(b_gate); MOE_CHECK_PTR(b_up); MOE_CHECK_PTR(scale);
+  MOE_CHECK_PTR(g); MOE_CHECK_PTR(u); MOE_CHECK_PTR(a); MOE_CHECK_PTR(a_out);
+  MOE_CHECK_ALIGN(x); MOE_CHECK_ALIGN(a_gu); MOE_CHECK_ALIGN(b_gate); MOE_CHECK_ALIGN(b_up);
+  MOE_CHECK_ALIGN(g); MOE_CHECK_ALIGN(u); MOE_CHECK_ALIGN(a); MOE_CHECK_ALIGN(v);
+  MOE_CHECK_ALIGN(g_out); MOE_CHECK_ALIGN(u_out); MOE_CHECK_ALIGN(a_out);
+  MOE_REQUIRE((g_out == nullptr) == (u_out == nullptr), MOE_ERR_INVALID_ARG, "g_out and u_out are wanted both or neither");
+  DropArgs drop;
+  if (int st = make_drop(rng, p, site, &drop)) return st;
+  MOE_CHECK_WS(forward_bytes(plan != nullptr, n, 2 * r, d));
+  uint16_t* vbuf = v != nullptr ? v : static_cast<uint16_t*>(ws);
+  float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + v_bytes(n, 2 * r));
+  const int S = slices(plan != nullptr, n, d);
+  ShrinkArgs s = {rows, {x, nullptr}, {a_gu, nullptr}, {0, 0}, 1, d, 2 * r, 2 * r, S, nullptr, vbuf, part, drop};
+  hipStream_t st = as_stream(stream);
+  if (drop.drop) launch_shrink<true>(s, 1, st);
+  else launch_shrink<false>(s, 1, st);
+  ExpandArgs e = {rows, vbuf, part, 2 * r, S, r, f, {b_gate, b_up}, scale, {g, u, a, nullptr}, {g_out, u_out, a_out},
+                  S > 1 ? v : nullptr, DropArgs{}};
+  launch_expand<kSwiglu, false>(e, st);
+  return check_launch("adapter_gate_up");
+}
+
+extern "C" int moe_adapter_down(const uint16_t* a, const int32_t* ids, const int32_t* row_token, const int32_t* offsets,
+                                const void* plan, int T, int n, int E, int L, int d, int f, int r, const uint16_t* a_down,
+                                const uint16_t* b_down, const float* scale, const int64_t* rng, float p, int site,
+                                const uint16_t* yexp, uint16_t* v, uint16_t* y_out, void* ws, size_t ws_bytes, void* stream) {
+  const Rows rows = {static_cast<const int32_t*>(plan), ids, row_token, offsets, T, n, E, L};
+  if (int st = check_rows(rows)) return st;
+  if (int st = check_dims(d, f, r)) return st;
+  MOE_CHECK_PTR(a); MOE_CHECK_PTR(a_down); MOE_CHECK_PTR(b_down); MOE_CHECK_PTR(scale); MOE_CHECK_PTR(yexp);
+  MOE_CHECK_PTR(y_out);
+  MOE_CHECK_ALIGN(a); MOE_CHECK_ALIGN(a_down); MOE_CHECK_ALIGN(b_down); MOE_CHECK_ALIGN(yexp); MOE_CHECK_ALIGN(v);
+  MOE_CHECK_ALIGN(y_out);
+  DropArgs drop;
+  if (int st = make_drop(rng, p, site, &drop)) return st;
+  MOE_CHECK_WS(forward_bytes(plan != nullptr, n, r, f));
+  uint16_t* vbuf = v != nullptr ? v : static_cast<uint16_t*>(ws);
+  float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + v_bytes(n, r));
+  const int S = slices(plan != nullptr, n, f);
+  ShrinkArgs s = {rows, {a, nullptr}, {a_down, nullptr}, {0, 0}, 0, f, r, r, S, nullptr, vbuf, part, drop};
+  hipStream_t st = as_stream(stream);
+  if (drop.drop) launch_shrink<true>(s, 1, st);
+  else launch_shrink<false>(s, 1, st);
+  ExpandArgs e = {rows, vbuf, part, r, S, r, d, {b_down, nullptr}, scale, {yexp, nullptr, nullptr, nullptr},
+                  {y_out, nullptr, nullptr}, S > 1 ? v : nullptr, DropArgs{}};
+  launch_expand<kAdd, false>(e, st);
+  return check_launch("adapter_down");
+}
+
+extern "C" int moe_adapter_down_bwd(const uint16_t* dyexp, const uint16_t* a, const uint16_t* v, const int32_t* ids,
+                                    const int32_t* row_token, const int32_t* offsets, const void* plan, int T, int n, int E,
+                                    int L, int d, int f, int r, const uint16_t* a_down, const uint16_t* b_down,
+                                    const float* scale, const int64_t* rng, float p, int site, const uint16_t* g,
+                                    const uint16_t* u, const uint16_t* dg, const uint16_t* du, uint16_t* dg_out,
+                                    uint16_t* du_out, uint16_t* d_a_down, uint16_t* d_b_down, void* ws, size_t ws_bytes,
+                                    void* stream) {
+  const Rows rows = {static_cast<const int32_t*>(plan), ids, row_token, offsets, T, n, E, L};
+  if (int st = check_rows(rows)) return st;
+  if (int st = check_dims(d, f, r)) return st;
+  MOE_CHECK_PTR(plan);
+  MOE_CHECK_PTR(dyexp); MOE_CHECK_PTR(a); MOE_CHECK_PTR(v); MOE_CHECK_PTR(a_down); MOE_CHECK_PTR(b_down);
+  MOE_CHECK_PTR(scale); MOE_CHECK_PTR(g); MOE_CHECK_PTR(u); MOE_CHECK_PTR(dg); MOE_CHECK_PTR(du);
+  MOE_CHECK_PTR(dg_out); MOE_CHECK_PTR(du_out); MOE_CHECK_PTR(d_a_down); MOE_CHECK_PTR(d_b_down);
+  MOE_CHECK_ALIGN(dyexp); MOE_CHECK_ALIGN(a); MOE_CHECK_ALIGN(v); MOE_CHECK_ALIGN(a_down); MOE_CHECK_ALIGN(b_down);
+  MOE_CHECK_ALIGN(g); MOE_CHECK_ALIGN(u); MOE_CHECK_ALIGN(dg); MOE_CHECK_ALIGN(du); MOE_CHECK_ALIGN(dg_out);
+  MOE_CHECK_ALIGN(du_out); MOE_CHECK_ALIGN(d_a_down); MOE_CHECK_ALIGN(d_b_down);
+  DropArgs drop;
+  if (int st = make_drop(rng, p, site, &drop)) return st;
+  MOE_CHECK_WS(down_bwd_bytes(n, d, f, r));
+  uint16_t* dv = static_cast<uint16_t*>(ws);
+  float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + v_bytes(n, r));
+  const int S = slices(true, n, d);
+  hipStream_t st = as_stream(stream);
+  const ShrinkArgs s = {rows, {dyexp, nullptr}, {b_down, nullptr}, {0, 0}, 0, d, r, r, S, scale, dv, part, DropArgs{}};
+  launch_shrink<false>(s, 1, st);
+  const ExpandArgs e = {rows, dv, part, r, S, r, f, {a_down, nullptr}, nullptr, {g, u, dg, du}, {dg_out, du_out, nullptr},
+                        S > 1 ? dv : nullptr, drop};
+  if (drop.drop) launch_expand<kSwigluBwd, true>(e, st);
+  else launch_expand<kSwigluBwd, false>(e, st);
+  const WgradArgs wb = {rows, v, {0, 0}, {dyexp, nullptr}, 0, r, r, d, scale, {d_b_down, nullptr}, part, DropArgs{}};
+  launch_wgrad<false>(wb, 1, st);
+  const WgradArgs wa = {rows, dv, {0, 0}, {a, nullptr}, 0, r, r, f, nullptr, {d_a_down, nullptr}, part, drop};
+  if (drop.drop) launch_wgrad<true>(wa, 1, st);
+  else launch_wgrad<false>(wa, 1, st);
+  return check_launch("adapter_down_bwd");
+}
+
+extern "C" int moe_adapter_gate_up_bwd(const uint16_t* dg, const uint16_t* du, const uint16_t* x, const uint16_t* v,
+                                       const int32_t* ids, const int32_t* row_token, const int32_t* offsets,
+                                       const void* plan, int T, int n, int E, int L, int d, int f, int r,
+                                       const uint16_t* a_gu, const uint16_t* b_gate, const uint16_t* b_up,
+                                       const float* scale, const int64_t* rng, float p, int site, const uint16_t* dxp,
+                                       uint16_t* dxp_out, uint16_t* d_a_gu, uint16_t* d_b_gate, uint16_t* d_b_up, void* ws,
+                                       size_t ws_bytes, void* stream) {
+  const Rows rows = {static_cast<const int32_t*>(plan), ids, row_token, offsets, T, n, E, L};
+  if (int st = check_rows(rows)) return st;
+  if (int st = check_dims(d, f, r)) return st;
+  MOE_CHECK_PTR(plan);
+  MOE_CHECK_PTR(dg); MOE_CHECK_PTR(du); MOE_CHECK_PTR(x); MOE_CHECK_PTR(v); MOE_CHECK_PTR(a_gu); MOE_CHECK_PTR(b_gate);
+  MOE_CHECK_PTR(b_up); MOE_CHECK_PTR(scale); MOE_CHECK_PTR(dxp); MOE_CHECK_PTR(dxp_out); MOE_CHECK_PTR(d_a_gu);
+  MOE_CHECK_PTR(d_b_gate); MOE_CHECK_PTR(d_b_up);
+  MOE_CHECK_ALIGN(dg); MOE_CHECK_ALIGN(du); MOE_CHECK_ALIGN(x); MOE_CHECK_ALIGN(v); MOE_CHECK_ALIGN(a_gu);
+  MOE_CHECK_ALIGN(b_gate); MOE_CHECK_ALIGN(b_up); MOE_CHECK_ALIGN(dxp); MOE_CHECK_ALIGN(dxp_out);
+  MOE_CHECK_ALIGN(d_a_gu); MOE_CHECK_ALIGN(d_b_gate); MOE_CHECK_ALIGN(d_b_up);
+  DropArgs drop;
+  if (int st = make_drop(rng, p, site, &drop)) return st;
+  MOE_CHECK_WS(gate_up_bwd_bytes(n, d, f, r));
+  uint16_t* dv = static_cast<uint16_t*>(ws);
+  float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + v_bytes(n, 2 * r));
+  const int S = slices(true, n, f);
+  hipStream_t st = as_stream(stream);
+  const ShrinkArgs s = {rows, {dg, du}, {b_gate, b_up}, {0, r}, 0, f, r, 2 * r, S, scale, dv, part, DropArgs{}};
+  launch_shrink<false>(s, 2, st);
+  const ExpandArgs e = {rows, dv, part, 2 * r, S, 2 * r, d, {a_gu, nullptr}, nullptr, {dxp, nullptr, nullptr, nullptr},
+                        {dxp_out, nullptr, nullptr}, S > 1 ? dv : nullptr, drop};
+  if (drop.drop) launch_expand<kAdd, true>(e, st);
+  else launch_expand<kAdd, false>(e, st);
+  const WgradArgs wb = {rows, v, {0, r}, {dg, du}, 0, 2 * r, r, f, scale, {d_b_gate, d_b_up}, part, DropArgs{}};
+  launch_wgrad<false>(wb, 2, st);
+  const WgradArgs wa = {rows, dv, {0, 0}, {x, nullptr}, 1, 2 * r, 2 * r, d, nullptr, {d_a_gu, nullptr}, part, drop};
+  if (drop.drop) launch_wgrad<true>(wa, 1, st);
+  else launch_wgrad<false>(wa, 1, st);
+  return check_launch("adapter_gate_up_bwd");
+}

@@ -12,6 +12,9 @@
 // rows (and gates) are read once per wave (lanes j < k load dest[t, j]) and kept in scalar
 // registers.  The combine backward, which also reduces whole rows to dot products, gives each
 // wave one token.  Accumulation is fp32 in slot order j = 0..k-1.
+#include <cmath>
+
+#include "dropout.h"
 #include "mx_common.h"
 
 namespace moe {
@@ -139,11 +142,13 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
                     pack_bf16x2(f[6], f[7]));
 }
 
-// y[t] = sum_j gate[t,j] * yexp[dest[t,j]]   (bf16 rows of d elements), fp32 in slot order
-template <int KM>
+// y[t] = sum_j gate[t,j] * yexp[dest[t,j]]   (bf16 rows of d elements), fp32 in slot order.
+// DROP: the sum times the dropout factors of y's elements, plus the residual's row where there is one, rounded once.
+template <int KM, bool DROP>
 __global__ __launch_bounds__(256) void combine_kernel(const uint16_t* __restrict__ yexp, const float* __restrict__ gate,
                                                       const int32_t* __restrict__ dest, int T, int d, int k, int nseg,
-                                                      uint16_t* __restrict__ y) {
+                                                      uint16_t* __restrict__ y, const uint16_t* __restrict__ res,
+                                                      DropArgs drop) {
   const SegItem it = seg_item(nseg);
   if (it.t >= T) return;
   int rows[KM];
@@ -156,6 +161,8 @@ __global__ __launch_bounds__(256) void combine_kernel(const uint16_t* __restrict
 #pragma unroll
   for (int j = 0; j < KM; ++j)
     if (j < k) v[j] = reinterpret_cast<const uint4*>(yexp + static_cast<long long>(rows[j]) * d)[it.c];
+  uint4 vres = make_uint4(0, 0, 0, 0);
+  if (DROP && res != nullptr) vres = reinterpret_cast<const uint4*>(res + it.t * d)[it.c];
   float acc[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) acc[i] = 0.f;
@@ -168,15 +175,46 @@ __global__ __launch_bounds__(256) void combine_kernel(const uint16_t* __restrict
       for (int i = 0; i < 8; ++i) acc[i] = fmaf(g[j], f[i], acc[i]);
     }
   }
+  if (DROP) {
+    if (drop.drop != 0) drop_apply(drop_key(drop), static_cast<uint32_t>(it.t), it.c, drop_scale(drop.drop), acc);
+    if (res != nullptr) {
+      float f[8];
+      unpack8(vres, f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] += f[i];
+    }
+  }
   reinterpret_cast<uint4*>(y + it.t * d)[it.c] = pack8(acc);
 }
 
+// y = the dropout factors times x (+ res): rows of d elements, one segment per wave.
+__global__ __launch_bounds__(256) void dropout_kernel(const uint16_t* __restrict__ x, int T, int d, int nseg,
+                                                      const uint16_t* __restrict__ res, uint16_t* __restrict__ y,
+                                                      DropArgs drop) {
+  const SegItem it = seg_item(nseg);
+  if (it.t >= T || it.c >= d / 8) return;
+  const uint4 v = reinterpret_cast<const uint4*>(x + it.t * d)[it.c];
+  uint4 vres = make_uint4(0, 0, 0, 0);
+  if (res != nullptr) vres = reinterpret_cast<const uint4*>(res + it.t * d)[it.c];
+  float f[8];
+  unpack8(v, f);
+  if (drop.drop != 0) drop_apply(drop_key(drop), static_cast<uint32_t>(it.t), it.c, drop_scale(drop.drop), f);
+  if (res != nullptr) {
+    float g[8];
+    unpack8(vres, g);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] += g[i];
+  }
+  reinterpret_cast<uint4*>(y + it.t * d)[it.c] = pack8(f);
+}
+
 // dyexp[dest[t,j]] = bf16(gate[t,j] * dy[t]);  d_gate[t,j] = <dy[t], yexp[dest[t,j]]>
-template <int KM>
+// DROP: with dy[t] times the dropout factors of y's elements, in fp32, for dy[t].
+template <int KM, bool DROP>
 __global__ __launch_bounds__(256) void combine_bwd_kernel(const uint16_t* __restrict__ dy, const uint16_t* __restrict__ yexp,
                                                           const float* __restrict__ gate, const int32_t* __restrict__ dest,
                                                           int T, int d, int k, uint16_t* __restrict__ dyexp,
-                                                          float* __restrict__ dgate) {
+                                                          float* __restrict__ dgate, DropArgs drop) {
   const long long t = static_cast<long long>(blockIdx.x) * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
   if (t >= T) return;
@@ -193,6 +231,17 @@ __global__ __launch_bounds__(256) void combine_bwd_kernel(const uint16_t* __rest
 #pragma unroll
     for (int u = 0; u < kUBwd; ++u)
       if (c0 + 64 * u < chunks) vdy[u] = dyrow[c0 + 64 * u];
+    [[maybe_unused]] float fd[kUBwd][8];
+    if constexpr (DROP) {
+      const DropKey key = drop_key(drop);
+#pragma unroll
+      for (int u = 0; u < kUBwd; ++u) {
+        if (c0 + 64 * u < chunks) {
+          unpack8(vdy[u], fd[u]);
+          if (drop.drop != 0) drop_apply(key, static_cast<uint32_t>(t), c0 + 64 * u, drop_scale(drop.drop), fd[u]);
+        }
+      }
+    }
 #pragma unroll
     for (int j = 0; j < KM; ++j) {
       if (j < k) {
@@ -206,7 +255,12 @@ __global__ __launch_bounds__(256) void combine_bwd_kernel(const uint16_t* __rest
         for (int u = 0; u < kUBwd; ++u) {
           if (c0 + 64 * u < chunks) {
             float fdy[8], fy[8], o[8];
-            unpack8(vdy[u], fdy);
+            if constexpr (DROP) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) fdy[i] = fd[u][i];
+            } else {
+              unpack8(vdy[u], fdy);
+            }
             unpack8(vy[u], fy);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -368,7 +422,29 @@ unsigned seg_grid(int T, int nseg) {
     else KERNEL<16><<<(GRID), 256, 0, (STREAM)>>>(__VA_ARGS__);                 \
   } while (0)
 
+// The same of a kernel with a second template argument.
+#define MOE_SEG_LAUNCH2(KERNEL, ARG, GRID, STREAM, K, ...)                         \
+  do {                                                                            \
+    if ((K) <= 4) KERNEL<4, ARG><<<(GRID), 256, 0, (STREAM)>>>(__VA_ARGS__);       \
+    else if ((K) <= 8) KERNEL<8, ARG><<<(GRID), 256, 0, (STREAM)>>>(__VA_ARGS__);  \
+    else KERNEL<16, ARG><<<(GRID), 256, 0, (STREAM)>>>(__VA_ARGS__);               \
+  } while (0)
+
 }  // namespace
+
+int make_drop(const int64_t* rng, float p, int site, DropArgs* out) {
+  // p in [0, 1) up to where it still rounds below 1 in steps of 2^-16 (a NaN fails the comparison)
+  MOE_REQUIRE(p >= 0.f && p * 65536.f < 65535.5f, MOE_ERR_INVALID_ARG,
+              "p = %g must be in [0, 1), at most 1 - 2^-16 after rounding to a multiple of 2^-16", static_cast<double>(p));
+  MOE_REQUIRE(site >= 0 && site < 16, MOE_ERR_INVALID_ARG, "site = %d must be in [0, 16)", site);
+  out->drop = static_cast<uint32_t>(rintf(p * 65536.f));
+  out->site = static_cast<uint32_t>(site);
+  out->rng = rng;
+  MOE_REQUIRE(out->drop == 0 || rng != nullptr, MOE_ERR_INVALID_ARG, "null pointer: rng");
+  MOE_REQUIRE((reinterpret_cast<uintptr_t>(rng) & 7u) == 0, MOE_ERR_INVALID_ARG, "pointer not 8-byte aligned: rng");
+  return MOE_OK;
+}
+
 }  // namespace moe
 
 using namespace moe;
@@ -416,8 +492,53 @@ extern "C" int moe_unpermute_combine(const uint16_t* yexp, const float* gate, co
   MOE_CHECK_ALIGN(yexp); MOE_CHECK_ALIGN(y);
   const int nseg = segs_of(d / 8);
   MOE_REQUIRE(static_cast<long long>(T) * nseg * 64 < (1LL << 32), MOE_ERR_UNSUPPORTED, "too many row segments");
-  MOE_SEG_LAUNCH(combine_kernel, seg_grid(T, nseg), as_stream(stream), k, yexp, gate, dest, T, d, k, nseg, y);
+  MOE_SEG_LAUNCH2(combine_kernel, false, seg_grid(T, nseg), as_stream(stream), k, yexp, gate, dest, T, d, k, nseg, y,
+                  nullptr, DropArgs{});
   return check_launch("combine");
+}
+
+extern "C" int moe_dropout(const uint16_t* x, const uint16_t* res, const int64_t* rng, float p, int site, int T, int d,
+                           uint16_t* y, void* stream) {
+  if (int st = check_rows(T, d, 1)) return st;
+  MOE_CHECK_PTR(x); MOE_CHECK_PTR(y);
+  MOE_CHECK_ALIGN(x); MOE_CHECK_ALIGN(y);
+  if (res) MOE_CHECK_ALIGN(res);
+  DropArgs drop;
+  if (int st = make_drop(rng, p, site, &drop)) return st;
+  const int nseg = segs_of(d / 8);
+  MOE_REQUIRE(static_cast<long long>(T) * nseg * 64 < (1LL << 32), MOE_ERR_UNSUPPORTED, "too many row segments");
+  dropout_kernel<<<seg_grid(T, nseg), 256, 0, as_stream(stream)>>>(x, T, d, nseg, res, y, drop);
+  return check_launch("dropout");
+}
+
+extern "C" int moe_unpermute_combine_dropout(const uint16_t* yexp, const float* gate, const int32_t* dest,
+                                             const uint16_t* res, const int64_t* rng, float p, int site, int T, int d,
+                                             int k, uint16_t* y, void* stream) {
+  if (int st = check_rows(T, d, k)) return st;
+  MOE_CHECK_PTR(yexp); MOE_CHECK_PTR(gate); MOE_CHECK_PTR(dest); MOE_CHECK_PTR(y);
+  MOE_CHECK_ALIGN(yexp); MOE_CHECK_ALIGN(y);
+  if (res) MOE_CHECK_ALIGN(res);
+  DropArgs drop;
+  if (int st = make_drop(rng, p, site, &drop)) return st;
+  const int nseg = segs_of(d / 8);
+  MOE_REQUIRE(static_cast<long long>(T) * nseg * 64 < (1LL << 32), MOE_ERR_UNSUPPORTED, "too many row segments");
+  MOE_SEG_LAUNCH2(combine_kernel, true, seg_grid(T, nseg), as_stream(stream), k, yexp, gate, dest, T, d, k, nseg, y, res,
+                  drop);
+  return check_launch("combine_dropout");
+}
+
+extern "C" int moe_unpermute_combine_dropout_bwd(const uint16_t* dy, const uint16_t* yexp, const float* gate,
+                                                 const int32_t* dest, const int64_t* rng, float p, int site, int T,
+                                                 int d, int k, uint16_t* dyexp, float* dgate, void* stream) {
+  if (int st = check_rows(T, d, k)) return st;
+  MOE_CHECK_PTR(dy); MOE_CHECK_PTR(yexp); MOE_CHECK_PTR(gate); MOE_CHECK_PTR(dest);
+  MOE_CHECK_PTR(dyexp); MOE_CHECK_PTR(dgate);
+  MOE_CHECK_ALIGN(dy); MOE_CHECK_ALIGN(yexp); MOE_CHECK_ALIGN(dyexp);
+  DropArgs drop;
+  if (int st = make_drop(rng, p, site, &drop)) return st;
+  MOE_SEG_LAUNCH2(combine_bwd_kernel, true, grid_for(T), as_stream(stream), k, dy, yexp, gate, dest, T, d, k, dyexp,
+                  dgate, drop);
+  return check_launch("combine_dropout_bwd");
 }
 
 extern "C" int moe_unpermute_combine_bwd(const uint16_t* dy, const uint16_t* yexp, const float* gate,
@@ -427,7 +548,8 @@ extern "C" int moe_unpermute_combine_bwd(const uint16_t* dy, const uint16_t* yex
   MOE_CHECK_PTR(dy); MOE_CHECK_PTR(yexp); MOE_CHECK_PTR(gate); MOE_CHECK_PTR(dest);
   MOE_CHECK_PTR(dyexp); MOE_CHECK_PTR(dgate);
   MOE_CHECK_ALIGN(dy); MOE_CHECK_ALIGN(yexp); MOE_CHECK_ALIGN(dyexp);
-  MOE_SEG_LAUNCH(combine_bwd_kernel, grid_for(T), as_stream(stream), k, dy, yexp, gate, dest, T, d, k, dyexp, dgate);
+  MOE_SEG_LAUNCH2(combine_bwd_kernel, false, grid_for(T), as_stream(stream), k, dy, yexp, gate, dest, T, d, k, dyexp,
+                  dgate, DropArgs{});
   return check_launch("combine_bwd");
 }
 

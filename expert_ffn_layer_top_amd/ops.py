@@ -10,6 +10,8 @@ Tensor conventions: bf16 tensors are torch.bfloat16; E4M3 elements and E8M0 scal
 torch.uint8 bytes; indices are torch.int32; gates and logits are torch.float32.
 """
 
+from dataclasses import dataclass
+
 import torch
 
 from ._lib import call, lib
@@ -406,6 +408,249 @@ def permute_bwd_router(dxp, dest, w_r, d_logits):
     call("moe_permute_bwd_router", _ptr(dxp), _ptr(dest), T, d, k, _ptr(w_r), _ptr(d_logits), E, _ptr(dx),
          _ptr(ws), nbytes, _stream(dxp))
     return dx
+
+
+# ---------------------------------------------------------------- dropout
+
+@dataclass(frozen=True)
+class Dropout:
+    """Random zeros with probability p (rounded to a multiple of 2^-16), the rest times 1 / (1 - p); the mask is never
+    stored.  rng: [2] int64 on the GPU, seed and offset of a counter-based generator: the same ones give the
+    same zeros (a backward needs them as its forward had them), another offset independent ones; the
+    kernels read them, so a replayed graph sees what the program wrote there.  site (0 to 15) keeps the matrices of one step apart."""
+    p: float
+    rng: torch.Tensor
+    site: int = 0
+
+
+def _drop(drop):
+    """(pointer of rng or None, p, site, rng or None) of a Dropout or None."""
+    if drop is None:
+        return None, 0.0, 0, None
+    if type(drop) is not Dropout:
+        raise TypeError(f"expected a Dropout, got {type(drop).__name__}")
+    if not 0.0 <= drop.p * 65536.0 < 65535.5:
+        raise ValueError(f"p = {drop.p} must be in [0, 1), at most 1 - 2^-16 after rounding to a multiple of 2^-16")
+    if not 0 <= drop.site < 16:
+        raise ValueError(f"site = {drop.site} must be in [0, 16)")
+    _is(drop.rng, torch.int64, (2,), "rng")
+    return drop.rng.data_ptr(), float(drop.p), int(drop.site), drop.rng
+
+
+def dropout(x, drop, residual=None):
+    """y [T,d] bf16 = the dropout factors times x [T,d] (+ residual), rounded once.  Its gradient is the same call
+    on dy with the same drop."""
+    T, d = _dims(x, torch.bfloat16, 2, "x")
+    if residual is not None:
+        _is(residual, torch.bfloat16, (T, d), "residual")
+    p_rng, p, site, rng = _drop(drop)
+    dev = _device_of(x, residual, rng)
+    y = _new((T, d), torch.bfloat16, dev)
+    _call_on(dev, "moe_dropout", _ptr(x), _ptr(residual), p_rng, p, site, T, d, _ptr(y))
+    return y
+
+
+def unpermute_combine_dropout(yexp, topk_gate, dest, drop, residual=None):
+    """y [T,d] bf16 = unpermute_combine's sum times the dropout factors (+ residual [T,d] bf16), rounded once."""
+    T, k = _dims(dest, torch.int32, 2, "dest")
+    d = _dims(yexp, torch.bfloat16, 2, "yexp")[1]
+    _is(yexp, torch.bfloat16, (T * k, d), "yexp")
+    _is(topk_gate, torch.float32, (T, k), "topk_gate")
+    if residual is not None:
+        _is(residual, torch.bfloat16, (T, d), "residual")
+    p_rng, p, site, rng = _drop(drop)
+    dev = _device_of(yexp, topk_gate, dest, residual, rng)
+    y = _new((T, d), torch.bfloat16, dev)
+    _call_on(dev, "moe_unpermute_combine_dropout", _ptr(yexp), _ptr(topk_gate), _ptr(dest), _ptr(residual), p_rng, p,
+             site, T, d, k, _ptr(y))
+    return y
+
+
+def unpermute_combine_dropout_bwd(dy, yexp, topk_gate, dest, drop):
+    """(dyexp [n,d] bf16, d_gate [T,k] fp32) of unpermute_combine_dropout with the same drop (the residual's gradient is
+    dy itself)."""
+    T, k = _dims(dest, torch.int32, 2, "dest")
+    d = _dims(dy, torch.bfloat16, 2, "dy")[1]
+    _is(dy, torch.bfloat16, (T, d), "dy")
+    _is(yexp, torch.bfloat16, (T * k, d), "yexp")
+    _is(topk_gate, torch.float32, (T, k), "topk_gate")
+    p_rng, p, site, rng = _drop(drop)
+    dev = _device_of(dy, yexp, topk_gate, dest, rng)
+    dyexp = _new((T * k, d), torch.bfloat16, dev)
+    dgate = _new((T, k), torch.float32, dev)
+    _call_on(dev, "moe_unpermute_combine_dropout_bwd", _ptr(dy), _ptr(yexp), _ptr(topk_gate), _ptr(dest), p_rng, p, site,
+             T, d, k, _ptr(dyexp), _ptr(dgate))
+    return dyexp, dgate
+
+
+# ---------------------------------------------------------------- low-rank adapters
+
+# Up to this many rows every row reads its adapter by itself in the forward; more are sorted by adapter first.
+ADAPTER_FEW_ROWS = 1024
+
+
+class AdapterPlan:
+    """Which adapter each routed row has (adapter_plan), as the adapter calls take it.  It holds for as long as its tensors
+    keep their contents."""
+
+    __slots__ = ("ids", "offsets", "row_token", "buf", "T", "n", "E", "L", "dev")
+
+    def _args(self):
+        return (_ptr(self.ids), _ptr(self.row_token), _ptr(self.offsets), _ptr(self.buf), self.T, self.n, self.E, self.L)
+
+
+def adapter_plan(ids, offsets, n_adapters, row_token=None, backward=False):
+    """An AdapterPlan of ids [T] int32 (each token's adapter; outside [0, n_adapters): none), the router's offsets [E+1]
+    and row_token [n] (None: row r is token r, n = T).  backward: for adapter_*_bwd too, whose sums need the rows
+    sorted by expert and adapter; without it few rows (n <= ADAPTER_FEW_ROWS) are left as they are."""
+    T = _dims(ids, torch.int32, 1, "ids")[0]
+    E = _dims(offsets, torch.int32, 1, "offsets")[0] - 1
+    n = T if row_token is None else _dims(row_token, torch.int32, 1, "row_token")[0]
+    if not (1 <= E <= 256 and 1 <= n_adapters <= 256):
+        raise ValueError(f"need 1 to 256 experts and adapters, got {E} and {n_adapters}")
+    if not (T >= 1 and 1 <= n <= 1 << 26):
+        raise ValueError(f"need T >= 1 tokens and 1 to 2^26 rows, got {T} and {n}")
+    plan = AdapterPlan()
+    plan.dev = dev = _device_of(ids, offsets, row_token)
+    plan.ids, plan.offsets, plan.row_token = ids, offsets, row_token
+    plan.T, plan.n, plan.E, plan.L = T, n, E, int(n_adapters)
+    plan.buf = None
+    if backward or n > ADAPTER_FEW_ROWS:
+        nbytes = lib.moe_adapter_plan_bytes(n, E, plan.L)
+        plan.buf = _new((nbytes,), torch.uint8, dev)
+        _call_on(dev, "moe_adapter_plan", _ptr(ids), _ptr(row_token), _ptr(offsets), T, n, E, plan.L, _ptr(plan.buf),
+                 nbytes)
+    return plan
+
+
+def _adapter_sizes(plan, r, d, f):
+    if type(plan) is not AdapterPlan:
+        raise TypeError(f"plan: expected an AdapterPlan, got {type(plan).__name__}")
+    if d < 64 or f < 64 or d % 64 or f % 64:
+        raise ValueError(f"d = {d} and f = {f} must be positive multiples of 64")
+    if not 8 <= r <= 64 or r % 8:
+        raise ValueError(f"rank r = {r} must be a multiple of 8 in [8, 64]")
+
+
+def _adapter_gu(plan, a_gu, b_gate, b_up, scale):
+    """(r, d, f) of the gate/up matrices, checked."""
+    if type(plan) is not AdapterPlan:
+        raise TypeError(f"plan: expected an AdapterPlan, got {type(plan).__name__}")
+    r, f = _dims(b_gate, torch.bfloat16, 4, "b_gate")[2:]
+    d = _dims(a_gu, torch.bfloat16, 4, "a_gu")[3]
+    _is(a_gu, torch.bfloat16, (plan.L, plan.E, 2 * r, d), "a_gu")
+    _is(b_gate, torch.bfloat16, (plan.L, plan.E, r, f), "b_gate")
+    _is(b_up, torch.bfloat16, (plan.L, plan.E, r, f), "b_up")
+    _is(scale, torch.float32, (plan.L,), "scale")
+    _adapter_sizes(plan, r, d, f)
+    return r, d, f
+
+
+def _adapter_d(plan, a_down, b_down, scale):
+    if type(plan) is not AdapterPlan:
+        raise TypeError(f"plan: expected an AdapterPlan, got {type(plan).__name__}")
+    r, f = _dims(a_down, torch.bfloat16, 4, "a_down")[2:]
+    d = _dims(b_down, torch.bfloat16, 4, "b_down")[3]
+    _is(a_down, torch.bfloat16, (plan.L, plan.E, r, f), "a_down")
+    _is(b_down, torch.bfloat16, (plan.L, plan.E, r, d), "b_down")
+    _is(scale, torch.float32, (plan.L,), "scale")
+    _adapter_sizes(plan, r, d, f)
+    return r, d, f
+
+
+def _adapter_ws(plan, d, f, r, backward):
+    nbytes = lib.moe_adapter_workspace_bytes(plan.n, d, f, r, plan.buf is not None, backward)
+    return _new((nbytes,), torch.uint8, plan.dev), nbytes
+
+
+def adapter_gate_up(x, g, u, a, plan, a_gu, b_gate, b_up, scale, drop=None, want_gu=True, want_v=False):
+    """(g, u, a [n,f], v [n,2r]) bf16: the first grouped product's g, u and a with every row's adapter added before SwiGLU
+    (rows without one: copies).  x [T,d] by token; a_gu [L,E,2r,d] (gate's ranks, then up's), b_gate, b_up [L,E,r,f]
+    (by rank), scale [L] fp32; drop: dropout of the adapters' input.  g and u are None without want_gu (a serving pass);
+    v, which the backward takes, without want_v."""
+    r, d, f = _adapter_gu(plan, a_gu, b_gate, b_up, scale)
+    n = plan.n
+    _is(x, torch.bfloat16, (plan.T, d), "x")
+    _is(g, torch.bfloat16, (n, f), "g")
+    _is(u, torch.bfloat16, (n, f), "u")
+    _is(a, torch.bfloat16, (n, f), "a")
+    p_rng, p, site, rng = _drop(drop)
+    dev = _device_of(plan.ids, x, g, u, a, a_gu, b_gate, b_up, scale, rng)
+    g2 = _new((n, f), torch.bfloat16, dev) if want_gu else None
+    u2 = _new((n, f), torch.bfloat16, dev) if want_gu else None
+    a2 = _new((n, f), torch.bfloat16, dev)
+    v = _new((n, 2 * r), torch.bfloat16, dev) if want_v else None
+    ws, nbytes = _adapter_ws(plan, d, f, r, False)
+    _call_on(dev, "moe_adapter_gate_up", _ptr(x), *plan._args(), d, f, r, _ptr(a_gu), _ptr(b_gate), _ptr(b_up),
+             _ptr(scale), p_rng, p, site, _ptr(g), _ptr(u), _ptr(a), _ptr(v), _ptr(g2), _ptr(u2), _ptr(a2), _ptr(ws), nbytes)
+    return g2, u2, a2, v
+
+
+def adapter_down(a, yexp, plan, a_down, b_down, scale, drop=None, want_v=False):
+    """(yexp [n,d], v [n,r] or None) bf16: the second grouped product's rows with every row's adapter added (rows without
+    one: copies).  a [n,f] from adapter_gate_up; a_down [L,E,r,f], b_down [L,E,r,d] (by rank), scale [L] fp32."""
+    r, d, f = _adapter_d(plan, a_down, b_down, scale)
+    n = plan.n
+    _is(a, torch.bfloat16, (n, f), "a")
+    _is(yexp, torch.bfloat16, (n, d), "yexp")
+    p_rng, p, site, rng = _drop(drop)
+    dev = _device_of(plan.ids, a, yexp, a_down, b_down, scale, rng)
+    y = _new((n, d), torch.bfloat16, dev)
+    v = _new((n, r), torch.bfloat16, dev) if want_v else None
+    ws, nbytes = _adapter_ws(plan, d, f, r, False)
+    _call_on(dev, "moe_adapter_down", _ptr(a), *plan._args(), d, f, r, _ptr(a_down), _ptr(b_down), _ptr(scale), p_rng, p,
+             site, _ptr(yexp), _ptr(v), _ptr(y), _ptr(ws), nbytes)
+    return y, v
+
+
+def _planned(plan):
+    if plan.buf is None:
+        raise ValueError("the backward needs a plan made with backward=True")
+
+
+def adapter_down_bwd(dyexp, a, v, g, u, dg, du, plan, a_down, b_down, scale, drop=None):
+    """(dg, du [n,f], d_a_down, d_b_down) bf16: the gradients of adapter_down's matrices, and dg, du of
+    grouped_gemm_dgrad_down with the adapters' share of da added through the SwiGLU backward.  a, g, u as adapter_gate_up gave
+    them, v and drop of adapter_down."""
+    r, d, f = _adapter_d(plan, a_down, b_down, scale)
+    _planned(plan)
+    n = plan.n
+    _is(dyexp, torch.bfloat16, (n, d), "dyexp")
+    _is(v, torch.bfloat16, (n, r), "v")
+    for t, name in ((a, "a"), (g, "g"), (u, "u"), (dg, "dg"), (du, "du")):
+        _is(t, torch.bfloat16, (n, f), name)
+    p_rng, p, site, rng = _drop(drop)
+    dev = _device_of(plan.ids, dyexp, a, v, g, u, dg, du, a_down, b_down, scale, rng)
+    dg2, du2 = _new((n, f), torch.bfloat16, dev), _new((n, f), torch.bfloat16, dev)
+    d_a, d_b = torch.empty_like(a_down), torch.empty_like(b_down)
+    ws, nbytes = _adapter_ws(plan, d, f, r, True)
+    _call_on(dev, "moe_adapter_down_bwd", _ptr(dyexp), _ptr(a), _ptr(v), *plan._args(), d, f, r, _ptr(a_down), _ptr(b_down),
+             _ptr(scale), p_rng, p, site, _ptr(g), _ptr(u), _ptr(dg), _ptr(du), _ptr(dg2), _ptr(du2), _ptr(d_a), _ptr(d_b),
+             _ptr(ws), nbytes)
+    return dg2, du2, d_a, d_b
+
+
+def adapter_gate_up_bwd(dg, du, x, v, dxp, plan, a_gu, b_gate, b_up, scale, drop=None):
+    """(dxp [n,d], d_a_gu, d_b_gate, d_b_up) bf16: the gradients of adapter_gate_up's matrices, and dxp of
+    grouped_gemm_dgrad_gate_up (of dg, du from adapter_down_bwd) with the adapters' share added.  x, v and drop of
+    adapter_gate_up."""
+    r, d, f = _adapter_gu(plan, a_gu, b_gate, b_up, scale)
+    _planned(plan)
+    n = plan.n
+    _is(dg, torch.bfloat16, (n, f), "dg")
+    _is(du, torch.bfloat16, (n, f), "du")
+    _is(x, torch.bfloat16, (plan.T, d), "x")
+    _is(v, torch.bfloat16, (n, 2 * r), "v")
+    _is(dxp, torch.bfloat16, (n, d), "dxp")
+    p_rng, p, site, rng = _drop(drop)
+    dev = _device_of(plan.ids, dg, du, x, v, dxp, a_gu, b_gate, b_up, scale, rng)
+    dxp2 = _new((n, d), torch.bfloat16, dev)
+    d_a, d_bg, d_bu = torch.empty_like(a_gu), torch.empty_like(b_gate), torch.empty_like(b_up)
+    ws, nbytes = _adapter_ws(plan, d, f, r, True)
+    _call_on(dev, "moe_adapter_gate_up_bwd", _ptr(dg), _ptr(du), _ptr(x), _ptr(v), *plan._args(), d, f, r, _ptr(a_gu),
+             _ptr(b_gate), _ptr(b_up), _ptr(scale), p_rng, p, site, _ptr(dxp), _ptr(dxp2), _ptr(d_a), _ptr(d_bg),
+             _ptr(d_bu), _ptr(ws), nbytes)
+    return dxp2, d_a, d_bg, d_bu
 
 
 # ---------------------------------------------------------------- MXFP8

@@ -286,6 +286,105 @@ int moe_permute_bwd_router(const uint16_t* dxp, const int32_t* dest, int T, int 
                            const float* d_logits, int E, uint16_t* dx, void* ws, size_t ws_bytes,
                            void* stream);
 
+/* ---------------------------------------------------------------- dropout
+ *
+ * Random zeros whose mask is never stored: every call that needs the factor of an element computes it again
+ * from the generator's seed and offset.  Element (r, c) of a matrix has the factor 0 where u(r, c) < D and
+ * 2^16 / (2^16 - D) elsewhere, D = p 2^16 rounded to a whole number; u(r, c) is piece c % 8 of 16 bits (the low half of a
+ * word first) of the Philox4x32 block (7 rounds) of the counter (c / 8 + site 2^28, r, offset's low half, offset's
+ * high half) under the key (seed's low half, seed's high half).
+ *   rng [2] int64 on the device: seed, offset.  It is read by the kernel, so a captured graph draws
+ *   new zeros on a replay where the program has advanced the offset; a backward needs it as its
+ *   forward had it.  p in [0, 1) (0: nothing is dropped, rng may be NULL); site in [0, 16) keeps the
+ *   matrices of one step apart.  Needs d a multiple of 64, pointers 16-byte aligned. */
+
+/* y [T,d] = the factors times x (+ res where given), fp32, rounded once: dropout of plain rows, and its
+ * own gradient (x = dy). */
+int moe_dropout(const uint16_t* x, const uint16_t* res_or_null, const int64_t* rng, float p, int site, int T, int d,
+                uint16_t* y, void* stream);
+
+/* moe_unpermute_combine with dropout of the combined rows and the residual added ([news] "Routing work
+ * stays on the GPU", the return path of the rowwise exchange):
+ * y[t] = (factors of row t) * sum_j topk_gate[t,j] * yexp[dest[t,j]] (+ res[t]), fp32, rounded once. */
+int moe_unpermute_combine_dropout(const uint16_t* yexp, const float* topk_gate, const int32_t* dest,
+                                  const uint16_t* res_or_null, const int64_t* rng, float p, int site, int T, int d,
+                                  int k, uint16_t* y, void* stream);
+
+/* Its gradient: moe_unpermute_combine_bwd of the factors times dy (in fp32).  The residual's is dy. */
+int moe_unpermute_combine_dropout_bwd(const uint16_t* dy, const uint16_t* yexp, const float* topk_gate,
+                                      const int32_t* dest, const int64_t* rng, float p, int site, int T, int d, int k,
+                                      uint16_t* dyexp, float* d_gate, void* stream);
+
+/* ---------------------------------------------------------------- low-rank adapters
+ *
+ * Adapters of many requests at once beside the experts' shared products ([news] lead paragraphs: a
+ * router sends each token to a small selection of experts; every one of L adapters has matrices of its own
+ * for each of the E experts).  Row r of the expert buffers belongs to expert e (offsets [E+1]), to the
+ * token t = row_token[r] (or r itself without row_token, n = T) and so to the adapter l = ids[t]; an
+ * id outside [0, L) means none: such a row's results are its inputs, bit for bit.
+ *   a_gu [L,E,2r,d] (gate's ranks, then up's), b_gate, b_up [L,E,r,f], a_down [L,E,r,f], b_down [L,E,r,d]:
+ *   bf16, B by rank like A (the transpose of the usual [out, r]); scale [L] fp32.  Adapters of a smaller rank are
+ *   padded with zeros.  r a multiple of 8 in [8, 64]; d and f multiples of 64; 1 <= L <= 256; n <= 2^26.
+ *   m: the dropout factors (above) of the adapters' inputs, element (grouped row, column); p = 0: none.
+ *   gate_up:  v = (m x[t]) A^T;  g' = g + s v_gate B_gate,  u' = u + s v_up B_up,  a' = silu(g') u'
+ *   down:     v = (m a) A^T;     y' = y + s v B
+ * Products of bf16 values are summed in fp32; v is rounded to bf16 between its two products, like every tensor
+ * that crosses a kernel's border here; g', u', y' are rounded once, and a' comes from the unrounded g', u'.
+ * Rows from offsets[E] on are left as they were. */
+
+/* The order of the rows by expert and adapter (a stable sort, so that sums run in a fixed order), made on the
+ * device for the calls below: `plan` is a buffer of moe_adapter_plan_bytes(n, E, L) bytes that holds it for as long as ids,
+ * row_token and offsets keep their contents.  The forward calls take NULL for it: every row then reads its
+ * adapter by itself, which is faster for few rows. */
+size_t moe_adapter_plan_bytes(int n, int E, int L);
+int moe_adapter_plan(const int32_t* ids, const int32_t* row_token_or_null, const int32_t* offsets, int T, int n,
+                     int E, int L, void* plan, size_t plan_bytes, void* stream);
+
+/* Workspace of the four calls below: of the forward ones (planned: whether they are given a plan), or with
+ * `backward` of the backward ones. */
+size_t moe_adapter_workspace_bytes(int n, int d, int f, int r, int planned, int backward);
+
+/* x [T,d] by token; g, u, a [n,f] as moe_grouped_gemm_gate_up wrote them (a is read for rows without an adapter
+ * only).  v_or_null [n,2r] is kept for the backward (0 for rows without an adapter); g_out and u_out may both be NULL (serving).
+ * Outputs must not overlap inputs. */
+int moe_adapter_gate_up(const uint16_t* x, const int32_t* ids, const int32_t* row_token_or_null, const int32_t* offsets,
+                        const void* plan_or_null, int T, int n, int E, int L, int d, int f, int r, const uint16_t* a_gu,
+                        const uint16_t* b_gate, const uint16_t* b_up, const float* scale, const int64_t* rng_or_null,
+                        float p, int site, const uint16_t* g, const uint16_t* u, const uint16_t* a, uint16_t* v_or_null,
+                        uint16_t* g_out_or_null, uint16_t* u_out_or_null, uint16_t* a_out, void* ws, size_t ws_bytes,
+                        void* stream);
+
+/* a [n,f] as moe_adapter_gate_up wrote it, yexp [n,d] the down product of it; v_or_null [n,r]. */
+int moe_adapter_down(const uint16_t* a, const int32_t* ids, const int32_t* row_token_or_null, const int32_t* offsets,
+                     const void* plan_or_null, int T, int n, int E, int L, int d, int f, int r, const uint16_t* a_down,
+                     const uint16_t* b_down, const float* scale, const int64_t* rng_or_null, float p, int site,
+                     const uint16_t* yexp, uint16_t* v_or_null, uint16_t* y_out, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradient of moe_adapter_down.  dyexp [n,d]; a, v, g, u of the forward (g, u as moe_adapter_gate_up wrote them);
+ * dg, du [n,f] as moe_grouped_gemm_dgrad_down wrote them, to which the adapters' share of da is added through the
+ * SwiGLU backward:
+ *   dv = s dyexp B^T (rounded to bf16),  d_b_down = s v^T dyexp,  d_a_down = dv^T (m a),  da = m (dv A),
+ *   dg' = dg + da u sg (1 + g (1 - sg)),  du' = du + da g sg,  sg = sigmoid(g)
+ * with the sums of the two weight gradients over the rows of one expert and adapter; zeros where there are none.
+ * rng, p, site as the forward had them. */
+int moe_adapter_down_bwd(const uint16_t* dyexp, const uint16_t* a, const uint16_t* v, const int32_t* ids,
+                         const int32_t* row_token_or_null, const int32_t* offsets, const void* plan, int T, int n, int E,
+                         int L, int d, int f, int r, const uint16_t* a_down, const uint16_t* b_down, const float* scale,
+                         const int64_t* rng_or_null, float p, int site, const uint16_t* g, const uint16_t* u,
+                         const uint16_t* dg, const uint16_t* du, uint16_t* dg_out, uint16_t* du_out, uint16_t* d_a_down,
+                         uint16_t* d_b_down, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradient of moe_adapter_gate_up.  dg, du [n,f] as moe_adapter_down_bwd wrote them, x, v of the forward, dxp [n,d] as
+ * moe_grouped_gemm_dgrad_gate_up wrote it from them:
+ *   dv = s [dg B_gate^T, du B_up^T] (rounded to bf16),  d_b_gate = s v_gate^T dg,  d_b_up = s v_up^T du,
+ *   d_a_gu = dv^T (m x[t]),  dxp' = dxp + m (dv A). */
+int moe_adapter_gate_up_bwd(const uint16_t* dg, const uint16_t* du, const uint16_t* x, const uint16_t* v,
+                            const int32_t* ids, const int32_t* row_token_or_null, const int32_t* offsets, const void* plan,
+                            int T, int n, int E, int L, int d, int f, int r, const uint16_t* a_gu, const uint16_t* b_gate,
+                            const uint16_t* b_up, const float* scale, const int64_t* rng_or_null, float p, int site,
+                            const uint16_t* dxp, uint16_t* dxp_out, uint16_t* d_a_gu, uint16_t* d_b_gate,
+                            uint16_t* d_b_up, void* ws, size_t ws_bytes, void* stream);
+
 /* ---------------------------------------------------------------- MXFP8 quantisation */
 
 /* MXFP8 block quantisation of a bf16 tensor in[batch][rows][cols]
