@@ -16,6 +16,10 @@
 // contraction; the 8 columns that it holds become 8 column tiles, of which tile i takes column 8 c + i from lane
 // c, so its accumulators hold 8 neighbouring columns and leave as 16-byte stores).
 //
+// Between its two products v is held as the sum of two bf16 values, hi (what is handed out as v) and lo (what hi lacks):
+// 16 bits of mantissa for one more MFMA each, where bf16 alone made the gradients 1.6 times less exact than
+// their own rounding does.
+//
 // Rows are taken in tiles of up to 64 rows of one expert and adapter, from a list that adapter_plan makes on the
 // device by a stable sort of each expert's rows by adapter, so sums run in a fixed order.  For few rows there is no
 // list: every row is a tile.
@@ -37,6 +41,13 @@ constexpr int kMaxAdapters = 256;
 
 __device__ __forceinline__ f32x4 mfma(uint4 a, uint4 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+// x = hi + lo up to 2^-17 of it; lo is 0 where hi is not finite.
+__device__ __forceinline__ float lo_of(float x, float hi) { return __builtin_isfinite(hi) ? x - hi : 0.f; }
+__device__ __forceinline__ void split_bf16(float x, uint16_t& hi, uint16_t& lo) {
+  hi = f32_to_bf16(x);
+  lo = f32_to_bf16(lo_of(x, bf16_to_f32(hi)));
 }
 
 // ---------------------------------------------------------------- the plan
@@ -334,7 +345,8 @@ struct ShrinkArgs {
   int gather;              // x by token (through row_token)
   int K, R, ldv, S;        // S > 1: slices of K whose fp32 sums go to part [S][n][ldv]
   const float* scale;      // null, or [L]: factor of v
-  uint16_t* v;
+  uint16_t* v;             // hi and lo [n][ldv]
+  uint16_t* vlo;
   float* part;
   DropArgs drop;
 };
@@ -432,7 +444,7 @@ __device__ __forceinline__ void shrink_run(const ShrinkArgs& a, const Tile& t, c
         if (a.S > 1)
           a.part[(static_cast<long long>(slice) * a.rows.n + r) * a.ldv + a.v0[which] + rank] = f * s[j];
         else
-          a.v[r * a.ldv + a.v0[which] + rank] = f32_to_bf16(f * s[j]);
+          split_bf16(f * s[j], a.v[r * a.ldv + a.v0[which] + rank], a.vlo[r * a.ldv + a.v0[which] + rank]);
       }
     }
   }
@@ -450,8 +462,10 @@ __global__ __launch_bounds__(256) void adapter_shrink_kernel(ShrinkArgs a) {
     if (t.count == 0) continue;
     if (t.l >= a.rows.L) {   // no adapter: v is 0 (with slices, expand writes that)
       if (a.S == 1)
-        for (int at = threadIdx.x; at < t.count * a.R; at += 256)
-          a.v[static_cast<long long>(row_at(a.rows, p, t.pos + at / a.R)) * a.ldv + a.v0[which] + at % a.R] = 0;
+        for (int at = threadIdx.x; at < t.count * a.R; at += 256) {
+          const long long to = static_cast<long long>(row_at(a.rows, p, t.pos + at / a.R)) * a.ldv + a.v0[which] + at % a.R;
+          a.v[to] = a.vlo[to] = 0;
+        }
       continue;
     }
     const int nb = (t.count + 15) / 16;
@@ -468,14 +482,16 @@ enum { kAdd = 0, kSwiglu = 1, kSwigluBwd = 2 };
 
 struct ExpandArgs {
   Rows rows;
-  const uint16_t* v;        // [n][ldv], or part [S][n][ldv]
+  const uint16_t* v;        // hi and lo [n][ldv], or part [S][n][ldv]
+  const uint16_t* vlo;
   const float* part;
   int ldv, S, R, N;         // R: ranks of one product
   const uint16_t* w[2];     // kSwiglu: gate and up (v's columns [0, R) and [R, 2 R))
   const float* scale;       // null, or [L]
   const uint16_t* in[4];    // kAdd: y; kSwiglu: g, u, a; kSwigluBwd: g, u, dg, du
   uint16_t* out[3];         // kAdd: y; kSwiglu: g, u (or null), a; kSwigluBwd: dg, du
-  uint16_t* v_out;          // with slices: v, where it is wanted
+  uint16_t* v_out;          // with slices: hi and lo, where they are wanted
+  uint16_t* vlo_out;
   DropArgs drop;
 };
 
@@ -523,23 +539,31 @@ __device__ __forceinline__ void load_w(const uint16_t* w, int R, int N, int col,
   }
 }
 
-// 8 ranks of one row of v, 0 past R; from slices: their fp32 sums in slice order, rounded once.
-__device__ __forceinline__ uint4 load_v(const ExpandArgs& a, long long row, int col) {
-  if (a.S == 1) return *reinterpret_cast<const uint4*>(a.v + row * a.ldv + col);
-  float f[8];
+// 8 ranks of one row of v, hi and lo; from slices: of their fp32 sums in slice order.
+__device__ __forceinline__ void load_v(const ExpandArgs& a, long long row, int col, uint4& hi, uint4& lo) {
+  if (a.S == 1) {
+    hi = *reinterpret_cast<const uint4*>(a.v + row * a.ldv + col);
+    lo = *reinterpret_cast<const uint4*>(a.vlo + row * a.ldv + col);
+    return;
+  }
+  float f[8], h[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) f[i] = 0.f;
   for (int s = 0; s < a.S; ++s) {
     const float4* at = reinterpret_cast<const float4*>(a.part + (static_cast<long long>(s) * a.rows.n + row) * a.ldv + col);
-    const float4 lo = at[0], hi = at[1];
-    f[0] += lo.x; f[1] += lo.y; f[2] += lo.z; f[3] += lo.w;
-    f[4] += hi.x; f[5] += hi.y; f[6] += hi.z; f[7] += hi.w;
+    const float4 x = at[0], y = at[1];
+    f[0] += x.x; f[1] += x.y; f[2] += x.z; f[3] += x.w;
+    f[4] += y.x; f[5] += y.y; f[6] += y.z; f[7] += y.w;
   }
-  return pack8(f);
+  hi = pack8(f);
+  unpack8(hi, h);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = lo_of(f[i], h[i]);
+  lo = pack8(f);
 }
 
 template <int KS, int MODE, bool DROP>
-__global__ __launch_bounds__(256) void adapter_expand_kernel(ExpandArgs a) {
+__global__ __launch_bounds__(256, KS == 1 ? 2 : 1) void adapter_expand_kernel(ExpandArgs a) {
   constexpr int NW = MODE == kSwiglu ? 2 : 1;
   constexpr int NOUT = MODE == kAdd ? 1 : MODE == kSwiglu ? 3 : 2;
   const PlanLayout p = plan_layout(a.rows.n, a.rows.E, a.rows.L);
@@ -557,8 +581,11 @@ __global__ __launch_bounds__(256) void adapter_expand_kernel(ExpandArgs a) {
     const int cc = live ? col : 0;
     if (t.l >= a.rows.L) {              // no adapter: copies
       if (a.v_out != nullptr && stripe == 0)
-        for (int at = lane; at < t.count * a.ldv; at += 64)
-          a.v_out[static_cast<long long>(row_at(a.rows, p, t.pos + at / a.ldv)) * a.ldv + at % a.ldv] = 0;
+        for (int at = lane; at < t.count * a.ldv; at += 64) {
+          const long long to = static_cast<long long>(row_at(a.rows, p, t.pos + at / a.ldv)) * a.ldv + at % a.ldv;
+          a.v_out[to] = 0;
+          if (a.vlo_out != nullptr) a.vlo_out[to] = 0;
+        }
       for (int m = q; m < t.count; m += 4) {
         const long long at = static_cast<long long>(row_at(a.rows, p, t.pos + m)) * a.N + cc;
 #pragma unroll
@@ -595,14 +622,19 @@ __global__ __launch_bounds__(256) void adapter_expand_kernel(ExpandArgs a) {
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
           const int rank = 32 * k + 8 * q;
-          uint4 vf = make_uint4(0, 0, 0, 0);
+          uint4 hi = make_uint4(0, 0, 0, 0), lo = hi;
           if (rank < a.R) {
-            vf = load_v(a, mine, m * a.R + rank);
-            if (a.v_out != nullptr && stripe == 0 && 16 * b + c < t.count)
-              *reinterpret_cast<uint4*>(a.v_out + static_cast<long long>(mine) * a.ldv + m * a.R + rank) = vf;
+            load_v(a, mine, m * a.R + rank, hi, lo);
+            if (a.v_out != nullptr && stripe == 0 && 16 * b + c < t.count) {
+              const long long to = static_cast<long long>(mine) * a.ldv + m * a.R + rank;
+              *reinterpret_cast<uint4*>(a.v_out + to) = hi;
+              if (a.vlo_out != nullptr) *reinterpret_cast<uint4*>(a.vlo_out + to) = lo;
+            }
           }
 #pragma unroll
-          for (int o = 0; o < 8; ++o) acc[m][o] = mfma(vf, wf[m][k][o], acc[m][o]);
+          for (int o = 0; o < 8; ++o) acc[m][o] = mfma(lo, wf[m][k][o], acc[m][o]);
+#pragma unroll
+          for (int o = 0; o < 8; ++o) acc[m][o] = mfma(hi, wf[m][k][o], acc[m][o]);
         }
       }
 #pragma unroll
@@ -660,6 +692,7 @@ __global__ __launch_bounds__(256) void adapter_expand_kernel(ExpandArgs a) {
 struct WgradArgs {
   Rows rows;
   const uint16_t* v;        // [n][ldv]
+  const uint16_t* vlo;      // LO: what v lacks
   int v0[2];                // first columns of up to two products (blockIdx.y): gate and up
   const uint16_t* y[2];
   int gather;               // y by token
@@ -675,8 +708,40 @@ struct WgradArgs {
 // pieces are longer than that), so a bit for the first keeps all apart.
 __device__ __forceinline__ long long piece_slot(int pos, int piece, bool first) { return 2LL * (pos / piece) + first; }
 
+// v's fragments for RT tiles of 16 ranks and 32 rows, 0 for rows from `left` on.
+template <int RT>
+__device__ __forceinline__ void load_vt(const uint16_t* v, int ldv, int R, int r0, const int (&row)[8], int left, uint4 (&vf)[RT]) {
+  const int c = threadIdx.x & 15, q = (threadIdx.x & 63) >> 4;
+  if constexpr (RT == 1) {
+    // ranks r0 + c: 8 rows' values of one rank each
+    const int rank = min(r0 + c, R - 1);
+    uint32_t w[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = 8 * q + j < left ? v[static_cast<long long>(row[j]) * ldv + rank] : 0u;
+    vf[0] = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+  } else {
+    // two tiles at a time take the even and the odd ones of 32 ranks: 4 bytes of 8 rows
+#pragma unroll
+    for (int m = 0; m < RT; m += 2) {
+      const int rank = min(r0 + 16 * m + 2 * c, R - 2);
+      uint32_t w[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        w[j] = 8 * q + j < left ? *reinterpret_cast<const uint32_t*>(v + static_cast<long long>(row[j]) * ldv + rank) : 0u;
+      uint32_t even[4], odd[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        even[j] = __builtin_amdgcn_perm(w[2 * j + 1], w[2 * j], 0x05040100u);
+        odd[j] = __builtin_amdgcn_perm(w[2 * j + 1], w[2 * j], 0x07060302u);
+      }
+      vf[m] = make_uint4(even[0], even[1], even[2], even[3]);
+      vf[m + 1] = make_uint4(odd[0], odd[1], odd[2], odd[3]);
+    }
+  }
+}
+
 // RT tiles of 16 ranks (from rank r0) x 128 columns over the rows of one piece, 32 rows a step.
-template <int RT, bool DROP>
+template <int RT, bool DROP, bool LO>
 __global__ __launch_bounds__(256) void adapter_wgrad_kernel(WgradArgs a) {
   const PlanLayout p = plan_layout(a.rows.n, a.rows.E, a.rows.L);
   const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4;
@@ -695,7 +760,6 @@ __global__ __launch_bounds__(256) void adapter_wgrad_kernel(WgradArgs a) {
     for (int m = 0; m < RT; ++m)
 #pragma unroll
       for (int o = 0; o < 8; ++o) acc[m][o] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const uint16_t* v = a.v + a.v0[which];
     for (int s = 0; s < t.count; s += 32) {
       const int left = t.count - s;
       const int mine = a.rows.plan[p.rows + t.pos + s + min(lane & 31, left - 1)];
@@ -708,33 +772,9 @@ __global__ __launch_bounds__(256) void adapter_wgrad_kernel(WgradArgs a) {
         row[j] = __shfl(mine, 8 * q + j, 64);
         yr[j] = *reinterpret_cast<const uint4*>(y + static_cast<long long>(__shfl(src, 8 * q + j, 64)) * a.C + cc);
       }
-      uint4 vf[RT];
-      if constexpr (RT == 1) {
-        // ranks r0 + c: 8 rows' values of one rank each
-        const int rank = min(r0 + c, a.R - 1);
-        uint32_t w[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = 8 * q + j < left ? v[static_cast<long long>(row[j]) * a.ldv + rank] : 0u;
-        vf[0] = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
-      } else {
-        // two tiles at a time take the even and the odd ones of 32 ranks: 4 bytes of 8 rows
-#pragma unroll
-        for (int m = 0; m < RT; m += 2) {
-          const int rank = min(r0 + 16 * m + 2 * c, a.R - 2);
-          uint32_t w[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            w[j] = 8 * q + j < left ? *reinterpret_cast<const uint32_t*>(v + static_cast<long long>(row[j]) * a.ldv + rank) : 0u;
-          uint32_t lo[4], hi[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            lo[j] = __builtin_amdgcn_perm(w[2 * j + 1], w[2 * j], 0x05040100u);
-            hi[j] = __builtin_amdgcn_perm(w[2 * j + 1], w[2 * j], 0x07060302u);
-          }
-          vf[m] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          vf[m + 1] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        }
-      }
+      uint4 vf[RT], vl[RT];
+      load_vt<RT>(a.v + a.v0[which], a.ldv, a.R, r0, row, left, vf);
+      if constexpr (LO) load_vt<RT>(a.vlo + a.v0[which], a.ldv, a.R, r0, row, left, vl);
       if (DROP) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) yr[j] = drop_zero(key, row[j], cc >> 3, yr[j]);
@@ -747,9 +787,14 @@ __global__ __launch_bounds__(256) void adapter_wgrad_kernel(WgradArgs a) {
       uint4 yf[8];
       transpose8(yr, yf);
 #pragma unroll
-      for (int m = 0; m < RT; ++m)
+      for (int m = 0; m < RT; ++m) {
+        if constexpr (LO) {
+#pragma unroll
+          for (int o = 0; o < 8; ++o) acc[m][o] = mfma(vl[m], yf[o], acc[m][o]);
+        }
 #pragma unroll
         for (int o = 0; o < 8; ++o) acc[m][o] = mfma(vf[m], yf[o], acc[m][o]);
+      }
     }
     float f = a.scale != nullptr ? a.scale[t.l] : 1.f;
     if (DROP) f *= drop_scale(a.drop.drop);
@@ -837,15 +882,15 @@ void launch_expand(const ExpandArgs& a, hipStream_t st) {
   else if constexpr (MODE == kAdd) adapter_expand_kernel<4, MODE, DROP><<<grid, 256, 0, st>>>(a);
 }
 
-template <bool DROP>
+template <bool DROP, bool LO>
 void launch_wgrad(const WgradArgs& a, int products, hipStream_t st) {
   const PlanLayout p = plan_layout(a.rows.n, a.rows.E, a.rows.L);
   const int rt = a.R <= 16 ? 1 : a.R <= 32 ? 2 : 4;
   const long long waves = static_cast<long long>(p.items_cap) * ((a.R + 16 * rt - 1) / (16 * rt)) * ((a.C + 127) / 128);
   const dim3 grid(grid_of((waves + 3) / 4), products);
-  if (rt == 1) adapter_wgrad_kernel<1, DROP><<<grid, 256, 0, st>>>(a);
-  else if (rt == 2) adapter_wgrad_kernel<2, DROP><<<grid, 256, 0, st>>>(a);
-  else adapter_wgrad_kernel<4, DROP><<<grid, 256, 0, st>>>(a);
+  if (rt == 1) adapter_wgrad_kernel<1, DROP, LO><<<grid, 256, 0, st>>>(a);
+  else if (rt == 2) adapter_wgrad_kernel<2, DROP, LO><<<grid, 256, 0, st>>>(a);
+  else adapter_wgrad_kernel<4, DROP, LO><<<grid, 256, 0, st>>>(a);
   const int piece = piece_rows(a.rows.n);
   if (a.rows.n > piece) {
     const long long blocks = (static_cast<long long>(a.R) * a.C + 2047) / 2048;
@@ -879,7 +924,7 @@ int check_dims(int d, int f, int r) {
 
 long long align256(long long b) { return (b + 255) / 256 * 256; }
 
-// Bytes of v (bf16), of its slices and of the weight gradients' pieces for a product pair of widths K -> R.
+// Bytes of v's hi or lo, of its slices and of the weight gradients' pieces for a product pair of widths K -> R.
 long long v_bytes(int n, int R) { return align256(2LL * n * R); }
 long long part_bytes(bool planned, int n, int R, int K) {
   const int s = slices(planned, n, K);
@@ -890,15 +935,15 @@ long long piece_bytes(int n, int products, int R, int C) {
   return n > piece ? align256(4LL * products * 2 * (n / piece + 1) * R * C) : 0;
 }
 
-long long forward_bytes(bool planned, int n, int R, int K) { return v_bytes(n, R) + part_bytes(planned, n, R, K); }
+long long forward_bytes(bool planned, int n, int R, int K) { return 2 * v_bytes(n, R) + part_bytes(planned, n, R, K); }
 
 long long max_ll(long long a, long long b) { return a > b ? a : b; }
 
 long long down_bwd_bytes(int n, int d, int f, int r) {
-  return v_bytes(n, r) + max_ll(part_bytes(true, n, r, d), max_ll(piece_bytes(n, 1, r, d), piece_bytes(n, 1, r, f)));
+  return 2 * v_bytes(n, r) + max_ll(part_bytes(true, n, r, d), max_ll(piece_bytes(n, 1, r, d), piece_bytes(n, 1, r, f)));
 }
 long long gate_up_bwd_bytes(int n, int d, int f, int r) {
-  return v_bytes(n, 2 * r) +
+  return 2 * v_bytes(n, 2 * r) +
          max_ll(part_bytes(true, n, 2 * r, f), max_ll(piece_bytes(n, 2, r, f), piece_bytes(n, 1, 2 * r, d)));
 }
 
@@ -961,14 +1006,15 @@ extern "C" int moe_adapter_gate_up(const uint16_t* x, const int32_t* ids, const 
   if (int st = make_drop(rng, p, site, &drop)) return st;
   MOE_CHECK_WS(forward_bytes(plan != nullptr, n, 2 * r, d));
   uint16_t* vbuf = v != nullptr ? v : static_cast<uint16_t*>(ws);
-  float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + v_bytes(n, 2 * r));
+  uint16_t* lo = reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + v_bytes(n, 2 * r));
+  float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + 2 * v_bytes(n, 2 * r));
   const int S = slices(plan != nullptr, n, d);
-  ShrinkArgs s = {rows, {x, nullptr}, {a_gu, nullptr}, {0, 0}, 1, d, 2 * r, 2 * r, S, nullptr, vbuf, part, drop};
+  ShrinkArgs s = {rows, {x, nullptr}, {a_gu, nullptr}, {0, 0}, 1, d, 2 * r, 2 * r, S, nullptr, vbuf, lo, part, drop};
   hipStream_t st = as_stream(stream);
   if (drop.drop) launch_shrink<true>(s, 1, st);
   else launch_shrink<false>(s, 1, st);
-  ExpandArgs e = {rows, vbuf, part, 2 * r, S, r, f, {b_gate, b_up}, scale, {g, u, a, nullptr}, {g_out, u_out, a_out},
-                  S > 1 ? v : nullptr, DropArgs{}};
+  ExpandArgs e = {rows, vbuf, lo, part, 2 * r, S, r, f, {b_gate, b_up}, scale, {g, u, a, nullptr}, {g_out, u_out, a_out},
+                  S > 1 ? v : nullptr, nullptr, DropArgs{}};
   launch_expand<kSwiglu, false>(e, st);
   return check_launch("adapter_gate_up");
 }
@@ -988,14 +1034,15 @@ extern "C" int moe_adapter_down(const uint16_t* a, const int32_t* ids, const int
   if (int st = make_drop(rng, p, site, &drop)) return st;
   MOE_CHECK_WS(forward_bytes(plan != nullptr, n, r, f));
   uint16_t* vbuf = v != nullptr ? v : static_cast<uint16_t*>(ws);
-  float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + v_bytes(n, r));
+  uint16_t* lo = reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + v_bytes(n, r));
+  float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + 2 * v_bytes(n, r));
   const int S = slices(plan != nullptr, n, f);
-  ShrinkArgs s = {rows, {a, nullptr}, {a_down, nullptr}, {0, 0}, 0, f, r, r, S, nullptr, vbuf, part, drop};
+  ShrinkArgs s = {rows, {a, nullptr}, {a_down, nullptr}, {0, 0}, 0, f, r, r, S, nullptr, vbuf, lo, part, drop};
   hipStream_t st = as_stream(stream);
   if (drop.drop) launch_shrink<true>(s, 1, st);
   else launch_shrink<false>(s, 1, st);
-  ExpandArgs e = {rows, vbuf, part, r, S, r, d, {b_down, nullptr}, scale, {yexp, nullptr, nullptr, nullptr},
-                  {y_out, nullptr, nullptr}, S > 1 ? v : nullptr, DropArgs{}};
+  ExpandArgs e = {rows, vbuf, lo, part, r, S, r, d, {b_down, nullptr}, scale, {yexp, nullptr, nullptr, nullptr},
+                  {y_out, nullptr, nullptr}, S > 1 ? v : nullptr, nullptr, DropArgs{}};
   launch_expand<kAdd, false>(e, st);
   return check_launch("adapter_down");
 }
@@ -1021,20 +1068,21 @@ extern "C" int moe_adapter_down_bwd(const uint16_t* dyexp, const uint16_t* a, co
   if (int st = make_drop(rng, p, site, &drop)) return st;
   MOE_CHECK_WS(down_bwd_bytes(n, d, f, r));
   uint16_t* dv = static_cast<uint16_t*>(ws);
-  float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + v_bytes(n, r));
+  uint16_t* lo = reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + v_bytes(n, r));
+  float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + 2 * v_bytes(n, r));
   const int S = slices(true, n, d);
   hipStream_t st = as_stream(stream);
-  const ShrinkArgs s = {rows, {dyexp, nullptr}, {b_down, nullptr}, {0, 0}, 0, d, r, r, S, scale, dv, part, DropArgs{}};
+  const ShrinkArgs s = {rows, {dyexp, nullptr}, {b_down, nullptr}, {0, 0}, 0, d, r, r, S, scale, dv, lo, part, DropArgs{}};
   launch_shrink<false>(s, 1, st);
-  const ExpandArgs e = {rows, dv, part, r, S, r, f, {a_down, nullptr}, nullptr, {g, u, dg, du}, {dg_out, du_out, nullptr},
-                        S > 1 ? dv : nullptr, drop};
+  const ExpandArgs e = {rows, dv, lo, part, r, S, r, f, {a_down, nullptr}, nullptr, {g, u, dg, du}, {dg_out, du_out, nullptr},
+                        S > 1 ? dv : nullptr, S > 1 ? lo : nullptr, drop};
   if (drop.drop) launch_expand<kSwigluBwd, true>(e, st);
   else launch_expand<kSwigluBwd, false>(e, st);
-  const WgradArgs wb = {rows, v, {0, 0}, {dyexp, nullptr}, 0, r, r, d, scale, {d_b_down, nullptr}, part, DropArgs{}};
-  launch_wgrad<false>(wb, 1, st);
-  const WgradArgs wa = {rows, dv, {0, 0}, {a, nullptr}, 0, r, r, f, nullptr, {d_a_down, nullptr}, part, drop};
-  if (drop.drop) launch_wgrad<true>(wa, 1, st);
-  else launch_wgrad<false>(wa, 1, st);
+  const WgradArgs wb = {rows, v, nullptr, {0, 0}, {dyexp, nullptr}, 0, r, r, d, scale, {d_b_down, nullptr}, part, DropArgs{}};
+  launch_wgrad<false, false>(wb, 1, st);
+  const WgradArgs wa = {rows, dv, lo, {0, 0}, {a, nullptr}, 0, r, r, f, nullptr, {d_a_down, nullptr}, part, drop};
+  if (drop.drop) launch_wgrad<true, true>(wa, 1, st);
+  else launch_wgrad<false, true>(wa, 1, st);
   return check_launch("adapter_down_bwd");
 }
 
@@ -1059,19 +1107,20 @@ extern "C" int moe_adapter_gate_up_bwd(const uint16_t* dg, const uint16_t* du, c
   if (int st = make_drop(rng, p, site, &drop)) return st;
   MOE_CHECK_WS(gate_up_bwd_bytes(n, d, f, r));
   uint16_t* dv = static_cast<uint16_t*>(ws);
-  float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + v_bytes(n, 2 * r));
+  uint16_t* lo = reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + v_bytes(n, 2 * r));
+  float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + 2 * v_bytes(n, 2 * r));
   const int S = slices(true, n, f);
   hipStream_t st = as_stream(stream);
-  const ShrinkArgs s = {rows, {dg, du}, {b_gate, b_up}, {0, r}, 0, f, r, 2 * r, S, scale, dv, part, DropArgs{}};
+  const ShrinkArgs s = {rows, {dg, du}, {b_gate, b_up}, {0, r}, 0, f, r, 2 * r, S, scale, dv, lo, part, DropArgs{}};
   launch_shrink<false>(s, 2, st);
-  const ExpandArgs e = {rows, dv, part, 2 * r, S, 2 * r, d, {a_gu, nullptr}, nullptr, {dxp, nullptr, nullptr, nullptr},
-                        {dxp_out, nullptr, nullptr}, S > 1 ? dv : nullptr, drop};
+  const ExpandArgs e = {rows, dv, lo, part, 2 * r, S, 2 * r, d, {a_gu, nullptr}, nullptr, {dxp, nullptr, nullptr, nullptr},
+                        {dxp_out, nullptr, nullptr}, S > 1 ? dv : nullptr, S > 1 ? lo : nullptr, drop};
   if (drop.drop) launch_expand<kAdd, true>(e, st);
   else launch_expand<kAdd, false>(e, st);
-  const WgradArgs wb = {rows, v, {0, r}, {dg, du}, 0, 2 * r, r, f, scale, {d_b_gate, d_b_up}, part, DropArgs{}};
-  launch_wgrad<false>(wb, 2, st);
-  const WgradArgs wa = {rows, dv, {0, 0}, {x, nullptr}, 1, 2 * r, 2 * r, d, nullptr, {d_a_gu, nullptr}, part, drop};
-  if (drop.drop) launch_wgrad<true>(wa, 1, st);
-  else launch_wgrad<false>(wa, 1, st);
+  const WgradArgs wb = {rows, v, nullptr, {0, r}, {dg, du}, 0, 2 * r, r, f, scale, {d_b_gate, d_b_up}, part, DropArgs{}};
+  launch_wgrad<false, false>(wb, 2, st);
+  const WgradArgs wa = {rows, dv, lo, {0, 0}, {x, nullptr}, 1, 2 * r, 2 * r, d, nullptr, {d_a_gu, nullptr}, part, drop};
+  if (drop.drop) launch_wgrad<true, true>(wa, 1, st);
+  else launch_wgrad<false, true>(wa, 1, st);
   return check_launch("adapter_gate_up_bwd");
 }

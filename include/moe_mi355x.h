@@ -328,8 +328,8 @@ int moe_unpermute_combine_dropout_bwd(const uint16_t* dy, const uint16_t* yexp, 
  *   m: the dropout factors (above) of the adapters' inputs, element (grouped row, column); p = 0: none.
  *   gate_up:  v = (m x[t]) A^T;  g' = g + s v_gate B_gate,  u' = u + s v_up B_up,  a' = silu(g') u'
  *   down:     v = (m a) A^T;     y' = y + s v B
- * Products of bf16 values are summed in fp32; v is rounded to bf16 between its two products, like every tensor
- * that crosses a kernel's border here; g', u', y' are rounded once, and a' comes from the unrounded g', u'.
+ * Products of bf16 values are summed in fp32; between its two products v (and dv of the backward) is held to 16 bits of
+ * mantissa, and handed out as bf16; g', u', y' are rounded once, and a' comes from the unrounded g', u'.
  * Rows from offsets[E] on are left as they were. */
 
 /* The order of the rows by expert and adapter (a stable sort, so that sums run in a fixed order), made on the
@@ -363,7 +363,7 @@ int moe_adapter_down(const uint16_t* a, const int32_t* ids, const int32_t* row_t
 /* Gradient of moe_adapter_down.  dyexp [n,d]; a, v, g, u of the forward (g, u as moe_adapter_gate_up wrote them);
  * dg, du [n,f] as moe_grouped_gemm_dgrad_down wrote them, to which the adapters' share of da is added through the
  * SwiGLU backward:
- *   dv = s dyexp B^T (rounded to bf16),  d_b_down = s v^T dyexp,  d_a_down = dv^T (m a),  da = m (dv A),
+ *   dv = s dyexp B^T,  d_b_down = s v^T dyexp,  d_a_down = dv^T (m a),  da = m (dv A),
  *   dg' = dg + da u sg (1 + g (1 - sg)),  du' = du + da g sg,  sg = sigmoid(g)
  * with the sums of the two weight gradients over the rows of one expert and adapter; zeros where there are none.
  * rng, p, site as the forward had them. */
@@ -376,7 +376,7 @@ int moe_adapter_down_bwd(const uint16_t* dyexp, const uint16_t* a, const uint16_
 
 /* Gradient of moe_adapter_gate_up.  dg, du [n,f] as moe_adapter_down_bwd wrote them, x, v of the forward, dxp [n,d] as
  * moe_grouped_gemm_dgrad_gate_up wrote it from them:
- *   dv = s [dg B_gate^T, du B_up^T] (rounded to bf16),  d_b_gate = s v_gate^T dg,  d_b_up = s v_up^T du,
+ *   dv = s [dg B_gate^T, du B_up^T],  d_b_gate = s v_gate^T dg,  d_b_up = s v_up^T du,
  *   d_a_gu = dv^T (m x[t]),  dxp' = dxp + m (dv A). */
 int moe_adapter_gate_up_bwd(const uint16_t* dg, const uint16_t* du, const uint16_t* x, const uint16_t* v,
                             const int32_t* ids, const int32_t* row_token_or_null, const int32_t* offsets, const void* plan,

@@ -2,8 +2,9 @@
 
 Tolerances, element by element.  A sum of N products of bf16 values in fp32 is off by at most N 2^-23 of the sum of
 magnitudes, in any order (each of up to N additions by 2^-24, and as much again for the way the matrix core aligns
-its terms); a result in bf16 by 2^-8 of it (half a step).  What is rounded between two products and not returned (dv of the
-backward: 2^-8 of each) counts with the magnitudes that it meets.  The logistic function in fp32 is
+its terms); a result in bf16 by 2^-8 of it (half a step).  v and dv are held as two bf16 values between their two products,
+off by at most 2^-16 (what the first lacks is at most 2^-8 of it, and is rounded by 2^-8 of that), and their error counts
+with the magnitudes that it meets in the second product.  The logistic function in fp32 is
 good to 2^-18 (exp of up to |x| < 32: |x| 2^-24 from its argument, and about 2 ulp each for exp and the reciprocal).
 """
 
@@ -18,6 +19,7 @@ from oracle import codecs, dropout
 pytestmark = pytest.mark.gpu
 
 U = 2.0 ** -8
+V = 2.0 ** -16
 SEED, OFFSET = 77, 1 << 33
 
 
@@ -84,24 +86,29 @@ def check_forward(c, plan, p=0.0):
     r, none = c["r"], c["l"] < 0
     g, u, a, v1 = ops().adapter_gate_up(c["t_x"], c["t_g"], c["t_u"], c["t_a"], plan, *up, drop=drop_of(p, 1), want_v=True)
     ref, mag = oracle.shrink(c["x"][c["token"]], c["a_gu"], c["e"], c["l"], mask(c, p, 1, c["d"]))
-    got_v1 = val(v1)
-    within(got_v1, ref, U * np.abs(ref) + c["d"] * 2.0 ** -23 * mag, "v1")
+    within(val(v1), ref, U * np.abs(ref) + c["d"] * 2.0 ** -23 * mag, "v1")
+    v1_off = V * np.abs(ref) + c["d"] * 2.0 ** -23 * mag
     tol, pre = {}, {}
-    for name, base, out, v in (("g", c["g"], g, got_v1[:, :r]), ("u", c["u"], u, got_v1[:, r:])):
-        add, mag = oracle.expand(v, c["b_gate" if name == "g" else "b_up"], c["e"], c["l"], c["scale"])
-        pre[name], tol[name] = base + add, (r + 4) * 2.0 ** -23 * (np.abs(base) + mag)
+    for name, base, out, at in (("g", c["g"], g, slice(0, r)), ("u", c["u"], u, slice(r, None))):
+        w = c["b_gate" if name == "g" else "b_up"]
+        add, mag = oracle.expand(ref[:, at], w, c["e"], c["l"], c["scale"])
+        _, off = oracle.expand(v1_off[:, at], w, c["e"], c["l"], c["scale"])
+        pre[name], tol[name] = base + add, off + (2 * r + 4) * 2.0 ** -23 * (np.abs(base) + mag)
         within(val(out), pre[name], U * np.abs(pre[name]) + tol[name], name)
     s = oracle.sigmoid(pre["g"])
     ref = np.where(none[:, None], c["a"], pre["g"] * s * pre["u"])
+    # silu has a slope of at most 1.1
     within(val(a), ref, U * np.abs(ref) + 2.0 ** -18 * np.abs(ref) + 1.2 * np.abs(pre["u"]) * tol["g"]
-           + np.abs(pre["g"] * s) * tol["u"] + 1e-30, "a")
+           + np.abs(pre["g"] * s) * tol["u"] + 1.2 * tol["g"] * tol["u"] + 1e-30, "a")
     for out, base in ((g, c["t_g"]), (u, c["t_u"]), (a, c["t_a"])):
         assert torch.equal(out[torch.from_numpy(none)], base[torch.from_numpy(none)])
     y, v2 = ops().adapter_down(a, c["t_y"], plan, *down, drop=drop_of(p, 2), want_v=True)
     ref, mag = oracle.shrink(val(a), c["a_down"], c["e"], c["l"], mask(c, p, 2, c["f"]))
     within(val(v2), ref, U * np.abs(ref) + c["f"] * 2.0 ** -23 * mag, "v2")
-    add, mag = oracle.expand(val(v2), c["b_down"], c["e"], c["l"], c["scale"])
-    within(val(y), c["y"] + add, U * np.abs(c["y"] + add) + (r + 4) * 2.0 ** -23 * (np.abs(c["y"]) + mag), "y")
+    v2_off = V * np.abs(ref) + c["f"] * 2.0 ** -23 * mag
+    add, mag = oracle.expand(ref, c["b_down"], c["e"], c["l"], c["scale"])
+    _, off = oracle.expand(v2_off, c["b_down"], c["e"], c["l"], c["scale"])
+    within(val(y), c["y"] + add, (U * np.abs(c["y"] + add) + 1.01 * off + (2 * r + 4) * 2.0 ** -23 * (np.abs(c["y"]) + mag)), "y")
     assert torch.equal(y[torch.from_numpy(none)], c["t_y"][torch.from_numpy(none)])
     # a serving pass: the same a and y, bit for bit
     g2, u2, a2, w1 = ops().adapter_gate_up(c["t_x"], c["t_g"], c["t_u"], c["t_a"], plan, *up, drop=drop_of(p, 1), want_gu=False)
@@ -109,11 +116,10 @@ def check_forward(c, plan, p=0.0):
     assert g2 is u2 is w1 is w2 is None and torch.equal(a, a2) and torch.equal(y, y2)
 
 
-def check_wgrad(out, v, y, c, shape, rounded, scale, what):
-    """v [n, R] exact up to `rounded` (2^-8 where it was rounded to bf16 on the way)."""
+def check_wgrad(out, v, y, c, shape, scale, what):
     ref, mag = oracle.wgrad(v, y, c["e"], c["l"], shape, scale)
     rows = max(1, int(np.max(np.bincount(c["e"][c["l"] >= 0], minlength=1), initial=1)))
-    within(val(out), ref, U * np.abs(ref) + (1 + U) * (rounded + (rows + 4) * 2.0 ** -23) * mag, what)
+    within(val(out), ref, U * np.abs(ref) + (1 + U) * (rows + 4) * 2.0 ** -23 * mag, what)
 
 
 def check_backward(c, plan, p=0.0):
@@ -125,17 +131,15 @@ def check_backward(c, plan, p=0.0):
                                               *down, drop=drop_of(p, 2))
     dv, mag = oracle.shrink(c["y"], c["b_down"], e, l)
     dv, mag = c["s"] * dv, c["s"] * mag
-    check_wgrad(d_b, c["v2"], c["y"], c, d_b.shape, 0.0, c["scale"], "d_b_down")
-    # dv is rounded to bf16 and off by its own sum before that
-    extra = np.max(mag / np.maximum(np.abs(dv), 1e-30), initial=0.0, where=np.abs(dv) > 0)
-    dv_off = U * np.abs(dv) + (d + 2) * 2.0 ** -23 * mag
+    check_wgrad(d_b, c["v2"], c["y"], c, d_b.shape, c["scale"], "d_b_down")
+    dv_off = V * np.abs(dv) + (d + 2) * 2.0 ** -23 * mag
     ref, wmag = oracle.wgrad(dv, c["a"] * m2, e, l, d_a.shape)
     _, off = oracle.wgrad(dv_off, np.abs(c["a"] * m2), e, l, d_a.shape)
     rows = c["n"]
-    within(val(d_a), ref, U * np.abs(ref) + (1 + U) * off + (rows + 4) * 2.0 ** -23 * wmag, ("d_a_down", extra))
+    within(val(d_a), ref, U * np.abs(ref) + (1 + U) * off + (rows + 4) * 2.0 ** -23 * 2 * wmag, "d_a_down")
     da, damag = oracle.expand(dv, c["a_down"], e, l)
     _, daoff = oracle.expand(dv_off, np.abs(c["a_down"]), e, l)
-    da, daoff = m2 * da, m2 * (daoff + (r + 4) * 2.0 ** -23 * damag)
+    da, daoff = m2 * da, m2 * (daoff + (2 * r + 4) * 2.0 ** -23 * damag)
     s = oracle.sigmoid(c["g"])
     for name, out, base, k in (("dg", dg, c["dg"], c["u"] * s * (1 + c["g"] * (1 - s))), ("du", du, c["du"], c["g"] * s)):
         ref = base + da * k
@@ -144,19 +148,19 @@ def check_backward(c, plan, p=0.0):
         assert torch.equal(out[none], c["t_" + name][none])
     hg, hu = val(dg), val(du)
     dxp, d_agu, d_bg, d_bu = ops().adapter_gate_up_bwd(dg, du, c["t_x"], c["t_v1"], c["t_dxp"], plan, *up, drop=drop_of(p, 1))
-    check_wgrad(d_bg, c["v1"][:, :r], hg, c, d_bg.shape, 0.0, c["scale"], "d_b_gate")
-    check_wgrad(d_bu, c["v1"][:, r:], hu, c, d_bu.shape, 0.0, c["scale"], "d_b_up")
+    check_wgrad(d_bg, c["v1"][:, :r], hg, c, d_bg.shape, c["scale"], "d_b_gate")
+    check_wgrad(d_bu, c["v1"][:, r:], hu, c, d_bu.shape, c["scale"], "d_b_up")
     parts = [oracle.shrink(h, c[w], e, l) for h, w in ((hg, "b_gate"), (hu, "b_up"))]
     dv, mag = (c["s"] * np.concatenate([q[i] for q in parts], axis=1) for i in (0, 1))
-    dv_off = U * np.abs(dv) + (f + 2) * 2.0 ** -23 * mag
+    dv_off = V * np.abs(dv) + (f + 2) * 2.0 ** -23 * mag
     x = c["x"][c["token"]] * m1
     ref, wmag = oracle.wgrad(dv, x, e, l, d_agu.shape)
     _, off = oracle.wgrad(dv_off, np.abs(x), e, l, d_agu.shape)
-    within(val(d_agu), ref, U * np.abs(ref) + (1 + U) * off + (rows + 4) * 2.0 ** -23 * wmag, "d_a_gu")
+    within(val(d_agu), ref, U * np.abs(ref) + (1 + U) * off + (rows + 4) * 2.0 ** -23 * 2 * wmag, "d_a_gu")
     add, mag = oracle.expand(dv, c["a_gu"], e, l)
     _, off = oracle.expand(dv_off, np.abs(c["a_gu"]), e, l)
     ref = c["dxp"] + m1 * add
-    within(val(dxp), ref, U * np.abs(ref) + (1 + U) * m1 * (off + (2 * r + 4) * 2.0 ** -23 * mag) + 2.0 ** -22 * np.abs(c["dxp"]), "dxp")
+    within(val(dxp), ref, U * np.abs(ref) + (1 + U) * m1 * (off + (4 * r + 4) * 2.0 ** -23 * mag) + 2.0 ** -22 * np.abs(c["dxp"]), "dxp")
     assert torch.equal(dxp[none], c["t_dxp"][none])
     # groups without rows: zeros
     empty = np.ones((c["L"], c["E"]), dtype=bool)
