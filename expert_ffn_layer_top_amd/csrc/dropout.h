@@ -22,7 +22,9 @@ struct DropKey {
   uint32_t k0, k1, o0, o1, site, drop;
 };
 
+// (Without dropout rng may be null, and is not read.)
 __device__ __forceinline__ DropKey drop_key(const DropArgs& a) {
+  if (a.drop == 0) return {0, 0, 0, 0, 0, 0};
   const uint64_t s = static_cast<uint64_t>(a.rng[0]), o = static_cast<uint64_t>(a.rng[1]);
   return {static_cast<uint32_t>(s), static_cast<uint32_t>(s >> 32), static_cast<uint32_t>(o),
           static_cast<uint32_t>(o >> 32), a.site << 28, a.drop};

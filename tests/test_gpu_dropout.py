@@ -94,6 +94,21 @@ def test_combine_and_its_gradient(T, k, E, d, p, res):
             assert torch.equal(a, b)
 
 
+def test_no_dropout_reads_no_generator():
+    """drop = None hands the library a null rng: the sums alone, with and without the residual."""
+    note("dropout without a generator")
+    g = np.random.default_rng(3)
+    T, k, d = 21, 3, 320
+    dest, gate = routing(g, T, k, 4)
+    y, dy, res = (bf16_to_dev(bf16(g, n, d)[0]) for n in (T * k, T, T))
+    args = (y, f32_to_dev(gate), i32_to_dev(dest))
+    assert torch.equal(ops().unpermute_combine_dropout(*args, None), ops().unpermute_combine(*args))
+    for a, b in zip(ops().unpermute_combine_dropout_bwd(dy, *args, None), ops().unpermute_combine_bwd(dy, *args)):
+        assert torch.equal(a, b)
+    assert torch.equal(ops().dropout(dy, None), dy)
+    assert torch.equal(ops().dropout(dy, None, residual=res), (dy.float() + res.float()).to(torch.bfloat16))
+
+
 def test_what_is_dropped_is_zero_whatever_it_was():
     note("dropout of infinities and NaN")
     T, d, p = 16, 256, 0.5
