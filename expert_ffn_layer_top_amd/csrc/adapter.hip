@@ -33,15 +33,20 @@ namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+// Fragments are native vectors: kept across a loop as structs, they become four registers each that are copied at its
+// head, which waits for their loads.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kTileRows = 64;      // rows of a tile
 constexpr int kPlanChunk = 512;    // rows of one expert that a workgroup of the sort takes
 constexpr int kMaxRank = 64;
 constexpr int kMaxAdapters = 256;
 
-__device__ __forceinline__ f32x4 mfma(uint4 a, uint4 b, f32x4 c) {
+__device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
+__device__ __forceinline__ u32x4 load16(const uint16_t* p) { return *reinterpret_cast<const u32x4*>(p); }
+__device__ __forceinline__ void store16(uint16_t* p, u32x4 v) { *reinterpret_cast<u32x4*>(p) = v; }
 
 // x = hi + lo up to 2^-17 of it; lo is 0 where hi is not finite.
 __device__ __forceinline__ float lo_of(float x, float hi) { return __builtin_isfinite(hi) ? x - hi : 0.f; }
@@ -67,7 +72,7 @@ struct Tile {
 // The plan's parts, as offsets in 4-byte words of its buffer.
 struct PlanLayout {
   int chunks, pairs, tiles_cap, items_cap, multi_cap;
-  long long rows, goff, tile0, tiles, items, multi, hist, words;
+  long long rows, toks, goff, tile0, tiles, items, multi, hist, words;
 };
 
 constexpr int kHeadTiles = 0, kHeadItems = 1, kHeadMulti = 2, kHeadWords = 16;
@@ -87,6 +92,7 @@ __host__ __device__ inline PlanLayout plan_layout(int n, int E, int L) {
     return here;
   };
   p.rows = take(n);
+  p.toks = take(n);
   p.goff = take(p.pairs + 1);
   p.tile0 = take(p.pairs);
   p.tiles = take(4LL * p.tiles_cap);
@@ -103,11 +109,15 @@ __device__ __forceinline__ int row_begin(const int32_t* offsets, int e, int n) {
   return o < 0 ? 0 : o > n ? n : o;
 }
 
+// A row's token, within [0, T), and its adapter, L for none (also where the token is no token).
+__device__ __forceinline__ int token_of(const int32_t* row_token, int row, int T) {
+  return row_token != nullptr ? min(max(row_token[row], 0), T - 1) : row;
+}
 __device__ __forceinline__ int adapter_of(const int32_t* ids, const int32_t* row_token, int row, int T, int L) {
   const int t = row_token != nullptr ? row_token[row] : row;
   if (t < 0 || t >= T) return L;
   const int l = ids[t];
-  return l >= 0 && l < L ? l : L;   // L: none
+  return l >= 0 && l < L ? l : L;
 }
 
 struct Chunk {
@@ -299,6 +309,7 @@ __global__ __launch_bounds__(256) void plan_place_kernel(const int32_t* __restri
     if (r >= c.end) continue;
     const int pos = before[g][l[i]] + rank[i], q = c.e * (L + 1) + l[i];
     plan[p.rows + pos] = r;
+    plan[p.toks + pos] = token_of(row_token, r, T);
     const int in = pos - plan[p.goff + q];
     if (in % kTileRows == 0)
       tiles[plan[p.tile0 + q] + in / kTileRows] = {pos, min(kTileRows, plan[p.goff + q + 1] - pos), c.e, l[i]};
@@ -318,7 +329,11 @@ struct Rows {
 // Tile `i`'s place; count 0: there is none (past the list, or a row behind the last expert's).
 // Called with i uniform in the wave, all lanes.
 __device__ __forceinline__ Tile tile_at(const Rows& rows, const PlanLayout& p, int i) {
-  if (rows.plan != nullptr) return reinterpret_cast<const Tile*>(rows.plan + p.tiles)[i];
+  if (rows.plan != nullptr) {
+    const int4 t = reinterpret_cast<const int4*>(rows.plan + p.tiles)[i];
+    return {__builtin_amdgcn_readfirstlane(t.x), __builtin_amdgcn_readfirstlane(t.y), __builtin_amdgcn_readfirstlane(t.z),
+            __builtin_amdgcn_readfirstlane(t.w)};
+  }
   int e = 0;
   for (int b = 0; b < rows.E; b += 64) {
     const int at = b + (threadIdx.x & 63);
@@ -333,6 +348,17 @@ __device__ __forceinline__ int n_tiles(const Rows& rows) { return rows.plan != n
 // Row at sorted position pos (clamped by the caller to the tile).
 __device__ __forceinline__ int row_at(const Rows& rows, const PlanLayout& p, int pos) {
   return rows.plan != nullptr ? rows.plan[p.rows + pos] : pos;
+}
+
+// A workgroup's items: those of XCD x (workgroups x mod 8) are one contiguous run of the order, so that the tiles of one
+// expert and adapter, which read the same matrix, and the columns of one tile, which read the same rows of v, share an
+// L2.  gridDim.x is a multiple of 8.
+struct Run {
+  long long at, end, step;
+};
+__device__ __forceinline__ Run xcd_run(long long items) {
+  const long long per = (items + 7) / 8, first = (blockIdx.x & 7) * per;
+  return {first + (blockIdx.x >> 3), first + per < items ? first + per : items, gridDim.x >> 3};
 }
 
 // ---------------------------------------------------------------- shrink
@@ -351,75 +377,98 @@ struct ShrinkArgs {
   DropArgs drop;
 };
 
-// One tile (NB blocks of 16 rows) times RT tiles of 16 ranks over K's units of 64 elements u0, u0 + 4, ...
-// A lane holds the rows 16 b + c and the ranks 16 t + c; rows past the tile and ranks past R are copies of the last
-// one, which nobody stores.
+// Staging of a wave: rows of 128 bytes (64 elements of K) of x and of W.  16-byte chunk k of row r is held at chunk
+// k ^ (r / 2 % 8), so that both the 8 rows that a wave writes at once and the 16 that it reads lie in different banks.
+// Within rows 8 i + r (writes) that depends on i by its lowest bit alone, within rows 16 b + r (reads) not on b.
+__device__ __forceinline__ int staged(int row, int chunk) { return row * 8 + (chunk ^ ((row >> 1) & 7)); }
+
+// A wave's own LDS accesses keep their order; this keeps the compiler from changing it.
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// One tile (NB blocks of 16 rows) times RT tiles of 16 ranks over K's units of 64 elements u0, u0 + 4, ...  A load takes
+// 8 rows of a whole cache line each.  (The matrix instruction's operand has 16 rows of 16 bytes in neighbouring
+// lanes; loaded like that, every lane is a cache line of its own and the address unit, at a line a cycle, is what
+// bounds: 3.8 TB/s of x at 32 ranks.)  So rows go through registers, where they wait for memory while the unit
+// before them is multiplied, into the wave's staging, and come from there as operands.  Rows past the tile and
+// ranks past R are copies of the last one, which nobody stores.
 template <int NB, int RT, bool DROP>
 __device__ __forceinline__ void shrink_tile(const ShrinkArgs& a, const Tile& t, const PlanLayout& p, const uint16_t* x,
-                                            const uint16_t* w, int u0, int u1, f32x4 (&acc)[NB][RT]) {
-  const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4;
-  const uint16_t* xp[NB];
-  const uint16_t* wp[RT];
-  uint32_t row[NB];
+                                            const uint16_t* w, int u0, int u1, u32x4* lds, f32x4 (&acc)[NB][RT]) {
+  const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4, lr = lane >> 3, lc = lane & 7;
+  const uint16_t* xp[2 * NB];
+  uint32_t row[2 * NB], wo[2 * RT];
 #pragma unroll
-  for (int b = 0; b < NB; ++b) {
-    const int r = row_at(a.rows, p, t.pos + min(16 * b + c, t.count - 1));
+  for (int i = 0; i < 2 * NB; ++i) {
+    const int pos = t.pos + min(8 * i + lr, t.count - 1), r = row_at(a.rows, p, pos);
     int src = r;
-    if (a.gather && a.rows.row_token != nullptr) src = min(max(a.rows.row_token[r], 0), a.rows.T - 1);
-    row[b] = static_cast<uint32_t>(r);
-    xp[b] = x + static_cast<long long>(src) * a.K + 8 * q;
-#pragma unroll
-    for (int i = 0; i < RT; ++i) acc[b][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (a.gather) src = a.rows.plan != nullptr ? a.rows.plan[p.toks + pos] : token_of(a.rows.row_token, r, a.rows.T);
+    row[i] = static_cast<uint32_t>(r);
+    xp[i] = x + static_cast<long long>(src) * a.K + 8 * lc;
   }
 #pragma unroll
-  for (int i = 0; i < RT; ++i) wp[i] = w + static_cast<long long>(min(16 * i + c, a.R - 1)) * a.K + 8 * q;
+  for (int i = 0; i < 2 * RT; ++i) wo[i] = static_cast<uint32_t>(min(8 * i + lr, a.R - 1)) * a.K + 8 * lc;
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int i = 0; i < RT; ++i) acc[b][i] = f32x4{0.f, 0.f, 0.f, 0.f};
   DropKey key;
   if (DROP) key = drop_key(a.drop);
-  uint4 xf[NB][2], wf[RT][2];
+  const int w0 = staged(lr, lc), w1 = staged(8 + lr, lc) - 64, f0 = staged(c, q), f1 = staged(c, 4 + q);
+  constexpr int kW = 16 * NB * 8;        // W's rows follow x's
+  u32x4 xr[2 * NB], wr[2 * RT];
   auto load = [&](int u) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int i = 0; i < 2 * NB; ++i) xr[i] = load16(xp[i] + 64 * u);
 #pragma unroll
-      for (int b = 0; b < NB; ++b) xf[b][h] = *reinterpret_cast<const uint4*>(xp[b] + 64 * u + 32 * h);
-#pragma unroll
-      for (int i = 0; i < RT; ++i) wf[i][h] = *reinterpret_cast<const uint4*>(wp[i] + 64 * u + 32 * h);
-    }
+    for (int i = 0; i < 2 * RT; ++i) wr[i] = load16(w + (wo[i] + 64u * u));
+    __builtin_amdgcn_sched_barrier(0);
   };
   if (u0 >= u1) return;
   load(u0);
   for (int u = u0; u < u1; u += 4) {
-    uint4 xc[NB][2], wc[RT][2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-#pragma unroll
-      for (int b = 0; b < NB; ++b) xc[b][h] = xf[b][h];
-#pragma unroll
-      for (int i = 0; i < RT; ++i) wc[i][h] = wf[i][h];
+    for (int i = 0; i < 2 * NB; ++i) {
+      if (DROP) xr[i] = drop_zero(key, row[i], 8 * u + lc, xr[i]);
+      lds[(i & 1 ? w1 : w0) + 64 * i] = xr[i];
     }
+#pragma unroll
+    for (int i = 0; i < 2 * RT; ++i) lds[(i & 1 ? w1 : w0) + kW + 64 * i] = wr[i];
+    wave_fence();
+    // (past the end the last unit is loaded again, and not used: a load under a condition makes the waits conservative)
     load(u + 4 < u1 ? u + 4 : u);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
+      u32x4 xf[NB];
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        if (DROP) xc[b][h] = drop_zero(key, row[b], 8 * u + 4 * h + q, xc[b][h]);
+      for (int b = 0; b < NB; ++b) xf[b] = lds[(h ? f1 : f0) + 128 * b];
 #pragma unroll
-        for (int i = 0; i < RT; ++i) acc[b][i] = mfma(xc[b][h], wc[i][h], acc[b][i]);
+      for (int i = 0; i < RT; ++i) {
+        const u32x4 wf = lds[(h ? f1 : f0) + kW + 128 * i];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) acc[b][i] = mfma(xf[b], wf, acc[b][i]);
       }
     }
+    wave_fence();
   }
 }
 
 // The four waves' sums joined through LDS, two tiles of ranks at a time, and stored.
 template <int NB, int RT, bool DROP>
 __device__ __forceinline__ void shrink_run(const ShrinkArgs& a, const Tile& t, const PlanLayout& p, int which, int slice,
-                                           f32x4* lds) {
+                                           u32x4* stage) {
+  f32x4* lds = reinterpret_cast<f32x4*>(stage);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int units = a.K / 64;
   const int s0 = static_cast<int>(static_cast<long long>(units) * slice / a.S);
   const int s1 = static_cast<int>(static_cast<long long>(units) * (slice + 1) / a.S);
   const uint16_t* w = a.w[which] + (static_cast<long long>(t.l) * a.rows.E + t.e) * a.R * a.K;
   f32x4 acc[NB][RT];
-  shrink_tile<NB, RT, DROP>(a, t, p, a.x[which], w, s0 + wave, s1, acc);
+  __syncthreads();    // the last tile's sums have been read
+  shrink_tile<NB, RT, DROP>(a, t, p, a.x[which], w, s0 + wave, s1, stage + wave * (4 + RT) * 128, acc);
   float f = a.scale != nullptr ? a.scale[t.l] : 1.f;
   if (DROP) f *= drop_scale(a.drop.drop);
   constexpr int G = RT < 2 ? RT : 2;
@@ -451,12 +500,13 @@ __device__ __forceinline__ void shrink_run(const ShrinkArgs& a, const Tile& t, c
 }
 
 template <int RT, bool DROP>
-__global__ __launch_bounds__(256) void adapter_shrink_kernel(ShrinkArgs a) {
-  __shared__ f32x4 lds[4 * 4 * (RT < 2 ? RT : 2) * 64];
+__global__ __launch_bounds__(256, RT <= 2 ? 3 : RT == 4 ? 2 : 1) void adapter_shrink_kernel(ShrinkArgs a) {
+  __shared__ u32x4 lds[4 * (4 + RT) * 128];   // 2 KiB for 16 rows or ranks; the sums take at most half of it
   const PlanLayout p = plan_layout(a.rows.n, a.rows.E, a.rows.L);
   const long long items = static_cast<long long>(n_tiles(a.rows)) * a.S;
   const int which = blockIdx.y;
-  for (long long i = blockIdx.x; i < items; i += gridDim.x) {
+  const Run run = xcd_run(items);
+  for (long long i = run.at; i < run.end; i += run.step) {
     const Tile t = tile_at(a.rows, p, static_cast<int>(i / a.S));
     const int slice = static_cast<int>(i % a.S);
     if (t.count == 0) continue;
@@ -471,7 +521,6 @@ __global__ __launch_bounds__(256) void adapter_shrink_kernel(ShrinkArgs a) {
     const int nb = (t.count + 15) / 16;
     if (nb == 1) shrink_run<1, RT, DROP>(a, t, p, which, slice, lds);
     else if (nb == 2) shrink_run<2, RT, DROP>(a, t, p, which, slice, lds);
-    else if (nb == 3) shrink_run<3, RT, DROP>(a, t, p, which, slice, lds);
     else shrink_run<4, RT, DROP>(a, t, p, which, slice, lds);
   }
 }
@@ -486,6 +535,7 @@ struct ExpandArgs {
   const uint16_t* vlo;
   const float* part;
   int ldv, S, R, N;         // R: ranks of one product
+  int parts;                // a tile's rows are shared among this many waves (1, 2 or 4)
   const uint16_t* w[2];     // kSwiglu: gate and up (v's columns [0, R) and [R, 2 R))
   const float* scale;       // null, or [L]
   const uint16_t* in[4];    // kAdd: y; kSwiglu: g, u, a; kSwigluBwd: g, u, dg, du
@@ -498,62 +548,74 @@ struct ExpandArgs {
 // Logistic function with the hardware reciprocal (about 1 ulp), as the experts' products have it.
 __device__ __forceinline__ float logistic(float x) { return __builtin_amdgcn_rcpf(1.0f + __expf(-x)); }
 
-__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
+__device__ __forceinline__ void unpack8(const u32x4& v, float (&f)[8]) {
   f[0] = bf16_lo(v.x); f[1] = bf16_hi(v.x); f[2] = bf16_lo(v.y); f[3] = bf16_hi(v.y);
   f[4] = bf16_lo(v.z); f[5] = bf16_hi(v.z); f[6] = bf16_lo(v.w); f[7] = bf16_hi(v.w);
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+__device__ __forceinline__ u32x4 pack8(const float (&f)[8]) {
+  return u32x4{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])};
 }
 
 // 8 rows (the contraction) of 8 columns -> for each column its 8 rows: tile i's fragment is o[i].
-__device__ __forceinline__ void transpose8(const uint4 (&r)[8], uint4 (&o)[8]) {
-  const uint32_t* in = reinterpret_cast<const uint32_t*>(r);
-  uint32_t* out = reinterpret_cast<uint32_t*>(o);
+__device__ __forceinline__ void transpose8(const u32x4 (&r)[8], u32x4 (&o)[8]) {
 #pragma unroll
   for (int j = 0; j < 4; ++j)        // rows 2 j, 2 j + 1
 #pragma unroll
     for (int h = 0; h < 4; ++h) {    // columns 2 h, 2 h + 1
-      const uint32_t lo = in[(2 * j) * 4 + h], hi = in[(2 * j + 1) * 4 + h];
-      out[(2 * h) * 4 + j] = __builtin_amdgcn_perm(hi, lo, 0x05040100u);
-      out[(2 * h + 1) * 4 + j] = __builtin_amdgcn_perm(hi, lo, 0x07060302u);
+      const uint32_t lo = r[2 * j][h], hi = r[2 * j + 1][h];
+      o[2 * h][j] = __builtin_amdgcn_perm(hi, lo, 0x05040100u);
+      o[2 * h + 1][j] = __builtin_amdgcn_perm(hi, lo, 0x07060302u);
     }
 }
 
 // w's fragments for 128 columns: ranks 32 k + 8 q .. + 7 of the columns that the lane holds, 0 past R.
 template <int KS>
-__device__ __forceinline__ void load_w(const uint16_t* w, int R, int N, int col, uint4 (&f)[KS][8]) {
+__device__ __forceinline__ void load_w(const uint16_t* w, int R, int N, int col, u32x4 (&f)[KS][8]) {
   const int q = (threadIdx.x & 63) >> 4;
 #pragma unroll
   for (int k = 0; k < KS; ++k) {
-    uint4 r[8];
+    u32x4 r[8];
     const bool live = 32 * k + 8 * q < R;
     const uint16_t* at = w + static_cast<long long>(live ? 32 * k + 8 * q : 0) * N + col;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      r[j] = *reinterpret_cast<const uint4*>(at + static_cast<long long>(j) * N);
-      if (!live) r[j] = make_uint4(0, 0, 0, 0);
+      r[j] = load16(at + static_cast<long long>(j) * N);
+      if (!live) r[j] = u32x4{0, 0, 0, 0};
     }
     transpose8(r, f[k]);
   }
 }
 
 // 8 ranks of one row of v, hi and lo; from slices: of their fp32 sums in slice order.
-__device__ __forceinline__ void load_v(const ExpandArgs& a, long long row, int col, uint4& hi, uint4& lo) {
+__device__ __forceinline__ void load_v(const ExpandArgs& a, long long row, int col, u32x4& hi, u32x4& lo) {
   if (a.S == 1) {
-    hi = *reinterpret_cast<const uint4*>(a.v + row * a.ldv + col);
-    lo = *reinterpret_cast<const uint4*>(a.vlo + row * a.ldv + col);
+    hi = load16(a.v + row * a.ldv + col);
+    lo = load16(a.vlo + row * a.ldv + col);
     return;
   }
   float f[8], h[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) f[i] = 0.f;
-  for (int s = 0; s < a.S; ++s) {
-    const float4* at = reinterpret_cast<const float4*>(a.part + (static_cast<long long>(s) * a.rows.n + row) * a.ldv + col);
-    const float4 x = at[0], y = at[1];
-    f[0] += x.x; f[1] += x.y; f[2] += x.z; f[3] += x.w;
-    f[4] += y.x; f[5] += y.y; f[6] += y.z; f[7] += y.w;
+  const float* at = a.part + row * a.ldv + col;
+  const long long step = static_cast<long long>(a.rows.n) * a.ldv;
+  for (int s = 0; s < a.S; s += 4) {       // four slices' loads in flight; past the last one it is read again and not added
+    f32x4 x[4], y[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float* from = at + min(s + j, a.S - 1) * step;
+      x[j] = *reinterpret_cast<const f32x4*>(from);
+      y[j] = *reinterpret_cast<const f32x4*>(from + 4);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (s + j >= a.S) break;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f[i] += x[j][i];
+        f[4 + i] += y[j][i];
+      }
+    }
   }
   hi = pack8(f);
   unpack8(hi, h);
@@ -563,19 +625,22 @@ __device__ __forceinline__ void load_v(const ExpandArgs& a, long long row, int c
 }
 
 template <int KS, int MODE, bool DROP>
-__global__ __launch_bounds__(256, KS == 1 ? 2 : 1) void adapter_expand_kernel(ExpandArgs a) {
+__global__ __launch_bounds__(256, KS == 1 || (KS == 2 && MODE != kSwiglu) ? 2 : 1) void adapter_expand_kernel(ExpandArgs a) {
   constexpr int NW = MODE == kSwiglu ? 2 : 1;
   constexpr int NOUT = MODE == kAdd ? 1 : MODE == kSwiglu ? 3 : 2;
   const PlanLayout p = plan_layout(a.rows.n, a.rows.E, a.rows.L);
   const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4;
   const int stripes = (a.N + 127) / 128;
-  const long long items = static_cast<long long>(n_tiles(a.rows)) * stripes, step = gridDim.x * 4LL;
+  const int each = stripes * a.parts, rows_each = kTileRows / a.parts;
+  const long long items = static_cast<long long>(n_tiles(a.rows)) * each, step = gridDim.x * 4LL;
   DropKey key;
   if (DROP) key = drop_key(a.drop);
   for (long long i = blockIdx.x * 4LL + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); i < items; i += step) {
-    const Tile t = tile_at(a.rows, p, static_cast<int>(i / stripes));
-    const int stripe = static_cast<int>(i % stripes);
-    if (t.count == 0) continue;
+    Tile t = tile_at(a.rows, p, static_cast<int>(i / each));
+    const int stripe = static_cast<int>(i % stripes), first = static_cast<int>(i % each / stripes) * rows_each;
+    t.pos += first;
+    t.count = min(t.count - first, rows_each);
+    if (t.count <= 0) continue;
     const int col = 128 * stripe + 8 * c;
     const bool live = col < a.N;        // the last stripe may be half
     const int cc = live ? col : 0;
@@ -591,11 +656,11 @@ __global__ __launch_bounds__(256, KS == 1 ? 2 : 1) void adapter_expand_kernel(Ex
 #pragma unroll
         for (int o = 0; o < NOUT; ++o)
           if (live && a.out[o] != nullptr)
-            *reinterpret_cast<uint4*>(a.out[o] + at) = *reinterpret_cast<const uint4*>(a.in[MODE == kSwigluBwd ? o + 2 : o] + at);
+            store16(a.out[o] + at, load16(a.in[MODE == kSwigluBwd ? o + 2 : o] + at));
       }
       continue;
     }
-    uint4 wf[NW][KS][8];
+    u32x4 wf[NW][KS][8];
     const long long g = (static_cast<long long>(t.l) * a.rows.E + t.e) * a.R * a.N;
 #pragma unroll
     for (int m = 0; m < NW; ++m) load_w<KS>(a.w[m] + g, a.R, a.N, cc, wf[m]);
@@ -605,14 +670,14 @@ __global__ __launch_bounds__(256, KS == 1 ? 2 : 1) void adapter_expand_kernel(Ex
     for (int b = 0; b < nb; ++b) {
       const int mine = row_at(a.rows, p, t.pos + min(16 * b + c, t.count - 1));
       int row[4];
-      uint4 in[4][MODE == kAdd ? 1 : MODE == kSwiglu ? 2 : 4];
+      u32x4 in[4][MODE == kAdd ? 1 : MODE == kSwiglu ? 2 : 4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         row[j] = __shfl(mine, 4 * q + j, 64);
         const long long at = static_cast<long long>(row[j]) * a.N + cc;
 #pragma unroll
         for (int o = 0; o < (MODE == kAdd ? 1 : MODE == kSwiglu ? 2 : 4); ++o)
-          in[j][o] = *reinterpret_cast<const uint4*>(a.in[o] + at);
+          in[j][o] = load16(a.in[o] + at);
       }
       f32x4 acc[NW][8];
 #pragma unroll
@@ -622,13 +687,13 @@ __global__ __launch_bounds__(256, KS == 1 ? 2 : 1) void adapter_expand_kernel(Ex
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
           const int rank = 32 * k + 8 * q;
-          uint4 hi = make_uint4(0, 0, 0, 0), lo = hi;
+          u32x4 hi = u32x4{0, 0, 0, 0}, lo = hi;
           if (rank < a.R) {
             load_v(a, mine, m * a.R + rank, hi, lo);
             if (a.v_out != nullptr && stripe == 0 && 16 * b + c < t.count) {
               const long long to = static_cast<long long>(mine) * a.ldv + m * a.R + rank;
-              *reinterpret_cast<uint4*>(a.v_out + to) = hi;
-              if (a.vlo_out != nullptr) *reinterpret_cast<uint4*>(a.vlo_out + to) = lo;
+              store16(a.v_out + to, hi);
+              if (a.vlo_out != nullptr) store16(a.vlo_out + to, lo);
             }
           }
 #pragma unroll
@@ -650,7 +715,7 @@ __global__ __launch_bounds__(256, KS == 1 ? 2 : 1) void adapter_expand_kernel(Ex
           if (DROP) drop_apply(key, row[j], col >> 3, 1.f, delta);
 #pragma unroll
           for (int o = 0; o < 8; ++o) x0[o] = fmaf(f, delta[o], x0[o]);
-          *reinterpret_cast<uint4*>(a.out[0] + at) = pack8(x0);
+          store16(a.out[0] + at, pack8(x0));
         } else if constexpr (MODE == kSwiglu) {
           float y[8];
           unpack8(in[j][1], x1);
@@ -661,10 +726,10 @@ __global__ __launch_bounds__(256, KS == 1 ? 2 : 1) void adapter_expand_kernel(Ex
             y[o] = x0[o] * logistic(x0[o]) * x1[o];
           }
           if (a.out[0] != nullptr) {
-            *reinterpret_cast<uint4*>(a.out[0] + at) = pack8(x0);
-            *reinterpret_cast<uint4*>(a.out[1] + at) = pack8(x1);
+            store16(a.out[0] + at, pack8(x0));
+            store16(a.out[1] + at, pack8(x1));
           }
-          *reinterpret_cast<uint4*>(a.out[2] + at) = pack8(y);
+          store16(a.out[2] + at, pack8(y));
         } else {
           float dg[8], du[8], delta[8];
           unpack8(in[j][1], x1);
@@ -679,8 +744,8 @@ __global__ __launch_bounds__(256, KS == 1 ? 2 : 1) void adapter_expand_kernel(Ex
             dg[o] = fmaf(da * x1[o], s * fmaf(x0[o], 1.f - s, 1.f), dg[o]);
             du[o] = fmaf(da, x0[o] * s, du[o]);
           }
-          *reinterpret_cast<uint4*>(a.out[0] + at) = pack8(dg);
-          *reinterpret_cast<uint4*>(a.out[1] + at) = pack8(du);
+          store16(a.out[0] + at, pack8(dg));
+          store16(a.out[1] + at, pack8(du));
         }
       }
     }
@@ -708,94 +773,123 @@ struct WgradArgs {
 // pieces are longer than that), so a bit for the first keeps all apart.
 __device__ __forceinline__ long long piece_slot(int pos, int piece, bool first) { return 2LL * (pos / piece) + first; }
 
-// v's fragments for RT tiles of 16 ranks and 32 rows, 0 for rows from `left` on.
-template <int RT>
-__device__ __forceinline__ void load_vt(const uint16_t* v, int ldv, int R, int r0, const int (&row)[8], int left, uint4 (&vf)[RT]) {
-  const int c = threadIdx.x & 15, q = (threadIdx.x & 63) >> 4;
-  if constexpr (RT == 1) {
-    // ranks r0 + c: 8 rows' values of one rank each
-    const int rank = min(r0 + c, R - 1);
-    uint32_t w[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = 8 * q + j < left ? v[static_cast<long long>(row[j]) * ldv + rank] : 0u;
-    vf[0] = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
-  } else {
-    // two tiles at a time take the even and the odd ones of 32 ranks: 4 bytes of 8 rows
-#pragma unroll
-    for (int m = 0; m < RT; m += 2) {
-      const int rank = min(r0 + 16 * m + 2 * c, R - 2);
-      uint32_t w[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        w[j] = 8 * q + j < left ? *reinterpret_cast<const uint32_t*>(v + static_cast<long long>(row[j]) * ldv + rank) : 0u;
-      uint32_t even[4], odd[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        even[j] = __builtin_amdgcn_perm(w[2 * j + 1], w[2 * j], 0x05040100u);
-        odd[j] = __builtin_amdgcn_perm(w[2 * j + 1], w[2 * j], 0x07060302u);
-      }
-      vf[m] = make_uint4(even[0], even[1], even[2], even[3]);
-      vf[m + 1] = make_uint4(odd[0], odd[1], odd[2], odd[3]);
-    }
-  }
-}
-
-// RT tiles of 16 ranks (from rank r0) x 128 columns over the rows of one piece, 32 rows a step.
+// RT tiles of 16 ranks (from rank r0) x 128 columns a wave over the rows of one piece, 64 rows a step.  The workgroup's waves take
+// neighbouring columns of the same rows, so v's 64 rows are staged once for all of them, transposed: pairs of rows [rank][32] in
+// LDS (padded to 36: the 16 ranks of a fragment's 16-byte reads lie in different banks).  y's rows go from memory into
+// registers half a step (32 rows) ahead, v's and the row numbers a whole one; loads past the piece read its last row.
 template <int RT, bool DROP, bool LO>
-__global__ __launch_bounds__(256) void adapter_wgrad_kernel(WgradArgs a) {
+__global__ __launch_bounds__(256, 2) void adapter_wgrad_kernel(WgradArgs a) {
+  constexpr int NV = LO ? 2 : 1, kItems = NV * RT * 64, NI = (kItems + 255) / 256, kPad = 36;
+  __shared__ uint32_t vt[2][NV][16 * RT][kPad];
+  // row and row of y, of steps s (read until its last product) and s + 1 while those of s + 2 come
+  __shared__ int ids[4][2][64];
   const PlanLayout p = plan_layout(a.rows.n, a.rows.E, a.rows.L);
-  const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4;
-  const int stripes = (a.C + 127) / 128, parts = (a.R + 16 * RT - 1) / (16 * RT), which = blockIdx.y;
+  const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int stripes = (a.C + 127) / 128, groups = (stripes + 3) / 4, per = (stripes + groups - 1) / groups;
+  const int parts = (a.R + 16 * RT - 1) / (16 * RT), which = blockIdx.y;
   const int piece = piece_rows(a.rows.n);
-  const long long items = static_cast<long long>(a.rows.plan[kHeadItems]) * parts * stripes, step = gridDim.x * 4LL;
+  const long long items = static_cast<long long>(a.rows.plan[kHeadItems]) * parts * groups;
   const uint16_t* y = a.y[which];
   DropKey key;
   if (DROP) key = drop_key(a.drop);
-  for (long long i = blockIdx.x * 4LL + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); i < items; i += step) {
-    const Tile t = reinterpret_cast<const Tile*>(a.rows.plan + p.items)[i / (parts * stripes)];
-    const int stripe = static_cast<int>(i % stripes), r0 = static_cast<int>(i / stripes % parts) * 16 * RT;
-    const int col = 128 * stripe + 8 * c, cc = col < a.C ? col : 0;
+  for (long long i = blockIdx.x; i < items; i += gridDim.x) {
+    const Tile t = reinterpret_cast<const Tile*>(a.rows.plan + p.items)[i / (parts * groups)];
+    const int stripe = static_cast<int>(i % groups) * per + wave, r0 = static_cast<int>(i / groups % parts) * 16 * RT;
+    const bool busy = wave < per && stripe < stripes;
+    const int col = 128 * stripe + 8 * c, cc = busy && col < a.C ? col : 0;
+    const int32_t* list = a.rows.plan + p.rows + t.pos;
+    const int32_t* srcs = a.gather ? a.rows.plan + p.toks + t.pos : list;
     f32x4 acc[RT][8];
 #pragma unroll
     for (int m = 0; m < RT; ++m)
 #pragma unroll
       for (int o = 0; o < 8; ++o) acc[m][o] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < t.count; s += 32) {
-      const int left = t.count - s;
-      const int mine = a.rows.plan[p.rows + t.pos + s + min(lane & 31, left - 1)];
-      int src = mine;
-      if (a.gather && a.rows.row_token != nullptr) src = min(max(a.rows.row_token[mine], 0), a.rows.T - 1);
-      uint4 yr[8];
-      int row[8];
+    if (t.count > 0) {
+      auto row_of = [&](int at) { return list[min(at, t.count - 1)]; };
+      auto src_of = [&](int at) { return srcs[min(at, t.count - 1)]; };
+      // v: item k of a thread is a pair of rows and 8 ranks of hi or lo
+      u32x4 vr[NI][2];
+      auto load_v = [&](int s) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        row[j] = __shfl(mine, 8 * q + j, 64);
-        yr[j] = *reinterpret_cast<const uint4*>(y + static_cast<long long>(__shfl(src, 8 * q + j, 64)) * a.C + cc);
-      }
-      uint4 vf[RT], vl[RT];
-      load_vt<RT>(a.v + a.v0[which], a.ldv, a.R, r0, row, left, vf);
-      if constexpr (LO) load_vt<RT>(a.vlo + a.v0[which], a.ldv, a.R, r0, row, left, vl);
-      if (DROP) {
+        for (int k = 0; k < NI; ++k) {
+          const int it = tid + 256 * k, pair = it & 31, rank = r0 + 8 * ((it >> 5) % (2 * RT));
+          const uint16_t* v = (LO && it >= RT * 64 ? a.vlo : a.v) + a.v0[which] + (rank < a.R ? rank : 0);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) yr[j] = drop_zero(key, row[j], cc >> 3, yr[j]);
-      }
-      if (left < 32) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (8 * q + j >= left) yr[j] = make_uint4(0, 0, 0, 0);
-      }
-      uint4 yf[8];
-      transpose8(yr, yf);
-#pragma unroll
-      for (int m = 0; m < RT; ++m) {
-        if constexpr (LO) {
-#pragma unroll
-          for (int o = 0; o < 8; ++o) acc[m][o] = mfma(vl[m], yf[o], acc[m][o]);
+          for (int h = 0; h < 2; ++h) vr[k][h] = load16(v + static_cast<long long>(ids[s & 3][0][2 * pair + h]) * a.ldv);
         }
+        __builtin_amdgcn_sched_barrier(0);
+      };
+      auto put_v = [&](int buf, int left) {
 #pragma unroll
-        for (int o = 0; o < 8; ++o) acc[m][o] = mfma(vf[m], yf[o], acc[m][o]);
+        for (int k = 0; k < NI; ++k) {
+          const int it = tid + 256 * k, pair = it & 31, ch = (it >> 5) % (2 * RT);
+          if (it >= kItems) continue;
+          uint32_t(*to)[kPad] = &vt[buf][LO && it >= RT * 64 ? 1 : 0][8 * ch];
+          const uint32_t m0 = 2 * pair < left ? ~0u : 0u, m1 = 2 * pair + 1 < left ? ~0u : 0u;
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            const uint32_t lo = vr[k][0][h] & m0, hi = vr[k][1][h] & m1;
+            to[2 * h][pair] = __builtin_amdgcn_perm(hi, lo, 0x05040100u);
+            to[2 * h + 1][pair] = __builtin_amdgcn_perm(hi, lo, 0x07060302u);
+          }
+        }
+      };
+      auto load_y = [&](u32x4 (&yr)[8], int s, int sub) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) yr[j] = load16(y + static_cast<long long>(ids[s & 3][1][32 * sub + 8 * q + j]) * a.C + cc);
+        __builtin_amdgcn_sched_barrier(0);
+      };
+      auto multiply = [&](u32x4 (&yr)[8], int s, int sub, int left) {
+        const int buf = s & 1;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int at = 32 * sub + 8 * q + j;
+          if (DROP) yr[j] = drop_zero(key, ids[s & 3][0][at], cc >> 3, yr[j]);
+          const uint32_t keep = at < left ? ~0u : 0u;
+          yr[j] &= u32x4{keep, keep, keep, keep};
+        }
+        u32x4 yf[8];
+        transpose8(yr, yf);
+#pragma unroll
+        for (int m = 0; m < RT; ++m)
+#pragma unroll
+          for (int n = NV - 1; n >= 0; --n) {
+            const u32x4 vf = *reinterpret_cast<const u32x4*>(&vt[buf][n][16 * m + c][16 * sub + 4 * q]);
+#pragma unroll
+            for (int o = 0; o < 8; ++o) acc[m][o] = mfma(vf, yf[o], acc[m][o]);
+          }
+        __builtin_amdgcn_sched_barrier(0);
+      };
+      __syncthreads();                   // the last item's reads are over
+      if (tid < 64) {
+        ids[0][0][tid] = row_of(tid);
+        ids[0][1][tid] = src_of(tid);
+      }
+      int next = row_of(64 + lane), next_src = src_of(64 + lane);
+      __syncthreads();
+      u32x4 ya[8], yb[8];
+      load_v(0);
+      load_y(ya, 0, 0);
+      const int steps = (t.count + 63) / 64;
+      for (int s = 0; s < steps; ++s) {
+        const int left = t.count - 64 * s;
+        put_v(s & 1, left);
+        if (tid < 64) {
+          ids[(s + 1) & 3][0][tid] = next;
+          ids[(s + 1) & 3][1][tid] = next_src;
+        }
+        __syncthreads();
+        next = row_of(64 * (s + 2) + lane);
+        next_src = src_of(64 * (s + 2) + lane);
+        load_v(s + 1);
+        load_y(yb, s, 1);
+        multiply(ya, s, 0, left);
+        load_y(ya, s + 1, 0);
+        multiply(yb, s, 1, left);
       }
     }
+    if (!busy) continue;
     float f = a.scale != nullptr ? a.scale[t.l] : 1.f;
     if (DROP) f *= drop_scale(a.drop.drop);
     const int32_t* goff = a.rows.plan + p.goff + t.e * (a.rows.L + 1) + t.l;
@@ -806,8 +900,7 @@ __global__ __launch_bounds__(256) void adapter_wgrad_kernel(WgradArgs a) {
     for (int m = 0; m < RT; ++m) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        // accumulator row 4 q + j of tile m
-        const int rank = RT == 1 ? r0 + 4 * q + j : r0 + 16 * (m & ~1) + 2 * (4 * q + j) + (m & 1);
+        const int rank = r0 + 16 * m + 4 * q + j;      // accumulator row 4 q + j of tile m
         if (rank >= a.R || col >= a.C) continue;
         const long long at = static_cast<long long>(rank) * a.C + col;
         float x[8];
@@ -817,22 +910,30 @@ __global__ __launch_bounds__(256) void adapter_wgrad_kernel(WgradArgs a) {
           *reinterpret_cast<float4*>(part + at) = make_float4(x[0], x[1], x[2], x[3]);
           *reinterpret_cast<float4*>(part + at + 4) = make_float4(x[4], x[5], x[6], x[7]);
         } else {
-          *reinterpret_cast<uint4*>(out + at) = pack8(x);
+          store16(out + at, pack8(x));
         }
       }
     }
   }
 }
 
-// Groups of several pieces: their sums in the order of the pieces.  gridDim.x workgroups to a group.
-__global__ __launch_bounds__(256) void adapter_join_kernel(WgradArgs a) {
+// Groups of several pieces: their sums in the order of the pieces.  gridDim.x workgroups to a group, blockIdx.z one of up to
+// three products.
+struct JoinArgs {
+  Rows rows;
+  const float* part[3];
+  uint16_t* out[3];
+  int R[3], C[3];
+};
+
+__global__ __launch_bounds__(256) void adapter_join_kernel(JoinArgs a) {
+  if (static_cast<int>(blockIdx.y) >= a.rows.plan[kHeadMulti]) return;
   const PlanLayout p = plan_layout(a.rows.n, a.rows.E, a.rows.L);
   const int which = blockIdx.z, piece = piece_rows(a.rows.n);
-  if (static_cast<int>(blockIdx.y) >= a.rows.plan[kHeadMulti]) return;
   const int pair = a.rows.plan[p.multi + blockIdx.y], e = pair / (a.rows.L + 1), l = pair - e * (a.rows.L + 1);
   const int begin = a.rows.plan[p.goff + pair], end = a.rows.plan[p.goff + pair + 1];
-  const long long size = static_cast<long long>(a.R) * a.C;
-  const float* part = a.part + which * 2LL * (a.rows.n / piece + 1) * size;
+  const long long size = static_cast<long long>(a.R[which]) * a.C[which];
+  const float* part = a.part[which];
   uint16_t* out = a.out[which] + (static_cast<long long>(l) * a.rows.E + e) * size;
   for (long long i = (blockIdx.x * 256LL + threadIdx.x) * 8; i < size; i += gridDim.x * 2048LL) {
     float x[8];
@@ -844,7 +945,7 @@ __global__ __launch_bounds__(256) void adapter_join_kernel(WgradArgs a) {
       x[0] += lo.x; x[1] += lo.y; x[2] += lo.z; x[3] += lo.w;
       x[4] += hi.x; x[5] += hi.y; x[6] += hi.z; x[7] += hi.w;
     }
-    *reinterpret_cast<uint4*>(out + i) = pack8(x);
+    store16(out + i, pack8(x));
   }
 }
 
@@ -859,11 +960,13 @@ int slices(bool planned, int n, int K) {
   const long long tiles = planned ? (n + kTileRows - 1) / kTileRows : n;
   const int most = (K / 64 + 3) / 4;
   const long long want = 512 / tiles;
-  const int s = want < 1 ? 1 : want > 16 ? 16 : static_cast<int>(want);
+  const int s = want < 1 ? 1 : want > 8 ? 8 : static_cast<int>(want);
   return s < most ? s : most;
 }
 
-unsigned grid_of(long long workgroups) { return static_cast<unsigned>(workgroups < kGridCap ? workgroups : kGridCap); }
+unsigned grid_of(long long workgroups) {
+  return static_cast<unsigned>(workgroups < kGridCap ? (workgroups + 7) / 8 * 8 : kGridCap);
+}
 
 template <bool DROP>
 void launch_shrink(const ShrinkArgs& a, int products, hipStream_t st) {
@@ -875,8 +978,12 @@ void launch_shrink(const ShrinkArgs& a, int products, hipStream_t st) {
 }
 
 template <int MODE, bool DROP>
-void launch_expand(const ExpandArgs& a, hipStream_t st) {
-  const unsigned grid = grid_of((static_cast<long long>(tiles_cap(a.rows)) * ((a.N + 127) / 128) + 3) / 4);
+void launch_expand(ExpandArgs a, hipStream_t st) {
+  const long long stripes = (a.N + 127) / 128, waves = tiles_cap(a.rows) * stripes;
+  // A wave walks its rows 16 at a time, each time waiting for memory: where a launch has few waves they take fewer rows.
+  const long long tiles = a.rows.plan != nullptr ? (a.rows.n + kTileRows - 1) / kTileRows : a.rows.n;
+  a.parts = a.rows.plan == nullptr || tiles * stripes >= 4096 ? 1 : tiles * stripes >= 2048 ? 2 : 4;
+  const unsigned grid = grid_of((waves * a.parts + 3) / 4);
   if (a.R <= 32) adapter_expand_kernel<1, MODE, DROP><<<grid, 256, 0, st>>>(a);
   else if (a.R <= 64) adapter_expand_kernel<2, MODE, DROP><<<grid, 256, 0, st>>>(a);
   else if constexpr (MODE == kAdd) adapter_expand_kernel<4, MODE, DROP><<<grid, 256, 0, st>>>(a);
@@ -885,17 +992,21 @@ void launch_expand(const ExpandArgs& a, hipStream_t st) {
 template <bool DROP, bool LO>
 void launch_wgrad(const WgradArgs& a, int products, hipStream_t st) {
   const PlanLayout p = plan_layout(a.rows.n, a.rows.E, a.rows.L);
-  const int rt = a.R <= 16 ? 1 : a.R <= 32 ? 2 : 4;
-  const long long waves = static_cast<long long>(p.items_cap) * ((a.R + 16 * rt - 1) / (16 * rt)) * ((a.C + 127) / 128);
-  const dim3 grid(grid_of((waves + 3) / 4), products);
+  const int rt = a.R <= 16 ? 1 : 2;
+  const int stripes = (a.C + 127) / 128;
+  const long long wgs = static_cast<long long>(p.items_cap) * ((a.R + 16 * rt - 1) / (16 * rt)) * ((stripes + 3) / 4);
+  const dim3 grid(grid_of(wgs), products);
   if (rt == 1) adapter_wgrad_kernel<1, DROP, LO><<<grid, 256, 0, st>>>(a);
-  else if (rt == 2) adapter_wgrad_kernel<2, DROP, LO><<<grid, 256, 0, st>>>(a);
-  else adapter_wgrad_kernel<4, DROP, LO><<<grid, 256, 0, st>>>(a);
+  else adapter_wgrad_kernel<2, DROP, LO><<<grid, 256, 0, st>>>(a);
+}
+
+// Joins the pieces of up to three products in one launch, where there can be groups of several.
+void launch_join(const JoinArgs& a, int products, hipStream_t st) {
   const int piece = piece_rows(a.rows.n);
-  if (a.rows.n > piece) {
-    const long long blocks = (static_cast<long long>(a.R) * a.C + 2047) / 2048;
-    adapter_join_kernel<<<dim3(static_cast<unsigned>(blocks < 64 ? blocks : 64), p.multi_cap, products), 256, 0, st>>>(a);
-  }
+  if (a.rows.n <= piece) return;
+  long long blocks = 0;
+  for (int i = 0; i < products; ++i) blocks = max(blocks, (static_cast<long long>(a.R[i]) * a.C[i] + 2047) / 2048);
+  adapter_join_kernel<<<dim3(static_cast<unsigned>(blocks < 64 ? blocks : 64), a.rows.n / piece + 1, products), 256, 0, st>>>(a);
 }
 
 int check_sizes(int T, int n, int E, int L) {
@@ -937,15 +1048,23 @@ long long piece_bytes(int n, int products, int R, int C) {
 
 long long forward_bytes(bool planned, int n, int R, int K) { return 2 * v_bytes(n, R) + part_bytes(planned, n, R, K); }
 
-long long max_ll(long long a, long long b) { return a > b ? a : b; }
-
-long long down_bwd_bytes(int n, int d, int f, int r) {
-  return 2 * v_bytes(n, r) + max_ll(part_bytes(true, n, r, d), max_ll(piece_bytes(n, 1, r, d), piece_bytes(n, 1, r, f)));
+// The workspace of a backward call: v's hi and lo [n][R], its slices, the pieces of the B's gradients (1 or 2 products
+// of C1 columns and r ranks) and of A's (R ranks, C2 columns).
+struct BwdSpace {
+  long long hi, lo, part, pieces_b, pieces_a, bytes;
+};
+BwdSpace bwd_space(int n, int r, int products, int C1, int R, int C2) {
+  BwdSpace w;
+  w.hi = 0;
+  w.lo = v_bytes(n, R);
+  w.part = 2 * v_bytes(n, R);
+  w.pieces_b = w.part + part_bytes(true, n, R, C1);
+  w.pieces_a = w.pieces_b + piece_bytes(n, products, r, C1);
+  w.bytes = w.pieces_a + piece_bytes(n, 1, R, C2);
+  return w;
 }
-long long gate_up_bwd_bytes(int n, int d, int f, int r) {
-  return 2 * v_bytes(n, 2 * r) +
-         max_ll(part_bytes(true, n, 2 * r, f), max_ll(piece_bytes(n, 2, r, f), piece_bytes(n, 1, 2 * r, d)));
-}
+BwdSpace down_bwd_space(int n, int d, int f, int r) { return bwd_space(n, r, 1, d, r, f); }
+BwdSpace gate_up_bwd_space(int n, int d, int f, int r) { return bwd_space(n, r, 2, f, 2 * r, d); }
 
 #define MOE_CHECK_WS(need)                                                                                     \
   do {                                                                                                         \
@@ -983,8 +1102,8 @@ extern "C" int moe_adapter_plan(const int32_t* ids, const int32_t* row_token, co
 extern "C" size_t moe_adapter_workspace_bytes(int n, int d, int f, int r, int planned, int backward) {
   if (check_sizes(1, n, 1, 1) || check_dims(d, f, r)) return 0;
   const bool p = planned != 0;
-  if (backward) return static_cast<size_t>(max_ll(down_bwd_bytes(n, d, f, r), gate_up_bwd_bytes(n, d, f, r)));
-  return static_cast<size_t>(max_ll(forward_bytes(p, n, 2 * r, d), forward_bytes(p, n, r, f)));
+  if (backward) return static_cast<size_t>(max(down_bwd_space(n, d, f, r).bytes, gate_up_bwd_space(n, d, f, r).bytes));
+  return static_cast<size_t>(max(forward_bytes(p, n, 2 * r, d), forward_bytes(p, n, r, f)));
 }
 
 extern "C" int moe_adapter_gate_up(const uint16_t* x, const int32_t* ids, const int32_t* row_token, const int32_t* offsets,
@@ -1013,7 +1132,7 @@ extern "C" int moe_adapter_gate_up(const uint16_t* x, const int32_t* ids, const 
   hipStream_t st = as_stream(stream);
   if (drop.drop) launch_shrink<true>(s, 1, st);
   else launch_shrink<false>(s, 1, st);
-  ExpandArgs e = {rows, vbuf, lo, part, 2 * r, S, r, f, {b_gate, b_up}, scale, {g, u, a, nullptr}, {g_out, u_out, a_out},
+  ExpandArgs e = {rows, vbuf, lo, part, 2 * r, S, r, f, 1, {b_gate, b_up}, scale, {g, u, a, nullptr}, {g_out, u_out, a_out},
                   S > 1 ? v : nullptr, nullptr, DropArgs{}};
   launch_expand<kSwiglu, false>(e, st);
   return check_launch("adapter_gate_up");
@@ -1041,7 +1160,7 @@ extern "C" int moe_adapter_down(const uint16_t* a, const int32_t* ids, const int
   hipStream_t st = as_stream(stream);
   if (drop.drop) launch_shrink<true>(s, 1, st);
   else launch_shrink<false>(s, 1, st);
-  ExpandArgs e = {rows, vbuf, lo, part, r, S, r, d, {b_down, nullptr}, scale, {yexp, nullptr, nullptr, nullptr},
+  ExpandArgs e = {rows, vbuf, lo, part, r, S, r, d, 1, {b_down, nullptr}, scale, {yexp, nullptr, nullptr, nullptr},
                   {y_out, nullptr, nullptr}, S > 1 ? v : nullptr, nullptr, DropArgs{}};
   launch_expand<kAdd, false>(e, st);
   return check_launch("adapter_down");
@@ -1066,23 +1185,29 @@ extern "C" int moe_adapter_down_bwd(const uint16_t* dyexp, const uint16_t* a, co
   MOE_CHECK_ALIGN(du_out); MOE_CHECK_ALIGN(d_a_down); MOE_CHECK_ALIGN(d_b_down);
   DropArgs drop;
   if (int st = make_drop(rng, p, site, &drop)) return st;
-  MOE_CHECK_WS(down_bwd_bytes(n, d, f, r));
-  uint16_t* dv = static_cast<uint16_t*>(ws);
-  uint16_t* lo = reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + v_bytes(n, r));
-  float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + 2 * v_bytes(n, r));
+  const BwdSpace space = down_bwd_space(n, d, f, r);
+  MOE_CHECK_WS(space.bytes);
+  char* base = static_cast<char*>(ws);
+  uint16_t* dv = reinterpret_cast<uint16_t*>(base + space.hi);
+  uint16_t* lo = reinterpret_cast<uint16_t*>(base + space.lo);
+  float* part = reinterpret_cast<float*>(base + space.part);
+  float* pieces_b = reinterpret_cast<float*>(base + space.pieces_b);
+  float* pieces_a = reinterpret_cast<float*>(base + space.pieces_a);
   const int S = slices(true, n, d);
   hipStream_t st = as_stream(stream);
+  // dyexp's second reader follows its first, so that what the last-level cache still holds of it is found there
   const ShrinkArgs s = {rows, {dyexp, nullptr}, {b_down, nullptr}, {0, 0}, 0, d, r, r, S, scale, dv, lo, part, DropArgs{}};
   launch_shrink<false>(s, 1, st);
-  const ExpandArgs e = {rows, dv, lo, part, r, S, r, f, {a_down, nullptr}, nullptr, {g, u, dg, du}, {dg_out, du_out, nullptr},
+  const WgradArgs wb = {rows, v, nullptr, {0, 0}, {dyexp, nullptr}, 0, r, r, d, scale, {d_b_down, nullptr}, pieces_b, DropArgs{}};
+  launch_wgrad<false, false>(wb, 1, st);
+  const ExpandArgs e = {rows, dv, lo, part, r, S, r, f, 1, {a_down, nullptr}, nullptr, {g, u, dg, du}, {dg_out, du_out, nullptr},
                         S > 1 ? dv : nullptr, S > 1 ? lo : nullptr, drop};
   if (drop.drop) launch_expand<kSwigluBwd, true>(e, st);
   else launch_expand<kSwigluBwd, false>(e, st);
-  const WgradArgs wb = {rows, v, nullptr, {0, 0}, {dyexp, nullptr}, 0, r, r, d, scale, {d_b_down, nullptr}, part, DropArgs{}};
-  launch_wgrad<false, false>(wb, 1, st);
-  const WgradArgs wa = {rows, dv, lo, {0, 0}, {a, nullptr}, 0, r, r, f, nullptr, {d_a_down, nullptr}, part, drop};
+  const WgradArgs wa = {rows, dv, lo, {0, 0}, {a, nullptr}, 0, r, r, f, nullptr, {d_a_down, nullptr}, pieces_a, drop};
   if (drop.drop) launch_wgrad<true, true>(wa, 1, st);
   else launch_wgrad<false, true>(wa, 1, st);
+  launch_join({rows, {pieces_b, pieces_a, nullptr}, {d_b_down, d_a_down, nullptr}, {r, r, 0}, {d, f, 0}}, 2, st);
   return check_launch("adapter_down_bwd");
 }
 
@@ -1105,22 +1230,28 @@ extern "C" int moe_adapter_gate_up_bwd(const uint16_t* dg, const uint16_t* du, c
   MOE_CHECK_ALIGN(d_a_gu); MOE_CHECK_ALIGN(d_b_gate); MOE_CHECK_ALIGN(d_b_up);
   DropArgs drop;
   if (int st = make_drop(rng, p, site, &drop)) return st;
-  MOE_CHECK_WS(gate_up_bwd_bytes(n, d, f, r));
-  uint16_t* dv = static_cast<uint16_t*>(ws);
-  uint16_t* lo = reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + v_bytes(n, 2 * r));
-  float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + 2 * v_bytes(n, 2 * r));
+  const BwdSpace space = gate_up_bwd_space(n, d, f, r);
+  MOE_CHECK_WS(space.bytes);
+  char* base = static_cast<char*>(ws);
+  uint16_t* dv = reinterpret_cast<uint16_t*>(base + space.hi);
+  uint16_t* lo = reinterpret_cast<uint16_t*>(base + space.lo);
+  float* part = reinterpret_cast<float*>(base + space.part);
+  float* pieces_b = reinterpret_cast<float*>(base + space.pieces_b);
+  float* pieces_a = reinterpret_cast<float*>(base + space.pieces_a);
   const int S = slices(true, n, f);
   hipStream_t st = as_stream(stream);
   const ShrinkArgs s = {rows, {dg, du}, {b_gate, b_up}, {0, r}, 0, f, r, 2 * r, S, scale, dv, lo, part, DropArgs{}};
   launch_shrink<false>(s, 2, st);
-  const ExpandArgs e = {rows, dv, lo, part, 2 * r, S, 2 * r, d, {a_gu, nullptr}, nullptr, {dxp, nullptr, nullptr, nullptr},
+  const WgradArgs wb = {rows, v, nullptr, {0, r}, {dg, du}, 0, 2 * r, r, f, scale, {d_b_gate, d_b_up}, pieces_b, DropArgs{}};
+  launch_wgrad<false, false>(wb, 2, st);
+  const ExpandArgs e = {rows, dv, lo, part, 2 * r, S, 2 * r, d, 1, {a_gu, nullptr}, nullptr, {dxp, nullptr, nullptr, nullptr},
                         {dxp_out, nullptr, nullptr}, S > 1 ? dv : nullptr, S > 1 ? lo : nullptr, drop};
   if (drop.drop) launch_expand<kAdd, true>(e, st);
   else launch_expand<kAdd, false>(e, st);
-  const WgradArgs wb = {rows, v, nullptr, {0, r}, {dg, du}, 0, 2 * r, r, f, scale, {d_b_gate, d_b_up}, part, DropArgs{}};
-  launch_wgrad<false, false>(wb, 2, st);
-  const WgradArgs wa = {rows, dv, lo, {0, 0}, {x, nullptr}, 1, 2 * r, 2 * r, d, nullptr, {d_a_gu, nullptr}, part, drop};
+  const WgradArgs wa = {rows, dv, lo, {0, 0}, {x, nullptr}, 1, 2 * r, 2 * r, d, nullptr, {d_a_gu, nullptr}, pieces_a, drop};
   if (drop.drop) launch_wgrad<true, true>(wa, 1, st);
   else launch_wgrad<false, true>(wa, 1, st);
+  const float* second = pieces_b + 2LL * (n / piece_rows(n) + 1) * r * f;
+  launch_join({rows, {pieces_b, second, pieces_a}, {d_b_gate, d_b_up, d_a_gu}, {r, r, 2 * r}, {f, f, d}}, 3, st);
   return check_launch("adapter_gate_up_bwd");
 }

@@ -33,14 +33,19 @@ __device__ __forceinline__ DropKey drop_key(const DropArgs& a) {
 // 2^16 / (2^16 - drop).
 __host__ __device__ __forceinline__ float drop_scale(uint32_t drop) { return 65536.0f / static_cast<float>(65536u - drop); }
 
+// a ^ b ^ c in one instruction.
+__device__ __forceinline__ uint32_t xor3(uint32_t a, uint32_t b, uint32_t c) {
+  return __builtin_amdgcn_bitop3_b32(a, b, c, 0x96);
+}
+
 // The 8 pieces of 16 bits of chunk `chunk` of row `row`: elements 2i and 2i + 1 are the low and high half of word i.
 __device__ __forceinline__ uint4 drop_bits(const DropKey& key, uint32_t row, uint32_t chunk) {
   uint32_t c0 = chunk | key.site, c1 = row, c2 = key.o0, c3 = key.o1, k0 = key.k0, k1 = key.k1;
 #pragma unroll
   for (int i = 0; i < 7; ++i) {
     const uint64_t m0 = static_cast<uint64_t>(c0) * 0xD2511F53u, m1 = static_cast<uint64_t>(c2) * 0xCD9E8D57u;
-    c0 = static_cast<uint32_t>(m1 >> 32) ^ c1 ^ k0;
-    c2 = static_cast<uint32_t>(m0 >> 32) ^ c3 ^ k1;
+    c0 = xor3(static_cast<uint32_t>(m1 >> 32), c1, k0);
+    c2 = xor3(static_cast<uint32_t>(m0 >> 32), c3, k1);
     c1 = static_cast<uint32_t>(m1);
     c3 = static_cast<uint32_t>(m0);
     k0 += 0x9E3779B9u;
@@ -61,14 +66,21 @@ __device__ __forceinline__ void drop_apply(const DropKey& key, uint32_t row, uin
 }
 
 // The chunk's 8 bf16 values with the dropped ones 0, the others as they are (the factor is left to the caller).
-__device__ __forceinline__ uint4 drop_zero(const DropKey& key, uint32_t row, uint32_t chunk, uint4 v) {
+typedef uint32_t drop_u32x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ drop_u32x4 drop_zero(const DropKey& key, uint32_t row, uint32_t chunk, drop_u32x4 v) {
+  // two 16-bit pieces at a time: min(max(u - (drop - 1), 0), 1) is 1 where u >= drop (drop > 0 here)
+  typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
   const uint4 b = drop_bits(key, row, chunk);
   const uint32_t w[4] = {b.x, b.y, b.z, b.w};
-  uint32_t o[4] = {v.x, v.y, v.z, v.w};
+  const unsigned short below = static_cast<unsigned short>(key.drop - 1);
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    o[i] &= ((w[i] & 0xffffu) >= key.drop ? 0xffffu : 0u) | ((w[i] >> 16) >= key.drop ? 0xffff0000u : 0u);
-  return make_uint4(o[0], o[1], o[2], o[3]);
+  for (int i = 0; i < 4; ++i) {
+    const u16x2 over = __builtin_elementwise_sub_sat(__builtin_bit_cast(u16x2, w[i]), u16x2{below, below});
+    const u16x2 keep = __builtin_elementwise_min(over, u16x2{1, 1});
+    const uint32_t x = v[i];
+    v[i] = __builtin_bit_cast(uint32_t, static_cast<u16x2>(__builtin_bit_cast(u16x2, x) * keep));
+  }
+  return v;
 }
 
 // Host: the arguments of a call, checked.  p is rounded to a multiple of 2^-16; p = 0 needs no rng.
