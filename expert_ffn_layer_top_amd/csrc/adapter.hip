@@ -334,13 +334,16 @@ __device__ __forceinline__ Tile tile_at(const Rows& rows, const PlanLayout& p, i
     return {__builtin_amdgcn_readfirstlane(t.x), __builtin_amdgcn_readfirstlane(t.y), __builtin_amdgcn_readfirstlane(t.z),
             __builtin_amdgcn_readfirstlane(t.w)};
   }
-  int e = 0;
-  for (int b = 0; b < rows.E; b += 64) {
-    const int at = b + (threadIdx.x & 63);
-    e += __popcll(__ballot(at < rows.E && rows.offsets[at + 1] <= i));
-  }
+  // (the row's token first: its adapter's number hangs on it)
+  const int l = adapter_of(rows.ids, rows.row_token, i, rows.T, rows.L);
+  const int lane = threadIdx.x & 63;
+  int end[4], e = 0;
+#pragma unroll
+  for (int b = 0; b < 4; ++b) end[b] = rows.offsets[min(64 * b + lane, rows.E - 1) + 1];
+#pragma unroll
+  for (int b = 0; b < 4; ++b) e += __popcll(__ballot(64 * b + lane < rows.E && end[b] <= i));
   if (e >= rows.E || i < rows.offsets[0]) return {i, 0, 0, rows.L};
-  return {i, 1, e, __builtin_amdgcn_readfirstlane(adapter_of(rows.ids, rows.row_token, i, rows.T, rows.L))};
+  return {i, 1, e, __builtin_amdgcn_readfirstlane(l)};
 }
 
 __device__ __forceinline__ int n_tiles(const Rows& rows) { return rows.plan != nullptr ? rows.plan[kHeadTiles] : rows.n; }
@@ -370,6 +373,7 @@ struct ShrinkArgs {
   int v0[2];               // their first columns in v
   int gather;              // x by token (through row_token)
   int K, R, ldv, S;        // S > 1: slices of K whose fp32 sums go to part [S][n][ldv]
+  int parts;               // a tile's rows are shared among this many workgroups (1, 2 or 4)
   const float* scale;      // null, or [L]: factor of v
   uint16_t* v;             // hi and lo [n][ldv]
   uint16_t* vlo;
@@ -503,13 +507,16 @@ template <int RT, bool DROP>
 __global__ __launch_bounds__(256, RT <= 2 ? 3 : RT == 4 ? 2 : 1) void adapter_shrink_kernel(ShrinkArgs a) {
   __shared__ u32x4 lds[4 * (4 + RT) * 128];   // 2 KiB for 16 rows or ranks; the sums take at most half of it
   const PlanLayout p = plan_layout(a.rows.n, a.rows.E, a.rows.L);
-  const long long items = static_cast<long long>(n_tiles(a.rows)) * a.S;
+  const int each = a.S * a.parts, rows_each = kTileRows / a.parts;
+  const long long items = static_cast<long long>(n_tiles(a.rows)) * each;
   const int which = blockIdx.y;
   const Run run = xcd_run(items);
   for (long long i = run.at; i < run.end; i += run.step) {
-    const Tile t = tile_at(a.rows, p, static_cast<int>(i / a.S));
-    const int slice = static_cast<int>(i % a.S);
-    if (t.count == 0) continue;
+    Tile t = tile_at(a.rows, p, static_cast<int>(i / each));
+    const int slice = static_cast<int>(i % a.S), first = static_cast<int>(i % each / a.S) * rows_each;
+    t.pos += first;
+    t.count = min(t.count - first, rows_each);
+    if (t.count <= 0) continue;
     if (t.l >= a.rows.L) {   // no adapter: v is 0 (with slices, expand writes that)
       if (a.S == 1)
         for (int at = threadIdx.x; at < t.count * a.R; at += 256) {
@@ -660,6 +667,22 @@ __global__ __launch_bounds__(256, KS == 1 || (KS == 2 && MODE != kSwiglu) ? 2 : 
       }
       continue;
     }
+    // the first 16 rows' loads before the matrices', on whose arrival everything else waits
+    constexpr int NI = MODE == kAdd ? 1 : MODE == kSwiglu ? 2 : 4;
+    int mine, row[4];
+    u32x4 in[4][NI];
+    auto load_rows = [&](int b) {
+      mine = row_at(a.rows, p, t.pos + min(16 * b + c, t.count - 1));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        row[j] = __shfl(mine, 4 * q + j, 64);
+        const long long at = static_cast<long long>(row[j]) * a.N + cc;
+#pragma unroll
+        for (int o = 0; o < NI; ++o) in[j][o] = load16(a.in[o] + at);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    load_rows(0);
     u32x4 wf[NW][KS][8];
     const long long g = (static_cast<long long>(t.l) * a.rows.E + t.e) * a.R * a.N;
 #pragma unroll
@@ -668,17 +691,7 @@ __global__ __launch_bounds__(256, KS == 1 || (KS == 2 && MODE != kSwiglu) ? 2 : 
     if (DROP) f *= drop_scale(a.drop.drop);
     const int nb = (t.count + 15) / 16;
     for (int b = 0; b < nb; ++b) {
-      const int mine = row_at(a.rows, p, t.pos + min(16 * b + c, t.count - 1));
-      int row[4];
-      u32x4 in[4][MODE == kAdd ? 1 : MODE == kSwiglu ? 2 : 4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        row[j] = __shfl(mine, 4 * q + j, 64);
-        const long long at = static_cast<long long>(row[j]) * a.N + cc;
-#pragma unroll
-        for (int o = 0; o < (MODE == kAdd ? 1 : MODE == kSwiglu ? 2 : 4); ++o)
-          in[j][o] = load16(a.in[o] + at);
-      }
+      if (b > 0) load_rows(b);
       f32x4 acc[NW][8];
 #pragma unroll
       for (int m = 0; m < NW; ++m) {
@@ -955,22 +968,32 @@ constexpr int kGridCap = 8192;   // workgroups of a launch; more tiles are taken
 
 int tiles_cap(const Rows& r) { return r.plan != nullptr ? plan_layout(r.n, r.E, r.L).tiles_cap : r.n; }
 
-// Slices of K: enough workgroups for the chip where there are few tiles, each with a unit for every wave.
-int slices(bool planned, int n, int K) {
-  const long long tiles = planned ? (n + kTileRows - 1) / kTileRows : n;
+// How the shrink's work is cut beyond tiles, to have workgroups enough for the chip: rows first (the matrices are read
+// again, from the second-level cache), then K into slices, each with a unit for every wave.
+struct Cut {
+  int parts, slices;
+};
+Cut shrink_cut(bool planned, int n, int K) {
+  long long tiles = planned ? (n + kTileRows - 1) / kTileRows : n;
+  Cut c = {1, 1};
+  if (planned) c.parts = tiles >= 1024 ? 1 : tiles >= 512 ? 2 : 4;
+  tiles *= c.parts;
   const int most = (K / 64 + 3) / 4;
   const long long want = 512 / tiles;
-  const int s = want < 1 ? 1 : want > 8 ? 8 : static_cast<int>(want);
-  return s < most ? s : most;
+  c.slices = want < 1 ? 1 : want > 8 ? 8 : static_cast<int>(want);
+  if (c.slices > most) c.slices = most;
+  return c;
 }
+int slices(bool planned, int n, int K) { return shrink_cut(planned, n, K).slices; }
 
 unsigned grid_of(long long workgroups) {
   return static_cast<unsigned>(workgroups < kGridCap ? (workgroups + 7) / 8 * 8 : kGridCap);
 }
 
 template <bool DROP>
-void launch_shrink(const ShrinkArgs& a, int products, hipStream_t st) {
-  const dim3 grid(grid_of(static_cast<long long>(tiles_cap(a.rows)) * a.S), products);
+void launch_shrink(ShrinkArgs a, int products, hipStream_t st) {
+  a.parts = shrink_cut(a.rows.plan != nullptr, a.rows.n, a.K).parts;
+  const dim3 grid(grid_of(static_cast<long long>(tiles_cap(a.rows)) * a.S * a.parts), products);
   if (a.R <= 16) adapter_shrink_kernel<1, DROP><<<grid, 256, 0, st>>>(a);
   else if (a.R <= 32) adapter_shrink_kernel<2, DROP><<<grid, 256, 0, st>>>(a);
   else if (a.R <= 64) adapter_shrink_kernel<4, DROP><<<grid, 256, 0, st>>>(a);
@@ -1128,7 +1151,7 @@ extern "C" int moe_adapter_gate_up(const uint16_t* x, const int32_t* ids, const 
   uint16_t* lo = reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + v_bytes(n, 2 * r));
   float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + 2 * v_bytes(n, 2 * r));
   const int S = slices(plan != nullptr, n, d);
-  ShrinkArgs s = {rows, {x, nullptr}, {a_gu, nullptr}, {0, 0}, 1, d, 2 * r, 2 * r, S, nullptr, vbuf, lo, part, drop};
+  ShrinkArgs s = {rows, {x, nullptr}, {a_gu, nullptr}, {0, 0}, 1, d, 2 * r, 2 * r, S, 1, nullptr, vbuf, lo, part, drop};
   hipStream_t st = as_stream(stream);
   if (drop.drop) launch_shrink<true>(s, 1, st);
   else launch_shrink<false>(s, 1, st);
@@ -1156,7 +1179,7 @@ extern "C" int moe_adapter_down(const uint16_t* a, const int32_t* ids, const int
   uint16_t* lo = reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + v_bytes(n, r));
   float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + 2 * v_bytes(n, r));
   const int S = slices(plan != nullptr, n, f);
-  ShrinkArgs s = {rows, {a, nullptr}, {a_down, nullptr}, {0, 0}, 0, f, r, r, S, nullptr, vbuf, lo, part, drop};
+  ShrinkArgs s = {rows, {a, nullptr}, {a_down, nullptr}, {0, 0}, 0, f, r, r, S, 1, nullptr, vbuf, lo, part, drop};
   hipStream_t st = as_stream(stream);
   if (drop.drop) launch_shrink<true>(s, 1, st);
   else launch_shrink<false>(s, 1, st);
@@ -1196,7 +1219,7 @@ extern "C" int moe_adapter_down_bwd(const uint16_t* dyexp, const uint16_t* a, co
   const int S = slices(true, n, d);
   hipStream_t st = as_stream(stream);
   // dyexp's second reader follows its first, so that what the last-level cache still holds of it is found there
-  const ShrinkArgs s = {rows, {dyexp, nullptr}, {b_down, nullptr}, {0, 0}, 0, d, r, r, S, scale, dv, lo, part, DropArgs{}};
+  const ShrinkArgs s = {rows, {dyexp, nullptr}, {b_down, nullptr}, {0, 0}, 0, d, r, r, S, 1, scale, dv, lo, part, DropArgs{}};
   launch_shrink<false>(s, 1, st);
   const WgradArgs wb = {rows, v, nullptr, {0, 0}, {dyexp, nullptr}, 0, r, r, d, scale, {d_b_down, nullptr}, pieces_b, DropArgs{}};
   launch_wgrad<false, false>(wb, 1, st);
@@ -1240,7 +1263,7 @@ extern "C" int moe_adapter_gate_up_bwd(const uint16_t* dg, const uint16_t* du, c
   float* pieces_a = reinterpret_cast<float*>(base + space.pieces_a);
   const int S = slices(true, n, f);
   hipStream_t st = as_stream(stream);
-  const ShrinkArgs s = {rows, {dg, du}, {b_gate, b_up}, {0, r}, 0, f, r, 2 * r, S, scale, dv, lo, part, DropArgs{}};
+  const ShrinkArgs s = {rows, {dg, du}, {b_gate, b_up}, {0, r}, 0, f, r, 2 * r, S, 1, scale, dv, lo, part, DropArgs{}};
   launch_shrink<false>(s, 2, st);
   const WgradArgs wb = {rows, v, nullptr, {0, r}, {dg, du}, 0, 2 * r, r, f, scale, {d_b_gate, d_b_up}, pieces_b, DropArgs{}};
   launch_wgrad<false, false>(wb, 2, st);

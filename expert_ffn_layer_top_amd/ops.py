@@ -493,10 +493,11 @@ class AdapterPlan:
     """Which adapter each routed row has (adapter_plan), as the adapter calls take it.  It holds for as long as its tensors
     keep their contents."""
 
-    __slots__ = ("ids", "offsets", "row_token", "buf", "T", "n", "E", "L", "dev")
+    __slots__ = ("ids", "offsets", "row_token", "buf", "T", "n", "E", "L", "dev", "_rows")
 
     def _args(self):
-        return (_ptr(self.ids), _ptr(self.row_token), _ptr(self.offsets), _ptr(self.buf), self.T, self.n, self.E, self.L)
+        """What every call passes of it (pointers and sizes)."""
+        return self._rows
 
 
 def adapter_plan(ids, offsets, n_adapters, row_token=None, backward=False):
@@ -515,11 +516,12 @@ def adapter_plan(ids, offsets, n_adapters, row_token=None, backward=False):
     plan.ids, plan.offsets, plan.row_token = ids, offsets, row_token
     plan.T, plan.n, plan.E, plan.L = T, n, E, int(n_adapters)
     plan.buf = None
+    p_ids, p_token, p_off = ids.data_ptr(), _ptr(row_token), offsets.data_ptr()
     if backward or n > ADAPTER_FEW_ROWS:
         nbytes = lib.moe_adapter_plan_bytes(n, E, plan.L)
         plan.buf = _new((nbytes,), torch.uint8, dev)
-        _call_on(dev, "moe_adapter_plan", _ptr(ids), _ptr(row_token), _ptr(offsets), T, n, E, plan.L, _ptr(plan.buf),
-                 nbytes)
+        _call_on(dev, "moe_adapter_plan", p_ids, p_token, p_off, T, n, E, plan.L, plan.buf.data_ptr(), nbytes)
+    plan._rows = (p_ids, p_token, p_off, _ptr(plan.buf), T, n, E, plan.L)
     return plan
 
 

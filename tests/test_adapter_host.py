@@ -74,6 +74,7 @@ def plan(backward=True):
     p.ids, p.offsets, p.row_token = z(T, dt=i32), z(E + 1, dt=i32), z(n, dt=i32)
     p.buf = z(64, dt=torch.uint8) if backward else None
     p.T, p.n, p.E, p.L, p.dev = T, n, E, L, -1
+    p._rows = (0, 0, 0, 0, T, n, E, L)
     return p
 
 
