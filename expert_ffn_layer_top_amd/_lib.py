@@ -77,7 +77,7 @@ SIGNATURES = {
     "moe_unpermute_combine_dropout_bwd": (_i, [_p, _p, _p, _p, _p, _f, _i, _i, _i, _i, _p, _p, _p]),
     "moe_adapter_plan_bytes": (_sz, [_i, _i, _i]),
     "moe_adapter_plan": (_i, [_p] * 3 + [_i] * 4 + [_p, _sz, _p]),
-    "moe_adapter_workspace_bytes": (_sz, [_i] * 6),
+    "moe_adapter_workspace_bytes": (_sz, [_i] * 8),
     "moe_adapter_gate_up": (_i, [_p] * 5 + [_i] * 7 + [_p] * 5 + [_f, _i] + [_p] * 8 + [_sz, _p]),
     "moe_adapter_down": (_i, [_p] * 5 + [_i] * 7 + [_p] * 4 + [_f, _i] + [_p] * 4 + [_sz, _p]),
     "moe_adapter_down_bwd": (_i, [_p] * 7 + [_i] * 7 + [_p] * 4 + [_f, _i] + [_p] * 9 + [_sz, _p]),

@@ -22,7 +22,7 @@
 //
 // Rows are taken in tiles of up to 64 rows of one expert and adapter, from a list that adapter_plan makes on the
 // device by a stable sort of each expert's rows by adapter, so sums run in a fixed order.  For few rows there is no
-// list: every row is a tile.
+// list, and one kernel does both products of a row.
 #include <hip/hip_runtime.h>
 
 #include "common.h"
@@ -319,39 +319,24 @@ __global__ __launch_bounds__(256) void plan_place_kernel(const int32_t* __restri
 // ---------------------------------------------------------------- the rows of a call
 
 struct Rows {
-  const int32_t* plan;        // null: every row is a tile
+  const int32_t* plan;        // null in the kernel of few rows only
   const int32_t* ids;
   const int32_t* row_token;   // null: row r is token r
   const int32_t* offsets;
   int T, n, E, L;
 };
 
-// Tile `i`'s place; count 0: there is none (past the list, or a row behind the last expert's).
-// Called with i uniform in the wave, all lanes.
+// Tile `i`, the same in all lanes.
 __device__ __forceinline__ Tile tile_at(const Rows& rows, const PlanLayout& p, int i) {
-  if (rows.plan != nullptr) {
-    const int4 t = reinterpret_cast<const int4*>(rows.plan + p.tiles)[i];
-    return {__builtin_amdgcn_readfirstlane(t.x), __builtin_amdgcn_readfirstlane(t.y), __builtin_amdgcn_readfirstlane(t.z),
-            __builtin_amdgcn_readfirstlane(t.w)};
-  }
-  // (the row's token first: its adapter's number hangs on it)
-  const int l = adapter_of(rows.ids, rows.row_token, i, rows.T, rows.L);
-  const int lane = threadIdx.x & 63;
-  int end[4], e = 0;
-#pragma unroll
-  for (int b = 0; b < 4; ++b) end[b] = rows.offsets[min(64 * b + lane, rows.E - 1) + 1];
-#pragma unroll
-  for (int b = 0; b < 4; ++b) e += __popcll(__ballot(64 * b + lane < rows.E && end[b] <= i));
-  if (e >= rows.E || i < rows.offsets[0]) return {i, 0, 0, rows.L};
-  return {i, 1, e, __builtin_amdgcn_readfirstlane(l)};
+  const int4 t = reinterpret_cast<const int4*>(rows.plan + p.tiles)[i];
+  return {__builtin_amdgcn_readfirstlane(t.x), __builtin_amdgcn_readfirstlane(t.y), __builtin_amdgcn_readfirstlane(t.z),
+          __builtin_amdgcn_readfirstlane(t.w)};
 }
 
-__device__ __forceinline__ int n_tiles(const Rows& rows) { return rows.plan != nullptr ? rows.plan[kHeadTiles] : rows.n; }
+__device__ __forceinline__ int n_tiles(const Rows& rows) { return rows.plan[kHeadTiles]; }
 
 // Row at sorted position pos (clamped by the caller to the tile).
-__device__ __forceinline__ int row_at(const Rows& rows, const PlanLayout& p, int pos) {
-  return rows.plan != nullptr ? rows.plan[p.rows + pos] : pos;
-}
+__device__ __forceinline__ int row_at(const Rows& rows, const PlanLayout& p, int pos) { return rows.plan[p.rows + pos]; }
 
 // A workgroup's items: those of XCD x (workgroups x mod 8) are one contiguous run of the order, so that the tiles of one
 // expert and adapter, which read the same matrix, and the columns of one tile, which read the same rows of v, share an
@@ -409,7 +394,7 @@ __device__ __forceinline__ void shrink_tile(const ShrinkArgs& a, const Tile& t, 
   for (int i = 0; i < 2 * NB; ++i) {
     const int pos = t.pos + min(8 * i + lr, t.count - 1), r = row_at(a.rows, p, pos);
     int src = r;
-    if (a.gather) src = a.rows.plan != nullptr ? a.rows.plan[p.toks + pos] : token_of(a.rows.row_token, r, a.rows.T);
+    if (a.gather) src = a.rows.plan[p.toks + pos];
     row[i] = static_cast<uint32_t>(r);
     xp[i] = x + static_cast<long long>(src) * a.K + 8 * lc;
   }
@@ -765,6 +750,166 @@ __global__ __launch_bounds__(256, KS == 1 || (KS == 2 && MODE != kSwiglu) ? 2 : 
   }
 }
 
+// ---------------------------------------------------------------- few rows
+
+// Both products of one row in a workgroup, without a plan: what few rows cost is the chain of loads that hang on each
+// other (token, adapter, matrices) and the launches, not bytes.  A wave takes RW ranks of A along whole cache lines, v meets in
+// LDS as fp32, and then a lane takes 8 columns of B for all ranks; the first 8 ranks of B, and the row's own values,
+// are on their way while A is read.  Products and sums are fp32 FMAs.
+struct RowArgs {
+  Rows rows;
+  const uint16_t* x;
+  int gather, K, R;         // R: rows of A
+  const uint16_t* a;
+  int N, r;                 // r: ranks of one product
+  const uint16_t* b[2];     // kSwiglu: gate and up
+  const float* scale;
+  const uint16_t* in[3];    // kAdd: y; kSwiglu: g, u, a
+  uint16_t* out[3];
+  uint16_t* v_out;          // [n][R] or null
+  DropArgs drop;
+};
+
+constexpr int kRowThreads = 512;
+
+template <int RW, int MODE, bool DROP>
+__global__ __launch_bounds__(kRowThreads) void adapter_row_kernel(RowArgs a) {
+  constexpr int NW = MODE == kSwiglu ? 2 : 1, NOUT = MODE == kSwiglu ? 3 : 1;
+  __shared__ float v[2 * kMaxRank];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), i = blockIdx.x;
+  // the row's token first: its adapter's number hangs on it
+  const int l = __builtin_amdgcn_readfirstlane(adapter_of(a.rows.ids, a.rows.row_token, i, a.rows.T, a.rows.L));
+  int end[4], e = 0;
+#pragma unroll
+  for (int b = 0; b < 4; ++b) end[b] = a.rows.offsets[min(64 * b + lane, a.rows.E - 1) + 1];
+#pragma unroll
+  for (int b = 0; b < 4; ++b) e += __popcll(__ballot(64 * b + lane < a.rows.E && end[b] <= i));
+  if (e >= a.rows.E || i < a.rows.offsets[0]) return;      // behind the last expert's rows
+  const long long row = static_cast<long long>(i) * a.N;
+  const int chunks = a.N / 8;
+  if (l >= a.rows.L) {                                     // no adapter: copies
+    for (int c = tid; c < chunks; c += kRowThreads)
+#pragma unroll
+      for (int o = 0; o < NOUT; ++o)
+        if (a.out[o] != nullptr) store16(a.out[o] + row + 8 * c, load16(a.in[o] + row + 8 * c));
+    if (a.v_out != nullptr && tid < a.R) a.v_out[static_cast<long long>(i) * a.R + tid] = 0;
+    return;
+  }
+  const long long g = static_cast<long long>(l) * a.rows.E + e;
+  const int mine = min(tid, chunks - 1);
+  u32x4 in[NW], bf[NW][8];
+#pragma unroll
+  for (int m = 0; m < NW; ++m) {
+    in[m] = load16(a.in[m] + row + 8 * mine);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) bf[m][k] = load16(a.b[m] + (g * a.r + k) * a.N + 8 * mine);
+  }
+  __builtin_amdgcn_sched_barrier(0);
+  {
+    const int src = a.gather ? token_of(a.rows.row_token, i, a.rows.T) : i;
+    const uint16_t* x = a.x + static_cast<long long>(src) * a.K;
+    const uint16_t* w[RW];
+    float sum[RW];
+#pragma unroll
+    for (int k = 0; k < RW; ++k) {
+      w[k] = a.a + (g * a.R + min(wave * RW + k, a.R - 1)) * a.K;
+      sum[k] = 0.f;
+    }
+    DropKey key;
+    if (DROP) key = drop_key(a.drop);
+    constexpr int U = RW <= 2 ? 4 : RW <= 4 ? 2 : 1;       // chunks of the row at a time
+    for (int c0 = lane; c0 < a.K / 8; c0 += 64 * U) {
+      u32x4 xf[U], wf[U][RW];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int c = min(c0 + 64 * u, a.K / 8 - 1);
+        xf[u] = load16(x + 8 * c);
+#pragma unroll
+        for (int k = 0; k < RW; ++k) wf[u][k] = load16(w[k] + 8 * c);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (c0 + 64 * u >= a.K / 8) break;
+        if (DROP) xf[u] = drop_zero(key, i, c0 + 64 * u, xf[u]);
+        float xs[8];
+        unpack8(xf[u], xs);
+#pragma unroll
+        for (int k = 0; k < RW; ++k) {
+          float ws[8];
+          unpack8(wf[u][k], ws);
+#pragma unroll
+          for (int o = 0; o < 8; ++o) sum[k] = fmaf(xs[o], ws[o], sum[k]);
+        }
+      }
+    }
+    const float f = DROP ? drop_scale(a.drop.drop) : 1.f;
+#pragma unroll
+    for (int k = 0; k < RW; ++k) {
+      const float t = wave_sum(sum[k]);
+      if (lane == 0 && wave * RW + k < a.R) v[wave * RW + k] = f * t;
+    }
+  }
+  __syncthreads();
+  if (a.v_out != nullptr && tid < a.R) a.v_out[static_cast<long long>(i) * a.R + tid] = f32_to_bf16(v[tid]);
+  const float s = a.scale[l];
+  for (int c = tid; c < chunks; c += kRowThreads) {
+    if (c != tid) {
+#pragma unroll
+      for (int m = 0; m < NW; ++m) {
+        in[m] = load16(a.in[m] + row + 8 * c);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) bf[m][k] = load16(a.b[m] + (g * a.r + k) * a.N + 8 * c);
+      }
+    }
+    float acc[NW][8];
+#pragma unroll
+    for (int m = 0; m < NW; ++m)
+#pragma unroll
+      for (int o = 0; o < 8; ++o) acc[m][o] = 0.f;
+    for (int k0 = 0; k0 < a.r; k0 += 8) {
+      u32x4 cur[NW][8];
+#pragma unroll
+      for (int m = 0; m < NW; ++m)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          cur[m][k] = bf[m][k];
+          if (k0 + 8 < a.r) bf[m][k] = load16(a.b[m] + (g * a.r + k0 + 8 + k) * a.N + 8 * c);
+        }
+#pragma unroll
+      for (int m = 0; m < NW; ++m)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          float ws[8];
+          unpack8(cur[m][k], ws);
+          const float vk = v[m * a.r + k0 + k];
+#pragma unroll
+          for (int o = 0; o < 8; ++o) acc[m][o] = fmaf(vk, ws[o], acc[m][o]);
+        }
+    }
+    float x0[8];
+    unpack8(in[0], x0);
+    if constexpr (MODE == kAdd) {
+#pragma unroll
+      for (int o = 0; o < 8; ++o) x0[o] = fmaf(s, acc[0][o], x0[o]);
+      store16(a.out[0] + row + 8 * c, pack8(x0));
+    } else {
+      float x1[8], y[8];
+      unpack8(in[NW - 1], x1);
+#pragma unroll
+      for (int o = 0; o < 8; ++o) {
+        x0[o] = fmaf(s, acc[0][o], x0[o]);
+        x1[o] = fmaf(s, acc[NW - 1][o], x1[o]);
+        y[o] = x0[o] * logistic(x0[o]) * x1[o];
+      }
+      if (a.out[0] != nullptr) {
+        store16(a.out[0] + row + 8 * c, pack8(x0));
+        store16(a.out[1] + row + 8 * c, pack8(x1));
+      }
+      store16(a.out[2] + row + 8 * c, pack8(y));
+    }
+  }
+}
+
 // ---------------------------------------------------------------- wgrad
 
 struct WgradArgs {
@@ -966,25 +1111,36 @@ __global__ __launch_bounds__(256) void adapter_join_kernel(JoinArgs a) {
 
 constexpr int kGridCap = 8192;   // workgroups of a launch; more tiles are taken in turn
 
-int tiles_cap(const Rows& r) { return r.plan != nullptr ? plan_layout(r.n, r.E, r.L).tiles_cap : r.n; }
+int tiles_cap(const Rows& r) { return plan_layout(r.n, r.E, r.L).tiles_cap; }
+
+// Tiles that a call is likely to have (their number is on the device): those of whole tiles, and one more for half of the
+// experts' adapters that can have rows.
+long long likely_tiles(int n, int E, int L) {
+  const long long groups = static_cast<long long>(E) * L;
+  return n / kTileRows + ((groups < n ? groups : n) + 1) / 2;
+}
+
+// Pieces of 16 rows or more that a tile is cut into, to have `want` of them where there are few tiles.
+int row_parts(int n, long long tiles, long long want) {
+  const long long rows = n / tiles;
+  return tiles >= want || rows < 32 ? 1 : 2 * tiles >= want || rows < 64 ? 2 : 4;
+}
 
 // How the shrink's work is cut beyond tiles, to have workgroups enough for the chip: rows first (the matrices are read
 // again, from the second-level cache), then K into slices, each with a unit for every wave.
 struct Cut {
   int parts, slices;
 };
-Cut shrink_cut(bool planned, int n, int K) {
-  long long tiles = planned ? (n + kTileRows - 1) / kTileRows : n;
-  Cut c = {1, 1};
-  if (planned) c.parts = tiles >= 1024 ? 1 : tiles >= 512 ? 2 : 4;
-  tiles *= c.parts;
+Cut shrink_cut(int n, int E, int L, int K) {
+  const long long tiles = likely_tiles(n, E, L);
+  Cut c = {row_parts(n, tiles, 1024), 1};
   const int most = (K / 64 + 3) / 4;
-  const long long want = 512 / tiles;
+  const long long want = 512 / (tiles * c.parts);
   c.slices = want < 1 ? 1 : want > 8 ? 8 : static_cast<int>(want);
   if (c.slices > most) c.slices = most;
   return c;
 }
-int slices(bool planned, int n, int K) { return shrink_cut(planned, n, K).slices; }
+int slices(int n, int E, int L, int K) { return shrink_cut(n, E, L, K).slices; }
 
 unsigned grid_of(long long workgroups) {
   return static_cast<unsigned>(workgroups < kGridCap ? (workgroups + 7) / 8 * 8 : kGridCap);
@@ -992,7 +1148,7 @@ unsigned grid_of(long long workgroups) {
 
 template <bool DROP>
 void launch_shrink(ShrinkArgs a, int products, hipStream_t st) {
-  a.parts = shrink_cut(a.rows.plan != nullptr, a.rows.n, a.K).parts;
+  a.parts = shrink_cut(a.rows.n, a.rows.E, a.rows.L, a.K).parts;
   const dim3 grid(grid_of(static_cast<long long>(tiles_cap(a.rows)) * a.S * a.parts), products);
   if (a.R <= 16) adapter_shrink_kernel<1, DROP><<<grid, 256, 0, st>>>(a);
   else if (a.R <= 32) adapter_shrink_kernel<2, DROP><<<grid, 256, 0, st>>>(a);
@@ -1004,12 +1160,21 @@ template <int MODE, bool DROP>
 void launch_expand(ExpandArgs a, hipStream_t st) {
   const long long stripes = (a.N + 127) / 128, waves = tiles_cap(a.rows) * stripes;
   // A wave walks its rows 16 at a time, each time waiting for memory: where a launch has few waves they take fewer rows.
-  const long long tiles = a.rows.plan != nullptr ? (a.rows.n + kTileRows - 1) / kTileRows : a.rows.n;
-  a.parts = a.rows.plan == nullptr || tiles * stripes >= 4096 ? 1 : tiles * stripes >= 2048 ? 2 : 4;
+  a.parts = row_parts(a.rows.n, likely_tiles(a.rows.n, a.rows.E, a.rows.L), (4096 + stripes - 1) / stripes);
   const unsigned grid = grid_of((waves * a.parts + 3) / 4);
   if (a.R <= 32) adapter_expand_kernel<1, MODE, DROP><<<grid, 256, 0, st>>>(a);
   else if (a.R <= 64) adapter_expand_kernel<2, MODE, DROP><<<grid, 256, 0, st>>>(a);
   else if constexpr (MODE == kAdd) adapter_expand_kernel<4, MODE, DROP><<<grid, 256, 0, st>>>(a);
+}
+
+template <int MODE, bool DROP>
+void launch_rows(const RowArgs& a, hipStream_t st) {
+  constexpr int W = kRowThreads / 64;
+  if (a.R <= W) adapter_row_kernel<1, MODE, DROP><<<a.rows.n, kRowThreads, 0, st>>>(a);
+  else if (a.R <= 2 * W) adapter_row_kernel<2, MODE, DROP><<<a.rows.n, kRowThreads, 0, st>>>(a);
+  else if (a.R <= 4 * W) adapter_row_kernel<4, MODE, DROP><<<a.rows.n, kRowThreads, 0, st>>>(a);
+  else if (a.R <= 8 * W) adapter_row_kernel<8, MODE, DROP><<<a.rows.n, kRowThreads, 0, st>>>(a);
+  else if constexpr (MODE == kSwiglu) adapter_row_kernel<16, MODE, DROP><<<a.rows.n, kRowThreads, 0, st>>>(a);
 }
 
 template <bool DROP, bool LO>
@@ -1060,8 +1225,8 @@ long long align256(long long b) { return (b + 255) / 256 * 256; }
 
 // Bytes of v's hi or lo, of its slices and of the weight gradients' pieces for a product pair of widths K -> R.
 long long v_bytes(int n, int R) { return align256(2LL * n * R); }
-long long part_bytes(bool planned, int n, int R, int K) {
-  const int s = slices(planned, n, K);
+long long part_bytes(int n, int E, int L, int R, int K) {
+  const int s = slices(n, E, L, K);
   return s > 1 ? align256(4LL * s * n * R) : 0;
 }
 long long piece_bytes(int n, int products, int R, int C) {
@@ -1069,25 +1234,27 @@ long long piece_bytes(int n, int products, int R, int C) {
   return n > piece ? align256(4LL * products * 2 * (n / piece + 1) * R * C) : 0;
 }
 
-long long forward_bytes(bool planned, int n, int R, int K) { return 2 * v_bytes(n, R) + part_bytes(planned, n, R, K); }
+long long forward_bytes(int n, int E, int L, int R, int K) {
+  return 2 * v_bytes(n, R) + part_bytes(n, E, L, R, K);
+}
 
 // The workspace of a backward call: v's hi and lo [n][R], its slices, the pieces of the B's gradients (1 or 2 products
 // of C1 columns and r ranks) and of A's (R ranks, C2 columns).
 struct BwdSpace {
   long long hi, lo, part, pieces_b, pieces_a, bytes;
 };
-BwdSpace bwd_space(int n, int r, int products, int C1, int R, int C2) {
+BwdSpace bwd_space(int n, int E, int L, int r, int products, int C1, int R, int C2) {
   BwdSpace w;
   w.hi = 0;
   w.lo = v_bytes(n, R);
   w.part = 2 * v_bytes(n, R);
-  w.pieces_b = w.part + part_bytes(true, n, R, C1);
+  w.pieces_b = w.part + part_bytes(n, E, L, R, C1);
   w.pieces_a = w.pieces_b + piece_bytes(n, products, r, C1);
   w.bytes = w.pieces_a + piece_bytes(n, 1, R, C2);
   return w;
 }
-BwdSpace down_bwd_space(int n, int d, int f, int r) { return bwd_space(n, r, 1, d, r, f); }
-BwdSpace gate_up_bwd_space(int n, int d, int f, int r) { return bwd_space(n, r, 2, f, 2 * r, d); }
+BwdSpace down_bwd_space(int n, int E, int L, int d, int f, int r) { return bwd_space(n, E, L, r, 1, d, r, f); }
+BwdSpace gate_up_bwd_space(int n, int E, int L, int d, int f, int r) { return bwd_space(n, E, L, r, 2, f, 2 * r, d); }
 
 #define MOE_CHECK_WS(need)                                                                                     \
   do {                                                                                                         \
@@ -1122,11 +1289,11 @@ extern "C" int moe_adapter_plan(const int32_t* ids, const int32_t* row_token, co
   return check_launch("adapter_plan");
 }
 
-extern "C" size_t moe_adapter_workspace_bytes(int n, int d, int f, int r, int planned, int backward) {
-  if (check_sizes(1, n, 1, 1) || check_dims(d, f, r)) return 0;
-  const bool p = planned != 0;
-  if (backward) return static_cast<size_t>(max(down_bwd_space(n, d, f, r).bytes, gate_up_bwd_space(n, d, f, r).bytes));
-  return static_cast<size_t>(max(forward_bytes(p, n, 2 * r, d), forward_bytes(p, n, r, f)));
+extern "C" size_t moe_adapter_workspace_bytes(int n, int E, int L, int d, int f, int r, int planned, int backward) {
+  if (check_sizes(1, n, E, L) || check_dims(d, f, r)) return 0;
+  if (backward) return static_cast<size_t>(max(down_bwd_space(n, E, L, d, f, r).bytes, gate_up_bwd_space(n, E, L, d, f, r).bytes));
+  if (!planned) return 0;      // one kernel, which keeps v to itself
+  return static_cast<size_t>(max(forward_bytes(n, E, L, 2 * r, d), forward_bytes(n, E, L, r, f)));
 }
 
 extern "C" int moe_adapter_gate_up(const uint16_t* x, const int32_t* ids, const int32_t* row_token, const int32_t* offsets,
@@ -1146,13 +1313,19 @@ extern "C" int moe_adapter_gate_up(const uint16_t* x, const int32_t* ids, const 
   MOE_REQUIRE((g_out == nullptr) == (u_out == nullptr), MOE_ERR_INVALID_ARG, "g_out and u_out are wanted both or neither");
   DropArgs drop;
   if (int st = make_drop(rng, p, site, &drop)) return st;
-  MOE_CHECK_WS(forward_bytes(plan != nullptr, n, 2 * r, d));
+  hipStream_t st = as_stream(stream);
+  if (plan == nullptr) {
+    const RowArgs k = {rows, x, 1, d, 2 * r, a_gu, f, r, {b_gate, b_up}, scale, {g, u, a}, {g_out, u_out, a_out}, v, drop};
+    if (drop.drop) launch_rows<kSwiglu, true>(k, st);
+    else launch_rows<kSwiglu, false>(k, st);
+    return check_launch("adapter_gate_up");
+  }
+  MOE_CHECK_WS(forward_bytes(n, E, L, 2 * r, d));
   uint16_t* vbuf = v != nullptr ? v : static_cast<uint16_t*>(ws);
   uint16_t* lo = reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + v_bytes(n, 2 * r));
   float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + 2 * v_bytes(n, 2 * r));
-  const int S = slices(plan != nullptr, n, d);
+  const int S = slices(n, E, L, d);
   ShrinkArgs s = {rows, {x, nullptr}, {a_gu, nullptr}, {0, 0}, 1, d, 2 * r, 2 * r, S, 1, nullptr, vbuf, lo, part, drop};
-  hipStream_t st = as_stream(stream);
   if (drop.drop) launch_shrink<true>(s, 1, st);
   else launch_shrink<false>(s, 1, st);
   ExpandArgs e = {rows, vbuf, lo, part, 2 * r, S, r, f, 1, {b_gate, b_up}, scale, {g, u, a, nullptr}, {g_out, u_out, a_out},
@@ -1174,13 +1347,20 @@ extern "C" int moe_adapter_down(const uint16_t* a, const int32_t* ids, const int
   MOE_CHECK_ALIGN(y_out);
   DropArgs drop;
   if (int st = make_drop(rng, p, site, &drop)) return st;
-  MOE_CHECK_WS(forward_bytes(plan != nullptr, n, r, f));
+  hipStream_t st = as_stream(stream);
+  if (plan == nullptr) {
+    const RowArgs k = {rows, a, 0, f, r, a_down, d, r, {b_down, nullptr}, scale, {yexp, nullptr, nullptr},
+                       {y_out, nullptr, nullptr}, v, drop};
+    if (drop.drop) launch_rows<kAdd, true>(k, st);
+    else launch_rows<kAdd, false>(k, st);
+    return check_launch("adapter_down");
+  }
+  MOE_CHECK_WS(forward_bytes(n, E, L, r, f));
   uint16_t* vbuf = v != nullptr ? v : static_cast<uint16_t*>(ws);
   uint16_t* lo = reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + v_bytes(n, r));
   float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + 2 * v_bytes(n, r));
-  const int S = slices(plan != nullptr, n, f);
+  const int S = slices(n, E, L, f);
   ShrinkArgs s = {rows, {a, nullptr}, {a_down, nullptr}, {0, 0}, 0, f, r, r, S, 1, nullptr, vbuf, lo, part, drop};
-  hipStream_t st = as_stream(stream);
   if (drop.drop) launch_shrink<true>(s, 1, st);
   else launch_shrink<false>(s, 1, st);
   ExpandArgs e = {rows, vbuf, lo, part, r, S, r, d, 1, {b_down, nullptr}, scale, {yexp, nullptr, nullptr, nullptr},
@@ -1208,7 +1388,7 @@ extern "C" int moe_adapter_down_bwd(const uint16_t* dyexp, const uint16_t* a, co
   MOE_CHECK_ALIGN(du_out); MOE_CHECK_ALIGN(d_a_down); MOE_CHECK_ALIGN(d_b_down);
   DropArgs drop;
   if (int st = make_drop(rng, p, site, &drop)) return st;
-  const BwdSpace space = down_bwd_space(n, d, f, r);
+  const BwdSpace space = down_bwd_space(n, E, L, d, f, r);
   MOE_CHECK_WS(space.bytes);
   char* base = static_cast<char*>(ws);
   uint16_t* dv = reinterpret_cast<uint16_t*>(base + space.hi);
@@ -1216,7 +1396,7 @@ extern "C" int moe_adapter_down_bwd(const uint16_t* dyexp, const uint16_t* a, co
   float* part = reinterpret_cast<float*>(base + space.part);
   float* pieces_b = reinterpret_cast<float*>(base + space.pieces_b);
   float* pieces_a = reinterpret_cast<float*>(base + space.pieces_a);
-  const int S = slices(true, n, d);
+  const int S = slices(n, E, L, d);
   hipStream_t st = as_stream(stream);
   // dyexp's second reader follows its first, so that what the last-level cache still holds of it is found there
   const ShrinkArgs s = {rows, {dyexp, nullptr}, {b_down, nullptr}, {0, 0}, 0, d, r, r, S, 1, scale, dv, lo, part, DropArgs{}};
@@ -1253,7 +1433,7 @@ extern "C" int moe_adapter_gate_up_bwd(const uint16_t* dg, const uint16_t* du, c
   MOE_CHECK_ALIGN(d_a_gu); MOE_CHECK_ALIGN(d_b_gate); MOE_CHECK_ALIGN(d_b_up);
   DropArgs drop;
   if (int st = make_drop(rng, p, site, &drop)) return st;
-  const BwdSpace space = gate_up_bwd_space(n, d, f, r);
+  const BwdSpace space = gate_up_bwd_space(n, E, L, d, f, r);
   MOE_CHECK_WS(space.bytes);
   char* base = static_cast<char*>(ws);
   uint16_t* dv = reinterpret_cast<uint16_t*>(base + space.hi);
@@ -1261,7 +1441,7 @@ extern "C" int moe_adapter_gate_up_bwd(const uint16_t* dg, const uint16_t* du, c
   float* part = reinterpret_cast<float*>(base + space.part);
   float* pieces_b = reinterpret_cast<float*>(base + space.pieces_b);
   float* pieces_a = reinterpret_cast<float*>(base + space.pieces_a);
-  const int S = slices(true, n, f);
+  const int S = slices(n, E, L, f);
   hipStream_t st = as_stream(stream);
   const ShrinkArgs s = {rows, {dg, du}, {b_gate, b_up}, {0, r}, 0, f, r, 2 * r, S, 1, scale, dv, lo, part, DropArgs{}};
   launch_shrink<false>(s, 2, st);

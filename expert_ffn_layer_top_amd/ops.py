@@ -486,7 +486,7 @@ def unpermute_combine_dropout_bwd(dy, yexp, topk_gate, dest, drop):
 # ---------------------------------------------------------------- low-rank adapters
 
 # Up to this many rows every row reads its adapter by itself in the forward; more are sorted by adapter first.
-ADAPTER_FEW_ROWS = 1024
+ADAPTER_FEW_ROWS = 512
 
 
 class AdapterPlan:
@@ -561,7 +561,9 @@ def _adapter_d(plan, a_down, b_down, scale):
 
 
 def _adapter_ws(plan, d, f, r, backward):
-    nbytes = lib.moe_adapter_workspace_bytes(plan.n, d, f, r, plan.buf is not None, backward)
+    if plan.buf is None:
+        return None, 0
+    nbytes = lib.moe_adapter_workspace_bytes(plan.n, plan.E, plan.L, d, f, r, plan.buf is not None, backward)
     return _new((nbytes,), torch.uint8, plan.dev), nbytes
 
 

@@ -340,9 +340,9 @@ size_t moe_adapter_plan_bytes(int n, int E, int L);
 int moe_adapter_plan(const int32_t* ids, const int32_t* row_token_or_null, const int32_t* offsets, int T, int n,
                      int E, int L, void* plan, size_t plan_bytes, void* stream);
 
-/* Workspace of the four calls below: of the forward ones (planned: whether they are given a plan), or with
- * `backward` of the backward ones. */
-size_t moe_adapter_workspace_bytes(int n, int d, int f, int r, int planned, int backward);
+/* Workspace of the four calls below: of the forward ones (planned: whether they are given a plan; without one none is
+ * needed), or with `backward` of the backward ones. */
+size_t moe_adapter_workspace_bytes(int n, int E, int L, int d, int f, int r, int planned, int backward);
 
 /* x [T,d] by token; g, u, a [n,f] as moe_grouped_gemm_gate_up wrote them (a is read for rows without an adapter
  * only).  v_or_null [n,2r] is kept for the backward (0 for rows without an adapter); g_out and u_out may both be NULL (serving).

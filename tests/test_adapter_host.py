@@ -170,8 +170,8 @@ def test_c_entry_points():
     assert planned(fake, fake, fake, 8, 16, 4, 3, odd, need) == INVALID
     assert planned(fake, fake, fake, 8, 16, 300, 3, fake, need) == UNSUPPORTED
     for bad in ((16, 96, 64, 8), (16, 64, 64, 12), (16, 64, 64, 72), (0, 64, 64, 8)):
-        assert lib.moe_adapter_workspace_bytes(*bad, 1, 0) == 0
-    ws = lib.moe_adapter_workspace_bytes(16, 192, 128, 16, 1, 0)
+        assert lib.moe_adapter_workspace_bytes(bad[0], 4, 3, *bad[1:], 1, 0) == 0
+    ws = lib.moe_adapter_workspace_bytes(16, 4, 3, 192, 128, 16, 1, 0)
     rows = (fake, fake, fake, fake, 8, 16, 4, 3)
 
     def gate_up(rows=rows, dims=(192, 128, 16), gu=(fake, fake), p=0.0, rng=None, ws_bytes=ws, x=fake, scale=fake):
@@ -181,7 +181,7 @@ def test_c_entry_points():
     assert gate_up(gu=(fake, None)) == INVALID and gate_up(p=0.5) == INVALID and gate_up(x=odd) == INVALID
     assert gate_up(scale=None) == INVALID and gate_up(ws_bytes=ws - 1) == WORKSPACE
     assert gate_up(rows=(fake, fake, fake, odd, 8, 16, 4, 3)) == INVALID
-    bwd = lib.moe_adapter_workspace_bytes(16, 192, 128, 16, 1, 1)
+    bwd = lib.moe_adapter_workspace_bytes(16, 4, 3, 192, 128, 16, 1, 1)
 
     def down_bwd(plan=fake, ws_bytes=bwd):
         return lib.moe_adapter_down_bwd(fake, fake, fake, fake, fake, fake, plan, 8, 16, 4, 3, 192, 128, 16, fake, fake, fake, None,

@@ -236,7 +236,7 @@ def test_rows_behind_the_last_expert_are_left_as_they_were(sort):
     plan = ops().adapter_plan(ids, offs, c["L"], row_token=token, backward=sort)
     fill = lambda cols: torch.full((c["n"], cols), 7.25, dtype=torch.bfloat16, device=dev())      # noqa: E731
     outs = dict(v=fill(32), g=fill(64), u=fill(64), a=fill(64))
-    nbytes = lib.moe_adapter_workspace_bytes(c["n"], 128, 64, 16, sort, False)
+    nbytes = lib.moe_adapter_workspace_bytes(c["n"], 4, 2, 128, 64, 16, sort, False)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev())
     p = lambda name: c["t_" + name].data_ptr()                                                    # noqa: E731
     stream = torch.cuda.current_stream().cuda_stream
