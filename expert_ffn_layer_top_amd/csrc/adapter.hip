@@ -38,7 +38,8 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kTileRows = 64;      // rows of a tile
-constexpr int kPlanChunk = 512;    // rows of one expert that a workgroup of the sort takes
+constexpr int kPlanBlock = 512;    // rows that a workgroup of the sort looks at together
+constexpr int kSmallPlan = 4096;   // up to this many rows one workgroup makes the whole plan
 constexpr int kMaxRank = 64;
 constexpr int kMaxAdapters = 256;
 
@@ -55,6 +56,13 @@ __device__ __forceinline__ void split_bf16(float x, uint16_t& hi, uint16_t& lo) 
   lo = f32_to_bf16(lo_of(x, bf16_to_f32(hi)));
 }
 
+// A wave's own LDS accesses keep their order; this keeps the compiler from changing it.
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // ---------------------------------------------------------------- the plan
 
 // Rows of one piece of a group's contraction in the weight gradients: pieces enough for the chip where few
@@ -63,6 +71,12 @@ __device__ __forceinline__ void split_bf16(float x, uint16_t& hi, uint16_t& lo) 
 __host__ __device__ inline int piece_rows(int n) {
   const int want = (n + 63) / 64;
   return want <= 512 ? 512 : want >= 2048 ? 2048 : (want + 31) / 32 * 32;
+}
+
+// Rows of one expert that a workgroup of the sort takes: about 128 workgroups and one for each expert, so that the scan
+// over an expert's chunks stays short.
+__host__ __device__ inline int chunk_rows(int n) {
+  return ((n + 127) / 128 + kPlanBlock - 1) / kPlanBlock * kPlanBlock;
 }
 
 struct Tile {
@@ -79,7 +93,7 @@ constexpr int kHeadTiles = 0, kHeadItems = 1, kHeadMulti = 2, kHeadWords = 16;
 
 __host__ __device__ inline PlanLayout plan_layout(int n, int E, int L) {
   PlanLayout p;
-  p.chunks = n / kPlanChunk + E;
+  p.chunks = n / chunk_rows(n) + E;
   p.pairs = E * (L + 1);
   const int groups = n < p.pairs ? n : p.pairs;
   p.tiles_cap = n / kTileRows + groups;
@@ -124,17 +138,17 @@ struct Chunk {
   int e, begin, end, index;   // index < 0: there is none
 };
 
-// The rows that chunk `want` holds: chunks are counted expert by expert, each of up to kPlanChunk rows of one.
+// The rows that chunk `want` holds: chunks are counted expert by expert, each of up to chunk_rows(n) rows of one.
 // All 256 threads call it (E <= 256: thread e looks at expert e).
 __device__ __forceinline__ Chunk find_chunk(const int32_t* offsets, int E, int n, int want) {
   __shared__ int sums[4], found[3];
-  const int e = threadIdx.x, lane = e & 63, wave = e >> 6;
+  const int e = threadIdx.x, lane = e & 63, wave = e >> 6, size = chunk_rows(n);
   int lo = 0, hi = 0;
   if (e < E) {
     lo = row_begin(offsets, e, n);
     hi = row_begin(offsets, e + 1, n);
   }
-  const int mine = hi > lo ? (hi - lo + kPlanChunk - 1) / kPlanChunk : 0;
+  const int mine = hi > lo ? (hi - lo + size - 1) / size : 0;
   int run = mine;
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
@@ -148,7 +162,7 @@ __device__ __forceinline__ Chunk find_chunk(const int32_t* offsets, int E, int n
   for (int w = 0; w < wave; ++w) base += sums[w];
   if (want >= base && want < base + mine) {
     found[0] = e;
-    found[1] = lo + (want - base) * kPlanChunk;
+    found[1] = lo + (want - base) * size;
     found[2] = hi;
   }
   __syncthreads();
@@ -156,7 +170,7 @@ __device__ __forceinline__ Chunk find_chunk(const int32_t* offsets, int E, int n
   c.e = found[0];
   c.index = c.e < 0 ? -1 : want;
   c.begin = found[1];
-  c.end = min(found[2], found[1] + kPlanChunk);
+  c.end = min(found[2], found[1] + size);
   return c;
 }
 
@@ -198,37 +212,22 @@ __device__ __forceinline__ int4 scan4(int4 v, int4* total) {
   return make_int4(base.x + run.x - v.x, base.y + run.y - v.y, base.z + run.z - v.z, base.w + run.w - v.w);
 }
 
-// Positions: of every (expert, adapter) in the sorted list, of its tiles, its pieces for the weight gradients and
-// of every chunk's rows of it.  One workgroup; a thread takes consecutive pairs (their number is E (L + 1)).
-__global__ __launch_bounds__(1024) void plan_scan_kernel(const int32_t* __restrict__ offsets, int n, int E, int L,
-                                                         int32_t* __restrict__ plan) {
-  __shared__ int chunk0[257];
-  const PlanLayout p = plan_layout(n, E, L);
+// Positions of every (expert, adapter) in the sorted list, of its tiles and of its pieces for the weight gradients.  1024
+// threads, of which each takes consecutive pairs (their number is E (L + 1)); count(q): a pair's rows, start(q, pos): told
+// where they begin.
+template <class Count, class Start>
+__device__ __forceinline__ void plan_positions(const PlanLayout& p, int n, int L, int32_t* plan, Count count, Start start) {
   int4 total;
-  {
-    int mine = 0;
-    if (threadIdx.x < static_cast<unsigned>(E)) {
-      const int lo = row_begin(offsets, threadIdx.x, n), hi = row_begin(offsets, threadIdx.x + 1, n);
-      mine = hi > lo ? (hi - lo + kPlanChunk - 1) / kPlanChunk : 0;
-    }
-    const int4 at = scan4(make_int4(mine, 0, 0, 0), &total);
-    if (threadIdx.x < static_cast<unsigned>(E)) chunk0[threadIdx.x] = at.x;
-    if (threadIdx.x == 0) chunk0[E] = total.x;
-    __syncthreads();
-  }
   const int per = (p.pairs + 1023) / 1024, first = threadIdx.x * per, last = min(first + per, p.pairs);
   const int piece = piece_rows(n);
-  int32_t* hist = plan + p.hist;
   int32_t* goff = plan + p.goff;
   int4 sum = make_int4(0, 0, 0, 0);   // rows, tiles, pieces, groups of several pieces
   for (int q = first; q < last; ++q) {
-    const int e = q / (L + 1), l = q - e * (L + 1);
-    int rows = 0;
-    for (int c = chunk0[e]; c < chunk0[e + 1]; ++c) rows += hist[static_cast<long long>(c) * (L + 1) + l];
+    const int rows = count(q);
     goff[q] = rows;
     sum.x += rows;
     sum.y += (rows + kTileRows - 1) / kTileRows;
-    if (l < L) {
+    if (q % (L + 1) < L) {
       sum.z += rows > piece ? (rows + piece - 1) / piece : 1;
       sum.w += rows > piece;
     }
@@ -239,13 +238,7 @@ __global__ __launch_bounds__(1024) void plan_scan_kernel(const int32_t* __restri
     const int e = q / (L + 1), l = q - e * (L + 1), rows = goff[q];
     goff[q] = at.x;
     plan[p.tile0 + q] = at.y;
-    int pos = at.x;
-    for (int c = chunk0[e]; c < chunk0[e + 1]; ++c) {
-      int32_t* h = &hist[static_cast<long long>(c) * (L + 1) + l];
-      const int here = *h;
-      *h = pos;
-      pos += here;
-    }
+    start(q, at.x);
     if (l < L) {
       const int pieces = rows > piece ? (rows + piece - 1) / piece : 1;
       for (int i = 0; i < pieces; ++i) items[at.z + i] = {at.x + i * piece, min(piece, rows - i * piece), e, l};
@@ -264,55 +257,155 @@ __global__ __launch_bounds__(1024) void plan_scan_kernel(const int32_t* __restri
   }
 }
 
+// The positions from the chunks' counts, which become the chunks' own positions.
+__global__ __launch_bounds__(1024) void plan_scan_kernel(const int32_t* __restrict__ offsets, int n, int E, int L,
+                                                         int32_t* __restrict__ plan) {
+  __shared__ int chunk0[257];
+  const PlanLayout p = plan_layout(n, E, L);
+  const int size = chunk_rows(n);
+  int mine = 0;
+  if (threadIdx.x < static_cast<unsigned>(E)) {
+    const int lo = row_begin(offsets, threadIdx.x, n), hi = row_begin(offsets, threadIdx.x + 1, n);
+    mine = hi > lo ? (hi - lo + size - 1) / size : 0;
+  }
+  int4 total;
+  const int4 at = scan4(make_int4(mine, 0, 0, 0), &total);
+  if (threadIdx.x < static_cast<unsigned>(E)) chunk0[threadIdx.x] = at.x;
+  if (threadIdx.x == 0) chunk0[E] = total.x;
+  __syncthreads();
+  int32_t* hist = plan + p.hist;
+  plan_positions(
+      p, n, L, plan,
+      [&](int q) {
+        const int e = q / (L + 1), l = q - e * (L + 1);
+        int rows = 0;
+#pragma unroll 8
+        for (int c = chunk0[e]; c < chunk0[e + 1]; ++c) rows += hist[static_cast<long long>(c) * (L + 1) + l];
+        return rows;
+      },
+      [&](int q, int pos) {
+        const int e = q / (L + 1), l = q - e * (L + 1);
+#pragma unroll 8
+        for (int c = chunk0[e]; c < chunk0[e + 1]; ++c) {
+          int32_t* h = &hist[static_cast<long long>(c) * (L + 1) + l];
+          const int here = *h;
+          *h = pos;
+          pos += here;
+        }
+      });
+}
+
+// Lanes of the wave whose `l` (9 bits) is this lane's, of those that are `live`.
+__device__ __forceinline__ unsigned long long same_lanes(int l, bool live) {
+  unsigned long long same = __ballot(live);
+  for (int b = 0; b < 9; ++b) {
+    const unsigned long long set = __ballot((l >> b) & 1);
+    same &= ((l >> b) & 1) ? set : ~set;
+  }
+  return same;
+}
+
+// A row's place in the list, and where it is a tile's first, the tile.
+__device__ __forceinline__ void place_row(int32_t* plan, const PlanLayout& p, const int32_t* row_token, int T, int L, int r,
+                                          int e, int l, int pos) {
+  const int q = e * (L + 1) + l, in = pos - plan[p.goff + q];
+  plan[p.rows + pos] = r;
+  plan[p.toks + pos] = token_of(row_token, r, T);
+  if (in % kTileRows == 0)
+    reinterpret_cast<Tile*>(plan + p.tiles)[plan[p.tile0 + q] + in / kTileRows] =
+        Tile{pos, min(kTileRows, plan[p.goff + q + 1] - pos), e, l};
+}
+
 // The sorted list and the tiles.  A row's rank among those of its adapter is its position's count of equal
-// adapters in the wave (ballots over the bits of the number), plus those of the chunk's earlier groups of 64.
+// adapters in the wave, plus those of the block's earlier groups of 64, plus the chunk's earlier blocks.
 __global__ __launch_bounds__(256) void plan_place_kernel(const int32_t* __restrict__ ids, const int32_t* __restrict__ row_token,
                                                          const int32_t* __restrict__ offsets, int T, int n, int E, int L,
                                                          int32_t* __restrict__ plan) {
-  constexpr int kGroups = kPlanChunk / 64;
-  __shared__ int before[kGroups][kMaxAdapters + 1];
+  constexpr int kGroups = kPlanBlock / 64;
+  __shared__ int before[kGroups][kMaxAdapters + 1], run[kMaxAdapters + 1];
   const PlanLayout p = plan_layout(n, E, L);
   const Chunk c = find_chunk(offsets, E, n, blockIdx.x);
   if (c.index < 0) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (int i = threadIdx.x; i < kGroups * (kMaxAdapters + 1); i += 256) (&before[0][0])[i] = 0;
-  __syncthreads();
-  int l[kGroups / 4], rank[kGroups / 4];
+  for (int a = threadIdx.x; a <= L; a += 256) run[a] = plan[p.hist + static_cast<long long>(blockIdx.x) * (L + 1) + a];
+  for (int begin = c.begin; begin < c.end; begin += kPlanBlock) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < kGroups * (kMaxAdapters + 1); i += 256) (&before[0][0])[i] = 0;
+    __syncthreads();
+    int l[kGroups / 4], rank[kGroups / 4];
 #pragma unroll
-  for (int i = 0; i < kGroups / 4; ++i) {
-    const int g = i * 4 + wave, r = c.begin + g * 64 + lane;
-    const bool live = r < c.end;
-    l[i] = live ? adapter_of(ids, row_token, r, T, L) : -1;
-    unsigned long long same = __ballot(live);
-    for (int b = 0; b < 9; ++b) {
-      const unsigned long long set = __ballot((l[i] >> b) & 1);
-      same &= ((l[i] >> b) & 1) ? set : ~set;
+    for (int i = 0; i < kGroups / 4; ++i) {
+      const int g = i * 4 + wave, r = begin + g * 64 + lane;
+      const bool live = r < c.end;
+      l[i] = live ? adapter_of(ids, row_token, r, T, L) : -1;
+      const unsigned long long same = same_lanes(l[i], live);
+      rank[i] = __popcll(same & ((1ull << lane) - 1));
+      if (live && rank[i] == 0) before[g][l[i]] = __popcll(same);
     }
-    rank[i] = __popcll(same & ((1ull << lane) - 1));
-    if (live && rank[i] == 0) before[g][l[i]] = __popcll(same);
-  }
-  __syncthreads();
-  for (int a = threadIdx.x; a <= L; a += 256) {
-    int run = plan[p.hist + static_cast<long long>(blockIdx.x) * (L + 1) + a];
+    __syncthreads();
+    for (int a = threadIdx.x; a <= L; a += 256) {
+      int at = run[a];
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
-      const int here = before[g][a];
-      before[g][a] = run;
-      run += here;
+      for (int g = 0; g < kGroups; ++g) {
+        const int here = before[g][a];
+        before[g][a] = at;
+        at += here;
+      }
+      run[a] = at;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kGroups / 4; ++i) {
+      const int g = i * 4 + wave, r = begin + g * 64 + lane;
+      if (r < c.end) place_row(plan, p, row_token, T, L, r, c.e, l[i], before[g][l[i]] + rank[i]);
     }
   }
+}
+
+// The whole plan of up to kSmallPlan rows in one workgroup: a wave walks the rows of one expert after another, 64 at a
+// time, and keeps their adapters and ranks in LDS until the positions are known.
+__global__ __launch_bounds__(1024) void plan_small_kernel(const int32_t* __restrict__ ids, const int32_t* __restrict__ row_token,
+                                                          const int32_t* __restrict__ offsets, int T, int n, int E, int L,
+                                                          int32_t* __restrict__ plan) {
+  __shared__ int begin[257], run[16][kMaxAdapters + 1];
+  __shared__ uint16_t adapter[kSmallPlan], rank[kSmallPlan];
+  const PlanLayout p = plan_layout(n, E, L);
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  if (tid <= E) begin[tid] = row_begin(offsets, tid, n);
+  for (int r = tid; r < n; r += 1024) adapter[r] = static_cast<uint16_t>(adapter_of(ids, row_token, r, T, L));
   __syncthreads();
-  Tile* tiles = reinterpret_cast<Tile*>(plan + p.tiles);
-#pragma unroll
-  for (int i = 0; i < kGroups / 4; ++i) {
-    const int g = i * 4 + wave, r = c.begin + g * 64 + lane;
-    if (r >= c.end) continue;
-    const int pos = before[g][l[i]] + rank[i], q = c.e * (L + 1) + l[i];
-    plan[p.rows + pos] = r;
-    plan[p.toks + pos] = token_of(row_token, r, T);
-    const int in = pos - plan[p.goff + q];
-    if (in % kTileRows == 0)
-      tiles[plan[p.tile0 + q] + in / kTileRows] = {pos, min(kTileRows, plan[p.goff + q + 1] - pos), c.e, l[i]};
+  for (int e = wave; e < E; e += 16) {
+    for (int a = lane; a <= L; a += 64) run[wave][a] = 0;
+    wave_fence();
+    for (int r0 = begin[e]; r0 < begin[e + 1]; r0 += 64) {
+      const int r = r0 + lane;
+      const bool live = r < begin[e + 1];
+      const int l = live ? adapter[r] : -1;
+      const unsigned long long same = same_lanes(l, live);
+      const int in = __popcll(same & ((1ull << lane) - 1)), before = live ? run[wave][l] : 0;
+      wave_fence();
+      if (live) rank[r] = static_cast<uint16_t>(before + in);
+      if (live && in == 0) run[wave][l] = before + __popcll(same);
+      wave_fence();
+    }
+    for (int a = lane; a <= L; a += 64) plan[p.tile0 + e * (L + 1) + a] = run[wave][a];
+    wave_fence();
+  }
+  __threadfence_block();
+  __syncthreads();
+  plan_positions(
+      p, n, L, plan, [&](int q) { return plan[p.tile0 + q]; }, [](int, int) {});
+  __threadfence_block();
+  __syncthreads();
+  for (int r = tid; r < n; r += 1024) {
+    int e = 0, past = E;             // the expert whose rows r is among: the last that begins at or before it
+    while (past - e > 1) {
+      const int mid = (e + past) / 2;
+      if (begin[mid] <= r) e = mid;
+      else past = mid;
+    }
+    if (r < begin[e] || r >= begin[e + 1]) continue;
+    place_row(plan, p, row_token, T, L, r, e, adapter[r], plan[p.goff + e * (L + 1) + adapter[r]] + rank[r]);
   }
 }
 
@@ -370,13 +463,6 @@ struct ShrinkArgs {
 // k ^ (r / 2 % 8), so that both the 8 rows that a wave writes at once and the 16 that it reads lie in different banks.
 // Within rows 8 i + r (writes) that depends on i by its lowest bit alone, within rows 16 b + r (reads) not on b.
 __device__ __forceinline__ int staged(int row, int chunk) { return row * 8 + (chunk ^ ((row >> 1) & 7)); }
-
-// A wave's own LDS accesses keep their order; this keeps the compiler from changing it.
-__device__ __forceinline__ void wave_fence() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
 
 // One tile (NB blocks of 16 rows) times RT tiles of 16 ranks over K's units of 64 elements u0, u0 + 4, ...  A load takes
 // 8 rows of a whole cache line each.  (The matrix instruction's operand has 16 rows of 16 bytes in neighbouring
@@ -1213,9 +1299,16 @@ int check_rows(const Rows& r) {
   return MOE_OK;
 }
 
+// Without a plan every row is a workgroup.
+int check_few(const Rows& r) {
+  MOE_REQUIRE(r.plan != nullptr || r.n <= 1 << 22, MOE_ERR_UNSUPPORTED, "more than 2^22 rows need a plan (got %d)", r.n);
+  return MOE_OK;
+}
+
 int check_dims(int d, int f, int r) {
-  MOE_REQUIRE(d >= 64 && d % 64 == 0, MOE_ERR_UNSUPPORTED, "d must be a positive multiple of 64 (got %d)", d);
-  MOE_REQUIRE(f >= 64 && f % 64 == 0, MOE_ERR_UNSUPPORTED, "f must be a positive multiple of 64 (got %d)", f);
+  // (a matrix of 128 ranks is addressed by 32 bits)
+  MOE_REQUIRE(d >= 64 && d % 64 == 0 && d <= 1 << 24, MOE_ERR_UNSUPPORTED, "d must be a multiple of 64 in [64, 2^24] (got %d)", d);
+  MOE_REQUIRE(f >= 64 && f % 64 == 0 && f <= 1 << 24, MOE_ERR_UNSUPPORTED, "f must be a multiple of 64 in [64, 2^24] (got %d)", f);
   MOE_REQUIRE(r >= 8 && r <= kMaxRank && r % 8 == 0, MOE_ERR_UNSUPPORTED, "r must be a multiple of 8 in [8, %d] (got %d)",
               kMaxRank, r);
   return MOE_OK;
@@ -1283,6 +1376,10 @@ extern "C" int moe_adapter_plan(const int32_t* ids, const int32_t* row_token, co
   MOE_CHECK_ALIGN(plan);
   hipStream_t st = as_stream(stream);
   int32_t* buf = static_cast<int32_t*>(plan);
+  if (n <= kSmallPlan) {
+    plan_small_kernel<<<1, 1024, 0, st>>>(ids, row_token, offsets, T, n, E, L, buf);
+    return check_launch("adapter_plan");
+  }
   plan_count_kernel<<<p.chunks, 256, 0, st>>>(ids, row_token, offsets, T, n, E, L, buf);
   plan_scan_kernel<<<1, 1024, 0, st>>>(offsets, n, E, L, buf);
   plan_place_kernel<<<p.chunks, 256, 0, st>>>(ids, row_token, offsets, T, n, E, L, buf);
@@ -1304,6 +1401,7 @@ extern "C" int moe_adapter_gate_up(const uint16_t* x, const int32_t* ids, const 
                                    void* ws, size_t ws_bytes, void* stream) {
   const Rows rows = {static_cast<const int32_t*>(plan), ids, row_token, offsets, T, n, E, L};
   if (int st = check_rows(rows)) return st;
+  if (int st = check_few(rows)) return st;
   if (int st = check_dims(d, f, r)) return st;
   MOE_CHECK_PTR(x); MOE_CHECK_PTR(a_gu); MOE_CHECK_PTR(b_gate); MOE_CHECK_PTR(b_up); MOE_CHECK_PTR(scale);
   MOE_CHECK_PTR(g); MOE_CHECK_PTR(u); MOE_CHECK_PTR(a); MOE_CHECK_PTR(a_out);
@@ -1340,6 +1438,7 @@ extern "C" int moe_adapter_down(const uint16_t* a, const int32_t* ids, const int
                                 const uint16_t* yexp, uint16_t* v, uint16_t* y_out, void* ws, size_t ws_bytes, void* stream) {
   const Rows rows = {static_cast<const int32_t*>(plan), ids, row_token, offsets, T, n, E, L};
   if (int st = check_rows(rows)) return st;
+  if (int st = check_few(rows)) return st;
   if (int st = check_dims(d, f, r)) return st;
   MOE_CHECK_PTR(a); MOE_CHECK_PTR(a_down); MOE_CHECK_PTR(b_down); MOE_CHECK_PTR(scale); MOE_CHECK_PTR(yexp);
   MOE_CHECK_PTR(y_out);

@@ -536,6 +536,7 @@ extern "C" int moe_unpermute_combine_dropout_bwd(const uint16_t* dy, const uint1
   MOE_CHECK_ALIGN(dy); MOE_CHECK_ALIGN(yexp); MOE_CHECK_ALIGN(dyexp);
   DropArgs drop;
   if (int st = make_drop(rng, p, site, &drop)) return st;
+  MOE_REQUIRE(T <= (1 << 26) - 4, MOE_ERR_UNSUPPORTED, "too many tokens for one launch");
   MOE_SEG_LAUNCH2(combine_bwd_kernel, true, grid_for(T), as_stream(stream), k, dy, yexp, gate, dest, T, d, k, dyexp,
                   dgate, drop);
   return check_launch("combine_dropout_bwd");

@@ -324,12 +324,14 @@ int moe_unpermute_combine_dropout_bwd(const uint16_t* dy, const uint16_t* yexp, 
  * id outside [0, L) means none: such a row's results are its inputs, bit for bit.
  *   a_gu [L,E,2r,d] (gate's ranks, then up's), b_gate, b_up [L,E,r,f], a_down [L,E,r,f], b_down [L,E,r,d]:
  *   bf16, B by rank like A (the transpose of the usual [out, r]); scale [L] fp32.  Adapters of a smaller rank are
- *   padded with zeros.  r a multiple of 8 in [8, 64]; d and f multiples of 64; 1 <= L <= 256; n <= 2^26.
+ *   padded with zeros.  r a multiple of 8 in [8, 64]; d and f multiples of 64, at most 2^24; 1 <= L <= 256;
+ *   n <= 2^26 (2^22 without a plan).
  *   m: the dropout factors (above) of the adapters' inputs, element (grouped row, column); p = 0: none.
  *   gate_up:  v = (m x[t]) A^T;  g' = g + s v_gate B_gate,  u' = u + s v_up B_up,  a' = silu(g') u'
  *   down:     v = (m a) A^T;     y' = y + s v B
  * Products of bf16 values are summed in fp32; between its two products v (and dv of the backward) is held to 16 bits of
  * mantissa, and handed out as bf16; g', u', y' are rounded once, and a' comes from the unrounded g', u'.
+ * The last bits of a row may differ with the number of rows in the call and with a plan, since sums are cut by them.
  * Rows from offsets[E] on are left as they were. */
 
 /* The order of the rows by expert and adapter (a stable sort, so that sums run in a fixed order), made on the

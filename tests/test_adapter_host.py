@@ -158,6 +158,7 @@ def test_c_entry_points():
     assert lib.moe_unpermute_combine_dropout(fake, fake, fake, None, fake, 0.5, 0, 4, 64, 17, fake, None) == UNSUPPORTED
     assert lib.moe_unpermute_combine_dropout(fake, None, fake, None, fake, 0.5, 0, 4, 64, 2, fake, None) == INVALID
     assert lib.moe_unpermute_combine_dropout_bwd(fake, fake, fake, fake, None, 0.5, 0, 4, 64, 2, fake, fake, None) == INVALID
+    assert lib.moe_unpermute_combine_dropout_bwd(fake, fake, fake, fake, fake, 0.5, 0, 1 << 26, 64, 2, fake, fake, None) == UNSUPPORTED
     assert lib.moe_adapter_plan_bytes(16, 4, 3) > 0
     for bad in ((0, 4, 3), (16, 0, 3), (16, 257, 3), (16, 4, 0), (16, 4, 257), ((1 << 26) + 1, 4, 3)):
         assert lib.moe_adapter_plan_bytes(*bad) == 0
@@ -179,6 +180,8 @@ def test_c_entry_points():
                                        fake, ws_bytes, None)
     assert gate_up(dims=(192, 128, 12)) == UNSUPPORTED and gate_up(dims=(100, 128, 16)) == UNSUPPORTED
     assert gate_up(gu=(fake, None)) == INVALID and gate_up(p=0.5) == INVALID and gate_up(x=odd) == INVALID
+    assert gate_up(dims=((1 << 24) + 64, 128, 16)) == UNSUPPORTED
+    assert gate_up(rows=(fake, fake, fake, None, 8, (1 << 22) + 1, 4, 3)) == UNSUPPORTED      # a workgroup a row
     assert gate_up(scale=None) == INVALID and gate_up(ws_bytes=ws - 1) == WORKSPACE
     assert gate_up(rows=(fake, fake, fake, odd, 8, 16, 4, 3)) == INVALID
     bwd = lib.moe_adapter_workspace_bytes(16, 4, 3, 192, 128, 16, 1, 1)

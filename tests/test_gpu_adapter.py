@@ -211,6 +211,38 @@ def test_more_rows_than_one_piece_of_a_contraction():
     check_backward(c, plan_of(c, True), p=0.1)
 
 
+@pytest.mark.parametrize("T,k,E,L,ids", [(70001, 1, 1, 3, "mixed"), (40000, 2, 3, 2, "outside"), (5000, 8, 64, 9, "mixed"),
+                                         (66000, 1, 2, 256, "mixed")])
+def test_many_rows(T, k, E, L, ids):
+    """Chunks of several blocks of the sort, experts of very different size; against the definition in 64 bits on the GPU, written with
+    every row's matrices gathered."""
+    note(f"adapter many rows {T} {k} {E} {L} {ids}")
+    d, f, r = 64, 64, 8
+    c = make(10, T, k, E, L, d, f, r, ids)
+    plan = plan_of(c, True)
+    e, l = (torch.from_numpy(c[name]).to(dev()) for name in "el")
+    has, l0 = (l >= 0)[:, None], l.clamp(min=0)
+    A, B, s = c["t_a_down"].double()[l0, e], c["t_b_down"].double()[l0, e], c["t_scale"].double()[l0][:, None]
+    y, v = ops().adapter_down(c["t_a"], c["t_y"], plan, c["t_a_down"], c["t_b_down"], c["t_scale"], want_v=True)
+    a64 = c["t_a"].double()
+    v64 = torch.where(has, (A * a64[:, None]).sum(2), 0.0)
+    vmag = (A * a64[:, None]).abs().sum(2)
+    assert bool(((v.double() - v64).abs() <= U * v64.abs() + f * 2.0 ** -23 * vmag).all())
+    y64 = c["t_y"].double() + torch.where(has, s * (B * v64[:, :, None]).sum(1), 0.0)
+    off = s * (B.abs() * (V * v64.abs() + f * 2.0 ** -23 * vmag)[:, :, None]).sum(1)
+    mag = c["t_y"].double().abs() + s * (B * v64[:, :, None]).abs().sum(1)
+    assert bool(((y.double() - y64).abs() <= U * y64.abs() + 1.01 * off + (2 * r + 4) * 2.0 ** -23 * mag).all())
+    out = ops().adapter_down_bwd(c["t_y"], c["t_a"], c["t_v2"], c["t_g"], c["t_u"], c["t_dg"], c["t_du"], plan, c["t_a_down"],
+                                 c["t_b_down"], c["t_scale"])
+    key = (l0 * E + e)[has[:, 0]]
+    part = (s * c["t_v2"].double())[has[:, 0]][:, :, None] * c["t_y"].double()[has[:, 0]][:, None]
+    want = torch.zeros((L * E, r, d), dtype=torch.float64, device=dev()).index_add_(0, key, part).view(L, E, r, d)
+    size = torch.zeros((L * E, r, d), dtype=torch.float64, device=dev()).index_add_(0, key, part.abs()).view(L, E, r, d)
+    rows = int(torch.bincount(key).max())
+    assert bool(((out[3].double() - want).abs() <= U * want.abs() + (1 + U) * (rows + 4) * 2.0 ** -23 * size).all())
+    assert torch.equal(out[0][~has[:, 0]], c["t_dg"][~has[:, 0]])
+
+
 def test_rows_are_tokens_without_row_token():
     note("adapter without row_token")
     c = make(4, 70, 1, 4, 2, 128, 128, 16)
@@ -288,6 +320,80 @@ def test_ranks_padded_with_zeros_add_nothing():
         b = ops().adapter_gate_up(c["t_x"], c["t_g"], c["t_u"], c["t_a"], plan, *small)
         for s, t in zip(a[:3], b[:3]):
             assert torch.equal(s, t)
+
+
+def test_rows_whose_offsets_pass_32_bits():
+    """yexp and dyexp of more than 4 GiB: the last rows, and a gradient that only they reach."""
+    note("adapter rows past 4 GiB")
+    n, d, f, r = 270000, 8192, 64, 8
+    g = torch.Generator(device=dev()).manual_seed(5)
+    bf = lambda *s, std=1.0: (torch.randn(s, generator=g, device=dev()) * std).to(torch.bfloat16)          # noqa: E731
+    a, y = bf(n, f), torch.zeros((n, d), dtype=torch.bfloat16, device=dev())
+    y[-70:] = bf(70, d)
+    A, B, s = bf(2, 1, r, f, std=f ** -0.5), bf(2, 1, r, d, std=r ** -0.5), torch.ones(2, device=dev())
+    ids = torch.zeros(n, dtype=torch.int32, device=dev())
+    ids[-70:] = 1
+    off = torch.tensor([0, n], dtype=torch.int32, device=dev())
+    plan = ops().adapter_plan(ids, off, 2, backward=True)
+    out, v = ops().adapter_down(a, y, plan, A, B, s, want_v=True)
+    v64 = a[-70:].double() @ A[1, 0].double().t()
+    vmag = a[-70:].double().abs() @ A[1, 0].double().abs().t()
+    want = y[-70:].double() + v64 @ B[1, 0].double()
+    off_v = V * v64.abs() + f * 2.0 ** -23 * vmag
+    tol = U * want.abs() + 1.01 * off_v @ B[1, 0].double().abs() + (2 * r + 4) * 2.0 ** -23 * (y[-70:].double().abs() + v64.abs() @ B[1, 0].double().abs())
+    assert bool(((out[-70:].double() - want).abs() <= tol).all())
+    zero = torch.zeros((n, f), dtype=torch.bfloat16, device=dev())
+    _, _, d_a, d_b = ops().adapter_down_bwd(y, a, v, zero, zero, zero, zero, plan, A, B, s)
+    assert torch.count_nonzero(d_a[0]) == 0 and torch.count_nonzero(d_b[0]) == 0        # y is 0 in all other rows
+    want = v[-70:].double().t() @ y[-70:].double()
+    mag = v[-70:].double().abs().t() @ y[-70:].double().abs()
+    assert bool(((d_b[1, 0].double() - want).abs() <= U * want.abs() + 80 * 2.0 ** -23 * mag).all())
+
+
+def test_matrices_whose_offsets_pass_32_bits():
+    """Adapters of more than 4 GiB: the last one, by both forms."""
+    note("adapters past 4 GiB")
+    L, E, r, d, f = 64, 64, 64, 4352, 64
+    a_gu = torch.zeros((L, E, 2 * r, d), dtype=torch.bfloat16, device=dev())
+    g = torch.Generator(device=dev()).manual_seed(6)
+    bf = lambda *s, std=1.0: (torch.randn(s, generator=g, device=dev()) * std).to(torch.bfloat16)          # noqa: E731
+    a_gu[-1, -1] = bf(2 * r, d, std=d ** -0.5)
+    b_gate, b_up = torch.zeros((2, L, E, r, f), dtype=torch.bfloat16, device=dev())
+    b_gate, b_up = b_gate.contiguous(), b_up.contiguous()
+    x, gb = bf(3, d), bf(3, f)
+    ids = torch.full((3,), L - 1, dtype=torch.int32, device=dev())
+    off = torch.zeros(E + 1, dtype=torch.int32, device=dev())
+    off[-1] = 3
+    v64 = x.double() @ a_gu[-1, -1].double().t()
+    vmag = x.double().abs() @ a_gu[-1, -1].double().abs().t()
+    for sort in (False, True):
+        plan = ops().adapter_plan(ids, off, L, backward=sort)
+        _, _, _, v = ops().adapter_gate_up(x, gb, gb, gb, plan, a_gu, b_gate, b_up, torch.ones(L, device=dev()), want_v=True)
+        assert bool(((v.double() - v64).abs() <= U * v64.abs() + d * 2.0 ** -23 * vmag).all())
+
+
+def test_two_streams_at_once():
+    """The same calls on two streams, each with plans and workspaces of its own, against one after the other."""
+    note("adapter on two streams")
+    cases = [make(20 + i, 700, 2, 4, 3, 192, 128, 16) for i in range(2)]
+    def step(c):
+        plan = plan_of(c, True)
+        up, down = [c["t_" + w] for w in ("a_gu", "b_gate", "b_up", "scale")], [c["t_" + w] for w in ("a_down", "b_down", "scale")]
+        g, u, a, v1 = ops().adapter_gate_up(c["t_x"], c["t_g"], c["t_u"], c["t_a"], plan, *up, want_v=True)
+        y, v2 = ops().adapter_down(a, c["t_y"], plan, *down, want_v=True)
+        one = ops().adapter_down_bwd(y, a, v2, g, u, c["t_dg"], c["t_du"], plan, *down)
+        return (g, u, a, v1, y, v2, *one, *ops().adapter_gate_up_bwd(one[0], one[1], c["t_x"], v1, c["t_dxp"], plan, *up))
+    want = [step(c) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = []
+    for c, s in zip(cases, streams):
+        with torch.cuda.stream(s):
+            got.append([step(c) for _ in range(3)])
+    torch.cuda.synchronize()
+    for w, runs in zip(want, got):
+        for run in runs:
+            assert all(torch.equal(s, t) for s, t in zip(w, run))
 
 
 def test_repeated_calls_give_the_same_bits():
