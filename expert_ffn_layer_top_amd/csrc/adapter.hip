@@ -503,9 +503,7 @@ __device__ __forceinline__ void shrink_tile(const ShrinkArgs& a, const Tile& t, 
     for (int i = 0; i < 2 * RT; ++i) wr[i] = load16(w + (wo[i] + 64u * u));
     __builtin_amdgcn_sched_barrier(0);
   };
-  if (u0 >= u1) return;
-  load(u0);
-  for (int u = u0; u < u1; u += 4) {
+  auto put = [&](int u) {
 #pragma unroll
     for (int i = 0; i < 2 * NB; ++i) {
       if (DROP) xr[i] = drop_zero(key, row[i], 8 * u + lc, xr[i]);
@@ -514,8 +512,8 @@ __device__ __forceinline__ void shrink_tile(const ShrinkArgs& a, const Tile& t, 
 #pragma unroll
     for (int i = 0; i < 2 * RT; ++i) lds[(i & 1 ? w1 : w0) + kW + 64 * i] = wr[i];
     wave_fence();
-    // (past the end the last unit is loaded again, and not used: a load under a condition makes the waits conservative)
-    load(u + 4 < u1 ? u + 4 : u);
+  };
+  auto multiply = [&] {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       u32x4 xf[NB];
@@ -529,7 +527,17 @@ __device__ __forceinline__ void shrink_tile(const ShrinkArgs& a, const Tile& t, 
       }
     }
     wave_fence();
+  };
+  if (u0 >= u1) return;
+  int u = u0;
+  load(u);
+  for (; u + 4 < u1; u += 4) {
+    put(u);
+    load(u + 4);
+    multiply();
   }
+  put(u);
+  multiply();
 }
 
 // The four waves' sums joined through LDS, two tiles of ranks at a time, and stored.
