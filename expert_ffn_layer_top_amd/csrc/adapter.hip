@@ -71,7 +71,7 @@ __device__ __forceinline__ void wave_fence() {
 // then have two pieces), and that of 32768 rows of one expert, wider, 703 and 745.
 __host__ __device__ inline int piece_rows(int n) {
   const int want = (n + 31) / 32;
-  return want <= 512 ? 512 : want >= 2048 ? 2048 : (want + 31) / 32 * 32;
+  return want <= 256 ? 256 : want >= 2048 ? 2048 : (want + 31) / 32 * 32;
 }
 
 // Rows of one expert that a workgroup of the sort takes: about 128 workgroups and one for each expert, so that the scan
@@ -584,7 +584,7 @@ __device__ __forceinline__ void shrink_run(const ShrinkArgs& a, const Tile& t, c
 }
 
 template <int RT, bool DROP>
-__global__ __launch_bounds__(256, RT <= 2 ? 3 : RT == 4 ? 2 : 1) void adapter_shrink_kernel(ShrinkArgs a) {
+__global__ __launch_bounds__(256, RT == 1 && !DROP ? 4 : RT <= 2 ? 3 : RT == 4 ? 2 : 1) void adapter_shrink_kernel(ShrinkArgs a) {
   __shared__ u32x4 lds[4 * (4 + RT) * 128];   // 2 KiB for 16 rows or ranks; the sums take at most half of it
   const PlanLayout p = plan_layout(a.rows.n, a.rows.E, a.rows.L);
   const int each = a.S * a.parts, rows_each = kTileRows / a.parts;
