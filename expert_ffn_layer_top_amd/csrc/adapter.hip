@@ -432,9 +432,10 @@ __device__ __forceinline__ int n_tiles(const Rows& rows) { return rows.plan[kHea
 // Row at sorted position pos (clamped by the caller to the tile).
 __device__ __forceinline__ int row_at(const Rows& rows, const PlanLayout& p, int pos) { return rows.plan[p.rows + pos]; }
 
-// A workgroup's items: those of XCD x (workgroups x mod 8) are one contiguous run of the order, so that the tiles of one
-// expert and adapter, which read the same matrix, and the columns of one tile, which read the same rows of v, share an
-// L2.  gridDim.x is a multiple of 8.
+// The shrink's items by workgroup: those of XCD x (workgroups x mod 8) are one contiguous run of the order, so that the
+// tiles of one expert and adapter, which read the same matrix, share an L2 (131072 rows of 4096 by 32 ranks: 274 -> 263
+// us).  gridDim.x is a multiple of 8.  Expand and the weight gradients take their items as they come: there, hot experts
+// left whole XCDs with more to do (82 -> 109 us and 260 -> 365 us in runs).
 struct Run {
   long long at, end, step;
 };
@@ -466,11 +467,15 @@ struct ShrinkArgs {
 __device__ __forceinline__ int staged(int row, int chunk) { return row * 8 + (chunk ^ ((row >> 1) & 7)); }
 
 // One tile (NB blocks of 16 rows) times RT tiles of 16 ranks over K's units of 64 elements u0, u0 + 4, ...  A load takes
-// 8 rows of a whole cache line each.  (The matrix instruction's operand has 16 rows of 16 bytes in neighbouring
-// lanes; loaded like that, every lane is a cache line of its own and the address unit, at a line a cycle, is what
-// bounds: 3.8 TB/s of x at 32 ranks.)  So rows go through registers, where they wait for memory while the unit
-// before them is multiplied, into the wave's staging, and come from there as operands.  Rows past the tile and
-// ranks past R are copies of the last one, which nobody stores.
+// 8 rows of a whole cache line each; rows go through registers, where they wait for memory while the unit before them
+// is multiplied, into the wave's staging, and come from there as operands.  Rows past the tile and ranks past R are copies
+// of the last one, which nobody stores.
+//
+// What bounds it is memory: 131072 rows of 4096 (1.07 GB) by 32 ranks of 512 matrices take 263 us, and the L2s miss 1.33 GB
+// in that time, 5.0 TB/s; a stream of the same rows alone reaches 5.5 to 6.  Loading fragments without the staging (16
+// rows of 16 bytes in neighbouring lanes) with two units of loads in registers took 282: registers left two waves per
+// SIMD, here there are three (four for 16 ranks, two for 64, one for 128).  A tile's K starting at a
+// place of its own, so that fewer workgroups read the same columns at once, changed nothing.
 template <int NB, int RT, bool DROP>
 __device__ __forceinline__ void shrink_tile(const ShrinkArgs& a, const Tile& t, const PlanLayout& p, const uint16_t* x,
                                             const uint16_t* w, int u0, int u1, u32x4* lds, f32x4 (&acc)[NB][RT]) {
@@ -613,6 +618,12 @@ __global__ __launch_bounds__(256, RT == 1 && !DROP ? 4 : RT <= 2 ? 3 : RT == 4 ?
 }
 
 // ---------------------------------------------------------------- expand
+//
+// A wave takes 16 rows after another of a tile and 128 columns, for which it holds W's fragments.  It reads what it adds to
+// and writes the sum, and that is what it costs: SwiGLU of 131072 x 2048 takes 483 us (2.7 GB, 5.6 TB/s), the addition to
+// 131072 x 7168 680 us (3.8 GB, 5.5 TB/s); a copy runs at 4.9.  The loads of the first 16 rows are issued before W's, on
+// whose arrival everything else waits; where a launch has few tiles their rows are shared among up to four waves (4012 rows
+// of 1344: 27 -> 14 us).
 
 enum { kAdd = 0, kSwiglu = 1, kSwigluBwd = 2 };
 
@@ -848,7 +859,8 @@ __global__ __launch_bounds__(256, KS == 1 || (KS == 2 && MODE != kSwiglu) ? 2 : 
 // ---------------------------------------------------------------- few rows
 
 // Both products of one row in a workgroup, without a plan: what few rows cost is the chain of loads that hang on each
-// other (token, adapter, matrices) and the launches, not bytes.  A wave takes RW ranks of A along whole cache lines, v meets in
+// other (token, adapter, matrices) and the launches, not bytes.  One token's 8 rows (d 4096, f 768, rank 16) take 10 us and 6
+// us (down), and a whole call 11 us of the host's time; as shrink and expand they took 14, 10 and 18 us.  A wave takes RW ranks of A along whole cache lines, v meets in
 // LDS as fp32, and then a lane takes 8 columns of B for all ranks; the first 8 ranks of B, and the row's own values,
 // are on their way while A is read.  Products and sums are fp32 FMAs.
 struct RowArgs {
@@ -1030,6 +1042,10 @@ __device__ __forceinline__ long long piece_slot(int pos, int piece, bool first) 
 // neighbouring columns of the same rows, so v's 64 rows are staged once for all of them, transposed: pairs of rows [rank][32] in
 // LDS (padded to 36: the 16 ranks of a fragment's 16-byte reads lie in different banks).  y's rows go from memory into
 // registers half a step (32 rows) ahead, v's and the row numbers a whole one; loads past the piece read its last row.
+//
+// Bound by memory and its latency: 131072 rows of 4096 by 32 ranks take 243 us (1.28 GB through the L2s' misses, 5.3 TB/s).
+// More than 32 ranks are a workgroup for each 32, whose second reading of y comes from the L2: 64 ranks take 320 us, where a
+// wave with all 64 (one wave per SIMD then) took 412, and a workgroup of eight waves, four for each half, 441.
 template <int RT, bool DROP, bool LO>
 __global__ __launch_bounds__(256, 2) void adapter_wgrad_kernel(WgradArgs a) {
   constexpr int NV = LO ? 2 : 1, kItems = NV * RT * 64, NI = (kItems + 255) / 256, kPad = 36;

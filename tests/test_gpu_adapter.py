@@ -330,7 +330,7 @@ def test_rows_whose_offsets_pass_32_bits():
     bf = lambda *s, std=1.0: (torch.randn(s, generator=g, device=dev()) * std).to(torch.bfloat16)          # noqa: E731
     a, y = bf(n, f), torch.zeros((n, d), dtype=torch.bfloat16, device=dev())
     y[-70:] = bf(70, d)
-    A, B, s = bf(2, 1, r, f, std=f ** -0.5), bf(2, 1, r, d, std=r ** -0.5), torch.ones(2, device=dev())
+    A, B, s = bf(2, 1, r, f, std=f ** -0.5), bf(2, 1, r, d, std=r ** -0.5), torch.ones(2, dtype=torch.float32, device=dev())
     ids = torch.zeros(n, dtype=torch.int32, device=dev())
     ids[-70:] = 1
     off = torch.tensor([0, n], dtype=torch.int32, device=dev())
@@ -368,7 +368,7 @@ def test_matrices_whose_offsets_pass_32_bits():
     vmag = x.double().abs() @ a_gu[-1, -1].double().abs().t()
     for sort in (False, True):
         plan = ops().adapter_plan(ids, off, L, backward=sort)
-        _, _, _, v = ops().adapter_gate_up(x, gb, gb, gb, plan, a_gu, b_gate, b_up, torch.ones(L, device=dev()), want_v=True)
+        _, _, _, v = ops().adapter_gate_up(x, gb, gb, gb, plan, a_gu, b_gate, b_up, torch.ones(L, dtype=torch.float32, device=dev()), want_v=True)
         assert bool(((v.double() - v64).abs() <= U * v64.abs() + d * 2.0 ** -23 * vmag).all())
 
 
