@@ -118,10 +118,23 @@ __host__ __device__ inline PlanLayout plan_layout(int n, int E, int L) {
   return p;
 }
 
-// Expert e's rows, whatever the offsets hold: within [0, n) and not negative in number.
-__device__ __forceinline__ int row_begin(const int32_t* offsets, int e, int n) {
-  const int o = offsets[e];
-  return o < 0 ? 0 : o > n ? n : o;
+// The experts' first rows, begin[0 .. E], from the offsets: within [0, n] and never falling, whatever the offsets hold, so
+// that the plan's parts hold whatever follows from them.  The first 256 threads of the workgroup do it, all call it.
+__device__ __forceinline__ void load_begins(const int32_t* offsets, int E, int n, int (&begin)[257]) {
+  __shared__ int most[4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int v = tid < 256 && tid <= E ? min(max(offsets[tid], 0), n) : 0;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int u = __shfl_up(v, o, 64);
+    if (lane >= o) v = max(v, u);
+  }
+  if (lane == 63 && wave < 4) most[wave] = v;
+  __syncthreads();
+  for (int w = 0; w < min(wave, 4); ++w) v = max(v, most[w]);
+  if (tid < 256 && tid <= E) begin[tid] = v;
+  if (tid == 255 && E == 256) begin[256] = max(v, min(max(offsets[256], 0), n));
+  __syncthreads();
 }
 
 // A row's token, within [0, T), and its adapter, L for none (also where the token is no token).
@@ -142,14 +155,11 @@ struct Chunk {
 // The rows that chunk `want` holds: chunks are counted expert by expert, each of up to chunk_rows(n) rows of one.
 // All 256 threads call it (E <= 256: thread e looks at expert e).
 __device__ __forceinline__ Chunk find_chunk(const int32_t* offsets, int E, int n, int want) {
-  __shared__ int sums[4], found[3];
+  __shared__ int sums[4], found[3], begin[257];
+  load_begins(offsets, E, n, begin);
   const int e = threadIdx.x, lane = e & 63, wave = e >> 6, size = chunk_rows(n);
-  int lo = 0, hi = 0;
-  if (e < E) {
-    lo = row_begin(offsets, e, n);
-    hi = row_begin(offsets, e + 1, n);
-  }
-  const int mine = hi > lo ? (hi - lo + size - 1) / size : 0;
+  const int lo = e < E ? begin[e] : 0, hi = e < E ? begin[e + 1] : 0;
+  const int mine = (hi - lo + size - 1) / size;
   int run = mine;
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
@@ -261,14 +271,12 @@ __device__ __forceinline__ void plan_positions(const PlanLayout& p, int n, int L
 // The positions from the chunks' counts, which become the chunks' own positions.
 __global__ __launch_bounds__(1024) void plan_scan_kernel(const int32_t* __restrict__ offsets, int n, int E, int L,
                                                          int32_t* __restrict__ plan) {
-  __shared__ int chunk0[257];
+  __shared__ int chunk0[257], begin[257];
   const PlanLayout p = plan_layout(n, E, L);
   const int size = chunk_rows(n);
+  load_begins(offsets, E, n, begin);
   int mine = 0;
-  if (threadIdx.x < static_cast<unsigned>(E)) {
-    const int lo = row_begin(offsets, threadIdx.x, n), hi = row_begin(offsets, threadIdx.x + 1, n);
-    mine = hi > lo ? (hi - lo + size - 1) / size : 0;
-  }
+  if (threadIdx.x < static_cast<unsigned>(E)) mine = (begin[threadIdx.x + 1] - begin[threadIdx.x] + size - 1) / size;
   int4 total;
   const int4 at = scan4(make_int4(mine, 0, 0, 0), &total);
   if (threadIdx.x < static_cast<unsigned>(E)) chunk0[threadIdx.x] = at.x;
@@ -372,7 +380,7 @@ __global__ __launch_bounds__(1024) void plan_small_kernel(const int32_t* __restr
   __shared__ uint16_t adapter[kSmallPlan], rank[kSmallPlan];
   const PlanLayout p = plan_layout(n, E, L);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  if (tid <= E) begin[tid] = row_begin(offsets, tid, n);
+  load_begins(offsets, E, n, begin);
   for (int r = tid; r < n; r += 1024) adapter[r] = static_cast<uint16_t>(adapter_of(ids, row_token, r, T, L));
   __syncthreads();
   for (int e = wave; e < E; e += 16) {
@@ -590,7 +598,7 @@ __device__ __forceinline__ void shrink_run(const ShrinkArgs& a, const Tile& t, c
 
 template <int RT, bool DROP>
 __global__ __launch_bounds__(256, RT == 1 && !DROP ? 4 : RT <= 2 ? 3 : RT == 4 ? 2 : 1) void adapter_shrink_kernel(ShrinkArgs a) {
-  __shared__ u32x4 lds[4 * (4 + RT) * 128];   // 2 KiB for 16 rows or ranks; the sums take at most half of it
+  __shared__ u32x4 lds[4 * (4 + RT) * 128];   // 2 KiB for 16 rows or ranks; the sums take at most two thirds of it
   const PlanLayout p = plan_layout(a.rows.n, a.rows.E, a.rows.L);
   const int each = a.S * a.parts, rows_each = kTileRows / a.parts;
   const long long items = static_cast<long long>(n_tiles(a.rows)) * each;

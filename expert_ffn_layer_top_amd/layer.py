@@ -205,6 +205,9 @@ def forward(x, weights, k, logits=None, mxfp8=False, want_probs=False, events=No
         raise ValueError("serving is a form of the block-128 products (fp8b), without recompute")
     if router is not None and (balance_weight is not None or want_probs):
         raise ValueError("balance_weight and want_probs belong to the softmax router, not to a ScoredRouter")
+    for name, drop in (("dropout", dropout), ("adapter_dropout", adapter_dropout)):
+        if drop is not None and type(drop) is not ops.Dropout:
+            raise TypeError(f"{name}: expected an ops.Dropout, got {type(drop).__name__}")
     if (adapters is None) != (adapter_ids is None):
         raise ValueError("adapters and adapter_ids go together")
     if adapter_dropout is not None and adapters is None:

@@ -144,6 +144,13 @@ def test_layer_options(kw, what):
         layer.forward(x, w, 1, logits=torch.zeros(4, 2), **kw)
 
 
+def test_layer_options_of_a_wrong_type():
+    x, w, ad = args()
+    for kw in (dict(dropout=0.1), dict(adapters=ad, adapter_ids=z(4, dt=i32), adapter_dropout=0.1)):
+        with pytest.raises(TypeError, match="Dropout"):
+            layer.forward(x, w, 1, logits=torch.zeros(4, 2), **kw)
+
+
 def test_c_entry_points():
     lib = _lib.lib
     fake, odd = ctypes.c_void_p(0x1000), ctypes.c_void_p(0x1008)

@@ -287,6 +287,28 @@ def test_rows_behind_the_last_expert_are_left_as_they_were(sort):
     assert torch.equal(whole[2][:end], outs["a"][:end])
 
 
+@pytest.mark.parametrize("n", [300, 6000])
+def test_offsets_that_fall_or_lie_outside_are_never_followed(n):
+    """Offsets are the router's; others only the device can see.  Read as their running maximum within [0, n], they still
+    give every row one place."""
+    note(f"adapter bad offsets n={n}")
+    c = make(11, n, 1, 4, 2, 64, 64, 8)
+    for bad in ([0, 250, 40, 2 ** 31 - 1, n], [-5, 7, n + 9, 3, 100], [5, 5, 5, 5, 5], [0, n, 0, n, 0]):
+        eff = np.maximum.accumulate(np.clip(np.array(bad, dtype=np.int64), 0, n))
+        off, tok, ids = i32_to_dev(np.array(bad, dtype=np.int64).astype(np.int32)), i32_to_dev(c["token"]), i32_to_dev(c["ids"])
+        plan = ops().adapter_plan(ids, off, 2, row_token=tok, backward=True)
+        e, l = (torch.from_numpy(v).to(dev()) for v in oracle.row_groups(c["ids"], eff, c["token"], n, 2))
+        y, v = ops().adapter_down(c["t_a"], c["t_y"], plan, c["t_a_down"], c["t_b_down"], c["t_scale"], want_v=True)
+        has = l >= 0
+        v64 = (c["t_a_down"].double()[l.clamp(min=0), e.clamp(min=0)] * c["t_a"].double()[:, None]).sum(2)
+        vmag = (c["t_a_down"].double()[l.clamp(min=0), e.clamp(min=0)] * c["t_a"].double()[:, None]).abs().sum(2)
+        assert bool(((v.double() - v64).abs() <= U * v64.abs() + 64 * 2.0 ** -23 * vmag)[has].all())
+        assert torch.equal(y[~has & (e >= 0)], c["t_y"][~has & (e >= 0)])
+        few = ops().adapter_down(c["t_a"], c["t_y"], ops().adapter_plan(ids, off, 2, row_token=tok), c["t_a_down"], c["t_b_down"], c["t_scale"])
+        torch.cuda.synchronize()
+        assert few[0].shape == y.shape
+
+
 def test_a_bad_row_stays_a_bad_row():
     """NaN and infinities in one row's inputs, and in an adapter that no row has, reach no other row."""
     note("adapter NaN rows")
