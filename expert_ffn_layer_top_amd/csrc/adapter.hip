@@ -74,7 +74,8 @@ __host__ __device__ inline int piece_rows(int n) {
   return want <= 256 ? 256 : want >= 2048 ? 2048 : (want + 31) / 32 * 32;
 }
 
-// Rows of one expert that a workgroup of the sort takes: about 128 workgroups and one for each expert, so that the scan
+// The sort takes 5.6 + 6.1 + 6.3 us for 32768 rows of 64 experts and one adapter, 12 for the scan with 32 adapters.
+// Rows of one expert that a workgroup of it takes: about 128 workgroups and one for each expert, so that the scan
 // over an expert's chunks stays short.
 __host__ __device__ inline int chunk_rows(int n) {
   return ((n + 127) / 128 + kPlanBlock - 1) / kPlanBlock * kPlanBlock;
@@ -372,7 +373,8 @@ __global__ __launch_bounds__(256) void plan_place_kernel(const int32_t* __restri
 }
 
 // The whole plan of up to kSmallPlan rows in one workgroup: a wave walks the rows of one expert after another, 64 at a
-// time, and keeps their adapters and ranks in LDS until the positions are known.
+// time, and keeps their adapters and ranks in LDS until the positions are known.  4012 rows take 12.7 us, a chain of
+// about ten accesses to memory with a barrier after each (in the three kernels of more rows 14.5, and two launches more).
 __global__ __launch_bounds__(1024) void plan_small_kernel(const int32_t* __restrict__ ids, const int32_t* __restrict__ row_token,
                                                           const int32_t* __restrict__ offsets, int T, int n, int E, int L,
                                                           int32_t* __restrict__ plan) {
@@ -380,8 +382,21 @@ __global__ __launch_bounds__(1024) void plan_small_kernel(const int32_t* __restr
   __shared__ uint16_t adapter[kSmallPlan], rank[kSmallPlan];
   const PlanLayout p = plan_layout(n, E, L);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  constexpr int kMine = kSmallPlan / 1024;
+  int token[kMine], mine[kMine];       // all loads at once
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) {
+    const int r = min(tid + 1024 * i, n - 1);
+    token[i] = row_token != nullptr ? row_token[r] : r;
+  }
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) mine[i] = ids[min(max(token[i], 0), T - 1)];
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) {
+    if (token[i] < 0 || token[i] >= T || mine[i] < 0 || mine[i] >= L) mine[i] = L;
+    if (tid + 1024 * i < n) adapter[tid + 1024 * i] = static_cast<uint16_t>(mine[i]);
+  }
   load_begins(offsets, E, n, begin);
-  for (int r = tid; r < n; r += 1024) adapter[r] = static_cast<uint16_t>(adapter_of(ids, row_token, r, T, L));
   __syncthreads();
   for (int e = wave; e < E; e += 16) {
     for (int a = lane; a <= L; a += 64) run[wave][a] = 0;
@@ -406,15 +421,31 @@ __global__ __launch_bounds__(1024) void plan_small_kernel(const int32_t* __restr
       p, n, L, plan, [&](int q) { return plan[p.tile0 + q]; }, [](int, int) {});
   __threadfence_block();
   __syncthreads();
-  for (int r = tid; r < n; r += 1024) {
-    int e = 0, past = E;             // the expert whose rows r is among: the last that begins at or before it
-    while (past - e > 1) {
-      const int mid = (e + past) / 2;
-      if (begin[mid] <= r) e = mid;
-      else past = mid;
-    }
-    if (r < begin[e] || r >= begin[e + 1]) continue;
-    place_row(plan, p, row_token, T, L, r, e, adapter[r], plan[p.goff + e * (L + 1) + adapter[r]] + rank[r]);
+  // the rows' experts (the last that begins at or before each), their groups' positions, and what is written
+  int e[kMine], first[kMine], past[kMine], tile0[kMine];
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) e[i] = 0;
+#pragma unroll
+  for (int step = 128; step > 0; step /= 2)
+#pragma unroll
+    for (int i = 0; i < kMine; ++i)
+      if (e[i] + step < E && begin[e[i] + step] <= tid + 1024 * i) e[i] += step;
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) {
+    const int q = e[i] * (L + 1) + mine[i];
+    first[i] = plan[p.goff + q];
+    past[i] = plan[p.goff + q + 1];
+    tile0[i] = plan[p.tile0 + q];
+  }
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) {
+    const int r = tid + 1024 * i;
+    if (r >= n || r < begin[e[i]] || r >= begin[e[i] + 1]) continue;
+    const int in = rank[r], pos = first[i] + in;
+    plan[p.rows + pos] = r;
+    plan[p.toks + pos] = min(max(token[i], 0), T - 1);
+    if (in % kTileRows == 0)
+      reinterpret_cast<Tile*>(plan + p.tiles)[tile0[i] + in / kTileRows] = Tile{pos, min(kTileRows, past[i] - pos), e[i], mine[i]};
   }
 }
 
@@ -474,7 +505,7 @@ struct ShrinkArgs {
 // Within rows 8 i + r (writes) that depends on i by its lowest bit alone, within rows 16 b + r (reads) not on b.
 __device__ __forceinline__ int staged(int row, int chunk) { return row * 8 + (chunk ^ ((row >> 1) & 7)); }
 
-// One tile (NB blocks of 16 rows) times RT tiles of 16 ranks over K's units of 64 elements u0, u0 + 4, ...  A load takes
+// One tile (NB blocks of 16 rows) times RT tiles of 16 ranks over K's units of 64 elements u0, u0 + STEP, ...  A load takes
 // 8 rows of a whole cache line each; rows go through registers, where they wait for memory while the unit before them
 // is multiplied, into the wave's staging, and come from there as operands.  Rows past the tile and ranks past R are copies
 // of the last one, which nobody stores.
@@ -482,9 +513,9 @@ __device__ __forceinline__ int staged(int row, int chunk) { return row * 8 + (ch
 // What bounds it is memory: 131072 rows of 4096 (1.07 GB) by 32 ranks of 512 matrices take 263 us, and the L2s miss 1.33 GB
 // in that time, 5.0 TB/s; a stream of the same rows alone reaches 5.5 to 6.  Loading fragments without the staging (16
 // rows of 16 bytes in neighbouring lanes) with two units of loads in registers took 282: registers left two waves per
-// SIMD, here there are three (four for 16 ranks, two for 64, one for 128).  A tile's K starting at a
+// SIMD, here there are three (four for 16 ranks without dropout, two for 64, one for 128).  A tile's K starting at a
 // place of its own, so that fewer workgroups read the same columns at once, changed nothing.
-template <int NB, int RT, bool DROP>
+template <int NB, int RT, bool DROP, int STEP = 4>
 __device__ __forceinline__ void shrink_tile(const ShrinkArgs& a, const Tile& t, const PlanLayout& p, const uint16_t* x,
                                             const uint16_t* w, int u0, int u1, u32x4* lds, f32x4 (&acc)[NB][RT]) {
   const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4, lr = lane >> 3, lc = lane & 7;
@@ -544,9 +575,9 @@ __device__ __forceinline__ void shrink_tile(const ShrinkArgs& a, const Tile& t, 
   if (u0 >= u1) return;
   int u = u0;
   load(u);
-  for (; u + 4 < u1; u += 4) {
+  for (; u + STEP < u1; u += STEP) {
     put(u);
-    load(u + 4);
+    load(u + STEP);
     multiply();
   }
   put(u);
@@ -631,7 +662,7 @@ __global__ __launch_bounds__(256, RT == 1 && !DROP ? 4 : RT <= 2 ? 3 : RT == 4 ?
 // and writes the sum, and that is what it costs: SwiGLU of 131072 x 2048 takes 483 us (2.7 GB, 5.6 TB/s), the addition to
 // 131072 x 7168 680 us (3.8 GB, 5.5 TB/s); a copy runs at 4.9.  The loads of the first 16 rows are issued before W's, on
 // whose arrival everything else waits; where a launch has few tiles their rows are shared among up to four waves (4012 rows
-// of 1344: 27 -> 14 us).
+// of 1344: 27 -> 14 us, before one kernel did both products of such calls).
 
 enum { kAdd = 0, kSwiglu = 1, kSwigluBwd = 2 };
 
@@ -730,6 +761,58 @@ __device__ __forceinline__ void load_v(const ExpandArgs& a, long long row, int c
   lo = pack8(f);
 }
 
+// The four rows of a lane: what was read (`in`) and the products' sums -> what is written.  `left`: rows that there are.
+template <int MODE, bool DROP, int NI, int NW>
+__device__ __forceinline__ void expand_store(const ExpandArgs& a, const u32x4 (&in)[4][NI], const f32x4 (&acc)[NW][8],
+                                             const int (&row)[4], int left, bool live, int col, float f, const DropKey& key) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (j >= left || !live) continue;
+    const long long at = static_cast<long long>(row[j]) * a.N + col;
+    float x0[8], x1[8];
+    unpack8(in[j][0], x0);
+    if constexpr (MODE == kAdd) {
+      float delta[8];
+#pragma unroll
+      for (int o = 0; o < 8; ++o) delta[o] = acc[0][o][j];
+      if (DROP) drop_apply(key, row[j], col >> 3, 1.f, delta);
+#pragma unroll
+      for (int o = 0; o < 8; ++o) x0[o] = fmaf(f, delta[o], x0[o]);
+      store16(a.out[0] + at, pack8(x0));
+    } else if constexpr (MODE == kSwiglu) {
+      float y[8];
+      unpack8(in[j][1], x1);
+#pragma unroll
+      for (int o = 0; o < 8; ++o) {
+        x0[o] = fmaf(f, acc[0][o][j], x0[o]);
+        x1[o] = fmaf(f, acc[NW - 1][o][j], x1[o]);
+        y[o] = x0[o] * logistic(x0[o]) * x1[o];
+      }
+      if (a.out[0] != nullptr) {
+        store16(a.out[0] + at, pack8(x0));
+        store16(a.out[1] + at, pack8(x1));
+      }
+      store16(a.out[2] + at, pack8(y));
+    } else {
+      float dg[8], du[8], delta[8];
+      unpack8(in[j][1], x1);
+      unpack8(in[j][2], dg);
+      unpack8(in[j][3], du);
+#pragma unroll
+      for (int o = 0; o < 8; ++o) delta[o] = acc[0][o][j];
+      if (DROP) drop_apply(key, row[j], col >> 3, 1.f, delta);
+#pragma unroll
+      for (int o = 0; o < 8; ++o) {
+        const float s = logistic(x0[o]), da = f * delta[o];
+        dg[o] = fmaf(da * x1[o], s * fmaf(x0[o], 1.f - s, 1.f), dg[o]);
+        du[o] = fmaf(da, x0[o] * s, du[o]);
+      }
+      store16(a.out[0] + at, pack8(dg));
+      store16(a.out[1] + at, pack8(du));
+    }
+  }
+}
+
 template <int KS, int MODE, bool DROP>
 __global__ __launch_bounds__(256, KS == 1 || (KS == 2 && MODE != kSwiglu) ? 2 : 1) void adapter_expand_kernel(ExpandArgs a) {
   constexpr int NW = MODE == kSwiglu ? 2 : 1;
@@ -814,51 +897,124 @@ __global__ __launch_bounds__(256, KS == 1 || (KS == 2 && MODE != kSwiglu) ? 2 : 
           for (int o = 0; o < 8; ++o) acc[m][o] = mfma(hi, wf[m][k][o], acc[m][o]);
         }
       }
+      expand_store<MODE, DROP>(a, in, acc, row, t.count - 16 * b - 4 * q, live, col, f, key);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- both products of a tile's rows
+
+// A workgroup makes v of up to ROWS rows of a tile, which stays in LDS (hi and lo), and then what is added to them: its waves take
+// K's units in turn, then the columns' stripes.  Where few tiles leave the chip idle, what shrink and expand cost is their two
+// launches and the chain of loads in each (4012 rows of 16 experts and 5 adapters, d 2112, f 1344: 18 and 16 us against 8 + 14
+// and 8 + 11).  Loading a wave's first stripe before v is made, so that it is there by then, took 37 us a call where this takes 35.
+// Calls with dropout, which are training's and of more rows, keep to the two kernels.
+constexpr int kBothWaves = 8;
+
+// v = x A^T of a unit's rows, NB blocks of 16, into vs (hi and lo).  The waves' sums meet in LDS, each wave's in its own staging.
+template <int NB, int RT, int ROWS>
+__device__ __forceinline__ void both_shrink(const ShrinkArgs& s, const ExpandArgs& a, const Tile& t, const PlanLayout& p,
+                                            const uint16_t* w, u32x4* lds, uint16_t (&vs)[2][ROWS][16 * RT + 8]) {
+  constexpr int kStage = (ROWS / 16 + RT) * 128;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  u32x4* stage = lds + wave * kStage;
+  f32x4 acc[NB][RT];
+  shrink_tile<NB, RT, false, kBothWaves>(s, t, p, s.x[0], w, wave, s.K / 64, stage, acc);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (16 * b + 4 * q + j >= t.count || !live) continue;
-        const long long at = static_cast<long long>(row[j]) * a.N + col;
-        float x0[8], x1[8];
-        unpack8(in[j][0], x0);
-        if constexpr (MODE == kAdd) {
-          float delta[8];
+  for (int b = 0; b < NB; ++b)
 #pragma unroll
-          for (int o = 0; o < 8; ++o) delta[o] = acc[0][o][j];
-          if (DROP) drop_apply(key, row[j], col >> 3, 1.f, delta);
+    for (int r = 0; r < RT; ++r) reinterpret_cast<f32x4*>(stage)[64 * (b * RT + r) + lane] = acc[b][r];
+  __syncthreads();
+  for (int at = tid; at < 64 * NB * RT; at += 64 * kBothWaves) {
+    f32x4 sum = reinterpret_cast<f32x4*>(lds)[at];
 #pragma unroll
-          for (int o = 0; o < 8; ++o) x0[o] = fmaf(f, delta[o], x0[o]);
-          store16(a.out[0] + at, pack8(x0));
-        } else if constexpr (MODE == kSwiglu) {
-          float y[8];
-          unpack8(in[j][1], x1);
+    for (int o = 1; o < kBothWaves; ++o) sum += reinterpret_cast<f32x4*>(lds + o * kStage)[at];
+    const int rank = at / 64 % RT * 16 + (at & 15), m = at / (64 * RT) * 16 + 4 * (at >> 4 & 3);
 #pragma unroll
-          for (int o = 0; o < 8; ++o) {
-            x0[o] = fmaf(f, acc[0][o][j], x0[o]);
-            x1[o] = fmaf(f, acc[NW - 1][o][j], x1[o]);
-            y[o] = x0[o] * logistic(x0[o]) * x1[o];
-          }
-          if (a.out[0] != nullptr) {
-            store16(a.out[0] + at, pack8(x0));
-            store16(a.out[1] + at, pack8(x1));
-          }
-          store16(a.out[2] + at, pack8(y));
-        } else {
-          float dg[8], du[8], delta[8];
-          unpack8(in[j][1], x1);
-          unpack8(in[j][2], dg);
-          unpack8(in[j][3], du);
+    for (int j = 0; j < 4; ++j) {
+      split_bf16(rank < s.R ? sum[j] : 0.f, vs[0][m + j][rank], vs[1][m + j][rank]);
+      if (a.v_out != nullptr && rank < s.R && m + j < t.count)
+        a.v_out[static_cast<long long>(row_at(a.rows, p, t.pos + m + j)) * a.ldv + rank] = vs[0][m + j][rank];
+    }
+  }
+  __syncthreads();
+}
+
+template <int RT, int MODE, int ROWS>
+__global__ __launch_bounds__(64 * kBothWaves) void adapter_both_kernel(ShrinkArgs s, ExpandArgs a) {
+  constexpr int NW = MODE == kSwiglu ? 2 : 1, NOUT = MODE == kSwiglu ? 3 : 1, KS = (16 * RT / NW + 31) / 32, NI = NW;
+  __shared__ u32x4 lds[kBothWaves * (ROWS / 16 + RT) * 128];
+  __shared__ alignas(16) uint16_t vs[2][ROWS][16 * RT + 8];     // (rows in different banks)
+  const PlanLayout p = plan_layout(a.rows.n, a.rows.E, a.rows.L);
+  const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int stripes = (a.N + 127) / 128;
+  constexpr int kParts = kTileRows / ROWS;
+  const long long items = static_cast<long long>(n_tiles(a.rows)) * kParts;
+  for (long long i = blockIdx.x; i < items; i += gridDim.x) {
+    Tile t = tile_at(a.rows, p, static_cast<int>(i / kParts));
+    const int first = static_cast<int>(i % kParts) * ROWS;
+    t.pos += first;
+    t.count = min(t.count - first, ROWS);
+    if (t.count <= 0) continue;
+    if (t.l >= a.rows.L) {              // no adapter: copies
+      const int chunks = a.N / 8;
+      for (int at = tid; at < t.count * chunks; at += 64 * kBothWaves) {
+        const long long to = static_cast<long long>(row_at(a.rows, p, t.pos + at / chunks)) * a.N + at % chunks * 8;
 #pragma unroll
-          for (int o = 0; o < 8; ++o) delta[o] = acc[0][o][j];
-          if (DROP) drop_apply(key, row[j], col >> 3, 1.f, delta);
+        for (int o = 0; o < NOUT; ++o)
+          if (a.out[o] != nullptr) store16(a.out[o] + to, load16(a.in[o] + to));
+      }
+      if (a.v_out != nullptr)
+        for (int at = tid; at < t.count * a.ldv; at += 64 * kBothWaves)
+          a.v_out[static_cast<long long>(row_at(a.rows, p, t.pos + at / a.ldv)) * a.ldv + at % a.ldv] = 0;
+      continue;
+    }
+    const long long group = static_cast<long long>(t.l) * a.rows.E + t.e;
+    const int nb = (t.count + 15) / 16;
+    const uint16_t* w = s.w[0] + group * s.R * s.K;
+    if (ROWS == 16 || nb == 1) both_shrink<1, RT, ROWS>(s, a, t, p, w, lds, vs);
+    else if (ROWS == 32 || nb == 2) both_shrink<2, RT, ROWS>(s, a, t, p, w, lds, vs);
+    else both_shrink<ROWS / 16, RT, ROWS>(s, a, t, p, w, lds, vs);
+    const float f = a.scale[t.l];
+    for (int stripe = wave; stripe < stripes; stripe += kBothWaves) {
+      const int col = 128 * stripe + 8 * c;
+      const bool live = col < a.N;        // the last stripe may be half
+      const int cc = live ? col : 0;
+      u32x4 in[4][NI], wf[NW][KS][8];
+      int row[4];
+      auto load_rows = [&](int b) {
+        const int mine = row_at(a.rows, p, t.pos + min(16 * b + c, t.count - 1));
 #pragma unroll
-          for (int o = 0; o < 8; ++o) {
-            const float s = logistic(x0[o]), da = f * delta[o];
-            dg[o] = fmaf(da * x1[o], s * fmaf(x0[o], 1.f - s, 1.f), dg[o]);
-            du[o] = fmaf(da, x0[o] * s, du[o]);
-          }
-          store16(a.out[0] + at, pack8(dg));
-          store16(a.out[1] + at, pack8(du));
+        for (int j = 0; j < 4; ++j) {
+          row[j] = __shfl(mine, 4 * q + j, 64);
+#pragma unroll
+          for (int o = 0; o < NI; ++o) in[j][o] = load16(a.in[o] + static_cast<long long>(row[j]) * a.N + cc);
         }
+        __builtin_amdgcn_sched_barrier(0);
+      };
+      load_rows(0);
+#pragma unroll
+      for (int m = 0; m < NW; ++m) load_w<KS>(a.w[m] + group * a.R * a.N, a.R, a.N, cc, wf[m]);
+      for (int b = 0; b < nb; ++b) {
+        if (b > 0) load_rows(b);
+        f32x4 acc[NW][8];
+#pragma unroll
+        for (int m = 0; m < NW; ++m) {
+#pragma unroll
+          for (int o = 0; o < 8; ++o) acc[m][o] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+            const int rank = 32 * k + 8 * q;
+#pragma unroll
+            for (int h = 1; h >= 0; --h) {
+              const u32x4 v = rank < a.R ? *reinterpret_cast<const u32x4*>(&vs[h][16 * b + c][m * a.R + rank]) : u32x4{0, 0, 0, 0};
+#pragma unroll
+              for (int o = 0; o < 8; ++o) acc[m][o] = mfma(v, wf[m][k][o], acc[m][o]);
+            }
+          }
+        }
+        expand_store<MODE, false>(a, in, acc, row, t.count - 16 * b - 4 * q, live, col, f, DropKey{});
       }
     }
   }
@@ -1286,6 +1442,35 @@ void launch_expand(ExpandArgs a, hipStream_t st) {
   else if constexpr (MODE == kAdd) adapter_expand_kernel<4, MODE, DROP><<<grid, 256, 0, st>>>(a);
 }
 
+// Rows of a workgroup's unit where one kernel makes v and what is added (adapter_both_kernel), 0 where two kernels do.  It
+// pays where the units fit the chip at once, a workgroup to a compute unit, parts of tiles without rows included; units are as small as
+// that allows.  Past that, only where tiles have few rows: there its matrices are its time, and two kernels wait for them
+// twice.  Gate/up, down and the plan, two kernels -> one, us: 16 experts x 5 adapters of 8 ranks (d 2112, f 1344), 1024 rows 50 ->
+// 32 (with 32 or 64 rows 37 and 41), 4096 52 -> 46 (16 rows 53, 64 rows 61), 8192 71 -> 69, 16384 113 -> 141; 64 x 8 of 16 (d 2048, f
+// 1024), 4096 rows 73 -> 66, 16384 143 -> 128, 65536 (46 rows a tile) 325 -> 336; 64 x 32 of 32, 1024 rows 121 -> 109, 16384 283 ->
+// 270, 65536 478 -> 475; 128 x 16 of 32 (d 4096, f 768), 1024 rows 126 -> 117, 16384 330 -> 336, 65536 612 -> 636.
+int both_rows(const Rows& r, int R) {
+  if (R > 64) return 0;
+  const long long tiles = likely_tiles(r.n, r.E, r.L), rows = r.n / tiles, groups = tiles - r.n / kTileRows;
+  if (rows > 8 && 4 * tiles <= 288 && r.n / 16 + groups <= 256) return 16;
+  if (rows > 32 && 2 * tiles <= 288 && r.n / 32 + groups <= 256) return 32;
+  return tiles <= 256 || (rows <= 32 && tiles <= 1280) ? 64 : 0;
+}
+
+template <int MODE, int ROWS>
+void launch_both_of(const ShrinkArgs& s, const ExpandArgs& e, hipStream_t st) {
+  const unsigned grid = grid_of(static_cast<long long>(kTileRows / ROWS) * tiles_cap(e.rows));
+  if (s.R <= 16) adapter_both_kernel<1, MODE, ROWS><<<grid, 64 * kBothWaves, 0, st>>>(s, e);
+  else if (s.R <= 32) adapter_both_kernel<2, MODE, ROWS><<<grid, 64 * kBothWaves, 0, st>>>(s, e);
+  else adapter_both_kernel<4, MODE, ROWS><<<grid, 64 * kBothWaves, 0, st>>>(s, e);
+}
+template <int MODE>
+void launch_both(int rows, const ShrinkArgs& s, const ExpandArgs& e, hipStream_t st) {
+  if (rows == 16) launch_both_of<MODE, 16>(s, e, st);
+  else if (rows == 32) launch_both_of<MODE, 32>(s, e, st);
+  else launch_both_of<MODE, 64>(s, e, st);
+}
+
 template <int MODE, bool DROP>
 void launch_rows(const RowArgs& a, hipStream_t st) {
   constexpr int W = kRowThreads / 64;
@@ -1457,10 +1642,16 @@ extern "C" int moe_adapter_gate_up(const uint16_t* x, const int32_t* ids, const 
   float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + 2 * v_bytes(n, 2 * r));
   const int S = slices(n, E, L, d);
   ShrinkArgs s = {rows, {x, nullptr}, {a_gu, nullptr}, {0, 0}, 1, d, 2 * r, 2 * r, S, 1, nullptr, vbuf, lo, part, drop};
-  if (drop.drop) launch_shrink<true>(s, 1, st);
-  else launch_shrink<false>(s, 1, st);
   ExpandArgs e = {rows, vbuf, lo, part, 2 * r, S, r, f, 1, {b_gate, b_up}, scale, {g, u, a, nullptr}, {g_out, u_out, a_out},
                   S > 1 ? v : nullptr, nullptr, DropArgs{}};
+  const int both = drop.drop == 0 ? both_rows(rows, 2 * r) : 0;
+  if (both) {
+    e.v_out = v;
+    launch_both<kSwiglu>(both, s, e, st);
+    return check_launch("adapter_gate_up");
+  }
+  if (drop.drop) launch_shrink<true>(s, 1, st);
+  else launch_shrink<false>(s, 1, st);
   launch_expand<kSwiglu, false>(e, st);
   return check_launch("adapter_gate_up");
 }
@@ -1493,10 +1684,16 @@ extern "C" int moe_adapter_down(const uint16_t* a, const int32_t* ids, const int
   float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + 2 * v_bytes(n, r));
   const int S = slices(n, E, L, f);
   ShrinkArgs s = {rows, {a, nullptr}, {a_down, nullptr}, {0, 0}, 0, f, r, r, S, 1, nullptr, vbuf, lo, part, drop};
-  if (drop.drop) launch_shrink<true>(s, 1, st);
-  else launch_shrink<false>(s, 1, st);
   ExpandArgs e = {rows, vbuf, lo, part, r, S, r, d, 1, {b_down, nullptr}, scale, {yexp, nullptr, nullptr, nullptr},
                   {y_out, nullptr, nullptr}, S > 1 ? v : nullptr, nullptr, DropArgs{}};
+  const int both = drop.drop == 0 ? both_rows(rows, r) : 0;
+  if (both) {
+    e.v_out = v;
+    launch_both<kAdd>(both, s, e, st);
+    return check_launch("adapter_down");
+  }
+  if (drop.drop) launch_shrink<true>(s, 1, st);
+  else launch_shrink<false>(s, 1, st);
   launch_expand<kAdd, false>(e, st);
   return check_launch("adapter_down");
 }
