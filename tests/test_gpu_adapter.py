@@ -192,6 +192,27 @@ def test_backward(T, k, E, L, d, f, r, ids):
     check_backward(c, plan_of(c, True))
 
 
+# (T, E, L, d, f): both products in one kernel by 16, 32 and 64 rows (full tiles, tiles of few rows), with more stripes of
+# columns than it has waves, and in two kernels
+FORMS = [(700, 4, 3, 64, 192), (150, 1, 2, 1088, 64), (90, 2, 1, 64, 1216), (5000, 4, 3, 64, 64), (9000, 2, 3, 64, 64),
+         (600, 16, 16, 64, 64), (3000, 30, 20, 64, 64), (17000, 1, 1, 64, 64)]
+
+
+@pytest.mark.parametrize("r", [8, 16, 24, 32, 64])
+@pytest.mark.parametrize("T,E,L,d,f", FORMS)
+def test_every_form_of_the_sorted_forward(T, E, L, d, f, r):
+    note(f"adapter forms {T} {E} {L} {d} {f} {r}")
+    c = make(12, T, 1, E, L, d, f, r)
+    check_forward(c, plan_of(c, True))
+
+
+@pytest.mark.parametrize("r", [8, 16, 24, 32, 64])
+def test_dropout_at_every_rank(r):
+    note(f"adapter dropout r={r}")
+    c = make(13, 150, 2, 3, 2, 192, 128, r)
+    check_forward(c, plan_of(c, True), p=0.25)
+
+
 @pytest.mark.parametrize("sort", [False, True], ids=["few", "sorted"])
 def test_dropout_of_the_inputs(sort):
     note(f"adapter dropout sorted={sort}")
