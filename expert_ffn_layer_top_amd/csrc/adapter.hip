@@ -1402,20 +1402,15 @@ int row_parts(int n, long long tiles, long long want) {
 }
 
 // How the shrink's work is cut beyond tiles, to have workgroups enough for the chip: rows first (the matrices are read
-// again, from the second-level cache), then K into slices, each with a unit for every wave.
-struct Cut {
-  int parts, slices;
-};
-Cut shrink_cut(int n, int E, int L, int K) {
-  const long long tiles = likely_tiles(n, E, L);
-  Cut c = {row_parts(n, tiles, 1024), 1};
+// again, from the second-level cache), then K into slices, each with a unit for every wave.  Two products in a launch are twice
+// the workgroups (32768 rows of 64 experts, dG and dU of 1024: 31 us in whole tiles, 36 in halves).
+int shrink_parts(int n, int E, int L, int products) { return row_parts(n, likely_tiles(n, E, L), 1024 / products); }
+int slices(int n, int E, int L, int K) {
   const int most = (K / 64 + 3) / 4;
-  const long long want = 512 / (tiles * c.parts);
-  c.slices = want < 1 ? 1 : want > 8 ? 8 : static_cast<int>(want);
-  if (c.slices > most) c.slices = most;
-  return c;
+  const long long want = 512 / (likely_tiles(n, E, L) * shrink_parts(n, E, L, 1));
+  const int s = want < 1 ? 1 : want > 8 ? 8 : static_cast<int>(want);
+  return s > most ? most : s;
 }
-int slices(int n, int E, int L, int K) { return shrink_cut(n, E, L, K).slices; }
 
 unsigned grid_of(long long workgroups) {
   return static_cast<unsigned>(workgroups < kGridCap ? (workgroups + 7) / 8 * 8 : kGridCap);
@@ -1423,7 +1418,7 @@ unsigned grid_of(long long workgroups) {
 
 template <bool DROP>
 void launch_shrink(ShrinkArgs a, int products, hipStream_t st) {
-  a.parts = shrink_cut(a.rows.n, a.rows.E, a.rows.L, a.K).parts;
+  a.parts = shrink_parts(a.rows.n, a.rows.E, a.rows.L, products);
   const dim3 grid(grid_of(static_cast<long long>(tiles_cap(a.rows)) * a.S * a.parts), products);
   if (a.R <= 16) adapter_shrink_kernel<1, DROP><<<grid, 256, 0, st>>>(a);
   else if (a.R <= 32) adapter_shrink_kernel<2, DROP><<<grid, 256, 0, st>>>(a);
