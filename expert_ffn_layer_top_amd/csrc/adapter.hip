@@ -851,14 +851,12 @@ __global__ __launch_bounds__(256, KS == 1 || (KS == 2 && MODE != kSwiglu) ? 2 : 
     }
     // the first 16 rows' loads before the matrices', on whose arrival everything else waits
     constexpr int NI = MODE == kAdd ? 1 : MODE == kSwiglu ? 2 : 4;
-    int mine, row[4];
+    const int all = row_at(a.rows, p, t.pos + min(lane, t.count - 1));    // the tile's rows, one a lane
     u32x4 in[4][NI];
     auto load_rows = [&](int b) {
-      mine = row_at(a.rows, p, t.pos + min(16 * b + c, t.count - 1));
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        row[j] = __shfl(mine, 4 * q + j, 64);
-        const long long at = static_cast<long long>(row[j]) * a.N + cc;
+        const long long at = static_cast<long long>(__shfl(all, 16 * b + 4 * q + j, 64)) * a.N + cc;
 #pragma unroll
         for (int o = 0; o < NI; ++o) in[j][o] = load16(a.in[o] + at);
       }
@@ -874,6 +872,10 @@ __global__ __launch_bounds__(256, KS == 1 || (KS == 2 && MODE != kSwiglu) ? 2 : 
     const int nb = (t.count + 15) / 16;
     for (int b = 0; b < nb; ++b) {
       if (b > 0) load_rows(b);
+      const int mine = __shfl(all, 16 * b + c, 64);
+      int row[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) row[j] = __shfl(all, 16 * b + 4 * q + j, 64);
       f32x4 acc[NW][8];
 #pragma unroll
       for (int m = 0; m < NW; ++m) {
@@ -971,7 +973,7 @@ __global__ __launch_bounds__(64 * kBothWaves) void adapter_both_kernel(ShrinkArg
       continue;
     }
     const long long group = static_cast<long long>(t.l) * a.rows.E + t.e;
-    const int nb = (t.count + 15) / 16;
+    const int nb = (t.count + 15) / 16, all = row_at(a.rows, p, t.pos + min(lane, t.count - 1));
     const uint16_t* w = s.w[0] + group * s.R * s.K;
     if (ROWS == 16 || nb == 1) both_shrink<1, RT, ROWS>(s, a, t, p, w, lds, vs);
     else if (ROWS == 32 || nb == 2) both_shrink<2, RT, ROWS>(s, a, t, p, w, lds, vs);
@@ -984,10 +986,9 @@ __global__ __launch_bounds__(64 * kBothWaves) void adapter_both_kernel(ShrinkArg
       u32x4 in[4][NI], wf[NW][KS][8];
       int row[4];
       auto load_rows = [&](int b) {
-        const int mine = row_at(a.rows, p, t.pos + min(16 * b + c, t.count - 1));
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          row[j] = __shfl(mine, 4 * q + j, 64);
+          row[j] = __shfl(all, 16 * b + 4 * q + j, 64);
 #pragma unroll
           for (int o = 0; o < NI; ++o) in[j][o] = load16(a.in[o] + static_cast<long long>(row[j]) * a.N + cc);
         }
