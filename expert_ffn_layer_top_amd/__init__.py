@@ -1,6 +1,7 @@
 """MoE expert-FFN layer hot path for MI355X (gfx950): router top-k (softmax, or scored with a
 balance bias and expert groups), device-resident routing metadata, rowwise permute,
-device-scheduled grouped GEMM SwiGLU experts in bf16, MXFP8 and block-128 E4M3, weighted unpermute-combine, and the backward, as hand-written HIP kernels behind a C ABI
+device-scheduled grouped GEMM SwiGLU experts in bf16, MXFP8 and block-128 E4M3, low-rank adapters of many requests beside
+them, weighted unpermute-combine (with dropout and a residual), and the backward, as hand-written HIP kernels behind a C ABI
 (include/moe_mi355x.h).
 
   ops    thin torch wrappers of every C entry point (marshalling only)

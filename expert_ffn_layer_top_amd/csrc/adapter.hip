@@ -10,19 +10,19 @@
 //   expand   y[row][C]  += s v[row][R] W       contracts over the rank:     B v, and A^T dv in the backward
 //   wgrad    dW[R][C]    = v^T y               contracts over the rows of one adapter and expert
 // B is stored by rank like A ([R][out]), so each of them serves A and B.  All three move far more bytes than
-// the matrix cores need time for (R operations per byte of x or y), so they are built as streams: operands go
-// straight from memory into the fragments of v_mfma_f32_16x16x32_bf16, without LDS, and what the fragments would
-// have transposed is permuted in registers (expand, wgrad: a lane loads 16 bytes of each of 8 rows along the
-// contraction; the 8 columns that it holds become 8 column tiles, of which tile i takes column 8 c + i from lane
-// c, so its accumulators hold 8 neighbouring columns and leave as 16-byte stores).
+// the matrix cores need time for (R operations per byte of x or y), so they are built as streams for
+// v_mfma_f32_16x16x32_bf16.  Shrink stages whole cache lines of x and W in LDS.  In expand and wgrad the long operands
+// go straight from memory into fragments, and what those would have transposed is permuted in registers: a lane loads 16
+// bytes of each of 8 rows along the contraction; the 8 columns that it holds become 8 column tiles, of which tile i takes
+// column 8 c + i from lane c, so its accumulators hold 8 neighbouring columns and leave as 16-byte stores.
 //
 // Between its two products v is held as the sum of two bf16 values, hi (what is handed out as v) and lo (what hi lacks):
 // 16 bits of mantissa for one more MFMA each, where bf16 alone made the gradients 1.6 times less exact than
 // their own rounding does.
 //
 // Rows are taken in tiles of up to 64 rows of one expert and adapter, from a list that adapter_plan makes on the
-// device by a stable sort of each expert's rows by adapter, so sums run in a fixed order.  For few rows there is no
-// list, and one kernel does both products of a row.
+// device by a stable sort of each expert's rows by adapter, so sums run in a fixed order.  Where tiles are few or small,
+// one kernel makes v and what is added; for few rows there is no list, and one kernel does both products of a row.
 #include <hip/hip_runtime.h>
 
 #include "common.h"
@@ -67,7 +67,7 @@ __device__ __forceinline__ void wave_fence() {
 
 // Rows of one piece of a group's contraction in the weight gradients: pieces enough for the chip where few
 // groups hold the rows, long enough that their fp32 partial sums (2 R C 4 bytes each) stay a fraction of the
-// rows' own bytes.  A 32nd of the rows: the backward of 32768 rows of 64 experts takes 363 us, 387 with a 64th (most experts
+// rows' own bytes.  A 32nd of the rows: the backward of 32768 rows of 64 experts took 363 us, 387 with a 64th (most experts
 // then have two pieces), and that of 32768 rows of one expert, wider, 703 and 745.
 __host__ __device__ inline int piece_rows(int n) {
   const int want = (n + 31) / 32;
@@ -660,7 +660,7 @@ __global__ __launch_bounds__(256, RT == 1 && !DROP ? 4 : RT <= 2 ? 3 : RT == 4 ?
 //
 // A wave takes 16 rows after another of a tile and 128 columns, for which it holds W's fragments.  It reads what it adds to
 // and writes the sum, and that is what it costs: SwiGLU of 131072 x 2048 takes 483 us (2.7 GB, 5.6 TB/s), the addition to
-// 131072 x 7168 680 us (3.8 GB, 5.5 TB/s); a copy runs at 4.9.  The loads of the first 16 rows are issued before W's, on
+// 131072 x 7168 674 us (3.8 GB, 5.5 TB/s); a copy runs at 4.9.  The loads of the first 16 rows are issued before W's, on
 // whose arrival everything else waits; where a launch has few tiles their rows are shared among up to four waves (4012 rows
 // of 1344: 27 -> 14 us, before one kernel did both products of such calls).
 
@@ -908,7 +908,7 @@ __global__ __launch_bounds__(256, KS == 1 || (KS == 2 && MODE != kSwiglu) ? 2 : 
 
 // A workgroup makes v of up to ROWS rows of a tile, which stays in LDS (hi and lo), and then what is added to them: its waves take
 // K's units in turn, then the columns' stripes.  Where few tiles leave the chip idle, what shrink and expand cost is their two
-// launches and the chain of loads in each (4012 rows of 16 experts and 5 adapters, d 2112, f 1344: 18 and 16 us against 8 + 14
+// launches and the chain of loads in each (4012 rows of 16 experts and 5 adapters, d 2112, f 1344: 17 and 15 us against 8 + 14
 // and 8 + 11).  Loading a wave's first stripe before v is made, so that it is there by then, took 37 us a call where this takes 35.
 // Calls with dropout, which are training's and of more rows, keep to the two kernels.
 constexpr int kBothWaves = 8;
@@ -1024,10 +1024,10 @@ __global__ __launch_bounds__(64 * kBothWaves) void adapter_both_kernel(ShrinkArg
 // ---------------------------------------------------------------- few rows
 
 // Both products of one row in a workgroup, without a plan: what few rows cost is the chain of loads that hang on each
-// other (token, adapter, matrices) and the launches, not bytes.  One token's 8 rows (d 4096, f 768, rank 16) take 10 us and 6
-// us (down), and a whole call 11 us of the host's time; as shrink and expand they took 14, 10 and 18 us.  A wave takes RW ranks of A along whole cache lines, v meets in
-// LDS as fp32, and then a lane takes 8 columns of B for all ranks; the first 8 ranks of B, and the row's own values,
-// are on their way while A is read.  Products and sums are fp32 FMAs.
+// other (token, adapter, matrices) and the launches, not bytes.  One token's 8 rows (d 4096, f 768, rank 16) take 10 us and
+// 6 us (down), and a whole call 11 us of the host's time; as shrink and expand they took 14, 10 and 18 us.  A wave takes RW
+// ranks of A along whole cache lines, v meets in LDS as fp32, and then a lane takes 8 columns of B for all ranks; the first
+// 8 ranks of B, and the row's own values, are on their way while A is read.  Products and sums are fp32 FMAs.
 struct RowArgs {
   Rows rows;
   const uint16_t* x;

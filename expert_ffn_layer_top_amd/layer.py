@@ -149,7 +149,7 @@ QUANT_CALLS_FWD = ("quant_a",)
 QUANT_CALLS = ("quant_dg", "quant_du", "quant_dyT", "quant_xT")
 # (block-128: "quant_dy" gives dYexp's row blocks and token blocks from one read, in place of quant_dyT)
 ROW_CALLS = ("route", "permute", "combine", "combine_bwd", "permute_bwd", "route_bwd")
-# (with adapters: the plan, two kernels for each forward call, four to seven for each backward one)
+# (with adapters: the plan, one or two kernels for each forward call, four to seven for each backward one)
 ADAPTER_CALLS = ("adapter_plan", "adapter_gate_up", "adapter_down", "adapter_down_bwd", "adapter_gate_up_bwd")
 # MXFP8: each expert's rows start at a multiple of MX_PAD on the padded token axis of the
 # weight-gradient operands.  128 = one K step of those products: every step's 128-byte piece of an
