@@ -16,9 +16,10 @@
 // bytes of each of 8 rows along the contraction; the 8 columns that it holds become 8 column tiles, of which tile i takes
 // column 8 c + i from lane c, so its accumulators hold 8 neighbouring columns and leave as 16-byte stores.
 //
-// Between its two products v is held as the sum of two bf16 values, hi (what is handed out as v) and lo (what hi lacks):
-// 16 bits of mantissa for one more MFMA each, where bf16 alone made the gradients 1.6 times less exact than
-// their own rounding does.
+// Between its two products v is held in fp32, and goes into the second one as the sum of three bf16 values, each what those
+// before it lack: 24 bits of mantissa, all that fp32 has.  With two of them (16 bits) 4 to 15 times as many results differ from the
+// rounded 64-bit ones (4012 rows of d 2112, f 1344: 2.0e-3 of a' against 1.2e-4, 7.7e-3 of y' against 5.0e-4), for a
+// percent or two: training forward of 131072 rows 1686 us against 1704, backward of 32768 359 and 368, of 131072 1940 and 1921.
 //
 // Rows are taken in tiles of up to 64 rows of one expert and adapter, from a list that adapter_plan makes on the
 // device by a stable sort of each expert's rows by adapter, so sums run in a fixed order.  Where tiles are few or small,
@@ -49,12 +50,9 @@ __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
 __device__ __forceinline__ u32x4 load16(const uint16_t* p) { return *reinterpret_cast<const u32x4*>(p); }
 __device__ __forceinline__ void store16(uint16_t* p, u32x4 v) { *reinterpret_cast<u32x4*>(p) = v; }
 
-// x = hi + lo up to 2^-17 of it; lo is 0 where hi is not finite.
-__device__ __forceinline__ float lo_of(float x, float hi) { return __builtin_isfinite(hi) ? x - hi : 0.f; }
-__device__ __forceinline__ void split_bf16(float x, uint16_t& hi, uint16_t& lo) {
-  hi = f32_to_bf16(x);
-  lo = f32_to_bf16(lo_of(x, bf16_to_f32(hi)));
-}
+// x = hi + mid + lo, three bf16 values (two rounded remainders of 24 bits leave at most 8); mid and lo are 0 where hi is not finite.
+__device__ __forceinline__ float lack(float x, float hi) { return __builtin_isfinite(hi) ? x - hi : 0.f; }
+constexpr int kSplit = 3;
 
 // A wave's own LDS accesses keep their order; this keeps the compiler from changing it.
 __device__ __forceinline__ void wave_fence() {
@@ -491,12 +489,11 @@ struct ShrinkArgs {
   const uint16_t* w[2];
   int v0[2];               // their first columns in v
   int gather;              // x by token (through row_token)
-  int K, R, ldv, S;        // S > 1: slices of K whose fp32 sums go to part [S][n][ldv]
+  int K, R, ldv, S;        // slices of K
   int parts;               // a tile's rows are shared among this many workgroups (1, 2 or 4)
   const float* scale;      // null, or [L]: factor of v
-  uint16_t* v;             // hi and lo [n][ldv]
-  uint16_t* vlo;
-  float* part;
+  float* part;             // v [S][n][ldv], the sums of the slices
+  uint16_t* v;             // [n][ldv], or null: v rounded, where there is one slice
   DropArgs drop;
 };
 
@@ -618,10 +615,8 @@ __device__ __forceinline__ void shrink_run(const ShrinkArgs& a, const Tile& t, c
       for (int j = 0; j < 4; ++j) {
         if (m + j >= t.count) break;
         const long long r = row_at(a.rows, p, t.pos + m + j);
-        if (a.S > 1)
-          a.part[(static_cast<long long>(slice) * a.rows.n + r) * a.ldv + a.v0[which] + rank] = f * s[j];
-        else
-          split_bf16(f * s[j], a.v[r * a.ldv + a.v0[which] + rank], a.vlo[r * a.ldv + a.v0[which] + rank]);
+        a.part[(static_cast<long long>(slice) * a.rows.n + r) * a.ldv + a.v0[which] + rank] = f * s[j];
+        if (a.v != nullptr && a.S == 1) a.v[r * a.ldv + a.v0[which] + rank] = f32_to_bf16(f * s[j]);
       }
     }
   }
@@ -641,12 +636,10 @@ __global__ __launch_bounds__(256, RT == 1 && !DROP ? 4 : RT <= 2 ? 3 : RT == 4 ?
     t.pos += first;
     t.count = min(t.count - first, rows_each);
     if (t.count <= 0) continue;
-    if (t.l >= a.rows.L) {   // no adapter: v is 0 (with slices, expand writes that)
-      if (a.S == 1)
-        for (int at = threadIdx.x; at < t.count * a.R; at += 256) {
-          const long long to = static_cast<long long>(row_at(a.rows, p, t.pos + at / a.R)) * a.ldv + a.v0[which] + at % a.R;
-          a.v[to] = a.vlo[to] = 0;
-        }
+    if (t.l >= a.rows.L) {   // no adapter: v is 0 (with slices, expand writes that), and nobody reads it here
+      if (a.v != nullptr && a.S == 1)
+        for (int at = threadIdx.x; at < t.count * a.R; at += 256)
+          a.v[static_cast<long long>(row_at(a.rows, p, t.pos + at / a.R)) * a.ldv + a.v0[which] + at % a.R] = 0;
       continue;
     }
     const int nb = (t.count + 15) / 16;
@@ -668,17 +661,15 @@ enum { kAdd = 0, kSwiglu = 1, kSwigluBwd = 2 };
 
 struct ExpandArgs {
   Rows rows;
-  const uint16_t* v;        // hi and lo [n][ldv], or part [S][n][ldv]
-  const uint16_t* vlo;
-  const float* part;
+  const float* part;        // v [S][n][ldv], as shrink left it
   int ldv, S, R, N;         // R: ranks of one product
   int parts;                // a tile's rows are shared among this many waves (1, 2 or 4)
   const uint16_t* w[2];     // kSwiglu: gate and up (v's columns [0, R) and [R, 2 R))
   const float* scale;       // null, or [L]
   const uint16_t* in[4];    // kAdd: y; kSwiglu: g, u, a; kSwigluBwd: g, u, dg, du
   uint16_t* out[3];         // kAdd: y; kSwiglu: g, u (or null), a; kSwigluBwd: dg, du
-  uint16_t* v_out;          // with slices: hi and lo, where they are wanted
-  uint16_t* vlo_out;
+  uint16_t* v_out;          // with slices: v rounded, and in fp32, where they are wanted
+  float* sum_out;
   DropArgs drop;
 };
 
@@ -724,17 +715,20 @@ __device__ __forceinline__ void load_w(const uint16_t* w, int R, int N, int col,
   }
 }
 
-// 8 ranks of one row of v, hi and lo; from slices: of their fp32 sums in slice order.
-__device__ __forceinline__ void load_v(const ExpandArgs& a, long long row, int col, u32x4& hi, u32x4& lo) {
+// 8 ranks of one row of v: the slices' sums in their order.
+__device__ __forceinline__ void load_v(const ExpandArgs& a, long long row, int col, float (&f)[8]) {
+  const float* at = a.part + row * a.ldv + col;
   if (a.S == 1) {
-    hi = load16(a.v + row * a.ldv + col);
-    lo = load16(a.vlo + row * a.ldv + col);
+    const f32x4 x = *reinterpret_cast<const f32x4*>(at), y = *reinterpret_cast<const f32x4*>(at + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[i] = x[i];
+      f[4 + i] = y[i];
+    }
     return;
   }
-  float f[8], h[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) f[i] = 0.f;
-  const float* at = a.part + row * a.ldv + col;
   const long long step = static_cast<long long>(a.rows.n) * a.ldv;
   for (int s = 0; s < a.S; s += 4) {       // four slices' loads in flight; past the last one it is read again and not added
     f32x4 x[4], y[4];
@@ -754,11 +748,18 @@ __device__ __forceinline__ void load_v(const ExpandArgs& a, long long row, int c
       }
     }
   }
-  hi = pack8(f);
-  unpack8(hi, h);
+}
+
+// The three bf16 values of 8 ranks, the smallest last.
+__device__ __forceinline__ void split8(float (&f)[8], u32x4 (&v)[kSplit]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = lo_of(f[i], h[i]);
-  lo = pack8(f);
+  for (int h = 0; h < kSplit; ++h) {
+    float g[8];
+    v[h] = pack8(f);
+    unpack8(v[h], g);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = lack(f[i], g[i]);
+  }
 }
 
 // The four rows of a lane: what was read (`in`) and the products' sums -> what is written.  `left`: rows that there are.
@@ -835,11 +836,8 @@ __global__ __launch_bounds__(256, KS == 1 || (KS == 2 && MODE != kSwiglu) ? 2 : 
     const int cc = live ? col : 0;
     if (t.l >= a.rows.L) {              // no adapter: copies
       if (a.v_out != nullptr && stripe == 0)
-        for (int at = lane; at < t.count * a.ldv; at += 64) {
-          const long long to = static_cast<long long>(row_at(a.rows, p, t.pos + at / a.ldv)) * a.ldv + at % a.ldv;
-          a.v_out[to] = 0;
-          if (a.vlo_out != nullptr) a.vlo_out[to] = 0;
-        }
+        for (int at = lane; at < t.count * a.ldv; at += 64)
+          a.v_out[static_cast<long long>(row_at(a.rows, p, t.pos + at / a.ldv)) * a.ldv + at % a.ldv] = 0;
       for (int m = q; m < t.count; m += 4) {
         const long long at = static_cast<long long>(row_at(a.rows, p, t.pos + m)) * a.N + cc;
 #pragma unroll
@@ -884,19 +882,24 @@ __global__ __launch_bounds__(256, KS == 1 || (KS == 2 && MODE != kSwiglu) ? 2 : 
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
           const int rank = 32 * k + 8 * q;
-          u32x4 hi = u32x4{0, 0, 0, 0}, lo = hi;
+          float x[8] = {};
           if (rank < a.R) {
-            load_v(a, mine, m * a.R + rank, hi, lo);
-            if (a.v_out != nullptr && stripe == 0 && 16 * b + c < t.count) {
+            load_v(a, mine, m * a.R + rank, x);
+            if (stripe == 0 && 16 * b + c < t.count) {
               const long long to = static_cast<long long>(mine) * a.ldv + m * a.R + rank;
-              store16(a.v_out + to, hi);
-              if (a.vlo_out != nullptr) store16(a.vlo_out + to, lo);
+              if (a.v_out != nullptr) store16(a.v_out + to, pack8(x));
+              if (a.sum_out != nullptr) {
+                *reinterpret_cast<f32x4*>(a.sum_out + to) = f32x4{x[0], x[1], x[2], x[3]};
+                *reinterpret_cast<f32x4*>(a.sum_out + to + 4) = f32x4{x[4], x[5], x[6], x[7]};
+              }
             }
           }
+          u32x4 v[kSplit];
+          split8(x, v);
 #pragma unroll
-          for (int o = 0; o < 8; ++o) acc[m][o] = mfma(lo, wf[m][k][o], acc[m][o]);
+          for (int h = kSplit - 1; h >= 0; --h)
 #pragma unroll
-          for (int o = 0; o < 8; ++o) acc[m][o] = mfma(hi, wf[m][k][o], acc[m][o]);
+            for (int o = 0; o < 8; ++o) acc[m][o] = mfma(v[h], wf[m][k][o], acc[m][o]);
         }
       }
       expand_store<MODE, DROP>(a, in, acc, row, t.count - 16 * b - 4 * q, live, col, f, key);
@@ -906,17 +909,17 @@ __global__ __launch_bounds__(256, KS == 1 || (KS == 2 && MODE != kSwiglu) ? 2 : 
 
 // ---------------------------------------------------------------- both products of a tile's rows
 
-// A workgroup makes v of up to ROWS rows of a tile, which stays in LDS (hi and lo), and then what is added to them: its waves take
+// A workgroup makes v of up to ROWS rows of a tile, which stays in LDS (as three bf16 values), and then what is added to them: its waves take
 // K's units in turn, then the columns' stripes.  Where few tiles leave the chip idle, what shrink and expand cost is their two
 // launches and the chain of loads in each (4012 rows of 16 experts and 5 adapters, d 2112, f 1344: 17 and 15 us against 8 + 14
 // and 8 + 11).  Loading a wave's first stripe before v is made, so that it is there by then, took 37 us a call where this takes 35.
 // Calls with dropout, which are training's and of more rows, keep to the two kernels.
 constexpr int kBothWaves = 8;
 
-// v = x A^T of a unit's rows, NB blocks of 16, into vs (hi and lo).  The waves' sums meet in LDS, each wave's in its own staging.
+// v = x A^T of a unit's rows, NB blocks of 16, into vs.  The waves' sums meet in LDS, each wave's in its own staging.
 template <int NB, int RT, int ROWS>
 __device__ __forceinline__ void both_shrink(const ShrinkArgs& s, const ExpandArgs& a, const Tile& t, const PlanLayout& p,
-                                            const uint16_t* w, u32x4* lds, uint16_t (&vs)[2][ROWS][16 * RT + 8]) {
+                                            const uint16_t* w, u32x4* lds, uint16_t (&vs)[kSplit][ROWS][16 * RT + 8]) {
   constexpr int kStage = (ROWS / 16 + RT) * 128;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   u32x4* stage = lds + wave * kStage;
@@ -934,7 +937,13 @@ __device__ __forceinline__ void both_shrink(const ShrinkArgs& s, const ExpandArg
     const int rank = at / 64 % RT * 16 + (at & 15), m = at / (64 * RT) * 16 + 4 * (at >> 4 & 3);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      split_bf16(rank < s.R ? sum[j] : 0.f, vs[0][m + j][rank], vs[1][m + j][rank]);
+      float x = rank < s.R ? sum[j] : 0.f;
+#pragma unroll
+      for (int h = 0; h < kSplit; ++h) {
+        const uint16_t here = f32_to_bf16(x);
+        vs[h][m + j][rank] = here;
+        x = lack(x, bf16_to_f32(here));
+      }
       if (a.v_out != nullptr && rank < s.R && m + j < t.count)
         a.v_out[static_cast<long long>(row_at(a.rows, p, t.pos + m + j)) * a.ldv + rank] = vs[0][m + j][rank];
     }
@@ -946,7 +955,7 @@ template <int RT, int MODE, int ROWS>
 __global__ __launch_bounds__(64 * kBothWaves) void adapter_both_kernel(ShrinkArgs s, ExpandArgs a) {
   constexpr int NW = MODE == kSwiglu ? 2 : 1, NOUT = MODE == kSwiglu ? 3 : 1, KS = (16 * RT / NW + 31) / 32, NI = NW;
   __shared__ u32x4 lds[kBothWaves * (ROWS / 16 + RT) * 128];
-  __shared__ alignas(16) uint16_t vs[2][ROWS][16 * RT + 8];     // (rows in different banks)
+  __shared__ alignas(16) uint16_t vs[kSplit][ROWS][16 * RT + 8];     // (rows in different banks)
   const PlanLayout p = plan_layout(a.rows.n, a.rows.E, a.rows.L);
   const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -1008,7 +1017,7 @@ __global__ __launch_bounds__(64 * kBothWaves) void adapter_both_kernel(ShrinkArg
           for (int k = 0; k < KS; ++k) {
             const int rank = 32 * k + 8 * q;
 #pragma unroll
-            for (int h = 1; h >= 0; --h) {
+            for (int h = kSplit - 1; h >= 0; --h) {
               const u32x4 v = rank < a.R ? *reinterpret_cast<const u32x4*>(&vs[h][16 * b + c][m * a.R + rank]) : u32x4{0, 0, 0, 0};
 #pragma unroll
               for (int o = 0; o < 8; ++o) acc[m][o] = mfma(v, wf[m][k][o], acc[m][o]);
@@ -1187,7 +1196,7 @@ __global__ __launch_bounds__(kRowThreads) void adapter_row_kernel(RowArgs a) {
 struct WgradArgs {
   Rows rows;
   const uint16_t* v;        // [n][ldv]
-  const uint16_t* vlo;      // LO: what v lacks
+  const float* vf;          // F32: the same in fp32 instead
   int v0[2];                // first columns of up to two products (blockIdx.y): gate and up
   const uint16_t* y[2];
   int gather;               // y by token
@@ -1211,9 +1220,11 @@ __device__ __forceinline__ long long piece_slot(int pos, int piece, bool first) 
 // Bound by memory and its latency: 131072 rows of 4096 by 32 ranks take 243 us (1.28 GB through the L2s' misses, 5.3 TB/s).
 // More than 32 ranks are a workgroup for each 32, whose second reading of y comes from the L2: 64 ranks take 320 us, where a
 // wave with all 64 (one wave per SIMD then) took 412, and a workgroup of eight waves, four for each half, 441.
-template <int RT, bool DROP, bool LO>
+template <int RT, bool DROP, bool F32>
 __global__ __launch_bounds__(256, 2) void adapter_wgrad_kernel(WgradArgs a) {
-  constexpr int NV = LO ? 2 : 1, kItems = NV * RT * 64, NI = (kItems + 255) / 256, kPad = 36;
+  // a thread stages a pair of rows and VR ranks: 16 bytes of each row
+  constexpr int NV = F32 ? kSplit : 1, VR = F32 ? 4 : 8, kItems = 32 * 16 * RT / VR, kPad = 36;
+  static_assert(kItems <= 256);
   __shared__ uint32_t vt[2][NV][16 * RT][kPad];
   // row and row of y, of steps s (read until its last product) and s + 1 while those of s + 2 come
   __shared__ int ids[4][2][64];
@@ -1242,30 +1253,34 @@ __global__ __launch_bounds__(256, 2) void adapter_wgrad_kernel(WgradArgs a) {
     if (t.count > 0) {
       auto row_of = [&](int at) { return list[min(at, t.count - 1)]; };
       auto src_of = [&](int at) { return srcs[min(at, t.count - 1)]; };
-      // v: item k of a thread is a pair of rows and 8 ranks of hi or lo
-      u32x4 vr[NI][2];
+      const int pair = tid & 31, vrank = r0 + VR * ((tid >> 5) % (16 * RT / VR)), vcol = a.v0[which] + (vrank < a.R ? vrank : 0);
+      u32x4 vr[2];
       auto load_v = [&](int s) {
 #pragma unroll
-        for (int k = 0; k < NI; ++k) {
-          const int it = tid + 256 * k, pair = it & 31, rank = r0 + 8 * ((it >> 5) % (2 * RT));
-          const uint16_t* v = (LO && it >= RT * 64 ? a.vlo : a.v) + a.v0[which] + (rank < a.R ? rank : 0);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) vr[k][h] = load16(v + static_cast<long long>(ids[s & 3][0][2 * pair + h]) * a.ldv);
+        for (int h = 0; h < 2; ++h) {
+          const long long at = static_cast<long long>(ids[s & 3][0][2 * pair + h]) * a.ldv + vcol;
+          vr[h] = F32 ? *reinterpret_cast<const u32x4*>(a.vf + at) : load16(a.v + at);
         }
         __builtin_amdgcn_sched_barrier(0);
       };
       auto put_v = [&](int buf, int left) {
+        if (tid >= kItems) return;
+        const uint32_t m0 = 2 * pair < left ? ~0u : 0u, m1 = 2 * pair + 1 < left ? ~0u : 0u;
 #pragma unroll
-        for (int k = 0; k < NI; ++k) {
-          const int it = tid + 256 * k, pair = it & 31, ch = (it >> 5) % (2 * RT);
-          if (it >= kItems) continue;
-          uint32_t(*to)[kPad] = &vt[buf][LO && it >= RT * 64 ? 1 : 0][8 * ch];
-          const uint32_t m0 = 2 * pair < left ? ~0u : 0u, m1 = 2 * pair + 1 < left ? ~0u : 0u;
+        for (int h = 0; h < 4; ++h) {
+          const uint32_t lo = vr[0][h] & m0, hi = vr[1][h] & m1;
+          if constexpr (F32) {
+            float x = __builtin_bit_cast(float, lo), y = __builtin_bit_cast(float, hi);
 #pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            const uint32_t lo = vr[k][0][h] & m0, hi = vr[k][1][h] & m1;
-            to[2 * h][pair] = __builtin_amdgcn_perm(hi, lo, 0x05040100u);
-            to[2 * h + 1][pair] = __builtin_amdgcn_perm(hi, lo, 0x07060302u);
+            for (int n = 0; n < NV; ++n) {
+              const uint32_t both = pack_bf16x2(x, y);
+              vt[buf][n][vrank - r0 + h][pair] = both;
+              x = lack(x, bf16_lo(both));
+              y = lack(y, bf16_hi(both));
+            }
+          } else {
+            vt[buf][0][vrank - r0 + 2 * h][pair] = __builtin_amdgcn_perm(hi, lo, 0x05040100u);
+            vt[buf][0][vrank - r0 + 2 * h + 1][pair] = __builtin_amdgcn_perm(hi, lo, 0x07060302u);
           }
         }
       };
@@ -1477,15 +1492,15 @@ void launch_rows(const RowArgs& a, hipStream_t st) {
   else if constexpr (MODE == kSwiglu) adapter_row_kernel<16, MODE, DROP><<<a.rows.n, kRowThreads, 0, st>>>(a);
 }
 
-template <bool DROP, bool LO>
+template <bool DROP, bool F32>
 void launch_wgrad(const WgradArgs& a, int products, hipStream_t st) {
   const PlanLayout p = plan_layout(a.rows.n, a.rows.E, a.rows.L);
   const int rt = a.R <= 16 ? 1 : 2;
   const int stripes = (a.C + 127) / 128;
   const long long wgs = static_cast<long long>(p.items_cap) * ((a.R + 16 * rt - 1) / (16 * rt)) * ((stripes + 3) / 4);
   const dim3 grid(grid_of(wgs), products);
-  if (rt == 1) adapter_wgrad_kernel<1, DROP, LO><<<grid, 256, 0, st>>>(a);
-  else adapter_wgrad_kernel<2, DROP, LO><<<grid, 256, 0, st>>>(a);
+  if (rt == 1) adapter_wgrad_kernel<1, DROP, F32><<<grid, 256, 0, st>>>(a);
+  else adapter_wgrad_kernel<2, DROP, F32><<<grid, 256, 0, st>>>(a);
 }
 
 // Joins the pieces of up to three products in one launch, where there can be groups of several.
@@ -1530,32 +1545,24 @@ int check_dims(int d, int f, int r) {
 
 long long align256(long long b) { return (b + 255) / 256 * 256; }
 
-// Bytes of v's hi or lo, of its slices and of the weight gradients' pieces for a product pair of widths K -> R.
-long long v_bytes(int n, int R) { return align256(2LL * n * R); }
-long long part_bytes(int n, int E, int L, int R, int K) {
-  const int s = slices(n, E, L, K);
-  return s > 1 ? align256(4LL * s * n * R) : 0;
-}
+// Bytes of v's slices (fp32 [S][n][R]) and of the weight gradients' pieces for a product pair of widths K -> R.
+long long part_bytes(int n, int E, int L, int R, int K) { return align256(4LL * slices(n, E, L, K) * n * R); }
 long long piece_bytes(int n, int products, int R, int C) {
   const int piece = piece_rows(n);
   return n > piece ? align256(4LL * products * 2 * (n / piece + 1) * R * C) : 0;
 }
 
-long long forward_bytes(int n, int E, int L, int R, int K) {
-  return 2 * v_bytes(n, R) + part_bytes(n, E, L, R, K);
-}
-
-// The workspace of a backward call: v's hi and lo [n][R], its slices, the pieces of the B's gradients (1 or 2 products
-// of C1 columns and r ranks) and of A's (R ranks, C2 columns).
+// The workspace of a backward call: v's slices, their sum [n][R] (the slice itself where there is one), the pieces of the B's
+// gradients (1 or 2 products of C1 columns and r ranks) and of A's (R ranks, C2 columns).
 struct BwdSpace {
-  long long hi, lo, part, pieces_b, pieces_a, bytes;
+  long long part, sum, pieces_b, pieces_a, bytes;
 };
 BwdSpace bwd_space(int n, int E, int L, int r, int products, int C1, int R, int C2) {
+  const bool sliced = slices(n, E, L, C1) > 1;
   BwdSpace w;
-  w.hi = 0;
-  w.lo = v_bytes(n, R);
-  w.part = 2 * v_bytes(n, R);
-  w.pieces_b = w.part + part_bytes(n, E, L, R, C1);
+  w.part = 0;
+  w.sum = sliced ? part_bytes(n, E, L, R, C1) : 0;
+  w.pieces_b = w.sum + align256(4LL * n * R);
   w.pieces_a = w.pieces_b + piece_bytes(n, products, r, C1);
   w.bytes = w.pieces_a + piece_bytes(n, 1, R, C2);
   return w;
@@ -1604,7 +1611,7 @@ extern "C" size_t moe_adapter_workspace_bytes(int n, int E, int L, int d, int f,
   if (check_sizes(1, n, E, L) || check_dims(d, f, r)) return 0;
   if (backward) return static_cast<size_t>(max(down_bwd_space(n, E, L, d, f, r).bytes, gate_up_bwd_space(n, E, L, d, f, r).bytes));
   if (!planned) return 0;      // one kernel, which keeps v to itself
-  return static_cast<size_t>(max(forward_bytes(n, E, L, 2 * r, d), forward_bytes(n, E, L, r, f)));
+  return static_cast<size_t>(max(part_bytes(n, E, L, 2 * r, d), part_bytes(n, E, L, r, f)));
 }
 
 extern "C" int moe_adapter_gate_up(const uint16_t* x, const int32_t* ids, const int32_t* row_token, const int32_t* offsets,
@@ -1632,13 +1639,11 @@ extern "C" int moe_adapter_gate_up(const uint16_t* x, const int32_t* ids, const 
     else launch_rows<kSwiglu, false>(k, st);
     return check_launch("adapter_gate_up");
   }
-  MOE_CHECK_WS(forward_bytes(n, E, L, 2 * r, d));
-  uint16_t* vbuf = v != nullptr ? v : static_cast<uint16_t*>(ws);
-  uint16_t* lo = reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + v_bytes(n, 2 * r));
-  float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + 2 * v_bytes(n, 2 * r));
+  MOE_CHECK_WS(part_bytes(n, E, L, 2 * r, d));
+  float* part = static_cast<float*>(ws);
   const int S = slices(n, E, L, d);
-  ShrinkArgs s = {rows, {x, nullptr}, {a_gu, nullptr}, {0, 0}, 1, d, 2 * r, 2 * r, S, 1, nullptr, vbuf, lo, part, drop};
-  ExpandArgs e = {rows, vbuf, lo, part, 2 * r, S, r, f, 1, {b_gate, b_up}, scale, {g, u, a, nullptr}, {g_out, u_out, a_out},
+  ShrinkArgs s = {rows, {x, nullptr}, {a_gu, nullptr}, {0, 0}, 1, d, 2 * r, 2 * r, S, 1, nullptr, part, v, drop};
+  ExpandArgs e = {rows, part, 2 * r, S, r, f, 1, {b_gate, b_up}, scale, {g, u, a, nullptr}, {g_out, u_out, a_out},
                   S > 1 ? v : nullptr, nullptr, DropArgs{}};
   const int both = drop.drop == 0 ? both_rows(rows, 2 * r) : 0;
   if (both) {
@@ -1674,13 +1679,11 @@ extern "C" int moe_adapter_down(const uint16_t* a, const int32_t* ids, const int
     else launch_rows<kAdd, false>(k, st);
     return check_launch("adapter_down");
   }
-  MOE_CHECK_WS(forward_bytes(n, E, L, r, f));
-  uint16_t* vbuf = v != nullptr ? v : static_cast<uint16_t*>(ws);
-  uint16_t* lo = reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + v_bytes(n, r));
-  float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + 2 * v_bytes(n, r));
+  MOE_CHECK_WS(part_bytes(n, E, L, r, f));
+  float* part = static_cast<float*>(ws);
   const int S = slices(n, E, L, f);
-  ShrinkArgs s = {rows, {a, nullptr}, {a_down, nullptr}, {0, 0}, 0, f, r, r, S, 1, nullptr, vbuf, lo, part, drop};
-  ExpandArgs e = {rows, vbuf, lo, part, r, S, r, d, 1, {b_down, nullptr}, scale, {yexp, nullptr, nullptr, nullptr},
+  ShrinkArgs s = {rows, {a, nullptr}, {a_down, nullptr}, {0, 0}, 0, f, r, r, S, 1, nullptr, part, v, drop};
+  ExpandArgs e = {rows, part, r, S, r, d, 1, {b_down, nullptr}, scale, {yexp, nullptr, nullptr, nullptr},
                   {y_out, nullptr, nullptr}, S > 1 ? v : nullptr, nullptr, DropArgs{}};
   const int both = drop.drop == 0 ? both_rows(rows, r) : 0;
   if (both) {
@@ -1716,23 +1719,22 @@ extern "C" int moe_adapter_down_bwd(const uint16_t* dyexp, const uint16_t* a, co
   const BwdSpace space = down_bwd_space(n, E, L, d, f, r);
   MOE_CHECK_WS(space.bytes);
   char* base = static_cast<char*>(ws);
-  uint16_t* dv = reinterpret_cast<uint16_t*>(base + space.hi);
-  uint16_t* lo = reinterpret_cast<uint16_t*>(base + space.lo);
   float* part = reinterpret_cast<float*>(base + space.part);
+  float* dv = reinterpret_cast<float*>(base + space.sum);
   float* pieces_b = reinterpret_cast<float*>(base + space.pieces_b);
   float* pieces_a = reinterpret_cast<float*>(base + space.pieces_a);
   const int S = slices(n, E, L, d);
   hipStream_t st = as_stream(stream);
   // dyexp's second reader follows its first, so that what the last-level cache still holds of it is found there
-  const ShrinkArgs s = {rows, {dyexp, nullptr}, {b_down, nullptr}, {0, 0}, 0, d, r, r, S, 1, scale, dv, lo, part, DropArgs{}};
+  const ShrinkArgs s = {rows, {dyexp, nullptr}, {b_down, nullptr}, {0, 0}, 0, d, r, r, S, 1, scale, part, nullptr, DropArgs{}};
   launch_shrink<false>(s, 1, st);
   const WgradArgs wb = {rows, v, nullptr, {0, 0}, {dyexp, nullptr}, 0, r, r, d, scale, {d_b_down, nullptr}, pieces_b, DropArgs{}};
   launch_wgrad<false, false>(wb, 1, st);
-  const ExpandArgs e = {rows, dv, lo, part, r, S, r, f, 1, {a_down, nullptr}, nullptr, {g, u, dg, du}, {dg_out, du_out, nullptr},
-                        S > 1 ? dv : nullptr, S > 1 ? lo : nullptr, drop};
+  const ExpandArgs e = {rows, part, r, S, r, f, 1, {a_down, nullptr}, nullptr, {g, u, dg, du}, {dg_out, du_out, nullptr},
+                        nullptr, S > 1 ? dv : nullptr, drop};
   if (drop.drop) launch_expand<kSwigluBwd, true>(e, st);
   else launch_expand<kSwigluBwd, false>(e, st);
-  const WgradArgs wa = {rows, dv, lo, {0, 0}, {a, nullptr}, 0, r, r, f, nullptr, {d_a_down, nullptr}, pieces_a, drop};
+  const WgradArgs wa = {rows, nullptr, dv, {0, 0}, {a, nullptr}, 0, r, r, f, nullptr, {d_a_down, nullptr}, pieces_a, drop};
   if (drop.drop) launch_wgrad<true, true>(wa, 1, st);
   else launch_wgrad<false, true>(wa, 1, st);
   launch_join({rows, {pieces_b, pieces_a, nullptr}, {d_b_down, d_a_down, nullptr}, {r, r, 0}, {d, f, 0}}, 2, st);
@@ -1761,22 +1763,21 @@ extern "C" int moe_adapter_gate_up_bwd(const uint16_t* dg, const uint16_t* du, c
   const BwdSpace space = gate_up_bwd_space(n, E, L, d, f, r);
   MOE_CHECK_WS(space.bytes);
   char* base = static_cast<char*>(ws);
-  uint16_t* dv = reinterpret_cast<uint16_t*>(base + space.hi);
-  uint16_t* lo = reinterpret_cast<uint16_t*>(base + space.lo);
   float* part = reinterpret_cast<float*>(base + space.part);
+  float* dv = reinterpret_cast<float*>(base + space.sum);
   float* pieces_b = reinterpret_cast<float*>(base + space.pieces_b);
   float* pieces_a = reinterpret_cast<float*>(base + space.pieces_a);
   const int S = slices(n, E, L, f);
   hipStream_t st = as_stream(stream);
-  const ShrinkArgs s = {rows, {dg, du}, {b_gate, b_up}, {0, r}, 0, f, r, 2 * r, S, 1, scale, dv, lo, part, DropArgs{}};
+  const ShrinkArgs s = {rows, {dg, du}, {b_gate, b_up}, {0, r}, 0, f, r, 2 * r, S, 1, scale, part, nullptr, DropArgs{}};
   launch_shrink<false>(s, 2, st);
   const WgradArgs wb = {rows, v, nullptr, {0, r}, {dg, du}, 0, 2 * r, r, f, scale, {d_b_gate, d_b_up}, pieces_b, DropArgs{}};
   launch_wgrad<false, false>(wb, 2, st);
-  const ExpandArgs e = {rows, dv, lo, part, 2 * r, S, 2 * r, d, 1, {a_gu, nullptr}, nullptr, {dxp, nullptr, nullptr, nullptr},
-                        {dxp_out, nullptr, nullptr}, S > 1 ? dv : nullptr, S > 1 ? lo : nullptr, drop};
+  const ExpandArgs e = {rows, part, 2 * r, S, 2 * r, d, 1, {a_gu, nullptr}, nullptr, {dxp, nullptr, nullptr, nullptr},
+                        {dxp_out, nullptr, nullptr}, nullptr, S > 1 ? dv : nullptr, drop};
   if (drop.drop) launch_expand<kAdd, true>(e, st);
   else launch_expand<kAdd, false>(e, st);
-  const WgradArgs wa = {rows, dv, lo, {0, 0}, {x, nullptr}, 1, 2 * r, 2 * r, d, nullptr, {d_a_gu, nullptr}, pieces_a, drop};
+  const WgradArgs wa = {rows, nullptr, dv, {0, 0}, {x, nullptr}, 1, 2 * r, 2 * r, d, nullptr, {d_a_gu, nullptr}, pieces_a, drop};
   if (drop.drop) launch_wgrad<true, true>(wa, 1, st);
   else launch_wgrad<false, true>(wa, 1, st);
   const float* second = pieces_b + 2LL * (n / piece_rows(n) + 1) * r * f;

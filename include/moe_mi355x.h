@@ -329,8 +329,8 @@ int moe_unpermute_combine_dropout_bwd(const uint16_t* dy, const uint16_t* yexp, 
  *   m: the dropout factors (above) of the adapters' inputs, element (grouped row, column); p = 0: none.
  *   gate_up:  v = (m x[t]) A^T;  g' = g + s v_gate B_gate,  u' = u + s v_up B_up,  a' = silu(g') u'
  *   down:     v = (m a) A^T;     y' = y + s v B
- * Products of bf16 values are summed in fp32; between its two products v (and dv of the backward) is held to 16 bits of
- * mantissa, and handed out as bf16; g', u', y' are rounded once, and a' comes from the unrounded g', u'.
+ * Products of bf16 values are summed in fp32; between its two products v (and dv of the backward) is held in fp32, and v is
+ * handed out as bf16; g', u', y' are rounded once, and a' comes from the unrounded g', u'.
  * The last bits of a row may differ with the number of rows in the call and with a plan, since sums are cut by them.
  * Rows from offsets[E] on are left as they were.  Offsets that fall or lie outside [0, n] give rows to other experts, and
  * no access out of bounds. */
