@@ -1060,12 +1060,16 @@ __global__ __launch_bounds__(kRowThreads) void adapter_row_kernel(RowArgs a) {
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), i = blockIdx.x;
   // the row's token first: its adapter's number hangs on it
   const int l = __builtin_amdgcn_readfirstlane(adapter_of(a.rows.ids, a.rows.row_token, i, a.rows.T, a.rows.L));
-  int end[4], e = 0;
+  // its expert: the first one whose rows end behind it (of offsets that fall too, what their running maximum says, as in a plan)
+  int end[4], e = a.rows.E;
 #pragma unroll
   for (int b = 0; b < 4; ++b) end[b] = a.rows.offsets[min(64 * b + lane, a.rows.E - 1) + 1];
 #pragma unroll
-  for (int b = 0; b < 4; ++b) e += __popcll(__ballot(64 * b + lane < a.rows.E && end[b] <= i));
-  if (e >= a.rows.E || i < a.rows.offsets[0]) return;      // behind the last expert's rows
+  for (int b = 3; b >= 0; --b) {
+    const unsigned long long behind = __ballot(64 * b + lane < a.rows.E && end[b] > i);
+    if (behind) e = 64 * b + __builtin_ctzll(behind);
+  }
+  if (e >= a.rows.E || i < a.rows.offsets[0]) return;      // behind the last expert's rows, or before the first's
   const long long row = static_cast<long long>(i) * a.N;
   const int chunks = a.N / 8;
   if (l >= a.rows.L) {                                     // no adapter: copies

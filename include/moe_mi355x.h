@@ -332,8 +332,8 @@ int moe_unpermute_combine_dropout_bwd(const uint16_t* dy, const uint16_t* yexp, 
  * Products of bf16 values are summed in fp32; between its two products v (and dv of the backward) is held in fp32, and v is
  * handed out as bf16; g', u', y' are rounded once, and a' comes from the unrounded g', u'.
  * The last bits of a row may differ with the number of rows in the call and with a plan, since sums are cut by them.
- * Rows from offsets[E] on are left as they were.  Offsets that fall or lie outside [0, n] give rows to other experts, and
- * no access out of bounds. */
+ * Rows from offsets[E] on are left as they were.  Offsets that fall or lie outside [0, n] are read as their running maximum
+ * within [0, n], with a plan and without one: rows go to other experts then, and no access goes out of bounds. */
 
 /* The order of the rows by expert and adapter (a stable sort, so that sums run in a fixed order), made on the
  * device for the calls below: `plan` is a buffer of moe_adapter_plan_bytes(n, E, L) bytes that holds it for as long as ids,
