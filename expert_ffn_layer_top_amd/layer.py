@@ -191,7 +191,8 @@ def forward(x, weights, k, logits=None, mxfp8=False, want_probs=False, events=No
     dropped dy to bf16 (its combine backward reads it in two products).  The generator's state is copied here, so the
     program may advance it before the backward.
     frozen: the layer's own weights get no gradients (the adapters alone are trained): the backward makes no dw_* and
-    the forward keeps nothing for them."""
+    the forward keeps nothing for them (neither the permuted input, unless recompute reads it, nor A's token blocks; without
+    adapters not x and A either)."""
     if not (fp8b is None or fp8b is True or fp8b is False or isinstance(fp8b, dict)):
         raise ValueError("fp8b must be True or the copies that Weights.quantize_fp8b returns")
     fp8b = True if fp8b is True else fp8b if isinstance(fp8b, dict) else None
@@ -220,7 +221,9 @@ def forward(x, weights, k, logits=None, mxfp8=False, want_probs=False, events=No
         raise ValueError("dropout and adapter_dropout need sites of their own (adapter_dropout takes its site and the next)")
     if router is not None:
         router = replace(router)         # the backward uses the settings this forward used
-    ctx = dict(x=x, k=k, mxfp8=mxfp8, balance_weight=balance_weight, router=router, serving=serving, frozen=frozen)
+    # for whom x and A are kept: the weight gradients and the adapters; the permuted input: the weight gradients and recompute
+    keep, keep_xp = adapters is not None or not frozen, recompute or not frozen
+    ctx = dict(x=x if keep else None, k=k, mxfp8=mxfp8, balance_weight=balance_weight, router=router, serving=serving, frozen=frozen)
     ctx["dropout"] = dropout = _kept(dropout)
     ctx["adapter_dropout"] = adapter_dropout = _kept(adapter_dropout)
     want_probs = want_probs or balance_weight is not None
@@ -247,7 +250,9 @@ def forward(x, weights, k, logits=None, mxfp8=False, want_probs=False, events=No
         q = weights.quantize_fp8b(transposed=not serving) if fp8b is True else fp8b
         ctx["fp8b_weights"] = q          # the backward uses the copies this forward used
         with _Span(events, "permute"):
-            ctx["xq"] = xq = ops.fp8b_quantize_rows(x, dest=r["dest"])
+            xq = ops.fp8b_quantize_rows(x, dest=r["dest"])
+        if keep_xp:
+            ctx["xq"] = xq
         with _Span(events, "gate_up"):
             g, u, a = ops.grouped_gemm_gate_up_fp8b(*xq, r["offsets"], *q["wg"], *q["wu"],
                                                     want_gu=plan is not None or not (serving or recompute))
@@ -263,7 +268,8 @@ def forward(x, weights, k, logits=None, mxfp8=False, want_probs=False, events=No
     elif not mxfp8:
         with _Span(events, "permute"):
             xp = ops.permute(x, r["dest"])
-        ctx["xp"] = xp
+        if keep_xp:
+            ctx["xp"] = xp
         with _Span(events, "gate_up"):
             g, u, a = ops.grouped_gemm_gate_up(xp, r["offsets"], weights.w_gate, weights.w_up)
         if plan is not None:
@@ -275,7 +281,8 @@ def forward(x, weights, k, logits=None, mxfp8=False, want_probs=False, events=No
         # x quantised along d on its way into the expert buffers (no token-major E4M3 copy)
         with _Span(events, "permute"):
             xpq, xps = ops.permute_quant_mx(x, r["dest"])
-        ctx["xpq"], ctx["xps"] = xpq, xps
+        if keep_xp:
+            ctx["xpq"], ctx["xps"] = xpq, xps
         ctx["mx_weights"] = q            # the backward uses the copies this forward used
         with _Span(events, "gate_up"):
             g, u, a = ops.grouped_gemm_gate_up(xpq, r["offsets"], q["wg"], q["wu"],
@@ -299,7 +306,7 @@ def forward(x, weights, k, logits=None, mxfp8=False, want_probs=False, events=No
         del g, u, a
         ctx.update(g=None, u=None, a=None, yexp=yexp)
     else:
-        ctx.update(g=g, u=u, a=a, yexp=yexp)
+        ctx.update(g=g, u=u, a=a if keep else None, yexp=yexp)
     with _Span(events, "combine"):
         if dropout is None and residual is None:
             ctx["y"] = ops.unpermute_combine(yexp, r["topk_gate"], r["dest"])

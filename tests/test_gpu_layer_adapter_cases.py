@@ -1,0 +1,39 @@
+"""More of the layer with adapters: what a frozen layer's forward keeps."""
+
+import pytest
+import torch
+
+from gpu_util import note
+from test_gpu_layer_adapter import GRADS, Case, mods
+
+pytestmark = pytest.mark.gpu
+
+FORMATS = pytest.mark.parametrize("fmt", [{}, dict(mxfp8=True), dict(fp8b=True)], ids=["bf16", "mxfp8", "fp8b"])
+PERMUTED = ("xp", "xq", "xpq", "xps")
+
+
+@FORMATS
+def test_a_frozen_forward_keeps_nothing_for_the_weights(fmt):
+    """The permuted input only where recompute reads it, no token blocks of A; without adapters neither x nor A.  The backward
+    gives the same bits as that of a layer that is trained whole."""
+    layer, _ = mods()
+    note(f"layer frozen keeps {fmt}")
+    c = Case(T=150, d=256, f=128)
+    for with_adapters in (True, False):
+        kw = dict(adapters=c.ad, adapter_ids=c.ids) if with_adapters else {}
+        whole = layer.forward(c.x, c.w, c.k, logits=c.logits, **kw, **fmt)
+        want = layer.backward(whole, c.w, c.dy)
+        held = [name for name in PERMUTED if name in whole]
+        assert held and whole["a"] is not None and whole["x"] is c.x
+        for recompute in (False, True):
+            ctx = layer.forward(c.x, c.w, c.k, logits=c.logits, frozen=True, recompute=recompute, **kw, **fmt)
+            assert [name for name in PERMUTED if name in ctx] == (held if recompute else [])
+            assert "aT" not in ctx and "aTs" not in ctx
+            assert (ctx["x"] is not None) == with_adapters and (ctx["a"] is not None) == (with_adapters and not recompute)
+            out = layer.backward(ctx, c.w, c.dy)
+            assert torch.equal(ctx["y"], whole["y"])
+            assert not any(name.startswith("dw_") for name in out)
+            for name in GRADS:
+                # (without adapters the MXFP8 backward of a layer trained whole quantises dYexp from fp32, not from bf16)
+                if name in out and (with_adapters or "mxfp8" not in fmt or name == "d_logits"):
+                    assert torch.equal(out[name], want[name]), (with_adapters, recompute, name)
