@@ -494,9 +494,10 @@ ADAPTER_FEW_ROWS = 512
 
 class AdapterPlan:
     """Which adapter each routed row has (adapter_plan), as the adapter calls take it.  It holds for as long as its tensors
-    keep their contents."""
+    keep their contents.  Calls on another stream than the one it was made on wait for that one by the program's own doing, as for any
+    tensor; the plan's own buffer is kept until they have run."""
 
-    __slots__ = ("ids", "offsets", "row_token", "buf", "T", "n", "E", "L", "dev", "_rows")
+    __slots__ = ("ids", "offsets", "row_token", "buf", "T", "n", "E", "L", "dev", "stream", "_rows")
 
     def _args(self):
         """What every call passes of it (pointers and sizes)."""
@@ -523,6 +524,7 @@ def adapter_plan(ids, offsets, n_adapters, row_token=None, backward=False):
     if backward or n > ADAPTER_FEW_ROWS:
         nbytes = lib.moe_adapter_plan_bytes(n, E, plan.L)
         plan.buf = _new((nbytes,), torch.uint8, dev)
+        plan.stream = torch._C._cuda_getCurrentRawStream(dev)
         _call_on(dev, "moe_adapter_plan", p_ids, p_token, p_off, T, n, E, plan.L, plan.buf.data_ptr(), nbytes)
     plan._rows = (p_ids, p_token, p_off, _ptr(plan.buf), T, n, E, plan.L)
     return plan
@@ -566,7 +568,10 @@ def _adapter_d(plan, a_down, b_down, scale):
 def _adapter_ws(plan, d, f, r, backward):
     if plan.buf is None:
         return None, 0
-    nbytes = lib.moe_adapter_workspace_bytes(plan.n, plan.E, plan.L, d, f, r, plan.buf is not None, backward)
+    if plan.stream != torch._C._cuda_getCurrentRawStream(plan.dev):
+        # nobody but the plan knows its buffer: without this its memory could be another tensor's before the call has run
+        plan.buf.record_stream(torch.cuda.current_stream(plan.dev))
+    nbytes = lib.moe_adapter_workspace_bytes(plan.n, plan.E, plan.L, d, f, r, True, backward)
     return _new((nbytes,), torch.uint8, plan.dev), nbytes
 
 

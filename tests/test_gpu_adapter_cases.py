@@ -66,3 +66,34 @@ def test_rows_outside_falling_offsets_are_left_as_they_were(sort):
         assert bool((t[torch.from_numpy(out)] == 7.25).all())
     ref, mag = oracle.shrink(c["a"], c["a_down"], c["e"], c["l"])
     within(val(v)[~out], ref[~out], (U * np.abs(ref) + 64 * 2.0 ** -23 * mag)[~out], "v")
+
+
+def test_a_plan_used_on_another_stream_and_dropped():
+    """Its buffer is not handed out again while the other stream's calls that read it are still to run."""
+    note("adapter plan on another stream")
+    n, d, f, r = 300000, 64, 64, 8
+    g = torch.Generator(device=dev()).manual_seed(1)
+    bf = lambda *s: torch.randn(s, generator=g, device=dev()).to(torch.bfloat16)          # noqa: E731
+    a, y, A, B = bf(n, f), bf(n, d), bf(2, 3, r, f), bf(2, 3, r, d)
+    scale = torch.ones(2, dtype=torch.float32, device=dev())
+    ids = torch.randint(-1, 2, (n,), generator=g, device=dev()).int()
+    off = torch.tensor([0, n // 3, n // 2, n], dtype=torch.int32, device=dev())
+    want = ops().adapter_down(a, y, ops().adapter_plan(ids, off, 2), A, B, scale)[0]
+    work = torch.randn(8192, 8192, generator=g, device=dev())
+    busy = work @ work
+    other = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    plan = ops().adapter_plan(ids, off, 2)
+    at, size = plan.buf.data_ptr(), plan.buf.numel()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(other):
+        for _ in range(8):
+            torch.mm(work, work, out=busy)          # a millisecond or more each
+        got = ops().adapter_down(a, y, plan, A, B, scale)[0]
+    del plan
+    again = torch.empty(size, dtype=torch.uint8, device=dev())
+    assert not other.query()                        # (the other stream was still at work when the memory was asked for)
+    assert again.data_ptr() != at
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
