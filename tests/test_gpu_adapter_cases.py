@@ -1,4 +1,7 @@
-"""More of the adapters' calls against 64 bits, with the tolerances derived in test_gpu_adapter.py: offsets that fall, in both forms."""
+"""More of the adapters' calls against 64 bits, with the tolerances derived in test_gpu_adapter.py (whose bound of v's error, that of two
+bf16 values, is wider than what fp32 needs): wide matrices of few rows, whose sums are cut into slices and columns into groups,
+dropout at every rank in every form, many rows in pieces of every length, offsets that fall, a plan on two streams.
+"""
 
 import numpy as np
 import pytest
@@ -6,7 +9,7 @@ import torch
 
 from gpu_util import dev, note
 from oracle import adapter as oracle
-from test_gpu_adapter import U, check_forward, make, ops, plan_of, val, within
+from test_gpu_adapter import U, check_backward, check_forward, make, ops, plan_of, val, within
 
 pytestmark = pytest.mark.gpu
 
@@ -97,3 +100,48 @@ def test_a_plan_used_on_another_stream_and_dropped():
     assert again.data_ptr() != at
     torch.cuda.synchronize()
     assert torch.equal(got, want)
+
+
+# (T, k, E, L, d, f, r): eight slices of 2112 and six of 1344, column groups of unequal width, ranks in two workgroups; many experts
+WIDE = [(40, 2, 3, 2, 2112, 1344, 16), (40, 2, 3, 2, 2112, 1344, 64), (40, 2, 3, 2, 1344, 2112, 40), (128, 2, 64, 1, 2048, 640, 8),
+        (9, 1, 1, 1, 4096, 576, 24)]
+
+
+@pytest.mark.parametrize("p", [0.0, 0.25], ids=["plain", "dropout"])
+@pytest.mark.parametrize("sort", [False, True], ids=["few", "sorted"])
+@pytest.mark.parametrize("T,k,E,L,d,f,r", WIDE)
+def test_forward_of_wide_matrices(T, k, E, L, d, f, r, sort, p):
+    note(f"adapter wide forward {T} {k} {E} {L} {d} {f} {r} sorted={sort} p={p}")
+    c = make(33, T, k, E, L, d, f, r)
+    check_forward(c, plan_of(c, sort), p=p)
+
+
+@pytest.mark.parametrize("p", [0.0, 0.1], ids=["plain", "dropout"])
+@pytest.mark.parametrize("T,k,E,L,d,f,r", WIDE)
+def test_backward_of_wide_matrices(T, k, E, L, d, f, r, p):
+    note(f"adapter wide backward {T} {k} {E} {L} {d} {f} {r} p={p}")
+    c = make(34, T, k, E, L, d, f, r)
+    check_backward(c, plan_of(c, True), p=p)
+
+
+@pytest.mark.parametrize("r", [8, 16, 24, 32, 40, 64])
+def test_dropout_at_every_rank_of_few_rows_and_of_the_backward(r):
+    note(f"adapter dropout few, backward r={r}")
+    c = make(35, 150, 2, 3, 2, 192, 128, r)
+    check_forward(c, plan_of(c, False), p=0.25)
+    check_backward(c, plan_of(c, True), p=0.1)
+
+
+# (T, E, L): pieces of 256, 640 and 2048 rows of a contraction, several to a group, next to groups of one
+@pytest.mark.parametrize("T,E,L,p", [(7000, 2, 3, 0.0), (20002, 1, 2, 0.1), (70001, 1, 1, 0.0)])
+def test_backward_of_many_rows(T, E, L, p):
+    note(f"adapter backward many rows {T} {E} {L} p={p}")
+    c = make(36, T, 1, E, L, 64, 64, 8)
+    check_backward(c, plan_of(c, True), p=p)
+
+
+def test_backward_of_many_rows_and_wide_matrices():
+    """Pieces, column groups and ranks in two workgroups together, and both products of gate/up."""
+    note("adapter backward many rows, wide")
+    c = make(37, 1500, 1, 2, 2, 1344, 640, 40)
+    check_backward(c, plan_of(c, True), p=0.1)
