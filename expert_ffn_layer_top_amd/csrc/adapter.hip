@@ -1488,9 +1488,11 @@ void launch_both(int rows, const ShrinkArgs& s, const ExpandArgs& e, hipStream_t
 
 template <int MODE, bool DROP>
 void launch_rows(const RowArgs& a, hipStream_t st) {
-  constexpr int W = kRowThreads / 64;
-  if (a.R <= W) adapter_row_kernel<1, MODE, DROP><<<a.rows.n, kRowThreads, 0, st>>>(a);
-  else if (a.R <= 2 * W) adapter_row_kernel<2, MODE, DROP><<<a.rows.n, kRowThreads, 0, st>>>(a);
+  constexpr int W = kRowThreads / 64;       // (8: gate/up has 16 ranks at the least, down 64 at the most)
+  if constexpr (MODE == kAdd) {
+    if (a.R <= W) return adapter_row_kernel<1, MODE, DROP><<<a.rows.n, kRowThreads, 0, st>>>(a);
+  }
+  if (a.R <= 2 * W) adapter_row_kernel<2, MODE, DROP><<<a.rows.n, kRowThreads, 0, st>>>(a);
   else if (a.R <= 4 * W) adapter_row_kernel<4, MODE, DROP><<<a.rows.n, kRowThreads, 0, st>>>(a);
   else if (a.R <= 8 * W) adapter_row_kernel<8, MODE, DROP><<<a.rows.n, kRowThreads, 0, st>>>(a);
   else if constexpr (MODE == kSwiglu) adapter_row_kernel<16, MODE, DROP><<<a.rows.n, kRowThreads, 0, st>>>(a);
