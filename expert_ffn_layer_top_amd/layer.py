@@ -149,7 +149,7 @@ QUANT_CALLS_FWD = ("quant_a",)
 QUANT_CALLS = ("quant_dg", "quant_du", "quant_dyT", "quant_xT")
 # (block-128: "quant_dy" gives dYexp's row blocks and token blocks from one read, in place of quant_dyT)
 ROW_CALLS = ("route", "permute", "combine", "combine_bwd", "permute_bwd", "route_bwd")
-# (with adapters: the plan, one or two kernels for each forward call, four to seven for each backward one)
+# (with adapters: the plan, one or two kernels for each forward call, four or five for each backward one)
 ADAPTER_CALLS = ("adapter_plan", "adapter_gate_up", "adapter_down", "adapter_down_bwd", "adapter_gate_up_bwd")
 # MXFP8: each expert's rows start at a multiple of MX_PAD on the padded token axis of the
 # weight-gradient operands.  128 = one K step of those products: every step's 128-byte piece of an
@@ -164,7 +164,7 @@ def forward(x, weights, k, logits=None, mxfp8=False, want_probs=False, events=No
     """Layer forward.  x [T, d] bf16; logits [T, E] fp32 unless weights.w_r is given.
     Returns the context dict that `backward` consumes (all intermediate tensors), with y.
     events: optional {name: (start, end)} of torch.cuda.Event pairs, recorded on the current
-    stream around the calls named in GEMM_CALLS and ROW_CALLS.
+    stream around the calls named in GEMM_CALLS, ROW_CALLS and, with adapters, ADAPTER_CALLS (and QUANT_CALLS in the 8-bit formats).
     recompute: keep neither G, U nor A (3 n f bf16 values) for the backward, which then runs the
     gate/up product again on the kept permuted input (per-layer activation recompute, [card]
     "Supercharging Olmo-core ...": used at the largest scale).  The 8-bit formats still keep A's token

@@ -1,4 +1,4 @@
-"""More of the layer with adapters: what a frozen layer's forward keeps."""
+"""More of the layer with adapters: what a frozen layer's forward keeps, the events around its calls."""
 
 import pytest
 import torch
@@ -37,3 +37,16 @@ def test_a_frozen_forward_keeps_nothing_for_the_weights(fmt):
                 # (without adapters the MXFP8 backward of a layer trained whole quantises dYexp from fp32, not from bf16)
                 if name in out and (with_adapters or "mxfp8" not in fmt or name == "d_logits"):
                     assert torch.equal(out[name], want[name]), (with_adapters, recompute, name)
+
+
+@FORMATS
+def test_events_bracket_every_call_of_the_adapters(fmt):
+    layer, _ = mods()
+    note(f"layer adapters events {fmt}")
+    c = Case(T=150, d=256, f=128)
+    events = {name: tuple(torch.cuda.Event(enable_timing=True) for _ in range(2)) for name in layer.ADAPTER_CALLS}
+    ctx = layer.forward(c.x, c.w, c.k, logits=c.logits, adapters=c.ad, adapter_ids=c.ids, events=events, **fmt)
+    layer.backward(ctx, c.w, c.dy, events=events)
+    torch.cuda.synchronize()
+    for name, (start, end) in events.items():
+        assert start.elapsed_time(end) > 0, name            # (an event that was not recorded raises)
