@@ -64,8 +64,9 @@ __device__ __forceinline__ void wave_fence() {
 // ---------------------------------------------------------------- the plan
 
 // Rows of one piece of a group's contraction in the weight gradients: pieces enough for the chip where few
-// groups hold the rows, long enough that their fp32 partial sums (2 R C 4 bytes each) stay a fraction of the
-// rows' own bytes.  A 32nd of the rows: the backward of 32768 rows of 64 experts took 363 us, 387 with a 64th (most experts
+// groups hold the rows.  A piece's fp32 sums are written and read, 8 R C bytes against the 2 C of each of its rows: with 2048 rows
+// an eighth of the rows' own bytes for 64 ranks and less for fewer, with 256 (up to 8192 rows) as much as they for 64 ranks and
+// twice that for A's 128 of gate/up.  A 32nd of the rows: the backward of 32768 rows of 64 experts took 363 us, 387 with a 64th (most experts
 // then have two pieces), and that of 32768 rows of one expert, wider, 703 and 745.
 __host__ __device__ inline int piece_rows(int n) {
   const int want = (n + 31) / 32;
@@ -507,10 +508,11 @@ __device__ __forceinline__ int staged(int row, int chunk) { return row * 8 + (ch
 // is multiplied, into the wave's staging, and come from there as operands.  Rows past the tile and ranks past R are copies
 // of the last one, which nobody stores.
 //
-// What bounds it is memory: 131072 rows of 4096 (1.07 GB) by 32 ranks of 512 matrices take 263 us, and the L2s miss 1.33 GB
-// in that time, 5.0 TB/s; a stream of the same rows alone reaches 5.5 to 6.  Loading fragments without the staging (16
+// What bounds it is memory: 131072 rows of 4096 (1.07 GB) by 32 ranks of 512 matrices take 250 to 263 us, and the L2s miss 1.33 GB
+// in that time, 5.0 to 5.3 TB/s; a stream of the same rows alone reaches 5.5 to 6.  Loading fragments without the staging (16
 // rows of 16 bytes in neighbouring lanes) with two units of loads in registers took 282: registers left two waves per
-// SIMD, here there are three (four for 16 ranks without dropout, two for 64, one for 128).  A tile's K starting at a
+// SIMD, here there are three (four for 16 ranks without dropout, two for 64, one for 128).  With dropout 32 ranks do not fit
+// three waves a SIMD and spill 18 registers (76 bytes of scratch a lane), 64 ranks 2.  A tile's K starting at a
 // place of its own, so that fewer workgroups read the same columns at once, changed nothing.
 template <int NB, int RT, bool DROP, int STEP = 4>
 __device__ __forceinline__ void shrink_tile(const ShrinkArgs& a, const Tile& t, const PlanLayout& p, const uint16_t* x,
@@ -652,8 +654,8 @@ __global__ __launch_bounds__(256, RT == 1 && !DROP ? 4 : RT <= 2 ? 3 : RT == 4 ?
 // ---------------------------------------------------------------- expand
 //
 // A wave takes 16 rows after another of a tile and 128 columns, for which it holds W's fragments.  It reads what it adds to
-// and writes the sum, and that is what it costs: SwiGLU of 131072 x 2048 takes 483 us (2.7 GB, 5.6 TB/s), the addition to
-// 131072 x 7168 674 us (3.8 GB, 5.5 TB/s); a copy runs at 4.9.  The loads of the first 16 rows are issued before W's, on
+// and writes the sum, and that is what it costs: SwiGLU of 131072 x 2048 takes 491 us (2.7 GB, 5.5 TB/s), the addition to
+// 131072 x 7168 685 us (3.8 GB, 5.5 TB/s); a copy runs at 4.9.  The loads of the first 16 rows are issued before W's, on
 // whose arrival everything else waits; where a launch has few tiles their rows are shared among up to four waves (4012 rows
 // of 1344: 27 -> 14 us, before one kernel did both products of such calls).
 
@@ -1222,8 +1224,8 @@ __device__ __forceinline__ long long piece_slot(int pos, int piece, bool first) 
 // registers half a step (32 rows) ahead, v's and the row numbers a whole one; loads past the piece read its last row.
 //
 // Bound by memory and its latency: 131072 rows of 4096 by 32 ranks take 243 us (1.28 GB through the L2s' misses, 5.3 TB/s).
-// More than 32 ranks are a workgroup for each 32, whose second reading of y comes from the L2: 64 ranks take 320 us, where a
-// wave with all 64 (one wave per SIMD then) took 412, and a workgroup of eight waves, four for each half, 441.
+// More than 32 ranks are a workgroup for each 32, whose second reading of y comes from the L2: 64 ranks of fp32 take 338 us.  With v in two
+// bf16 values they took 320, where a wave with all 64 (one wave per SIMD then) took 412, and a workgroup of eight waves, four for each half, 441.
 template <int RT, bool DROP, bool F32>
 __global__ __launch_bounds__(256, 2) void adapter_wgrad_kernel(WgradArgs a) {
   // a thread stages a pair of rows and VR ranks: 16 bytes of each row
@@ -1409,7 +1411,8 @@ constexpr int kGridCap = 8192;   // workgroups of a launch; more tiles are taken
 int tiles_cap(const Rows& r) { return plan_layout(r.n, r.E, r.L).tiles_cap; }
 
 // Tiles that a call is likely to have (their number is on the device): those of whole tiles, and one more for half of the
-// experts' adapters that can have rows.
+// experts' adapters that can have rows.  Of many adapters loaded and few in use it is too high, and such calls are cut into fewer pieces
+// than the chip could take: 4096 rows of 64 experts and 256 adapters count 2112, also where one adapter has them all and there are about 64.
 long long likely_tiles(int n, int E, int L) {
   const long long groups = static_cast<long long>(E) * L;
   return n / kTileRows + ((groups < n ? groups : n) + 1) / 2;
@@ -1463,7 +1466,8 @@ void launch_expand(ExpandArgs a, hipStream_t st) {
 // twice.  Gate/up, down and the plan, two kernels -> one, us: 16 experts x 5 adapters of 8 ranks (d 2112, f 1344), 1024 rows 50 ->
 // 32 (with 32 or 64 rows 37 and 41), 4096 52 -> 46 (16 rows 53, 64 rows 61), 8192 71 -> 69, 16384 113 -> 141; 64 x 8 of 16 (d 2048, f
 // 1024), 4096 rows 73 -> 66, 16384 143 -> 128, 65536 (46 rows a tile) 325 -> 336; 64 x 32 of 32, 1024 rows 121 -> 109, 16384 283 ->
-// 270, 65536 478 -> 475; 128 x 16 of 32 (d 4096, f 768), 1024 rows 126 -> 117, 16384 330 -> 336, 65536 612 -> 636.
+// 270, 65536 478 -> 475; 128 x 16 of 32 (d 4096, f 768), 1024 rows 126 -> 117, 16384 (exactly at the limit of 1280, on the wrong side by two
+// percent) 330 -> 336, 65536 612 -> 636.
 int both_rows(const Rows& r, int R) {
   if (R > 64) return 0;
   const long long tiles = likely_tiles(r.n, r.E, r.L), rows = r.n / tiles, groups = tiles - r.n / kTileRows;

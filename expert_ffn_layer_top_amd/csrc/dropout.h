@@ -6,8 +6,8 @@
 // one Philox4x32 block (Salmon, Moraes, Dror, Shaw, "Parallel random numbers: as easy as 1, 2, 3", SC 2011) with 7
 // rounds, the least that the paper finds to pass every test of its battery, of the counter (c / 8 + site 2^28, r, offset) under
 // the seed as the key: a chunk costs 14 full 32 x 32 products, the slow part (quarter rate).  Kernels that read 2
-// bytes an element and do little else notice it: the adapters' A x of 131072 rows of 7168 takes 325 us without and 350 to 390
-// with dropout, their weight gradient of 32768 rows of 2048 31 and 37.
+// bytes an element and do little else notice it: the adapters' A x of 131072 rows of 7168 takes 323 us without and 350 to 390
+// with dropout (part of it registers that do not fit), their weight gradient of 32768 rows of 2048 27 and 42.
 #pragma once
 
 #include "common.h"

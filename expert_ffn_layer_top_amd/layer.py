@@ -184,7 +184,8 @@ def forward(x, weights, k, logits=None, mxfp8=False, want_probs=False, events=No
     serving: a forward that no backward follows; block-128 products only, which then write neither
     G nor U, make no token blocks of A and need no transposed copies of the weights.
     adapters, adapter_ids: an Adapters and each token's number in it ([T] int32; outside [0, L): none, that
-    token's rows are the layer's own).
+    token's rows are the layer's own).  Their form for few rows (ops.ADAPTER_FEW_ROWS) is that of a serving forward; a forward
+    that a backward may follow sorts the rows, however few.
     adapter_dropout: an ops.Dropout of the adapters' inputs (gate/up's at its site, down's at the next one).
     dropout: an ops.Dropout of the combined output; residual [T, d] bf16: added to it.  Then y = residual +
     dropout(combined); the residual's gradient is dy, and dx does not hold it.  Under mxfp8 the backward rounds the

@@ -488,7 +488,8 @@ def unpermute_combine_dropout_bwd(dy, yexp, topk_gate, dest, drop):
 # Up to this many rows every row reads its adapter by itself in the forward; more are sorted by adapter first.  Both
 # calls and the plan, us at 512 rows and at 1024: 64 experts, 8 adapters of rank 16 (d 2048, f 1024) 36 and 62 by row, 45 and 49
 # sorted; 128 experts, 16 adapters (d 4096, f 768) 52 and 108, 70 and 124; one expert, 32 adapters 45 and 80, 40 and 43; eight
-# experts, one adapter of rank 64 83 and 155, 70 and 81.
+# experts, one adapter of rank 64 83 and 155, 70 and 81.  So at the limit the rows by themselves are faster by 9 and 18 us with many experts,
+# and slower by 5 and 13 with few experts or a large rank: it is one limit for all.
 ADAPTER_FEW_ROWS = 512
 
 

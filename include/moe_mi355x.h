@@ -331,6 +331,7 @@ int moe_unpermute_combine_dropout_bwd(const uint16_t* dy, const uint16_t* yexp, 
  *   down:     v = (m a) A^T;     y' = y + s v B
  * Products of bf16 values are summed in fp32; between its two products v (and dv of the backward) is held in fp32, and v is
  * handed out as bf16; g', u', y' are rounded once, and a' comes from the unrounded g', u'.
+ * An infinite element of B makes NaN of the columns that it reaches where there is a plan (v meets it in parts, some of them 0).
  * The last bits of a row may differ with the number of rows in the call and with a plan, since sums are cut by them.
  * Rows from offsets[E] on are left as they were.  Offsets that fall or lie outside [0, n] are read as their running maximum
  * within [0, n], with a plan and without one: rows go to other experts then, and no access goes out of bounds. */
