@@ -102,6 +102,38 @@ def test_a_plan_used_on_another_stream_and_dropped():
     assert torch.equal(got, want)
 
 
+def test_a_plan_made_before_a_capture():
+    """Calls captured with a plan of eager work, replayed with eager work in between; the plan is dropped after the last replay."""
+    note("adapter plan before a capture")
+    c = make(38, 700, 2, 4, 3, 192, 128, 16)
+    plan = plan_of(c, True)
+    up, down = [c["t_" + w] for w in ("a_gu", "b_gate", "b_up", "scale")], [c["t_" + w] for w in ("a_down", "b_down", "scale")]
+
+    def step():
+        g, u, a, v1 = ops().adapter_gate_up(c["t_x"], c["t_g"], c["t_u"], c["t_a"], plan, *up, want_v=True)
+        y, v2 = ops().adapter_down(a, c["t_y"], plan, *down, want_v=True)
+        return (g, u, a, v1, y, v2, *ops().adapter_down_bwd(c["t_y"], a, v2, g, u, c["t_dg"], c["t_du"], plan, *down))
+    want = [t.clone() for t in step()]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for i in range(3):
+        for t in got:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(s, t) for s, t in zip(got, want)), i
+        assert all(torch.equal(s, t) for s, t in zip(step(), want)), i
+    del plan, graph, got
+    torch.cuda.synchronize()
+    check_forward(c, plan_of(c, True))
+
+
 # (T, k, E, L, d, f, r): eight slices of 2112 and six of 1344, column groups of unequal width, ranks in two workgroups; many experts
 WIDE = [(40, 2, 3, 2, 2112, 1344, 16), (40, 2, 3, 2, 2112, 1344, 64), (40, 2, 3, 2, 1344, 2112, 40), (128, 2, 64, 1, 2048, 640, 8),
         (9, 1, 1, 1, 4096, 576, 24)]

@@ -112,11 +112,8 @@ def lacks(v):
 
 
 @pytest.mark.parametrize("p", [0.0, 0.5], ids=["plain", "dropout"])
-@pytest.mark.parametrize("sort", [False, True], ids=["few", "sorted"])
-@pytest.mark.parametrize("n,E,L,d,f,r", SIZES)
+@pytest.mark.parametrize("n,E,L,d,f,r,sort", [(*size, sort) for size in SIZES for sort in (False, True) if sort or size[0] <= 512])
 def test_forward(n, E, L, d, f, r, sort, p):
-    if n > 512 and not sort:
-        pytest.skip("more rows are always sorted")
     note(f"adapter exact forward {n} {E} {L} {d} {f} {r} sorted={sort} p={p}")
     c = make(n, E, L, d, f, r)
     plan = ops().adapter_plan(i32_to_dev(c["ids"]), i32_to_dev(c["off"]), L, backward=sort)

@@ -50,3 +50,19 @@ def test_events_bracket_every_call_of_the_adapters(fmt):
     torch.cuda.synchronize()
     for name, (start, end) in events.items():
         assert start.elapsed_time(end) > 0, name            # (an event that was not recorded raises)
+
+
+@FORMATS
+def test_a_frozen_layer_that_owns_its_router_needs_no_x(fmt):
+    layer, _ = mods()
+    note(f"layer frozen with its router {fmt}")
+    c = Case(T=150, d=256, f=128)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    w = layer.Weights(c.w.w_gate, c.w.w_up, c.w.w_down, w_r=torch.randn((256, c.E), generator=g, device="cuda", dtype=torch.float32) / 16)
+    for kw in ({}, dict(adapters=c.ad, adapter_ids=c.ids)):
+        want = layer.backward(layer.forward(c.x, w, c.k, **kw, **fmt), w, c.dy)
+        out = layer.backward(layer.forward(c.x, w, c.k, frozen=True, **kw, **fmt), w, c.dy)
+        assert "dw_r" in want and not any(name.startswith("dw_") for name in out)
+        for name in ("d_logits", "dx"):
+            if kw or "mxfp8" not in fmt or name == "d_logits":
+                assert torch.equal(out[name], want[name]), name
